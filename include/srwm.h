@@ -21,9 +21,11 @@
  *
  * Common rules for every entry point below:
  *   - Pointers are DEVICE memory (cudaMalloc'd or managed) of fp32, contiguous,
- *     16-byte aligned.  The caller owns all buffers.  srwm_forward,
- *     srwm_forward_balanced, srwm_forward_balanced_noalloc, srwm_forward_from,
- *     srwm_step and srwm_backward make no device allocation.
+ *     16-byte aligned, unless an entry point says otherwise.  The caller owns
+ *     all buffers.  srwm_forward, srwm_forward_balanced,
+ *     srwm_forward_balanced_noalloc, srwm_forward_from, srwm_step,
+ *     srwm_backward and the srwm_linattn_* and srwm_groupnorm_* entry points
+ *     make no device allocation.
  *   - State the library keeps, per device, for the life of the process:
  *       * the device status word (srwm_last_device_status), a file-scope
  *         __device__ variable, present once the library is loaded; its device
@@ -45,8 +47,9 @@
  *     stream) and the call returns without waiting.  Argument errors are
  *     returned before anything is enqueued; nothing is written then.
  *   - Supported: d in {16, 32, 64}, n_lr in {1, 4}, softmax_input in {0, 1}.
- *   - Outputs must not overlap inputs or each other (srwm_step alone allows
- *     W_out == W_in exactly, for an in-place update).
+ *   - Outputs must not overlap inputs or each other (srwm_step and
+ *     srwm_linattn_step alone allow the state's output to be its input
+ *     exactly, for an in-place update).
  *   - Results are deterministic: the same inputs give the same bits.
  */
 #ifndef SRWM_H
@@ -69,6 +72,20 @@ enum srwm_status {
     SRWM_ERR_CUDA = 6,        /* a CUDA runtime call failed (launch, attribute, ...)      */
     SRWM_ERR_TIMEOUT = 7,     /* a kernel gave up a bounded wait (see srwm_last_device_status) */
     SRWM_ERR_NOT_DEVICE = 8   /* a pointer is not device-accessible CUDA memory           */
+};
+
+/* Element types of the operators that take more than fp32 (linear attention, group norm). */
+enum srwm_dtype {
+    SRWM_F32 = 0,
+    SRWM_BF16 = 1,
+    SRWM_F16 = 2
+};
+
+/* Activations of srwm_groupnorm_forward and srwm_groupnorm_backward. */
+enum srwm_activation {
+    SRWM_ACT_NONE = 0,
+    SRWM_ACT_SILU = 1,   /* z * sigmoid(z) */
+    SRWM_ACT_RELU = 2    /* max(z, 0); slope 0 at z <= 0 */
 };
 
 /*
@@ -302,6 +319,139 @@ size_t srwm_layer_workspace_bytes(int B, int T, int H, int d, int n_lr, int d_ff
  * calls made afterwards.  SRWM_ERR_UNSUPPORTED for any other mode.
  */
 int srwm_debug_set_layer_gemm(int mode);
+
+/*
+ * srwm_linattn_forward -- linear attention with a decay per head, over whole
+ * sequences (a prompt, or a training batch's forward pass).  It is the fast
+ * weight memory without self-reference: per sequence b and head h, with
+ * g = exp(log_decay[h]),
+ *   S_t = g S_{t-1} + k_t v_t^T          (S_0 = S_init[b,h], or 0)
+ *   o_t = scale * S_t^T q_t
+ * for t = 1 .. n_b, n_b the sequence's length.  Computed in chunks of d tokens:
+ * inside a chunk as a masked product, from earlier chunks through the state.
+ *
+ *   q, k, v    [B, T, H, d] of `dtype`; token (b, t) starts at element
+ *              (b * T + t) * ld, its H * d values are contiguous.  So the
+ *              three may be contiguous (ld = H * d) or slices of one packed
+ *              projection [B, T, 3, H, d] (ld = 3 * H * d).
+ *   ld         elements between two tokens' rows of q, k and v: at least
+ *              H * d, a multiple of 16 bytes
+ *   log_decay  [H] fp32, log g <= 0; 0 keeps everything (the sum over all
+ *              tokens), -infinity keeps the current token alone.  Values above
+ *              0 are taken as 0.
+ *   S_init     [B, H, d, d] fp32 (row = index of k, column = index of v), or
+ *              NULL for zero
+ *   lengths    [B] int32 on the device (4-byte aligned), the valid tokens of
+ *              each sequence (its first ones), or NULL for T each; a value below 0 counts as 0,
+ *              one above T as T.  Rows of q, k, v at and past the length are
+ *              not read, so they may hold anything.
+ *   dtype      enum srwm_dtype of q, k, v and o
+ *   scale      factor on o, e.g. 1 / sqrt(d)
+ *   o          [B, T, H, d] of `dtype`, contiguous, written; rows at and past
+ *              a sequence's length get zeros
+ *   S_final    [B, H, d, d] fp32, written: S at the sequence's end (S_init,
+ *              or 0, for an empty one); or NULL
+ *   workspace  device scratch of srwm_linattn_workspace_bytes(...) bytes,
+ *              16-byte aligned, contents irrelevant on entry, untouched by
+ *              others until the work on `stream` ends
+ *
+ * Supported: d in {16, 32, 64}; T = 0 is valid (q, k, v, o may be NULL then).
+ * States are fp32 and every sum is accumulated in fp32.  The products run on
+ * the tensor cores in fp16 after scaling by powers of two: fp32 inputs as
+ * (high, low) pairs, which keeps about 22 bits relative to the largest
+ * magnitude among 16 neighbouring tokens of a head.  Inputs must be finite:
+ * an infinity or NaN in a valid token reaches every output of its sequence
+ * and head from its chunk on, and of no other.
+ */
+size_t srwm_linattn_workspace_bytes(int B, int T, int H, int d);
+int srwm_linattn_forward(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
+                         const float* S_init, const int* lengths, int dtype, int B, int T, int H, int d,
+                         float scale, void* o, float* S_final, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * srwm_linattn_step -- one token of the same recurrence for every sequence
+ * (decoding): S_out = g S_in + k v^T, o = scale * S_out^T q.  Feeding S_out
+ * back as S_in token by token reproduces srwm_linattn_forward.
+ *
+ *   q, k, v  [B, H, d] of `dtype`, sequence b at element b * ld (as above)
+ *   S_in     [B, H, d, d] fp32
+ *   o        [B, H, d] of `dtype`, contiguous, written
+ *   S_out    [B, H, d, d] fp32, written; may be the same pointer as S_in (in
+ *            place) but must not partially overlap it
+ */
+int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
+                      const float* S_in, int dtype, int B, int H, int d, float scale, void* o, float* S_out,
+                      void* stream);
+
+/*
+ * srwm_linattn_backward -- gradients through srwm_linattn_forward, from the
+ * cotangents of o and (optionally) of S_final, for the same q, k, v, ld,
+ * log_decay, S_init, lengths, dtype, sizes and scale.  With D_t = dL/dS_t
+ * (D_n = dS_final + scale q_n do_n^T, D_t = scale q_t do_t^T + g D_{t+1}):
+ *   dq_t = scale * S_t do_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t,
+ *   dS_init = g D_1 (dS_final for an empty sequence).
+ * The decay is a constant of the head: it gets no gradient.
+ *
+ *   do_        [B, T, H, d] of `dtype`, contiguous: dL/do (not read at and
+ *              past a sequence's length)
+ *   dS_final   [B, H, d, d] fp32: dL/dS_final, or NULL for zero
+ *   dq, dk, dv [B, T, H, d] of `dtype`, token rows ld_grad elements apart
+ *              (same rules as ld; the three may interleave in one packed
+ *              array), written; rows at and past the length get zeros
+ *   dS_init    [B, H, d, d] fp32, written; or NULL
+ *   workspace  device scratch of srwm_linattn_backward_workspace_bytes(...)
+ */
+size_t srwm_linattn_backward_workspace_bytes(int B, int T, int H, int d);
+int srwm_linattn_backward(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
+                          const float* S_init, const int* lengths, int dtype, int B, int T, int H, int d,
+                          float scale, const void* do_, const float* dS_final, void* dq, void* dk, void* dv,
+                          long long ld_grad, float* dS_init, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * srwm_groupnorm_forward -- group normalisation with an activation, channels
+ * last: y = act((x - mean) * rstd * gamma + beta), where mean and the biased
+ * variance are taken over the L positions and the C/G neighbouring channels of
+ * one sample and group, and rstd = 1 / sqrt(var + eps).  With L = 1, N = B*T,
+ * C = H*d and G = H it is the norm of each head's output of a token.
+ *
+ *   x         [N, L, C] of `dtype`, contiguous
+ *   gamma     [C] fp32, or NULL for ones
+ *   beta      [C] fp32, or NULL for zeros
+ *   eps       > 0
+ *   activation  enum srwm_activation
+ *   y         [N, L, C] of `dtype`, written
+ *   mean, rstd  [N, G] fp32, written (srwm_groupnorm_backward reads them);
+ *             or NULL, both or either
+ *   workspace device scratch of srwm_groupnorm_workspace_bytes(...) bytes,
+ *             16-byte aligned, untouched by others until the work ends
+ *
+ * Supported: G divides C, C a multiple of 8 and at most 8192; N >= 0, L >= 1
+ * (N = 0 does nothing; x and y may be NULL then).  Statistics are fp32, the
+ * variance from deviations from the mean.
+ */
+size_t srwm_groupnorm_workspace_bytes(long long N, long long L, int C, int G);
+int srwm_groupnorm_forward(const void* x, const float* gamma, const float* beta, int dtype, long long N,
+                           long long L, int C, int G, float eps, int activation, void* y, float* mean,
+                           float* rstd, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * srwm_groupnorm_backward -- gradients through srwm_groupnorm_forward, from
+ * dy = dL/dy and the forward pass's x, mean and rstd (the mean and rstd of the
+ * same x: the derivative of both is part of dx).
+ *
+ *   dx        [N, L, C] of `dtype`, written
+ *   dgamma, dbeta  [C] fp32, written (zeros for N = 0): sums over all samples
+ *             and positions in a fixed order; or NULL, both or either
+ * ReLU's slope is taken at the sign of its argument evaluated in fp64 where
+ * fp32 cannot tell it.
+ */
+size_t srwm_groupnorm_backward_workspace_bytes(long long N, long long L, int C, int G);
+int srwm_groupnorm_backward(const void* x, const float* gamma, const float* beta, const float* mean,
+                            const float* rstd, const void* dy, int dtype, long long N, long long L, int C, int G,
+                            int activation, void* dx, float* dgamma, float* dbeta, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* srwm_status_string(int status);

@@ -19,11 +19,18 @@ SRWM_OK = 0
 SRWM_ERR_SHAPE = 2
 SRWM_ERR_TIMEOUT = 7
 
+# enum srwm_dtype and enum srwm_activation
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
+
 EXPORTS = ("srwm_forward", "srwm_forward_balanced", "srwm_forward_balanced_noalloc",
            "srwm_forward_workspace_bytes", "srwm_forward_from", "srwm_forward_host",
            "srwm_forward_host_workspace_bytes",
            "srwm_step", "srwm_backward", "srwm_backward_workspace_bytes",
-           "srwm_layer_forward", "srwm_layer_workspace_bytes", "srwm_debug_set_layer_gemm", "srwm_status_string", "srwm_last_device_status", "srwm_set_wait_limit_ns",
+           "srwm_layer_forward", "srwm_layer_workspace_bytes", "srwm_debug_set_layer_gemm",
+           "srwm_linattn_forward", "srwm_linattn_workspace_bytes", "srwm_linattn_step", "srwm_linattn_backward",
+           "srwm_linattn_backward_workspace_bytes", "srwm_groupnorm_forward", "srwm_groupnorm_workspace_bytes",
+           "srwm_groupnorm_backward", "srwm_groupnorm_backward_workspace_bytes", "srwm_status_string", "srwm_last_device_status", "srwm_set_wait_limit_ns",
            "srwm_debug_skip_x_chunk", "srwm_debug_set_segment_len", "srwm_debug_wrap_len",
            "srwm_debug_wrap_pieces", "srwm_debug_chunk_plan", "srwm_probe_fma")
 
@@ -84,6 +91,25 @@ def _lib():
         lib.srwm_layer_workspace_bytes.restype = SZ
         lib.srwm_debug_set_layer_gemm.argtypes = [I]
         lib.srwm_debug_set_layer_gemm.restype = I
+        F = ctypes.c_float
+        lib.srwm_linattn_workspace_bytes.argtypes = [I, I, I, I]
+        lib.srwm_linattn_workspace_bytes.restype = SZ
+        lib.srwm_linattn_forward.argtypes = [P, P, P, LL, P, P, P, I, I, I, I, I, F, P, P, P, SZ, P]
+        lib.srwm_linattn_forward.restype = I
+        lib.srwm_linattn_step.argtypes = [P, P, P, LL, P, P, I, I, I, I, F, P, P, P]
+        lib.srwm_linattn_step.restype = I
+        lib.srwm_linattn_backward_workspace_bytes.argtypes = [I, I, I, I]
+        lib.srwm_linattn_backward_workspace_bytes.restype = SZ
+        lib.srwm_linattn_backward.argtypes = [P, P, P, LL, P, P, P, I, I, I, I, I, F, P, P, P, P, P, LL, P, P, SZ, P]
+        lib.srwm_linattn_backward.restype = I
+        lib.srwm_groupnorm_workspace_bytes.argtypes = [LL, LL, I, I]
+        lib.srwm_groupnorm_workspace_bytes.restype = SZ
+        lib.srwm_groupnorm_forward.argtypes = [P, P, P, I, LL, LL, I, I, F, I, P, P, P, P, SZ, P]
+        lib.srwm_groupnorm_forward.restype = I
+        lib.srwm_groupnorm_backward_workspace_bytes.argtypes = [LL, LL, I, I]
+        lib.srwm_groupnorm_backward_workspace_bytes.restype = SZ
+        lib.srwm_groupnorm_backward.argtypes = [P, P, P, P, P, P, I, LL, LL, I, I, I, P, P, P, P, SZ, P]
+        lib.srwm_groupnorm_backward.restype = I
         lib.srwm_status_string.argtypes = [I]
         lib.srwm_status_string.restype = ctypes.c_char_p
         lib.srwm_last_device_status.argtypes = [P]
@@ -355,6 +381,227 @@ def srwm_layer_forward(u, H, n_lr, softmax_input, ln1_gamma, ln1_beta, W0, ln2_g
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(rc, "srwm_layer_forward")
     return out, W_final
+
+
+def _arr(t, name, shape, dtype, optional=False):
+    """The address of a contiguous CUDA tensor of this shape and type."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr() if t.numel() else None
+
+
+def _token_rows(tensors, names, dtype):
+    """The addresses of [B,T,H,d] (or [B,H,d]) tensors whose tokens lie one
+    common distance apart, and that distance in elements."""
+    shape, ld = tensors[0].shape, None
+    H, d = shape[-2:]
+    for t, name in zip(tensors, names):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype or not t.is_cuda:
+            raise ValueError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.numel() == 0:
+            continue
+        st = t.stride()
+        B, T = (shape[0], shape[1]) if t.dim() == 4 else (shape[0], 1)
+        mine = H * d if B * T == 1 else st[1] if T > 1 else st[0]
+        if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d) or (T > 1 and B > 1 and st[0] != T * mine):
+            raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
+        if ld is None or B * T == 1:
+            ld = mine
+        elif ld != mine:
+            raise ValueError(f"{', '.join(names)} must have the same strides")
+    return [t.data_ptr() if t.numel() else None for t in tensors], H * d if ld is None else ld
+
+
+def _scratch(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace
+
+
+def _dtype_code(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    return code
+
+
+def _check_lengths(lengths, B):
+    if lengths is None:
+        return None
+    if not isinstance(lengths, torch.Tensor) or lengths.dtype != torch.int32 or not lengths.is_cuda or \
+            not lengths.is_contiguous() or lengths.shape != (B,):
+        raise ValueError(f"lengths must be a contiguous int32 CUDA tensor of {B} values")
+    return lengths.data_ptr()
+
+
+def srwm_linattn_workspace_bytes(B, T, H, d) -> int:
+    return int(_lib().srwm_linattn_workspace_bytes(int(B), int(T), int(H), int(d)))
+
+
+def srwm_linattn_forward(q, k, v, log_decay, scale=None, S_init=None, lengths=None, o=None, S_final=None,
+                         workspace=None, stream=None):
+    """Linear attention with a decay per head: S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k, v [B,T,H,d] are float32, bfloat16 or float16 CUDA tensors, contiguous
+    or views of one packed projection ([B,T,3,H,d].unbind(2)); log_decay [H],
+    S_init [B,H,d,d] (None: zero) and S_final [B,H,d,d] are float32, lengths
+    [B] int32 counts each sequence's valid tokens (None: T); scale is
+    1/sqrt(d) unless given.  Returns (o [B,T,H,d], S_final)."""
+    code = _dtype_code(q, "q")
+    B, T, H, d = q.shape
+    (pq, pk, pv), ld = _token_rows((q, k, v), ("q", "k", "v"), q.dtype)
+    if o is None:
+        o = torch.empty((B, T, H, d), dtype=q.dtype, device=q.device)
+    if S_final is None:
+        S_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+    lib = _lib()
+    workspace = _scratch(workspace, max(16, lib.srwm_linattn_workspace_bytes(B, T, H, d)), q.device)
+    rc = lib.srwm_linattn_forward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
+                                  _arr(S_init, "S_init", (B, H, d, d), torch.float32, True),
+                                  _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
+                                  _arr(o, "o", (B, T, H, d), q.dtype),
+                                  _arr(S_final, "S_final", (B, H, d, d), torch.float32), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(rc, "srwm_linattn_forward")
+    return o, S_final
+
+
+def srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale=None, o_t=None, S_out=None, stream=None):
+    """One token of srwm_linattn_forward from per-sequence states: q_t, k_t, v_t [B,H,d] -> (o_t [B,H,d], S_out).
+
+    S_out may be S_in itself (in-place update)."""
+    code = _dtype_code(q_t, "q_t")
+    B, H, d = q_t.shape
+    (pq, pk, pv), ld = _token_rows((q_t, k_t, v_t), ("q_t", "k_t", "v_t"), q_t.dtype)
+    if o_t is None:
+        o_t = torch.empty((B, H, d), dtype=q_t.dtype, device=q_t.device)
+    if S_out is None:
+        S_out = torch.empty((B, H, d, d), dtype=torch.float32, device=q_t.device)
+    rc = _lib().srwm_linattn_step(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
+                                  _arr(S_in, "S_in", (B, H, d, d), torch.float32), code, B, H, d,
+                                  d ** -0.5 if scale is None else scale, _arr(o_t, "o_t", (B, H, d), q_t.dtype),
+                                  _arr(S_out, "S_out", (B, H, d, d), torch.float32), _stream_handle(stream))
+    _check(rc, "srwm_linattn_step")
+    return o_t, S_out
+
+
+def srwm_linattn_backward_workspace_bytes(B, T, H, d) -> int:
+    return int(_lib().srwm_linattn_backward_workspace_bytes(int(B), int(T), int(H), int(d)))
+
+
+def srwm_linattn_backward(q, k, v, log_decay, do, scale=None, S_init=None, lengths=None, dS_final=None, dq=None,
+                          dk=None, dv=None, dS_init=None, workspace=None, stream=None):
+    """Gradients through srwm_linattn_forward from do [B,T,H,d] and dS_final [B,H,d,d] (None: zero).
+
+    dq, dk, dv may be views of one packed [B,T,3,H,d] array.  Returns
+    (dq, dk, dv, dS_init); the decay gets no gradient."""
+    code = _dtype_code(q, "q")
+    B, T, H, d = q.shape
+    (pq, pk, pv), ld = _token_rows((q, k, v), ("q", "k", "v"), q.dtype)
+    given = (dq is not None) + (dk is not None) + (dv is not None)
+    if given == 0:
+        dq, dk, dv = (torch.empty((B, T, H, d), dtype=q.dtype, device=q.device) for _ in range(3))
+    elif given < 3:
+        raise ValueError("dq, dk and dv: give all three or none")
+    (pdq, pdk, pdv), ldg = _token_rows((dq, dk, dv), ("dq", "dk", "dv"), q.dtype)
+    if dq.shape != q.shape:
+        raise ValueError(f"dq has shape {tuple(dq.shape)}, expected {tuple(q.shape)}")
+    if dS_init is None:
+        dS_init = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+    lib = _lib()
+    workspace = _scratch(workspace, max(16, lib.srwm_linattn_backward_workspace_bytes(B, T, H, d)), q.device)
+    rc = lib.srwm_linattn_backward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
+                                   _arr(S_init, "S_init", (B, H, d, d), torch.float32, True),
+                                   _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
+                                   _arr(do, "do", (B, T, H, d), q.dtype),
+                                   _arr(dS_final, "dS_final", (B, H, d, d), torch.float32, True), pdq, pdk, pdv, ldg,
+                                   _arr(dS_init, "dS_init", (B, H, d, d), torch.float32), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(rc, "srwm_linattn_backward")
+    return dq, dk, dv, dS_init
+
+
+def srwm_groupnorm_workspace_bytes(N, L, C, G) -> int:
+    return int(_lib().srwm_groupnorm_workspace_bytes(int(N), int(L), int(C), int(G)))
+
+
+def _activation_code(activation):
+    code = _ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    return code
+
+
+def srwm_groupnorm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", y=None, mean=None, rstd=None,
+                           workspace=None, stream=None):
+    """Group norm with an activation, channels last: y = act((x - mean) * rstd * gamma + beta).
+
+    x [N,L,C] is a contiguous float32, bfloat16 or float16 CUDA tensor; the
+    statistics are over the L positions and the C/groups channels of a sample's
+    group; gamma, beta [C] are float32 or None (ones, zeros); activation is
+    "none", "silu" or "relu".  Returns (y, mean [N,groups], rstd [N,groups])."""
+    code = _dtype_code(x, "x")
+    N, L, C = x.shape
+    if y is None:
+        y = torch.empty_like(x)
+    if mean is None:
+        mean = torch.empty((N, groups), dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty((N, groups), dtype=torch.float32, device=x.device)
+    lib = _lib()
+    workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_workspace_bytes(N, L, C, groups)), x.device)
+    rc = lib.srwm_groupnorm_forward(_arr(x, "x", (N, L, C), x.dtype), _arr(gamma, "gamma", (C,), torch.float32, True),
+                                    _arr(beta, "beta", (C,), torch.float32, True), code, N, L, C, groups, eps,
+                                    _activation_code(activation), _arr(y, "y", (N, L, C), x.dtype),
+                                    _arr(mean, "mean", (N, groups), torch.float32),
+                                    _arr(rstd, "rstd", (N, groups), torch.float32), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(rc, "srwm_groupnorm_forward")
+    return y, mean, rstd
+
+
+def srwm_groupnorm_backward_workspace_bytes(N, L, C, G) -> int:
+    return int(_lib().srwm_groupnorm_backward_workspace_bytes(int(N), int(L), int(C), int(G)))
+
+
+def srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation="none", dx=None, dgamma=None,
+                            dbeta=None, workspace=None, stream=None):
+    """Gradients through srwm_groupnorm_forward from dy [N,L,C] and the forward
+    pass's mean and rstd.  Returns (dx, dgamma [C], dbeta [C])."""
+    code = _dtype_code(x, "x")
+    N, L, C = x.shape
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dgamma is None:
+        dgamma = torch.empty((C,), dtype=torch.float32, device=x.device)
+    if dbeta is None:
+        dbeta = torch.empty((C,), dtype=torch.float32, device=x.device)
+    lib = _lib()
+    workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_backward_workspace_bytes(N, L, C, groups)), x.device)
+    rc = lib.srwm_groupnorm_backward(_arr(x, "x", (N, L, C), x.dtype), _arr(gamma, "gamma", (C,), torch.float32, True),
+                                     _arr(beta, "beta", (C,), torch.float32, True),
+                                     _arr(mean, "mean", (N, groups), torch.float32),
+                                     _arr(rstd, "rstd", (N, groups), torch.float32), _arr(dy, "dy", (N, L, C), x.dtype),
+                                     code, N, L, C, groups, _activation_code(activation),
+                                     _arr(dx, "dx", (N, L, C), x.dtype), _arr(dgamma, "dgamma", (C,), torch.float32),
+                                     _arr(dbeta, "dbeta", (C,), torch.float32), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(rc, "srwm_groupnorm_backward")
+    return dx, dgamma, dbeta
 
 
 def srwm_debug_set_layer_gemm(mode: int) -> None:
