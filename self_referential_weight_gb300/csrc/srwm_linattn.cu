@@ -1,105 +1,193 @@
-// srwm_linattn.cu -- linear attention with a decay per head: token-by-token
-// kernels, one thread per state column.
+// srwm_linattn.cu -- linear attention with a decay per head: the launches of
+// the chunked kernel (srwm_linattn.cuh), and the single-token kernel.
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "srwm.h"
 #include "srwm_check.h"
-#include "srwm_elem.cuh"
-#include "srwm_linattn.h"
+#include "srwm_linattn.cuh"
 
 namespace srwm {
 namespace {
 
-__device__ __forceinline__ float decay_log2(float log_decay)
+constexpr int kMaxDevices = 64;
+
+template <typename E, int D>
+constexpr int blocks_per_sm()
 {
-    return fmaxf(fminf(log_decay, 0.f) * 1.4426950408889634f, -16384.f);
+    return D == 64 ? (sizeof(E) == 4 ? 2 : 3) : D == 32 ? 8 : 20;
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(D) linattn_kernel(const LinParams p)
+__global__ void __launch_bounds__(LinTile<E, D>::kThreads, blocks_per_sm<E, D>())
+    linattn_kernel(const __grid_constant__ LinParams p)
 {
-    const LinRole& r = p.role[blockIdx.y];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, j = threadIdx.x;
-    __shared__ float sa[D], sb[D];
-    const float g = exp2f(decay_log2(p.log_decay[h]));
-    const int n = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    float s[D];
-    const size_t base = static_cast<size_t>(blockIdx.x) * D * D;
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-        s[i] = r.x_in ? r.x_in[base + (r.transposed ? j * D + i : i * D + j)] : 0.f;
-    for (int i = 0; i < n; ++i) {
-        const long long row = static_cast<long long>(b) * p.T + (r.reverse ? n - 1 - i : i);
-        __syncthreads();
-        sa[j] = to_f(static_cast<const E*>(r.a)[row * r.lda + h * D + j]);
-        sb[j] = to_f(static_cast<const E*>(r.b)[row * r.ldb + h * D + j]);
-        const float c = r.alpha_u * to_f(static_cast<const E*>(r.c)[row * r.ldc + h * D + j]);
-        __syncthreads();
-        float acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < D; ++k) {
-            s[k] = fmaf(sb[k], c, r.reverse ? s[k] : g * s[k]);
-            acc = fmaf(sa[k], s[k], acc);
-            if (r.reverse) s[k] *= g;
-        }
-        static_cast<E*>(r.out)[row * r.ldo + h * D + j] = from_f<E>(r.alpha_o * acc);
-    }
-    for (int t = n; t < p.T; ++t)
-        static_cast<E*>(r.out)[(static_cast<long long>(b) * p.T + t) * r.ldo + h * D + j] = from_f<E>(0.f);
-    if (r.x_out)
-#pragma unroll
-        for (int i = 0; i < D; ++i) r.x_out[base + (r.transposed ? j * D + i : i * D + j)] = s[i];
+    linattn_body<E, D, false>(p);
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(D) linattn_step_kernel(const E* q, const E* k, const E* v, long long ld,
-                                                         const float* log_decay, const float* S_in, int H, float scale,
-                                                         E* o, float* S_out)
+__global__ void __launch_bounds__(LinTile<E, D>::kThreads, blocks_per_sm<E, D>())
+    linattn_state_kernel(const __grid_constant__ LinParams p)
 {
-    const int b = blockIdx.x / H, h = blockIdx.x % H, j = threadIdx.x;
-    const float g = exp2f(decay_log2(log_decay[h]));
-    const size_t base = static_cast<size_t>(blockIdx.x) * D * D;
+    linattn_body<E, D, true>(p);
+}
+
+// One token: S_out = g S_in + k v^T, o = scale S_out^T q.  Bound by the state,
+// read and written once.  kWarps warps per stream; a lane holds float4 pieces
+// of rows `stride` apart, all loaded before the first is used.
+template <typename E, int D>
+__global__ void __launch_bounds__(128) linattn_step_kernel(const E* __restrict__ q, const E* __restrict__ k,
+                                                           const E* __restrict__ v, long long ld,
+                                                           const float* __restrict__ log_decay, const float* S_in,
+                                                           int streams, int H, float scale, E* __restrict__ o,
+                                                           float* S_out)
+{
+    constexpr int kWarps = D == 64 ? 4 : 1, kStreams = 4 / kWarps, kCols = D / 4;   // float4 columns
+    constexpr int stride = 32 * kWarps / kCols, kRows = D / stride;
+    __shared__ float4 s_o[D == 64 ? 4 : 1][16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stream = blockIdx.x * kStreams + warp / kWarps;
+    if (stream >= streams) return;   // whole warps, and only where a warp works alone
+    const int b = stream / H, h = stream % H;
+    const int t = (warp % kWarps) * 32 + lane, c = t % kCols, r0 = t / kCols;
+    const size_t base = static_cast<size_t>(stream) * D * D;
+    const float4* in = reinterpret_cast<const float4*>(S_in + base);
+    float4 s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i] = in[(r0 + i * stride) * kCols + c];
     const long long row = b * ld + h * D;
-    const float vj = to_f(v[row + j]);
-    float acc = 0.f;
-    for (int i = 0; i < D; ++i) {
-        const float s = fmaf(to_f(k[row + i]), vj, g * S_in[base + i * D + j]);
-        S_out[base + i * D + j] = s;
-        acc = fmaf(to_f(q[row + i]), s, acc);
+    float qv[kRows], kv[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        qv[i] = to_f(q[row + r0 + i * stride]);
+        kv[i] = to_f(k[row + r0 + i * stride]);
     }
-    o[static_cast<size_t>(blockIdx.x) * D + j] = from_f<E>(scale * acc);
+    const float4 vv = make_float4(to_f(v[row + 4 * c]), to_f(v[row + 4 * c + 1]), to_f(v[row + 4 * c + 2]),
+                                  to_f(v[row + 4 * c + 3]));
+    const Decay g = decay_over(decay_log2(log_decay[h]), 1);
+    float4* out = reinterpret_cast<float4*>(S_out + base);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float4 n;
+        n.x = fmaf(s[i].x, g.m, fmaf(kv[i], vv.x, s[i].x * g.c));
+        n.y = fmaf(s[i].y, g.m, fmaf(kv[i], vv.y, s[i].y * g.c));
+        n.z = fmaf(s[i].z, g.m, fmaf(kv[i], vv.z, s[i].z * g.c));
+        n.w = fmaf(s[i].w, g.m, fmaf(kv[i], vv.w, s[i].w * g.c));
+        out[(r0 + i * stride) * kCols + c] = n;
+        a.x = fmaf(qv[i], n.x, a.x);
+        a.y = fmaf(qv[i], n.y, a.y);
+        a.z = fmaf(qv[i], n.z, a.z);
+        a.w = fmaf(qv[i], n.w, a.w);
+    }
+#pragma unroll
+    for (int m = kCols; m < 32; m *= 2) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, m);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, m);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, m);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, m);
+    }
+    if constexpr (kWarps > 1) {
+        if (lane < kCols) s_o[warp][lane] = a;
+        __syncthreads();
+        if (warp != 0) return;
+        a = s_o[0][lane % kCols];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 x = s_o[w][lane % kCols];
+            a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+        }
+    }
+    if (lane < kCols) {
+        E* oo = o + static_cast<size_t>(stream) * D + 4 * lane;
+        oo[0] = from_f<E>(scale * a.x);
+        oo[1] = from_f<E>(scale * a.y);
+        oo[2] = from_f<E>(scale * a.z);
+        oo[3] = from_f<E>(scale * a.w);
+    }
+}
+
+// Lets a kernel take more than 48 KB of shared memory, once per device.
+int allow_smem(const void* kernel, int bytes, std::atomic<bool>* done)
+{
+    if (bytes <= 48 * 1024) return SRWM_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    if (done[dev].load()) return SRWM_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    done[dev].store(true);
+    return SRWM_OK;
+}
+
+template <typename E, int D>
+int launch(int roles, int slots, const LinParams& p, cudaStream_t st)
+{
+    using L = LinTile<E, D>;
+    static std::atomic<bool> main_ok[kMaxDevices], state_ok[kMaxDevices];
+    int rc = allow_smem(reinterpret_cast<const void*>(linattn_kernel<E, D>), L::kSmem, main_ok);
+    if (rc != SRWM_OK) return rc;
+    const unsigned streams = static_cast<unsigned>(p.B) * p.H;
+    if (p.segments > 1) {
+        rc = allow_smem(reinterpret_cast<const void*>(linattn_state_kernel<E, D>), L::kSmemState, state_ok);
+        if (rc != SRWM_OK) return rc;
+        linattn_state_kernel<E, D><<<dim3(streams * (p.segments - 1), slots), L::kThreads, L::kSmemState, st>>>(p);
+    }
+    linattn_kernel<E, D><<<dim3(streams * p.segments, roles), L::kThreads, L::kSmem, st>>>(p);
+    return launched();
 }
 
 template <typename E>
-int launch(int d, int roles, const LinParams& p, cudaStream_t st)
+int by_width(int d, int roles, int slots, const LinParams& p, cudaStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(p.B) * p.H, roles);
-    if (d == 16) linattn_kernel<E, 16><<<grid, 16, 0, st>>>(p);
-    if (d == 32) linattn_kernel<E, 32><<<grid, 32, 0, st>>>(p);
-    if (d == 64) linattn_kernel<E, 64><<<grid, 64, 0, st>>>(p);
-    return launched();
+    if (d == 16) return launch<E, 16>(roles, slots, p, st);
+    if (d == 32) return launch<E, 32>(roles, slots, p, st);
+    return launch<E, 64>(roles, slots, p, st);
 }
 
 template <typename E>
 int launch_step(int d, const void* q, const void* k, const void* v, long long ld, const float* lg, const float* S_in,
                 int B, int H, float scale, void* o, float* S_out, cudaStream_t st)
 {
-    const unsigned grid = static_cast<unsigned>(B) * H;
+    const int streams = B * H;
+    const unsigned grid = d == 64 ? streams : (streams + 3) / 4;
     const E *qe = static_cast<const E*>(q), *ke = static_cast<const E*>(k), *ve = static_cast<const E*>(v);
     E* oe = static_cast<E*>(o);
-    if (d == 16) linattn_step_kernel<E, 16><<<grid, 16, 0, st>>>(qe, ke, ve, ld, lg, S_in, H, scale, oe, S_out);
-    if (d == 32) linattn_step_kernel<E, 32><<<grid, 32, 0, st>>>(qe, ke, ve, ld, lg, S_in, H, scale, oe, S_out);
-    if (d == 64) linattn_step_kernel<E, 64><<<grid, 64, 0, st>>>(qe, ke, ve, ld, lg, S_in, H, scale, oe, S_out);
+    if (d == 16)
+        linattn_step_kernel<E, 16><<<grid, 128, 0, st>>>(qe, ke, ve, ld, lg, S_in, streams, H, scale, oe, S_out);
+    else if (d == 32)
+        linattn_step_kernel<E, 32><<<grid, 128, 0, st>>>(qe, ke, ve, ld, lg, S_in, streams, H, scale, oe, S_out);
+    else
+        linattn_step_kernel<E, 64><<<grid, 128, 0, st>>>(qe, ke, ve, ld, lg, S_in, streams, H, scale, oe, S_out);
     return launched();
 }
 
 }  // namespace
 
-int linattn_launch(int dtype, int d, int roles, const LinParams& p, cudaStream_t st)
+LinPlan linattn_plan(int B, int T, int H, int d, int roles)
 {
-    if (dtype == SRWM_F32) return launch<float>(d, roles, p, st);
-    if (dtype == SRWM_BF16) return launch<__nv_bfloat16>(d, roles, p, st);
-    return launch<__half>(d, roles, p, st);
+    // CTAs that the GPU holds at once, about, at each width
+    const long long slots = 152LL * (d == 64 ? 2 : d == 32 ? 8 : 20);
+    const long long ctas = static_cast<long long>(B) * H * roles;
+    const int chunks = T / d + (T % d != 0);
+    long long segments = ctas * 2 > slots ? 1 : slots / ctas;
+    if (segments > chunks / 8) segments = chunks / 8;   // at least 8 chunks each: the split reads two tensors again
+    if (segments < 2) return {chunks > 0 ? chunks * d : d, 1};
+    const int per = static_cast<int>((chunks + segments - 1) / segments);
+    return {per * d, (chunks + per - 1) / per};
+}
+
+int linattn_launch(int dtype, int d, int roles, int slots, const LinParams& p, cudaStream_t st)
+{
+    if (dtype == SRWM_F32) return by_width<float>(d, roles, slots, p, st);
+    if (dtype == SRWM_BF16) return by_width<__nv_bfloat16>(d, roles, slots, p, st);
+    return by_width<__half>(d, roles, slots, p, st);
 }
 
 int linattn_step_launch(int dtype, int d, const void* q, const void* k, const void* v, long long ld,

@@ -27,7 +27,11 @@ struct LinRole {
     float* x_out;                       // [B, H, d, d] or NULL
     int transposed;                     // x_in / x_out hold X^T
     int reverse;
-    float alpha_u, alpha_o;
+    float alpha_u_man;                  // alpha_u = alpha_u_man * 2^alpha_u_exp, 1 <= |alpha_u_man| < 2 or 0
+    int alpha_u_exp;
+    float alpha_o;
+    int state_slot;                     // whose segment states start this role's segments,
+    int state_transposed;               // and whether they are X^T
 };
 
 struct LinParams {
@@ -35,9 +39,24 @@ struct LinParams {
     const float* log_decay;             // [H]
     const int* lengths;                 // [B] or NULL
     int B, T, H;
+    // The long axis may be split into segments of seg_len positions (a multiple
+    // of d).  The state each segment but the last adds is computed first, from
+    // zero, by one pass for each of `slots` roles (state_role[slot]), into
+    // seg_state [slots][segments][B * H][d * d] (the last segment's is unused);
+    // then every segment starts from the decayed sum of the earlier ones'.
+    int seg_len, segments;
+    float* seg_state;
+    int state_role[2];
 };
 
-int linattn_launch(int dtype, int d, int roles, const LinParams& p, cudaStream_t st);
+// How a call of these sizes is split: segments and their length.  `roles` CTAs
+// run per stream and segment (3 in the backward pass, 1 in the forward pass).
+struct LinPlan {
+    int seg_len, segments;
+};
+LinPlan linattn_plan(int B, int T, int H, int d, int roles);
+
+int linattn_launch(int dtype, int d, int roles, int slots, const LinParams& p, cudaStream_t st);
 int linattn_step_launch(int dtype, int d, const void* q, const void* k, const void* v, long long ld,
                         const float* log_decay, const float* S_in, int B, int H, float scale, void* o, float* S_out,
                         cudaStream_t st);

@@ -2,6 +2,8 @@
 // argument checks, and each call as roles of the one primitive (srwm_linattn.h).
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "srwm.h"
 #include "srwm_check.h"
 #include "srwm_linattn.h"
@@ -15,7 +17,7 @@ bool supported(int d) { return d == 16 || d == 32 || d == 64; }
 bool sizes_ok(long long B, long long T, long long H, long long d)
 {
     if (B <= 0 || H <= 0 || T < 0 || d <= 0) return false;
-    return B * H <= 0x7fffffffLL && H * d <= 0x7fffffffLL && T <= (1LL << 46) / (B * H * d);
+    return B * H <= 0x3fffffffLL && H * d <= 0x7fffffffLL && T <= 0x3fffffffLL && T <= (1LL << 46) / (B * H * d);
 }
 
 // A token-row array: rows of H * d elements, ld elements apart.
@@ -48,18 +50,34 @@ int check_align(std::initializer_list<const void*> ptrs)
     return SRWM_OK;
 }
 
+// Segment states (none when the axis is not split).
+size_t scratch(int B, int T, int H, int d, int roles, int slots)
+{
+    const srwm::LinPlan plan = srwm::linattn_plan(B, T, H, d, roles);
+    if (plan.segments == 1) return 256;
+    return srwm::round256(static_cast<size_t>(slots) * plan.segments * B * H * d * d * 4);
+}
+
+void set_plan(srwm::LinParams& p, int d, int roles, void* workspace)
+{
+    const srwm::LinPlan plan = srwm::linattn_plan(p.B, p.T, p.H, d, roles);
+    p.seg_len = plan.seg_len;
+    p.segments = plan.segments;
+    p.seg_state = static_cast<float*>(workspace);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t srwm_linattn_workspace_bytes(int B, int T, int H, int d)
 {
-    return sizes_ok(B, T, H, d) && supported(d) ? 256 : 0;
+    return sizes_ok(B, T, H, d) && supported(d) ? scratch(B, T, H, d, 1, 1) : 0;
 }
 
 size_t srwm_linattn_backward_workspace_bytes(int B, int T, int H, int d)
 {
-    return srwm_linattn_workspace_bytes(B, T, H, d);
+    return sizes_ok(B, T, H, d) && supported(d) ? scratch(B, T, H, d, 3, 2) : 0;
 }
 
 int srwm_linattn_forward(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
@@ -72,7 +90,7 @@ int srwm_linattn_forward(const void* q, const void* k, const void* v, long long 
     const size_t e = srwm::dtype_bytes(dtype);
     if (!supported(d) || e == 0) return SRWM_ERR_UNSUPPORTED;
     const size_t need = srwm_linattn_workspace_bytes(B, T, H, d);
-    if (!ld_ok(ld, H, d, e) || workspace_bytes < need) return SRWM_ERR_SHAPE;
+    if (!ld_ok(ld, H, d, e) || workspace_bytes < need || !std::isfinite(scale)) return SRWM_ERR_SHAPE;
     int rc = check_align({q, k, v, log_decay, S_init, o, S_final, workspace});
     if (rc != SRWM_OK) return rc;
     if (reinterpret_cast<uintptr_t>(lengths) % 4 != 0) return SRWM_ERR_ALIGN;
@@ -91,8 +109,10 @@ int srwm_linattn_forward(const void* q, const void* k, const void* v, long long 
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.B = B, p.T = T, p.H = H;
-    p.role[0] = {q, k, v, ld, ld, ld, o, static_cast<long long>(H) * d, S_init, S_final, 0, 0, 1.f, scale};
-    return srwm::linattn_launch(dtype, d, 1, p, static_cast<cudaStream_t>(stream));
+    p.role[0] = {q, k, v, ld, ld, ld, o, static_cast<long long>(H) * d, S_init, S_final, 0, 0, 1.f, 0, scale, 0, 0};
+    p.state_role[0] = 0;
+    set_plan(p, d, 1, workspace);
+    return srwm::linattn_launch(dtype, d, 1, 1, p, static_cast<cudaStream_t>(stream));
 }
 
 int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
@@ -103,7 +123,7 @@ int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld,
     if (!sizes_ok(B, 1, H, d)) return SRWM_ERR_SHAPE;
     const size_t e = srwm::dtype_bytes(dtype);
     if (!supported(d) || e == 0) return SRWM_ERR_UNSUPPORTED;
-    if (!ld_ok(ld, H, d, e)) return SRWM_ERR_SHAPE;
+    if (!ld_ok(ld, H, d, e) || !std::isfinite(scale)) return SRWM_ERR_SHAPE;
     int rc = check_align({q, k, v, log_decay, S_in, o, S_out});
     if (rc != SRWM_OK) return rc;
     const size_t state = static_cast<size_t>(B) * H * d * d * 4;
@@ -129,7 +149,8 @@ int srwm_linattn_backward(const void* q, const void* k, const void* v, long long
     const size_t e = srwm::dtype_bytes(dtype);
     if (!supported(d) || e == 0) return SRWM_ERR_UNSUPPORTED;
     const size_t need = srwm_linattn_backward_workspace_bytes(B, T, H, d);
-    if (!ld_ok(ld, H, d, e) || !ld_ok(ld_grad, H, d, e) || workspace_bytes < need) return SRWM_ERR_SHAPE;
+    if (!ld_ok(ld, H, d, e) || !ld_ok(ld_grad, H, d, e) || workspace_bytes < need || !std::isfinite(scale))
+        return SRWM_ERR_SHAPE;
     int rc = check_align({q, k, v, log_decay, S_init, do_, dS_final, dq, dk, dv, dS_init, workspace});
     if (rc != SRWM_OK) return rc;
     if (reinterpret_cast<uintptr_t>(lengths) % 4 != 0) return SRWM_ERR_ALIGN;
@@ -150,10 +171,16 @@ int srwm_linattn_backward(const void* q, const void* k, const void* v, long long
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.B = B, p.T = T, p.H = H;
-    p.role[0] = {do_, v, k, hd, ld, ld, dq, ld_grad, S_init, nullptr, 1, 0, 1.f, scale};
-    p.role[1] = {k, q, do_, ld, ld, hd, dv, ld_grad, dS_final, dS_init, 0, 1, scale, 1.f};
-    p.role[2] = {v, do_, q, ld, hd, ld, dk, ld_grad, dS_final, nullptr, 1, 1, scale, 1.f};
-    return srwm::linattn_launch(dtype, d, 3, p, static_cast<cudaStream_t>(stream));
+    // dq runs on S^T (from v and k), dv on D (from q and do), dk on D^T
+    int ex = 0;
+    const float man = 2.f * std::frexp(scale, &ex);
+    p.role[0] = {do_, v, k, hd, ld, ld, dq, ld_grad, S_init, nullptr, 1, 0, 1.f, 0, scale, 0, 0};
+    p.role[1] = {k, q, do_, ld, ld, hd, dv, ld_grad, dS_final, dS_init, 0, 1, man, ex - 1, 1.f, 1, 0};
+    p.role[2] = {v, do_, q, ld, hd, ld, dk, ld_grad, dS_final, nullptr, 1, 1, man, ex - 1, 1.f, 1, 1};
+    p.state_role[0] = 0;
+    p.state_role[1] = 1;
+    set_plan(p, d, 3, workspace);
+    return srwm::linattn_launch(dtype, d, 3, 2, p,static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
