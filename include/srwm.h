@@ -428,7 +428,7 @@ int srwm_linattn_backward(const void* q, const void* k, const void* v, long long
  *             16-byte aligned, untouched by others until the work ends
  *
  * Supported: G divides C, C a multiple of 8 and at most 8192; N >= 0, L >= 1
- * (N = 0 does nothing; x and y may be NULL then).  Statistics are fp32, the
+ * (N = 0 does nothing; x and y may be NULL then), N * G below 2^31.  Statistics are fp32, the
  * variance from deviations from the mean.
  */
 size_t srwm_groupnorm_workspace_bytes(long long N, long long L, int C, int G);

@@ -1,38 +1,129 @@
 // srwm_groupnorm.cu -- group norm with an activation, channels last, and its
-// gradients: one CTA per sample and group, one per channel for dgamma, dbeta.
+// gradients.
+//
+//   xh = (x - mean) rstd,  z = xh gamma + beta,  y = act(z)
+//   dz = dy act'(z),  A_c = sum dz,  B_c = sum dz xh  (over a sample's positions)
+//   dx = rstd (dz gamma - m1 - xh m2),  m1 = mean of dz gamma over the group
+//      = sum_c gamma_c A_c / count,  m2 = sum_c gamma_c B_c / count
+//   dbeta_c, dgamma_c = sums of A_c, B_c over the samples
+// Everything here is bound by memory: x (and dy) is to be read once and y (dx)
+// written once.  What differs with the shape is where a group's values wait for
+// their statistics, so there are four ways (gn_plan):
+//   rows   L = 1 and a group of a power of two of 16-byte vectors, up to a
+//          warp's 32: one vector per thread in registers, statistics by shuffles.
+//   line   L = 1 otherwise: one warp per group, its values re-read from L1.
+//   slab   a cluster of up to 8 CTAs holds a sample (or some of its groups) in
+//          shared memory, a range of positions each; statistics are exchanged
+//          through distributed shared memory.
+//   split  larger samples: per-channel statistics of ranges of positions to
+//          scratch, a merge per group, and a second read of x (and dy).
+// A thread keeps one vector of channels throughout, so per-channel values
+// (gamma, beta, statistics, gradient sums) stay in registers.  All sums run in
+// a fixed order.  Variances are of deviations from a mean (two passes where the
+// values are at hand, else Welford's update), merged pairwise by
+//   mean = m_a + d n_b / n,  M2 = M2_a + M2_b + d^2 n_a n_b / n,  d = m_b - m_a.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "srwm.h"
 #include "srwm_check.h"
 #include "srwm_elem.cuh"
 #include "srwm_groupnorm.h"
+#include "srwm_mma.cuh"
+#include "srwm_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace srwm {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMaxDevices = 64;
+constexpr int kSms = 152;
+constexpr int kMaxCluster = 8;
+constexpr int kRowThreads = 256;
+constexpr int kSmemMost = 227 * 1024;    // of a CTA
+constexpr int kSlabGood = 48 * 1024;     // with this many, four CTAs share an SM and their loads overlap
 
+// ---------------------------------------------------------------- values
+template <typename E>
+constexpr int vec = 16 / static_cast<int>(sizeof(E));
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4], float)
+{
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8], __nv_bfloat16)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8], __half)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack_half2(w[k]);
+        f[2 * k] = v.x;
+        f[2 * k + 1] = v.y;
+    }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4], float)
+{
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <typename E>
+__device__ __forceinline__ uint4 pack(const float (&f)[8], E)
+{
+    union {
+        E e[8];
+        uint4 u;
+    } v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v.e[k] = from_f<E>(f[k]);
+    return v.u;
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 load_vec(const void* p, size_t element)
+{
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p) + element));
+}
+template <typename E>
+__device__ __forceinline__ void store_vec(void* p, size_t element, const uint4& v)
+{
+    *reinterpret_cast<uint4*>(static_cast<E*>(p) + element) = v;
+}
+
+// ---------------------------------------------------------------- activation
 template <int ACT>
 __device__ __forceinline__ float act(float z)
 {
-    if constexpr (ACT == SRWM_ACT_SILU) return z / (1.f + expf(-z));
+    if constexpr (ACT == SRWM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
     if constexpr (ACT == SRWM_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
     return z;
 }
 
-// Slope of the activation at z = xh * g + b, xh = (x - mean) * rstd.
+// Slope of the activation at z = (x - mean) rstd g + b.
 template <int ACT>
-__device__ __forceinline__ float slope(float x, float mean, float rstd, float g, float b)
+__device__ __forceinline__ float slope(float x, float mean, float rstd, float g, float b, float xh)
 {
-    const float xh = (x - mean) * rstd, z = fmaf(xh, g, b);
     if constexpr (ACT == SRWM_ACT_SILU) {
-        const float e = 1.f / (1.f + expf(-z));
+        const float z = fmaf(xh, g, b);
+        const float e = __fdividef(1.f, 1.f + __expf(-z));
         return e * fmaf(z, 1.f - e, 1.f);
     }
     if constexpr (ACT == SRWM_ACT_RELU) {
+        const float z = fmaf(xh, g, b);
         // the side of the border decides a whole term of the gradient: within
         // fp32's error of it (a few roundings of both terms) it is taken in fp64
-        if (fabsf(z) <= 1e-5f * (fabsf(x * rstd * g) + fabsf(mean * rstd * g) + fabsf(b))) {
+        if (fabsf(z) <= 1e-6f * (fabsf(x * rstd * g) + fabsf(mean * rstd * g) + fabsf(b))) {
             const double zd = (static_cast<double>(x) - mean) * rstd * g + b;
             return zd > 0.0 ? 1.f : 0.f;
         }
@@ -41,112 +132,852 @@ __device__ __forceinline__ float slope(float x, float mean, float rstd, float g,
     return 1.f;
 }
 
-__device__ float block_sum(float v)
+// ---------------------------------------------------------------- statistics
+struct Stat {
+    float n, mean, m2;
+};
+__device__ __forceinline__ Stat merge(const Stat& a, const Stat& b)
 {
-    __shared__ float s[kThreads];
-    __syncthreads();
-    s[threadIdx.x] = v;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
+    if (b.n == 0.f) return a;
+    if (a.n == 0.f) return b;
+    const float n = a.n + b.n, d = b.mean - a.mean, f = b.n / n;
+    return {n, fmaf(d, f, a.mean), a.m2 + fmaf(d * d, a.n * f, b.m2)};
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum over aligned sets of `lanes` neighbouring lanes, lanes a power of two.
+__device__ __forceinline__ float lanes_sum(float v, int lanes)
+{
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int V>
+struct Channels {   // per-channel values of a thread's vector
+    float gamma[V], beta[V];
+    __device__ __forceinline__ Channels(const GnParams& p, int c)
+    {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            gamma[k] = p.gamma ? p.gamma[c + k] : 1.f;
+            beta[k] = p.beta ? p.beta[c + k] : 0.f;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- rows
+// Block of kRowThreads: `slots` rows of `tile` vectors.  A thread's rows are
+// `slots` * gridDim.x apart; U of them are in flight at once.
+struct RowTile {
+    int tile, slots, lanes;   // lanes: of one group
+};
+template <typename E>
+__host__ __device__ RowTile row_tile(int C, int G)
+{
+    const int cv = C / vec<E>;
+    RowTile t;
+    t.tile = cv < kRowThreads ? cv : kRowThreads;
+    t.slots = kRowThreads / t.tile;
+    t.lanes = C / G / vec<E>;
+    return t;
+}
+
+template <typename E, int ACT, int U>
+__global__ void __launch_bounds__(kRowThreads) gn_rows_kernel(const GnParams p)
+{
+    constexpr int V = vec<E>;
+    const RowTile rt = row_tile<E>(p.C, p.G);
+    const int slot = threadIdx.x / rt.tile, c = (blockIdx.y * kRowThreads + threadIdx.x % rt.tile) * V;
+    const bool on = slot < rt.slots && c < p.C;
+    const Channels<V> ch(p, on ? c : 0);
+    const float inv = 1.f / static_cast<float>(rt.lanes * V);
+    const long long step = static_cast<long long>(gridDim.x) * rt.slots;
+    for (long long base = static_cast<long long>(blockIdx.x) * rt.slots; base < p.N; base += step * U) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * step + slot;
+            raw[u] = on && row < p.N ? load_vec<E>(p.x, static_cast<size_t>(row) * p.C + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * step + slot;
+            float x[V], s = 0.f, q = 0.f;
+            unpack(raw[u], x, E{});
+#pragma unroll
+            for (int k = 0; k < V; ++k) s += x[k];
+            const float mean = lanes_sum(s, rt.lanes) * inv;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                x[k] -= mean;
+                q = fmaf(x[k], x[k], q);
+            }
+            const float rstd = 1.f / sqrtf(lanes_sum(q, rt.lanes) * inv + p.eps);
+            if (on && row < p.N) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) x[k] = act<ACT>(fmaf(x[k] * rstd, ch.gamma[k], ch.beta[k]));
+                store_vec<E>(p.y, static_cast<size_t>(row) * p.C + c, pack(x, E{}));
+                if ((threadIdx.x & (rt.lanes - 1)) == 0) {
+                    const size_t g = static_cast<size_t>(row) * p.G + c / (rt.lanes * V);
+                    if (p.mean) p.mean[g] = mean;
+                    if (p.rstd) p.rstd[g] = rstd;
+                }
+            }
+        }
+    }
+}
+
+// Adds the threads' per-channel sums over the block's slots and writes them as
+// partial `index`: part [.., 2, C], A (dbeta) then B (dgamma).
+template <int V>
+__device__ __forceinline__ void write_partial(const GnParams& p, float* smem, const float (&a)[V], const float (&b)[V],
+                                              int slot, int slots, int tile, int c, int c0, bool on, long long index)
+{
+    float* out = p.part + static_cast<size_t>(index) * 2 * p.C;
+    const int width = tile * V;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
         __syncthreads();
-    }
-    return s[0];
-}
-
-template <typename E, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_kernel(const GnParams p)
-{
-    const long long n = blockIdx.x;
-    const int g = blockIdx.y, cg = p.C / p.G;
-    const long long count = p.L * cg;
-    const E* x = static_cast<const E*>(p.x) + n * p.L * p.C + g * cg;
-    E* y = static_cast<E*>(p.y) + n * p.L * p.C + g * cg;
-    float a = 0.f;
-    for (long long i = threadIdx.x; i < count; i += kThreads) a += to_f(x[i / cg * p.C + i % cg]);
-    const float mean = block_sum(a) / count;
-    a = 0.f;
-    for (long long i = threadIdx.x; i < count; i += kThreads) {
-        const float d = to_f(x[i / cg * p.C + i % cg]) - mean;
-        a = fmaf(d, d, a);
-    }
-    const float rstd = 1.f / sqrtf(block_sum(a) / count + p.eps);
-    for (long long i = threadIdx.x; i < count; i += kThreads) {
-        const int c = g * cg + i % cg;
-        const float xh = (to_f(x[i / cg * p.C + i % cg]) - mean) * rstd;
-        y[i / cg * p.C + i % cg] = from_f<E>(act<ACT>(fmaf(xh, p.gamma ? p.gamma[c] : 1.f, p.beta ? p.beta[c] : 0.f)));
-    }
-    if (threadIdx.x == 0) {
-        if (p.mean) p.mean[n * p.G + g] = mean;
-        if (p.rstd) p.rstd[n * p.G + g] = rstd;
+        if (on)
+#pragma unroll
+            for (int k = 0; k < V; ++k) smem[slot * width + (c - c0) + k] = which ? b[k] : a[k];
+        __syncthreads();
+        for (int i = threadIdx.x; i < width && c0 + i < p.C; i += blockDim.x) {
+            float s = 0.f;
+            for (int k = 0; k < slots; ++k) s += smem[k * width + i];
+            out[which * p.C + c0 + i] = s;
+        }
     }
 }
 
-template <typename E, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_dx_kernel(const GnParams p)
+template <typename E, int ACT, int U>
+__global__ void __launch_bounds__(kRowThreads) gn_rows_grad_kernel(const GnParams p)
 {
-    const long long n = blockIdx.x;
-    const int g = blockIdx.y, cg = p.C / p.G;
-    const long long count = p.L * cg, base = n * p.L * p.C + g * cg;
-    const E *x = static_cast<const E*>(p.x) + base, *dy = static_cast<const E*>(p.dy) + base;
-    E* dx = static_cast<E*>(p.dx) + base;
-    const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
+    constexpr int V = vec<E>;
+    __shared__ float s_part[kRowThreads * V];
+    const RowTile rt = row_tile<E>(p.C, p.G);
+    const int slot = threadIdx.x / rt.tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % rt.tile * V;
+    const bool on = slot < rt.slots && c < p.C;
+    const Channels<V> ch(p, on ? c : 0);
+    const float inv = 1.f / static_cast<float>(rt.lanes * V);
+    const long long step = static_cast<long long>(gridDim.x) * rt.slots;
+    float A[V], B[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = B[k] = 0.f;
+    for (long long base = static_cast<long long>(blockIdx.x) * rt.slots; base < p.N; base += step * U) {
+        uint4 rx[U], rd[U];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * step + slot;
+            const bool ok = on && row < p.N;
+            const size_t at = static_cast<size_t>(row) * p.C + c, g = static_cast<size_t>(row) * p.G + c / (rt.lanes * V);
+            rx[u] = ok ? load_vec<E>(p.x, at) : make_uint4(0, 0, 0, 0);
+            rd[u] = ok ? load_vec<E>(p.dy, at) : make_uint4(0, 0, 0, 0);
+            mean[u] = ok ? __ldg(p.mean + g) : 0.f;
+            rstd[u] = ok ? __ldg(p.rstd + g) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * step + slot;
+            float x[V], d[V], s1 = 0.f, s2 = 0.f;
+            unpack(rx[u], x, E{});
+            unpack(rd[u], d, E{});
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float xh = (x[k] - mean[u]) * rstd[u];
+                const float dz = d[k] * slope<ACT>(x[k], mean[u], rstd[u], ch.gamma[k], ch.beta[k], xh);
+                A[k] += dz;
+                B[k] = fmaf(dz, xh, B[k]);
+                x[k] = xh;
+                d[k] = dz * ch.gamma[k];
+                s1 += d[k];
+                s2 = fmaf(d[k], xh, s2);
+            }
+            s1 = lanes_sum(s1, rt.lanes) * inv;
+            s2 = lanes_sum(s2, rt.lanes) * inv;
+            if (on && row < p.N) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) x[k] = rstd[u] * (d[k] - fmaf(x[k], s2, s1));
+                store_vec<E>(p.dx, static_cast<size_t>(row) * p.C + c, pack(x, E{}));
+            }
+        }
+    }
+    if (p.dgamma || p.dbeta) write_partial<V>(p, s_part, A, B, slot, rt.slots, rt.tile, c, c0, on, blockIdx.x);
+}
+
+// dbeta, dgamma: the partials' sums over their index, in a fixed order.
+__global__ void __launch_bounds__(256) gn_param_kernel(const GnParams p, long long partials)
+{
+    __shared__ float s[2][8][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float a = 0.f, b = 0.f;
-    auto dh = [&](long long i, float* xh) {
-        const int c = g * cg + i % cg;
-        const float xv = to_f(x[i / cg * p.C + i % cg]), ga = p.gamma ? p.gamma[c] : 1.f;
-        *xh = (xv - mean) * rstd;
-        return to_f(dy[i / cg * p.C + i % cg]) * slope<ACT>(xv, mean, rstd, ga, p.beta ? p.beta[c] : 0.f) * ga;
+    if (c < p.C)
+#pragma unroll 4
+        for (long long i = w; i < partials; i += 8) {
+            a += p.part[static_cast<size_t>(i) * 2 * p.C + c];
+            b += p.part[static_cast<size_t>(i) * 2 * p.C + p.C + c];
+        }
+    s[0][w][lane] = a;
+    s[1][w][lane] = b;
+    __syncthreads();
+    if (w < 2 && c < p.C) {
+        a = 0.f;
+        for (int k = 0; k < 8; ++k) a += s[w][k][lane];
+        float* out = w == 0 ? p.dbeta : p.dgamma;
+        if (out) out[c] = a;
+    }
+}
+
+// ---------------------------------------------------------------- line
+// One warp per (row, group) of any width; the row's values are read again from L1.
+template <typename E, int ACT, bool GRAD>
+__global__ void __launch_bounds__(128) gn_line_kernel(const GnParams p)
+{
+    const int lane = threadIdx.x & 31, width = p.C / p.G;
+    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (item >= p.N * p.G) return;
+    const int c0 = static_cast<int>(item % p.G) * width;
+    const size_t at = static_cast<size_t>(item / p.G) * p.C + c0;
+    const E* x = static_cast<const E*>(p.x) + at;
+    const float inv = 1.f / static_cast<float>(width);
+    auto gamma = [&](int i) { return p.gamma ? p.gamma[c0 + i] : 1.f; };
+    auto beta = [&](int i) { return p.beta ? p.beta[c0 + i] : 0.f; };
+    if constexpr (!GRAD) {
+        float s = 0.f, q = 0.f;
+        for (int i = lane; i < width; i += 32) s += to_f(x[i]);
+        const float mean = warp_sum(s) * inv;
+        for (int i = lane; i < width; i += 32) {
+            const float d = to_f(x[i]) - mean;
+            q = fmaf(d, d, q);
+        }
+        const float rstd = 1.f / sqrtf(warp_sum(q) * inv + p.eps);
+        E* y = static_cast<E*>(p.y) + at;
+        for (int i = lane; i < width; i += 32)
+            y[i] = from_f<E>(act<ACT>(fmaf((to_f(x[i]) - mean) * rstd, gamma(i), beta(i))));
+        if (lane == 0) {
+            if (p.mean) p.mean[item] = mean;
+            if (p.rstd) p.rstd[item] = rstd;
+        }
+    } else {
+        const E* dy = static_cast<const E*>(p.dy) + at;
+        const float mean = p.mean[item], rstd = p.rstd[item];
+        float s1 = 0.f, s2 = 0.f;
+        auto dh = [&](int i, float& xh) {
+            const float xv = to_f(x[i]);
+            xh = (xv - mean) * rstd;
+            return to_f(dy[i]) * slope<ACT>(xv, mean, rstd, gamma(i), beta(i), xh) * gamma(i);
+        };
+        for (int i = lane; i < width; i += 32) {
+            float xh;
+            const float v = dh(i, xh);
+            s1 += v;
+            s2 = fmaf(v, xh, s2);
+        }
+        s1 = warp_sum(s1) * inv;
+        s2 = warp_sum(s2) * inv;
+        E* dx = static_cast<E*>(p.dx) + at;
+        for (int i = lane; i < width; i += 32) {
+            float xh;
+            const float v = dh(i, xh);
+            dx[i] = from_f<E>(rstd * (v - fmaf(xh, s2, s1)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- slab
+struct SlabPlan {
+    int threads, cluster;    // CTAs per cluster, each with `rows` positions
+    int rows, groups, cblk;  // groups and channels of a channel block
+    int grid_x;              // clusters * cluster
+};
+
+// Shared memory: the values (positions rounded up to whole passes of the
+// slots), per-slot channel sums (two kinds in the backward pass) and its
+// running sums, statistics of every group.
+long long slab_smem(const SlabPlan& s, int e, bool grad)
+{
+    const int tile = s.cblk * e / 16, slots = s.threads / tile;
+    const long long values = static_cast<long long>(s.rows + slots - 1) / slots * slots * tile * 16;
+    return (grad ? 2 : 1) * (values + slots * s.cblk * 4) + (grad ? 2 * s.cblk * 4 : 0) + s.groups * 4 * 4;
+}
+
+template <typename E, int ACT, bool GRAD>
+__global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const SlabPlan sp)
+{
+    constexpr int V = vec<E>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = sp.cluster > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    const int tile = sp.cblk / V, slots = sp.threads / tile, width = p.C / p.G;
+    const int slot = threadIdx.x / tile, cl = threadIdx.x % tile * V, c0 = blockIdx.y * sp.cblk;
+    const bool on = slot < slots;
+    const long long r0 = static_cast<long long>(rank) * sp.rows;
+    const int rows = static_cast<int>(max(0LL, min(static_cast<long long>(sp.rows), p.L - r0)));   // this CTA's positions
+    const int mine = on && slot < rows ? (rows - slot + slots - 1) / slots : 0;                  // this thread's
+    const int stride = slots * tile;   // vectors between a thread's consecutive positions
+    const int per_cta = (sp.rows + slots - 1) / slots * stride;
+    uint4* sx = reinterpret_cast<uint4*>(smem);
+    uint4* sd = sx + per_cta;
+    float* s_part = reinterpret_cast<float*>(sx + (GRAD ? 2 : 1) * per_cta);
+    float* s_part2 = s_part + slots * sp.cblk;
+    float* s_sum = s_part2 + (GRAD ? slots * sp.cblk : 0);    // backward: running A, B per channel
+    float* s_stat = s_part + (GRAD ? 2 : 1) * slots * sp.cblk + (GRAD ? 2 * sp.cblk : 0);
+    float* s_own = s_stat;                     // [groups][2]: this CTA's, read by the cluster
+    float* s_all = s_stat + 2 * sp.groups;     // [groups][2]: the sample's
+    const uint32_t ax = smem_u32(sx + threadIdx.x), ad = smem_u32(sd + threadIdx.x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = sp.threads >> 5;
+    const Channels<V> ch(p, c0 + cl);
+    int gl[V];   // the local group of each channel
+#pragma unroll
+    for (int k = 0; k < V; ++k) gl[k] = (cl + k) / width;
+    const float count = static_cast<float>(rows) * width, total = static_cast<float>(p.L) * width;
+    if constexpr (GRAD)
+        for (int i = threadIdx.x; i < 2 * sp.cblk; i += sp.threads) s_sum[i] = 0.f;
+
+    // The sum of a group over the slots and its channels of f(slot, channel).
+    auto group_sum = [&](int g, auto f) {
+        float s = 0.f;
+        for (int i = lane; i < slots * width; i += 32) s += f(i / width, g * width + i % width);
+        return warp_sum(s);
     };
-    for (long long i = threadIdx.x; i < count; i += kThreads) {
-        float xh;
-        const float v = dh(i, &xh);
-        a += v;
-        b = fmaf(v, xh, b);
+
+    const long long clusters = gridDim.x / sp.cluster;
+    for (long long n = blockIdx.x / sp.cluster; n < p.N; n += clusters) {
+        const size_t at0 = (static_cast<size_t>(n) * p.L + r0 + slot) * p.C + c0 + cl;
+        for (int i = 0; i < mine; ++i) {
+            const size_t at = at0 + static_cast<size_t>(i) * slots * p.C;
+            cp_async16(ax + i * stride * 16, static_cast<const E*>(p.x) + at, true);
+            if constexpr (GRAD) cp_async16(ad + i * stride * 16, static_cast<const E*>(p.dy) + at, true);
+        }
+        cp_async_commit();
+        float mean[V], rstd[V];
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const size_t g = static_cast<size_t>(n) * p.G + c0 / width + gl[k];
+                mean[k] = p.mean[g];
+                rstd[k] = p.rstd[g];
+            }
+        }
+        cp_async_wait<0>();   // a thread reads only what it copied
+        float a[V], b[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[k] = b[k] = 0.f;
+        if constexpr (!GRAD) {
+            for (int i = 0; i < mine; ++i) {
+                float x[V];
+                unpack(sx[threadIdx.x + i * stride], x, E{});
+#pragma unroll
+                for (int k = 0; k < V; ++k) a[k] += x[k];
+            }
+            if (on)
+#pragma unroll
+                for (int k = 0; k < V; ++k) s_part[slot * sp.cblk + cl + k] = a[k];
+            __syncthreads();
+            for (int g = warp; g < sp.groups; g += warps) {
+                const float s = group_sum(g, [&](int i, int c) { return s_part[i * sp.cblk + c]; });
+                if (lane == 0) s_own[2 * g] = rows > 0 ? s / count : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < V; ++k) mean[k] = s_own[2 * gl[k]];
+            for (int i = 0; i < mine; ++i) {
+                float x[V];
+                unpack(sx[threadIdx.x + i * stride], x, E{});
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float d = x[k] - mean[k];
+                    b[k] = fmaf(d, d, b[k]);
+                }
+            }
+            if (on)
+#pragma unroll
+                for (int k = 0; k < V; ++k) s_part[slot * sp.cblk + cl + k] = b[k];
+            __syncthreads();
+            for (int g = warp; g < sp.groups; g += warps) {
+                const float s = group_sum(g, [&](int i, int c) { return s_part[i * sp.cblk + c]; });
+                if (lane == 0) s_own[2 * g + 1] = s;
+            }
+            if (sp.cluster > 1) cluster.sync(); else __syncthreads();
+            for (int g = threadIdx.x; g < sp.groups; g += sp.threads) {
+                Stat s{0.f, 0.f, 0.f};
+                for (int r = 0; r < sp.cluster; ++r) {
+                    const float* o = sp.cluster > 1 ? cluster.map_shared_rank(s_own, r) : s_own;
+                    const float rr = static_cast<float>(max(0LL, min(static_cast<long long>(sp.rows), p.L - static_cast<long long>(r) * sp.rows)));
+                    s = merge(s, Stat{rr * width, o[2 * g], o[2 * g + 1]});
+                }
+                const float rs = 1.f / sqrtf(s.m2 / total + p.eps);
+                s_all[2 * g] = s.mean;
+                s_all[2 * g + 1] = rs;
+                if (rank == 0) {
+                    const size_t gi = static_cast<size_t>(n) * p.G + c0 / width + g;
+                    if (p.mean) p.mean[gi] = s.mean;
+                    if (p.rstd) p.rstd[gi] = rs;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                mean[k] = s_all[2 * gl[k]];
+                rstd[k] = s_all[2 * gl[k] + 1] * ch.gamma[k];
+            }
+            for (int i = 0; i < mine; ++i) {
+                float x[V];
+                unpack(sx[threadIdx.x + i * stride], x, E{});
+#pragma unroll
+                for (int k = 0; k < V; ++k) x[k] = act<ACT>(fmaf(x[k] - mean[k], rstd[k], ch.beta[k]));
+                store_vec<E>(p.y, at0 + static_cast<size_t>(i) * slots * p.C, pack(x, E{}));
+            }
+        } else {
+            for (int i = 0; i < mine; ++i) {
+                float x[V], d[V];
+                unpack(sx[threadIdx.x + i * stride], x, E{});
+                unpack(sd[threadIdx.x + i * stride], d, E{});
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float xh = (x[k] - mean[k]) * rstd[k];
+                    const float dz = d[k] * slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
+                    a[k] += dz;
+                    b[k] = fmaf(dz, xh, b[k]);
+                }
+            }
+            if (on)
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    s_part[slot * sp.cblk + cl + k] = a[k];
+                    s_part2[slot * sp.cblk + cl + k] = b[k];
+                }
+            __syncthreads();
+            for (int c = threadIdx.x; c < sp.cblk; c += sp.threads) {   // slots together; into the running sums
+                float sa = 0.f, sb = 0.f;
+                for (int i = 0; i < slots; ++i) {
+                    sa += s_part[i * sp.cblk + c];
+                    sb += s_part2[i * sp.cblk + c];
+                }
+                s_sum[c] += sa;
+                s_sum[sp.cblk + c] += sb;
+                s_part[c] = sa;      // only this thread reads or writes column c from here to the barrier
+                s_part2[c] = sb;
+            }
+            __syncthreads();
+            for (int g = warp; g < sp.groups; g += warps) {
+                float u = 0.f, w = 0.f;
+                for (int i = lane; i < width; i += 32) {
+                    const float ga = p.gamma ? p.gamma[c0 + g * width + i] : 1.f;
+                    u = fmaf(ga, s_part[g * width + i], u);
+                    w = fmaf(ga, s_part2[g * width + i], w);
+                }
+                u = warp_sum(u);
+                w = warp_sum(w);
+                if (lane == 0) {
+                    s_own[2 * g] = u;
+                    s_own[2 * g + 1] = w;
+                }
+            }
+            if (sp.cluster > 1) cluster.sync(); else __syncthreads();
+            for (int g = threadIdx.x; g < sp.groups; g += sp.threads) {
+                float u = 0.f, w = 0.f;
+                for (int r = 0; r < sp.cluster; ++r) {
+                    const float* o = sp.cluster > 1 ? cluster.map_shared_rank(s_own, r) : s_own;
+                    u += o[2 * g];
+                    w += o[2 * g + 1];
+                }
+                s_all[2 * g] = u / total;
+                s_all[2 * g + 1] = w / total;
+            }
+            __syncthreads();
+            float m1[V], m2[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                m1[k] = s_all[2 * gl[k]];
+                m2[k] = s_all[2 * gl[k] + 1];
+            }
+            for (int i = 0; i < mine; ++i) {
+                float x[V], d[V];
+                unpack(sx[threadIdx.x + i * stride], x, E{});
+                unpack(sd[threadIdx.x + i * stride], d, E{});
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float xh = (x[k] - mean[k]) * rstd[k];
+                    const float dz = d[k] * slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
+                    x[k] = rstd[k] * (dz * ch.gamma[k] - fmaf(xh, m2[k], m1[k]));
+                }
+                store_vec<E>(p.dx, at0 + static_cast<size_t>(i) * slots * p.C, pack(x, E{}));
+            }
+        }
+        // the cluster has read this CTA's statistics before they change or it exits
+        if (sp.cluster > 1) cluster.sync(); else __syncthreads();
     }
-    a = block_sum(a) / count;
-    b = block_sum(b) / count;
-    for (long long i = threadIdx.x; i < count; i += kThreads) {
-        float xh;
-        const float v = dh(i, &xh);
-        dx[i / cg * p.C + i % cg] = from_f<E>(rstd * (v - a - xh * b));
+    if constexpr (GRAD) {
+        if (p.dgamma || p.dbeta) {
+            float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.C + c0;
+            for (int c = threadIdx.x; c < sp.cblk; c += sp.threads) {
+                out[c] = s_sum[c];
+                out[p.C + c] = s_sum[sp.cblk + c];
+            }
+        }
     }
 }
 
-template <typename E, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_dparam_kernel(const GnParams p)
+// ---------------------------------------------------------------- split
+// Scratch: per sample, range of positions and channel (mean, M2) or (A, B) as
+// [N][ranges][2][C]; then per sample and group (mean, rstd) or (m1, m2).
+struct SplitPlan {
+    int rows, ranges;   // positions of a range
+};
+
+__device__ __forceinline__ float* split_groups(const GnParams& p, const SplitPlan& s)
 {
-    const int c = blockIdx.x, g = c / (p.C / p.G);
-    const float ga = p.gamma ? p.gamma[c] : 1.f, be = p.beta ? p.beta[c] : 0.f;
-    float a = 0.f, b = 0.f;
-    for (long long i = threadIdx.x; i < p.N * p.L; i += kThreads) {
-        const long long n = i / p.L;
-        const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
-        const float xv = to_f(static_cast<const E*>(p.x)[i * p.C + c]);
-        const float dz = to_f(static_cast<const E*>(p.dy)[i * p.C + c]) * slope<ACT>(xv, mean, rstd, ga, be);
-        a = fmaf(dz, (xv - mean) * rstd, a);
-        b += dz;
+    return p.part + static_cast<size_t>(p.N) * s.ranges * 2 * p.C;
+}
+
+// STAGE 0: a range's per-channel values; 1: the second pass over it.
+template <typename E, int ACT, bool GRAD, int STAGE>
+__global__ void __launch_bounds__(kRowThreads) gn_split_kernel(const GnParams p, const SplitPlan sp)
+{
+    constexpr int V = vec<E>;
+    __shared__ float s_part[kRowThreads * V];
+    const int cv = p.C / V, tile = min(cv, kRowThreads), slots = kRowThreads / tile, width = p.C / p.G;
+    const int slot = threadIdx.x / tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % tile * V;
+    const bool on = slot < slots && c < p.C;
+    const long long n = blockIdx.x / sp.ranges, range = blockIdx.x % sp.ranges;
+    const long long r0 = range * sp.rows, r1 = min(r0 + sp.rows, p.L);
+    const Channels<V> ch(p, on ? c : 0);
+    float mean[V], rstd[V], m1[V], m2[V];
+    if (GRAD || STAGE == 1)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const size_t g = static_cast<size_t>(n) * p.G + (on ? c + k : 0) / width;
+            const float* st = split_groups(p, sp) + 2 * g;
+            mean[k] = GRAD ? p.mean[g] : st[0];
+            rstd[k] = GRAD ? p.rstd[g] : st[1];
+            m1[k] = GRAD && STAGE == 1 ? st[0] : 0.f;
+            m2[k] = GRAD && STAGE == 1 ? st[1] : 0.f;
+        }
+    float a[V], b[V], seen = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] = b[k] = 0.f;
+    if (on)
+#pragma unroll 4
+        for (long long r = r0 + slot; r < r1; r += slots) {
+            const size_t at = (static_cast<size_t>(n) * p.L + r) * p.C + c;
+            float x[V], d[V];
+            unpack(load_vec<E>(p.x, at), x, E{});
+            if constexpr (GRAD) unpack(load_vec<E>(p.dy, at), d, E{});
+            if constexpr (!GRAD && STAGE == 0) {
+                seen += 1.f;
+                const float f = __fdividef(1.f, seen);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float e = x[k] - a[k];
+                    a[k] = fmaf(e, f, a[k]);
+                    b[k] = fmaf(e, x[k] - a[k], b[k]);
+                }
+            } else if constexpr (!GRAD) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) x[k] = act<ACT>(fmaf((x[k] - mean[k]) * rstd[k], ch.gamma[k], ch.beta[k]));
+                store_vec<E>(p.y, at, pack(x, E{}));
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float xh = (x[k] - mean[k]) * rstd[k];
+                    const float dz = d[k] * slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
+                    if constexpr (STAGE == 0) {
+                        a[k] += dz;
+                        b[k] = fmaf(dz, xh, b[k]);
+                    } else {
+                        x[k] = rstd[k] * (dz * ch.gamma[k] - fmaf(xh, m2[k], m1[k]));
+                    }
+                }
+                if constexpr (STAGE == 1) store_vec<E>(p.dx, at, pack(x, E{}));
+            }
+        }
+    if constexpr (STAGE == 1) return;
+    if constexpr (GRAD) {
+        write_partial<V>(p, s_part, a, b, slot, slots, tile, c, c0, on, blockIdx.x);
+    } else {
+        // the slots' statistics of a channel together: means first, then M2 beside the merged mean
+        __shared__ float s_part2[kRowThreads * V];
+        const int wide = tile * V;
+        if (on)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                s_part[slot * wide + (c - c0) + k] = a[k];
+                s_part2[slot * wide + (c - c0) + k] = b[k];
+            }
+        __syncthreads();
+        float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.C;
+        for (int i = threadIdx.x; i < wide && c0 + i < p.C; i += kRowThreads) {
+            Stat s{0.f, 0.f, 0.f};
+            for (int k = 0; k < slots; ++k) {
+                const long long rows = r1 - r0 > k ? (r1 - r0 - k + slots - 1) / slots : 0;
+                s = merge(s, Stat{static_cast<float>(rows), s_part[k * wide + i], s_part2[k * wide + i]});
+            }
+            out[c0 + i] = s.mean;
+            out[p.C + c0 + i] = s.m2;
+        }
     }
-    a = block_sum(a);
-    b = block_sum(b);
-    if (threadIdx.x == 0) {
-        if (p.dgamma) p.dgamma[c] = a;
-        if (p.dbeta) p.dbeta[c] = b;
+}
+
+// One CTA per sample and group: its ranges' and channels' values together.
+template <bool GRAD>
+__global__ void __launch_bounds__(128) gn_merge_kernel(const GnParams p, const SplitPlan sp)
+{
+    __shared__ float s0[128], s1[128], s2[128];
+    const long long n = blockIdx.x / p.G;
+    const int g = blockIdx.x % p.G, width = p.C / p.G, t = threadIdx.x;
+    const float* in = p.part + static_cast<size_t>(n) * sp.ranges * 2 * p.C + g * width;
+    const long long items = static_cast<long long>(sp.ranges) * width;
+    Stat s{0.f, 0.f, 0.f};
+    for (long long i = t; i < items; i += 128) {
+        const long long range = i / width;
+        const int c = static_cast<int>(i % width);
+        const float u = in[range * 2 * p.C + c], w = in[range * 2 * p.C + p.C + c];
+        if constexpr (GRAD) {
+            const float ga = p.gamma ? p.gamma[g * width + c] : 1.f;
+            s.mean = fmaf(ga, u, s.mean);
+            s.m2 = fmaf(ga, w, s.m2);
+        } else {
+            s = merge(s, Stat{static_cast<float>(min(static_cast<long long>(sp.rows), p.L - range * sp.rows)), u, w});
+        }
     }
+    s0[t] = s.n, s1[t] = s.mean, s2[t] = s.m2;
+    for (int o = 64; o > 0; o >>= 1) {
+        __syncthreads();
+        if (t < o) {
+            if constexpr (GRAD) {
+                s1[t] += s1[t + o];
+                s2[t] += s2[t + o];
+            } else {
+                const Stat m = merge(Stat{s0[t], s1[t], s2[t]}, Stat{s0[t + o], s1[t + o], s2[t + o]});
+                s0[t] = m.n, s1[t] = m.mean, s2[t] = m.m2;
+            }
+        }
+    }
+    if (t == 0) {
+        const float total = static_cast<float>(p.L) * width;
+        float* out = split_groups(p, sp) + 2 * static_cast<size_t>(blockIdx.x);
+        if constexpr (GRAD) {
+            out[0] = s1[0] / total;
+            out[1] = s2[0] / total;
+        } else {
+            const float rstd = 1.f / sqrtf(s2[0] / total + p.eps);
+            out[0] = s1[0];
+            out[1] = rstd;
+            if (p.mean) p.mean[blockIdx.x] = s1[0];
+            if (p.rstd) p.rstd[blockIdx.x] = rstd;
+        }
+    }
+}
+
+// dz's channel sums over ranges of rows with statistics of their own (L = 1, the line way).
+template <typename E, int ACT>
+__global__ void __launch_bounds__(kRowThreads) gn_line_param_kernel(const GnParams p, long long rows)
+{
+    constexpr int V = vec<E>;
+    __shared__ float s_part[kRowThreads * V];
+    const int tile = min(p.C / V, kRowThreads), slots = kRowThreads / tile, width = p.C / p.G;
+    const int slot = threadIdx.x / tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % tile * V;
+    const bool on = slot < slots && c < p.C;
+    const Channels<V> ch(p, on ? c : 0);
+    float a[V], b[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] = b[k] = 0.f;
+    const long long r0 = blockIdx.x * rows, r1 = min(r0 + rows, p.N);
+    if (on)
+        for (long long r = r0 + slot; r < r1; r += slots) {
+            float x[V], d[V];
+            unpack(load_vec<E>(p.x, static_cast<size_t>(r) * p.C + c), x, E{});
+            unpack(load_vec<E>(p.dy, static_cast<size_t>(r) * p.C + c), d, E{});
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const size_t g = static_cast<size_t>(r) * p.G + (c + k) / width;
+                const float mean = p.mean[g], rstd = p.rstd[g], xh = (x[k] - mean) * rstd;
+                const float dz = d[k] * slope<ACT>(x[k], mean, rstd, ch.gamma[k], ch.beta[k], xh);
+                a[k] += dz;
+                b[k] = fmaf(dz, xh, b[k]);
+            }
+        }
+    write_partial<V>(p, s_part, a, b, slot, slots, tile, c, c0, on, blockIdx.x);
+}
+
+// ---------------------------------------------------------------- the choice
+enum Way { kRows, kLine, kSlab, kSplit };
+
+struct GnPlan {
+    Way way;
+    SlabPlan slab;
+    SplitPlan split;
+    int grid_x, grid_y;
+    long long partials;   // of the parameter gradients
+    size_t scratch;       // floats
+};
+
+GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
+{
+    GnPlan g{};
+    const int V = 16 / e, cv = C / V, width = C / G;
+    g.grid_y = (cv + kRowThreads - 1) / kRowThreads;
+    const int lanes = width / V;
+    if (L == 1 && width % V == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0) {
+        g.way = kRows;
+        const int tile = std::min(cv, kRowThreads), slots = kRowThreads / tile;
+        const long long blocks = (N + slots - 1) / slots;
+        // enough blocks for the GPU several times over; each keeps its channels' gamma and beta, and its sums
+        g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * 8 / std::min(g.grid_y, 4))));
+        g.partials = g.grid_x;
+        g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
+        return g;
+    }
+    if (L == 1) {
+        g.way = kLine;
+        g.grid_x = static_cast<int>((N * G + 3) / 4);
+        g.partials = std::max(1LL, std::min((N + 31) / 32, 4LL * kSms));
+        g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
+        return g;
+    }
+    // The slab: as few CTAs per sample as hold it well; more of them, then fewer
+    // channels each (at least 64 bytes of a position), while a CTA holds too
+    // much or the GPU is not filled.
+    SlabPlan s{};
+    s.cluster = 1;
+    s.groups = G;
+    const long long copies = grad ? 2 : 1;
+    auto bytes = [&] { return copies * ((L + s.cluster - 1) / s.cluster) * s.groups * width * e; };
+    auto can_halve = [&] {
+        return s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0 && (s.groups / 2 * width * e) >= 64;
+    };
+    while (s.groups * width / V > 256 && s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0) s.groups /= 2;
+    for (;;) {
+        const bool full = N * s.cluster * (G / s.groups) >= 2 * kSms;
+        if (bytes() <= kSlabGood && (full || bytes() <= 8192)) break;
+        if (s.cluster < kMaxCluster && L >= 2 * s.cluster)
+            s.cluster *= 2;
+        else if (can_halve())
+            s.groups /= 2;
+        else
+            break;
+    }
+    s.cblk = s.groups * width;
+    const int tile = s.cblk / V;
+    s.rows = static_cast<int>((L + s.cluster - 1) / s.cluster);
+    const long long vectors = static_cast<long long>(s.rows) * tile;
+    s.threads = vectors >= 1024 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
+    while (s.threads < tile) s.threads *= 2;
+    if (tile <= 256 && slab_smem(s, e, grad) <= kSmemMost) {
+        g.way = kSlab;
+        g.grid_y = G / s.groups;
+        // the backward pass keeps its channel sums over several samples: fewer partials
+        const long long clusters = grad ? std::max(1LL, std::min(N, static_cast<long long>(kSms) * 8 / s.cluster)) : N;
+        g.grid_x = static_cast<int>(std::min(clusters, 0x7fffffffLL / s.cluster) * s.cluster);
+        s.grid_x = g.grid_x;
+        g.slab = s;
+        g.partials = g.grid_x;
+        g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
+        return g;
+    }
+    g.way = kSplit;
+    const long long want = std::max(1LL, 8LL * kSms / std::max(1LL, N * g.grid_y));   // ranges to fill the GPU
+    long long ranges = std::min(want, (L + 15) / 16);
+    g.split.rows = static_cast<int>((L + ranges - 1) / ranges);
+    g.split.ranges = static_cast<int>((L + g.split.rows - 1) / g.split.rows);
+    g.grid_x = static_cast<int>(N * g.split.ranges);
+    g.partials = N * g.split.ranges;
+    g.scratch = static_cast<size_t>(g.partials) * 2 * C + static_cast<size_t>(N) * G * 2;
+    return g;
+}
+
+int allow_smem(const void* kernel, std::atomic<bool>* done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    if (done[dev].load()) return SRWM_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    done[dev].store(true);
+    return SRWM_OK;
+}
+
+template <typename E, int ACT, bool GRAD>
+int launch_slab(const GnParams& p, const GnPlan& g, cudaStream_t st)
+{
+    static std::atomic<bool> ok[kMaxDevices];
+    auto kernel = gn_slab_kernel<E, ACT, GRAD>;
+    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), ok);
+    if (rc != SRWM_OK) return rc;
+    const SlabPlan& s = g.slab;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(g.grid_x, g.grid_y);
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(slab_smem(s, sizeof(E), GRAD));
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, p, s) != cudaSuccess) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    return SRWM_OK;
 }
 
 template <typename E, int ACT>
 int forward(const GnParams& p, cudaStream_t st)
 {
-    gn_kernel<E, ACT><<<dim3(static_cast<unsigned>(p.N), p.G), kThreads, 0, st>>>(p);
+    const GnPlan g = gn_plan(sizeof(E), p.N, p.L, p.C, p.G, false);
+    if (g.way == kRows)
+        gn_rows_kernel<E, ACT, 4><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p);
+    else if (g.way == kLine)
+        gn_line_kernel<E, ACT, false><<<g.grid_x, 128, 0, st>>>(p);
+    else if (g.way == kSlab)
+        return launch_slab<E, ACT, false>(p, g, st);
+    else {
+        gn_split_kernel<E, ACT, false, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+        gn_merge_kernel<false><<<static_cast<unsigned>(p.N * p.G), 128, 0, st>>>(p, g.split);
+        gn_split_kernel<E, ACT, false, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+    }
     return launched();
 }
 
 template <typename E, int ACT>
 int backward(const GnParams& p, cudaStream_t st)
 {
-    if (p.N > 0) gn_dx_kernel<E, ACT><<<dim3(static_cast<unsigned>(p.N), p.G), kThreads, 0, st>>>(p);
-    gn_dparam_kernel<E, ACT><<<p.C, kThreads, 0, st>>>(p);
+    GnPlan g = gn_plan(sizeof(E), p.N, p.L, p.C, p.G, true);
+    const bool params = p.dgamma || p.dbeta;
+    int rc = SRWM_OK;
+    if (p.N == 0)
+        g.partials = 0;
+    else if (g.way == kRows)
+        gn_rows_grad_kernel<E, ACT, 2><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p);
+    else if (g.way == kLine) {
+        gn_line_kernel<E, ACT, true><<<g.grid_x, 128, 0, st>>>(p);
+        if (params)
+            gn_line_param_kernel<E, ACT><<<dim3(static_cast<unsigned>(g.partials), g.grid_y), kRowThreads, 0, st>>>(
+                p, (p.N + g.partials - 1) / g.partials);
+    } else if (g.way == kSlab)
+        rc = launch_slab<E, ACT, true>(p, g, st);
+    else {
+        gn_split_kernel<E, ACT, true, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+        gn_merge_kernel<true><<<static_cast<unsigned>(p.N * p.G), 128, 0, st>>>(p, g.split);
+        gn_split_kernel<E, ACT, true, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+    }
+    if (rc != SRWM_OK) return rc;
+    if (params) gn_param_kernel<<<(p.C + 31) / 32, 256, 0, st>>>(p, g.partials);
     return launched();
 }
 
@@ -167,10 +998,17 @@ int by_type(bool back, int dtype, int activation, const GnParams& p, cudaStream_
     return by_act<__half>(back, activation, p, st);
 }
 
+// Enough for either width of type: the call's own plan may need less.
+size_t scratch(long long N, long long L, int C, int G, bool grad)
+{
+    const size_t a = gn_plan(4, N, L, C, G, grad).scratch, b = gn_plan(2, N, L, C, G, grad).scratch;
+    return std::max<size_t>(256, round256(std::max(a, b) * 4));
+}
+
 }  // namespace
 
-size_t groupnorm_scratch(long long, long long, int, int) { return 256; }
-size_t groupnorm_backward_scratch(long long, long long, int, int) { return 256; }
+size_t groupnorm_scratch(long long N, long long L, int C, int G) { return scratch(N, L, C, G, false); }
+size_t groupnorm_backward_scratch(long long N, long long L, int C, int G) { return scratch(N, L, C, G, true); }
 
 int groupnorm_launch(int dtype, int activation, const GnParams& p, cudaStream_t st)
 {

@@ -16,7 +16,7 @@ int check_sizes(int dtype, long long N, long long L, int C, int G, int activatio
 {
     if (N < 0 || L <= 0 || C <= 0 || G <= 0) return SRWM_ERR_SHAPE;
     if (N > 0x7fffffffLL || L > 0x7fffffffLL || (N > 0 && L > (1LL << 46) / N / C)) return SRWM_ERR_SHAPE;
-    if (C % G != 0) return SRWM_ERR_SHAPE;
+    if (C % G != 0 || N * G > 0x7fffffffLL) return SRWM_ERR_SHAPE;
     if (C % 8 != 0 || C > kMaxChannels || srwm::dtype_bytes(dtype) == 0) return SRWM_ERR_UNSUPPORTED;
     if (activation != SRWM_ACT_NONE && activation != SRWM_ACT_SILU && activation != SRWM_ACT_RELU)
         return SRWM_ERR_UNSUPPORTED;
