@@ -383,25 +383,46 @@ def srwm_layer_forward(u, H, n_lr, softmax_input, ln1_gamma, ln1_beta, W0, ln2_g
     return out, W_final
 
 
-def _arr(t, name, shape, dtype, optional=False):
-    """The address of a contiguous CUDA tensor of this shape and type."""
-    if t is None and optional:
-        return None
+def _refuse(t, name, shape, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr() if t.numel() else None
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _token_rows(tensors, names, dtype):
-    """The addresses of [B,T,H,d] (or [B,H,d]) tensors whose tokens lie one
-    common distance apart, and that distance in elements."""
-    shape, ld = tensors[0].shape, None
+def _arr(t, name, shape, dtype):
+    """The address of a contiguous CUDA tensor of this shape and type (0 when empty)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, shape, dtype)
+
+
+def _maybe(t, name, shape, dtype):
+    return None if t is None else _arr(t, name, shape, dtype)
+
+
+def _current(t):
+    """The raw handle of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on(stream):
+    """A context in which `stream` is current: what a call allocates then belongs to the stream that uses it."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _token_rows(x, y, z, names, dtype):
+    """The addresses of three [B,T,H,d] (or [B,H,d]) tensors whose tokens lie
+    one common distance apart, and that distance in elements."""
+    shape = x.shape
+    if x.is_contiguous() and isinstance(y, torch.Tensor) and isinstance(z, torch.Tensor) and y.is_contiguous() and \
+            z.is_contiguous() and x.dtype is dtype and y.dtype is dtype and z.dtype is dtype and \
+            y.shape == shape and z.shape == shape and x.is_cuda and y.is_cuda and z.is_cuda:
+        return x.data_ptr(), y.data_ptr(), z.data_ptr(), shape[-1] * shape[-2]
     H, d = shape[-2:]
-    for t, name in zip(tensors, names):
+    ld = None
+    for t, name in zip((x, y, z), names):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype != dtype or not t.is_cuda:
@@ -412,14 +433,14 @@ def _token_rows(tensors, names, dtype):
             continue
         st = t.stride()
         B, T = (shape[0], shape[1]) if t.dim() == 4 else (shape[0], 1)
-        mine = H * d if B * T == 1 else st[1] if T > 1 else st[0]
+        mine = H * d if B * T == 1 else st[1] if t.dim() == 4 and T > 1 else st[0]
         if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d) or (T > 1 and B > 1 and st[0] != T * mine):
             raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
-        if ld is None or B * T == 1:
+        if ld is None:
             ld = mine
         elif ld != mine:
             raise ValueError(f"{', '.join(names)} must have the same strides")
-    return [t.data_ptr() if t.numel() else None for t in tensors], H * d if ld is None else ld
+    return x.data_ptr(), y.data_ptr(), z.data_ptr(), H * d if ld is None else ld
 
 
 def _scratch(workspace, need, device):
@@ -461,9 +482,12 @@ def srwm_linattn_forward(q, k, v, log_decay, scale=None, S_init=None, lengths=No
     S_init [B,H,d,d] (None: zero) and S_final [B,H,d,d] are float32, lengths
     [B] int32 counts each sequence's valid tokens (None: T); scale is
     1/sqrt(d) unless given.  Returns (o [B,T,H,d], S_final)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_linattn_forward(q, k, v, log_decay, scale, S_init, lengths, o, S_final, workspace)
     code = _dtype_code(q, "q")
     B, T, H, d = q.shape
-    (pq, pk, pv), ld = _token_rows((q, k, v), ("q", "k", "v"), q.dtype)
+    pq, pk, pv, ld = _token_rows(q, k, v, ("q", "k", "v"), q.dtype)
     if o is None:
         o = torch.empty((B, T, H, d), dtype=q.dtype, device=q.device)
     if S_final is None:
@@ -471,11 +495,11 @@ def srwm_linattn_forward(q, k, v, log_decay, scale=None, S_init=None, lengths=No
     lib = _lib()
     workspace = _scratch(workspace, max(16, lib.srwm_linattn_workspace_bytes(B, T, H, d)), q.device)
     rc = lib.srwm_linattn_forward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
-                                  _arr(S_init, "S_init", (B, H, d, d), torch.float32, True),
+                                  _maybe(S_init, "S_init", (B, H, d, d), torch.float32),
                                   _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
                                   _arr(o, "o", (B, T, H, d), q.dtype),
                                   _arr(S_final, "S_final", (B, H, d, d), torch.float32), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                                  workspace.numel() * workspace.element_size(), _current(q))
     _check(rc, "srwm_linattn_forward")
     return o, S_final
 
@@ -484,9 +508,12 @@ def srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale=None, o_t=None, S_ou
     """One token of srwm_linattn_forward from per-sequence states: q_t, k_t, v_t [B,H,d] -> (o_t [B,H,d], S_out).
 
     S_out may be S_in itself (in-place update)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale, o_t, S_out)
     code = _dtype_code(q_t, "q_t")
     B, H, d = q_t.shape
-    (pq, pk, pv), ld = _token_rows((q_t, k_t, v_t), ("q_t", "k_t", "v_t"), q_t.dtype)
+    pq, pk, pv, ld = _token_rows(q_t, k_t, v_t, ("q_t", "k_t", "v_t"), q_t.dtype)
     if o_t is None:
         o_t = torch.empty((B, H, d), dtype=q_t.dtype, device=q_t.device)
     if S_out is None:
@@ -494,7 +521,7 @@ def srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale=None, o_t=None, S_ou
     rc = _lib().srwm_linattn_step(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
                                   _arr(S_in, "S_in", (B, H, d, d), torch.float32), code, B, H, d,
                                   d ** -0.5 if scale is None else scale, _arr(o_t, "o_t", (B, H, d), q_t.dtype),
-                                  _arr(S_out, "S_out", (B, H, d, d), torch.float32), _stream_handle(stream))
+                                  _arr(S_out, "S_out", (B, H, d, d), torch.float32), _current(q_t))
     _check(rc, "srwm_linattn_step")
     return o_t, S_out
 
@@ -509,15 +536,19 @@ def srwm_linattn_backward(q, k, v, log_decay, do, scale=None, S_init=None, lengt
 
     dq, dk, dv may be views of one packed [B,T,3,H,d] array.  Returns
     (dq, dk, dv, dS_init); the decay gets no gradient."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_linattn_backward(q, k, v, log_decay, do, scale, S_init, lengths, dS_final, dq, dk, dv,
+                                         dS_init, workspace)
     code = _dtype_code(q, "q")
     B, T, H, d = q.shape
-    (pq, pk, pv), ld = _token_rows((q, k, v), ("q", "k", "v"), q.dtype)
+    pq, pk, pv, ld = _token_rows(q, k, v, ("q", "k", "v"), q.dtype)
     given = (dq is not None) + (dk is not None) + (dv is not None)
     if given == 0:
         dq, dk, dv = (torch.empty((B, T, H, d), dtype=q.dtype, device=q.device) for _ in range(3))
     elif given < 3:
         raise ValueError("dq, dk and dv: give all three or none")
-    (pdq, pdk, pdv), ldg = _token_rows((dq, dk, dv), ("dq", "dk", "dv"), q.dtype)
+    pdq, pdk, pdv, ldg = _token_rows(dq, dk, dv, ("dq", "dk", "dv"), q.dtype)
     if dq.shape != q.shape:
         raise ValueError(f"dq has shape {tuple(dq.shape)}, expected {tuple(q.shape)}")
     if dS_init is None:
@@ -525,12 +556,12 @@ def srwm_linattn_backward(q, k, v, log_decay, do, scale=None, S_init=None, lengt
     lib = _lib()
     workspace = _scratch(workspace, max(16, lib.srwm_linattn_backward_workspace_bytes(B, T, H, d)), q.device)
     rc = lib.srwm_linattn_backward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
-                                   _arr(S_init, "S_init", (B, H, d, d), torch.float32, True),
+                                   _maybe(S_init, "S_init", (B, H, d, d), torch.float32),
                                    _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
                                    _arr(do, "do", (B, T, H, d), q.dtype),
-                                   _arr(dS_final, "dS_final", (B, H, d, d), torch.float32, True), pdq, pdk, pdv, ldg,
+                                   _maybe(dS_final, "dS_final", (B, H, d, d), torch.float32), pdq, pdk, pdv, ldg,
                                    _arr(dS_init, "dS_init", (B, H, d, d), torch.float32), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                                   workspace.numel() * workspace.element_size(), _current(q))
     _check(rc, "srwm_linattn_backward")
     return dq, dk, dv, dS_init
 
@@ -554,22 +585,25 @@ def srwm_groupnorm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", 
     statistics are over the L positions and the C/groups channels of a sample's
     group; gamma, beta [C] are float32 or None (ones, zeros); activation is
     "none", "silu" or "relu".  Returns (y, mean [N,groups], rstd [N,groups])."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_groupnorm_forward(x, gamma, beta, groups, eps, activation, y, mean, rstd, workspace)
     code = _dtype_code(x, "x")
     N, L, C = x.shape
     if y is None:
-        y = torch.empty_like(x)
+        y = torch.empty((N, L, C), dtype=x.dtype, device=x.device)
     if mean is None:
         mean = torch.empty((N, groups), dtype=torch.float32, device=x.device)
     if rstd is None:
         rstd = torch.empty((N, groups), dtype=torch.float32, device=x.device)
     lib = _lib()
     workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_workspace_bytes(N, L, C, groups)), x.device)
-    rc = lib.srwm_groupnorm_forward(_arr(x, "x", (N, L, C), x.dtype), _arr(gamma, "gamma", (C,), torch.float32, True),
-                                    _arr(beta, "beta", (C,), torch.float32, True), code, N, L, C, groups, eps,
+    rc = lib.srwm_groupnorm_forward(_arr(x, "x", (N, L, C), x.dtype), _maybe(gamma, "gamma", (C,), torch.float32),
+                                    _maybe(beta, "beta", (C,), torch.float32), code, N, L, C, groups, eps,
                                     _activation_code(activation), _arr(y, "y", (N, L, C), x.dtype),
                                     _arr(mean, "mean", (N, groups), torch.float32),
                                     _arr(rstd, "rstd", (N, groups), torch.float32), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                                    workspace.numel() * workspace.element_size(), _current(x))
     _check(rc, "srwm_groupnorm_forward")
     return y, mean, rstd
 
@@ -582,24 +616,28 @@ def srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation="
                             dbeta=None, workspace=None, stream=None):
     """Gradients through srwm_groupnorm_forward from dy [N,L,C] and the forward
     pass's mean and rstd.  Returns (dx, dgamma [C], dbeta [C])."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation, dx, dgamma, dbeta,
+                                           workspace)
     code = _dtype_code(x, "x")
     N, L, C = x.shape
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = torch.empty((N, L, C), dtype=x.dtype, device=x.device)
     if dgamma is None:
         dgamma = torch.empty((C,), dtype=torch.float32, device=x.device)
     if dbeta is None:
         dbeta = torch.empty((C,), dtype=torch.float32, device=x.device)
     lib = _lib()
     workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_backward_workspace_bytes(N, L, C, groups)), x.device)
-    rc = lib.srwm_groupnorm_backward(_arr(x, "x", (N, L, C), x.dtype), _arr(gamma, "gamma", (C,), torch.float32, True),
-                                     _arr(beta, "beta", (C,), torch.float32, True),
+    rc = lib.srwm_groupnorm_backward(_arr(x, "x", (N, L, C), x.dtype), _maybe(gamma, "gamma", (C,), torch.float32),
+                                     _maybe(beta, "beta", (C,), torch.float32),
                                      _arr(mean, "mean", (N, groups), torch.float32),
                                      _arr(rstd, "rstd", (N, groups), torch.float32), _arr(dy, "dy", (N, L, C), x.dtype),
                                      code, N, L, C, groups, _activation_code(activation),
                                      _arr(dx, "dx", (N, L, C), x.dtype), _arr(dgamma, "dgamma", (C,), torch.float32),
                                      _arr(dbeta, "dbeta", (C,), torch.float32), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                                     workspace.numel() * workspace.element_size(), _current(x))
     _check(rc, "srwm_groupnorm_backward")
     return dx, dgamma, dbeta
 
