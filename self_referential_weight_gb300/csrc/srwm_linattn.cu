@@ -16,7 +16,7 @@ constexpr int kMaxDevices = 64;
 template <typename E, int D>
 constexpr int blocks_per_sm()
 {
-    return D == 64 ? (sizeof(E) == 4 ? 2 : 3) : D == 32 ? 8 : 20;
+    return D == 64 ? 2 : D == 32 ? 4 : 10;
 }
 
 template <typename E, int D>
