@@ -78,16 +78,16 @@ __device__ __forceinline__ uint4 pack(const float (&f)[4], float)
 {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
+__device__ __forceinline__ uint32_t pack2(float x, float y, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y, __half) { return pack_half2(x, y); }
 template <typename E>
 __device__ __forceinline__ uint4 pack(const float (&f)[8], E)
 {
-    union {
-        E e[8];
-        uint4 u;
-    } v;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v.e[k] = from_f<E>(f[k]);
-    return v.u;
+    return make_uint4(pack2(f[0], f[1], E{}), pack2(f[2], f[3], E{}), pack2(f[4], f[5], E{}), pack2(f[6], f[7], E{}));
 }
 
 template <typename E>
@@ -102,10 +102,19 @@ __device__ __forceinline__ void store_vec(void* p, size_t element, const uint4& 
 }
 
 // ---------------------------------------------------------------- activation
+// sigmoid(z), good to a few units of 2^-23: exp underflows to 0 and overflows to
+// infinity, whose reciprocal is 0.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+    return rcp_approx(1.f + e);
+}
+
 template <int ACT>
 __device__ __forceinline__ float act(float z)
 {
-    if constexpr (ACT == SRWM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if constexpr (ACT == SRWM_ACT_SILU) return z * sigmoid(z);
     if constexpr (ACT == SRWM_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
     return z;
 }
@@ -116,7 +125,7 @@ __device__ __forceinline__ float slope(float x, float mean, float rstd, float g,
 {
     if constexpr (ACT == SRWM_ACT_SILU) {
         const float z = fmaf(xh, g, b);
-        const float e = __fdividef(1.f, 1.f + __expf(-z));
+        const float e = sigmoid(z);
         return e * fmaf(z, 1.f - e, 1.f);
     }
     if constexpr (ACT == SRWM_ACT_RELU) {
@@ -151,11 +160,13 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Sum over aligned sets of `lanes` neighbouring lanes, lanes a power of two.
-__device__ __forceinline__ float lanes_sum(float v, int lanes)
+// Sums over aligned sets of `lanes` neighbouring lanes, lanes a power of two.
+template <int U>
+__device__ __forceinline__ void lanes_sum(float (&v)[U], int lanes)
 {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
 }
 
 template <int V>
@@ -189,7 +200,7 @@ __host__ __device__ RowTile row_tile(int C, int G)
 }
 
 template <typename E, int ACT, int U>
-__global__ void __launch_bounds__(kRowThreads) gn_rows_kernel(const GnParams p)
+__global__ void __launch_bounds__(kRowThreads, 3) gn_rows_kernel(const GnParams p)
 {
     constexpr int V = vec<E>;
     const RowTile rt = row_tile<E>(p.C, p.G);
@@ -197,35 +208,45 @@ __global__ void __launch_bounds__(kRowThreads) gn_rows_kernel(const GnParams p)
     const bool on = slot < rt.slots && c < p.C;
     const Channels<V> ch(p, on ? c : 0);
     const float inv = 1.f / static_cast<float>(rt.lanes * V);
+    const int group = c / (rt.lanes * V);
     const long long step = static_cast<long long>(gridDim.x) * rt.slots;
     for (long long base = static_cast<long long>(blockIdx.x) * rt.slots; base < p.N; base += step * U) {
-        uint4 raw[U];
+        float x[U][V], sum[U], sq[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = base + u * step + slot;
-            raw[u] = on && row < p.N ? load_vec<E>(p.x, static_cast<size_t>(row) * p.C + c) : make_uint4(0, 0, 0, 0);
+            unpack(on && row < p.N ? load_vec<E>(p.x, static_cast<size_t>(row) * p.C + c) : make_uint4(0, 0, 0, 0), x[u],
+                   E{});
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long row = base + u * step + slot;
-            float x[V], s = 0.f, q = 0.f;
-            unpack(raw[u], x, E{});
+            sum[u] = 0.f;
 #pragma unroll
-            for (int k = 0; k < V; ++k) s += x[k];
-            const float mean = lanes_sum(s, rt.lanes) * inv;
+            for (int k = 0; k < V; ++k) sum[u] += x[u][k];
+        }
+        lanes_sum(sum, rt.lanes);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            sum[u] *= inv;
+            sq[u] = 0.f;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                x[k] -= mean;
-                q = fmaf(x[k], x[k], q);
+                x[u][k] -= sum[u];
+                sq[u] = fmaf(x[u][k], x[u][k], sq[u]);
             }
-            const float rstd = 1.f / sqrtf(lanes_sum(q, rt.lanes) * inv + p.eps);
+        }
+        lanes_sum(sq, rt.lanes);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long row = base + u * step + slot;
+            const float rstd = rsqrtf(fmaf(sq[u], inv, p.eps));
             if (on && row < p.N) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) x[k] = act<ACT>(fmaf(x[k] * rstd, ch.gamma[k], ch.beta[k]));
-                store_vec<E>(p.y, static_cast<size_t>(row) * p.C + c, pack(x, E{}));
+                for (int k = 0; k < V; ++k) x[u][k] = act<ACT>(fmaf(x[u][k] * rstd, ch.gamma[k], ch.beta[k]));
+                store_vec<E>(p.y, static_cast<size_t>(row) * p.C + c, pack(x[u], E{}));
                 if ((threadIdx.x & (rt.lanes - 1)) == 0) {
-                    const size_t g = static_cast<size_t>(row) * p.G + c / (rt.lanes * V);
-                    if (p.mean) p.mean[g] = mean;
+                    const size_t g = static_cast<size_t>(row) * p.G + group;
+                    if (p.mean) p.mean[g] = sum[u];
                     if (p.rstd) p.rstd[g] = rstd;
                 }
             }
@@ -257,7 +278,7 @@ __device__ __forceinline__ void write_partial(const GnParams& p, float* smem, co
 }
 
 template <typename E, int ACT, int U>
-__global__ void __launch_bounds__(kRowThreads) gn_rows_grad_kernel(const GnParams p)
+__global__ void __launch_bounds__(kRowThreads, 3) gn_rows_grad_kernel(const GnParams p)
 {
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
@@ -266,72 +287,82 @@ __global__ void __launch_bounds__(kRowThreads) gn_rows_grad_kernel(const GnParam
     const bool on = slot < rt.slots && c < p.C;
     const Channels<V> ch(p, on ? c : 0);
     const float inv = 1.f / static_cast<float>(rt.lanes * V);
+    const int group = c / (rt.lanes * V);
     const long long step = static_cast<long long>(gridDim.x) * rt.slots;
     float A[V], B[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) A[k] = B[k] = 0.f;
     for (long long base = static_cast<long long>(blockIdx.x) * rt.slots; base < p.N; base += step * U) {
         uint4 rx[U], rd[U];
-        float mean[U], rstd[U];
+        float mean[U], rstd[U], s1[U], s2[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = base + u * step + slot;
             const bool ok = on && row < p.N;
-            const size_t at = static_cast<size_t>(row) * p.C + c, g = static_cast<size_t>(row) * p.G + c / (rt.lanes * V);
+            const size_t at = static_cast<size_t>(row) * p.C + c, g = static_cast<size_t>(row) * p.G + group;
             rx[u] = ok ? load_vec<E>(p.x, at) : make_uint4(0, 0, 0, 0);
             rd[u] = ok ? load_vec<E>(p.dy, at) : make_uint4(0, 0, 0, 0);
             mean[u] = ok ? __ldg(p.mean + g) : 0.f;
             rstd[u] = ok ? __ldg(p.rstd + g) : 0.f;
         }
+        float x[U][V], d[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            unpack(rx[u], x[u], E{});
+            unpack(rd[u], d[u], E{});
+            s1[u] = s2[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float xh = (x[u][k] - mean[u]) * rstd[u];
+                const float dz = d[u][k] * slope<ACT>(x[u][k], mean[u], rstd[u], ch.gamma[k], ch.beta[k], xh);
+                A[k] += dz;
+                B[k] = fmaf(dz, xh, B[k]);
+                x[u][k] = xh;
+                d[u][k] = dz * ch.gamma[k];
+                s1[u] += d[u][k];
+                s2[u] = fmaf(d[u][k], xh, s2[u]);
+            }
+        }
+        lanes_sum(s1, rt.lanes);
+        lanes_sum(s2, rt.lanes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long row = base + u * step + slot;
-            float x[V], d[V], s1 = 0.f, s2 = 0.f;
-            unpack(rx[u], x, E{});
-            unpack(rd[u], d, E{});
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float xh = (x[k] - mean[u]) * rstd[u];
-                const float dz = d[k] * slope<ACT>(x[k], mean[u], rstd[u], ch.gamma[k], ch.beta[k], xh);
-                A[k] += dz;
-                B[k] = fmaf(dz, xh, B[k]);
-                x[k] = xh;
-                d[k] = dz * ch.gamma[k];
-                s1 += d[k];
-                s2 = fmaf(d[k], xh, s2);
-            }
-            s1 = lanes_sum(s1, rt.lanes) * inv;
-            s2 = lanes_sum(s2, rt.lanes) * inv;
+            const float m1 = s1[u] * inv, m2 = s2[u] * inv;
             if (on && row < p.N) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) x[k] = rstd[u] * (d[k] - fmaf(x[k], s2, s1));
-                store_vec<E>(p.dx, static_cast<size_t>(row) * p.C + c, pack(x, E{}));
+                for (int k = 0; k < V; ++k) x[u][k] = rstd[u] * (d[u][k] - fmaf(x[u][k], m2, m1));
+                store_vec<E>(p.dx, static_cast<size_t>(row) * p.C + c, pack(x[u], E{}));
             }
         }
     }
     if (p.dgamma || p.dbeta) write_partial<V>(p, s_part, A, B, slot, rt.slots, rt.tile, c, c0, on, blockIdx.x);
 }
 
-// dbeta, dgamma: the partials' sums over their index, in a fixed order.
-__global__ void __launch_bounds__(256) gn_param_kernel(const GnParams p, long long partials)
+// dbeta, dgamma: the partials' sums over their index, in a fixed order.  Eight
+// channels per block, so that every partial of a few hundred is in flight at once.
+__global__ void __launch_bounds__(1024) gn_param_kernel(const GnParams p, long long partials)
 {
-    __shared__ float s[2][8][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    __shared__ float s[2][128][9];
+    const int t = threadIdx.x & 7, w = threadIdx.x >> 3, c = blockIdx.x * 8 + t;
     float a = 0.f, b = 0.f;
-    if (c < p.C)
-#pragma unroll 4
-        for (long long i = w; i < partials; i += 8) {
-            a += p.part[static_cast<size_t>(i) * 2 * p.C + c];
-            b += p.part[static_cast<size_t>(i) * 2 * p.C + p.C + c];
+#pragma unroll 8
+    for (long long i = w; i < partials; i += 128) {
+        a += p.part[static_cast<size_t>(i) * 2 * p.C + c];
+        b += p.part[static_cast<size_t>(i) * 2 * p.C + p.C + c];
+    }
+    s[0][w][t] = a;
+    s[1][w][t] = b;
+    for (int o = 64; o > 0; o >>= 1) {
+        __syncthreads();
+        if (w < o) {
+            s[0][w][t] += s[0][w + o][t];
+            s[1][w][t] += s[1][w + o][t];
         }
-    s[0][w][lane] = a;
-    s[1][w][lane] = b;
-    __syncthreads();
-    if (w < 2 && c < p.C) {
-        a = 0.f;
-        for (int k = 0; k < 8; ++k) a += s[w][k][lane];
-        float* out = w == 0 ? p.dbeta : p.dgamma;
-        if (out) out[c] = a;
+    }
+    if (w == 0) {
+        if (p.dbeta) p.dbeta[c] = s[0][0][t];
+        if (p.dgamma) p.dgamma[c] = s[1][0][t];
     }
 }
 
@@ -357,7 +388,7 @@ __global__ void __launch_bounds__(128) gn_line_kernel(const GnParams p)
             const float d = to_f(x[i]) - mean;
             q = fmaf(d, d, q);
         }
-        const float rstd = 1.f / sqrtf(warp_sum(q) * inv + p.eps);
+        const float rstd = rsqrtf(fmaf(warp_sum(q), inv, p.eps));
         E* y = static_cast<E*>(p.y) + at;
         for (int i = lane; i < width; i += 32)
             y[i] = from_f<E>(act<ACT>(fmaf((to_f(x[i]) - mean) * rstd, gamma(i), beta(i))));
@@ -435,16 +466,42 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = sp.threads >> 5;
     const Channels<V> ch(p, c0 + cl);
     int gl[V];   // the local group of each channel
+    gl[0] = cl / width;
+    int left = width - cl % width;   // of that group, from channel k on
 #pragma unroll
-    for (int k = 0; k < V; ++k) gl[k] = (cl + k) / width;
+    for (int k = 1; k < V; ++k) {
+        const bool next = --left == 0;
+        gl[k] = gl[k - 1] + next;
+        if (next) left = width;
+    }
     const float count = static_cast<float>(rows) * width, total = static_cast<float>(p.L) * width;
     if constexpr (GRAD)
         for (int i = threadIdx.x; i < 2 * sp.cblk; i += sp.threads) s_sum[i] = 0.f;
 
-    // The sum of a group over the slots and its channels of f(slot, channel).
-    auto group_sum = [&](int g, auto f) {
+    // Per-slot sums of units, a thread's vector where groups are whole vectors and else a channel; a group's
+    // `per` units over all slots together.
+    const bool whole = width % V == 0;
+    const int units = whole ? tile : sp.cblk, per = whole ? width / V : width;
+    auto put = [&](const float (&v)[V]) {
+        if (!on) return;
+        if (whole) {
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < V; ++k) s += v[k];
+            s_part[slot * units + cl / V] = s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) s_part[slot * units + cl + k] = v[k];
+        }
+    };
+    auto group_sum = [&](int g) {
         float s = 0.f;
-        for (int i = lane; i < slots * width; i += 32) s += f(i / width, g * width + i % width);
+        if ((per & (per - 1)) == 0 && per <= 32) {
+            for (int i = lane / per; i < slots; i += 32 / per) s += s_part[i * units + g * per + (lane & (per - 1))];
+        } else {
+            for (int i = 0; i < slots; ++i)
+                for (int c = lane; c < per; c += 32) s += s_part[i * units + g * per + c];
+        }
         return warp_sum(s);
     };
 
@@ -477,12 +534,10 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
 #pragma unroll
                 for (int k = 0; k < V; ++k) a[k] += x[k];
             }
-            if (on)
-#pragma unroll
-                for (int k = 0; k < V; ++k) s_part[slot * sp.cblk + cl + k] = a[k];
+            put(a);
             __syncthreads();
             for (int g = warp; g < sp.groups; g += warps) {
-                const float s = group_sum(g, [&](int i, int c) { return s_part[i * sp.cblk + c]; });
+                const float s = group_sum(g);
                 if (lane == 0) s_own[2 * g] = rows > 0 ? s / count : 0.f;
             }
             __syncthreads();
@@ -497,12 +552,10 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
                     b[k] = fmaf(d, d, b[k]);
                 }
             }
-            if (on)
-#pragma unroll
-                for (int k = 0; k < V; ++k) s_part[slot * sp.cblk + cl + k] = b[k];
+            put(b);
             __syncthreads();
             for (int g = warp; g < sp.groups; g += warps) {
-                const float s = group_sum(g, [&](int i, int c) { return s_part[i * sp.cblk + c]; });
+                const float s = group_sum(g);
                 if (lane == 0) s_own[2 * g + 1] = s;
             }
             if (sp.cluster > 1) cluster.sync(); else __syncthreads();
@@ -513,7 +566,7 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
                     const float rr = static_cast<float>(max(0LL, min(static_cast<long long>(sp.rows), p.L - static_cast<long long>(r) * sp.rows)));
                     s = merge(s, Stat{rr * width, o[2 * g], o[2 * g + 1]});
                 }
-                const float rs = 1.f / sqrtf(s.m2 / total + p.eps);
+                const float rs = rsqrtf(s.m2 / total + p.eps);
                 s_all[2 * g] = s.mean;
                 s_all[2 * g + 1] = rs;
                 if (rank == 0) {
@@ -768,7 +821,7 @@ __global__ void __launch_bounds__(128) gn_merge_kernel(const GnParams p, const S
             out[0] = s1[0] / total;
             out[1] = s2[0] / total;
         } else {
-            const float rstd = 1.f / sqrtf(s2[0] / total + p.eps);
+            const float rstd = rsqrtf(s2[0] / total + p.eps);
             out[0] = s1[0];
             out[1] = rstd;
             if (p.mean) p.mean[blockIdx.x] = s1[0];
@@ -831,7 +884,7 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
         const int tile = std::min(cv, kRowThreads), slots = kRowThreads / tile;
         const long long blocks = (N + slots - 1) / slots;
         // enough blocks for the GPU several times over; each keeps its channels' gamma and beta, and its sums
-        g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * 8 / std::min(g.grid_y, 4))));
+        g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * 3 * (grad ? 1 : 2))));
         g.partials = g.grid_x;
         g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
         return g;
@@ -869,7 +922,7 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     const int tile = s.cblk / V;
     s.rows = static_cast<int>((L + s.cluster - 1) / s.cluster);
     const long long vectors = static_cast<long long>(s.rows) * tile;
-    s.threads = vectors >= 1024 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
+    s.threads = vectors >= 8192 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
     while (s.threads < tile) s.threads *= 2;
     if (tile <= 256 && slab_smem(s, e, grad) <= kSmemMost) {
         g.way = kSlab;
@@ -963,7 +1016,7 @@ int backward(const GnParams& p, cudaStream_t st)
     if (p.N == 0)
         g.partials = 0;
     else if (g.way == kRows)
-        gn_rows_grad_kernel<E, ACT, 2><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p);
+        gn_rows_grad_kernel<E, ACT, 16 / vec<E>><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p);
     else if (g.way == kLine) {
         gn_line_kernel<E, ACT, true><<<g.grid_x, 128, 0, st>>>(p);
         if (params)
@@ -977,7 +1030,7 @@ int backward(const GnParams& p, cudaStream_t st)
         gn_split_kernel<E, ACT, true, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
     }
     if (rc != SRWM_OK) return rc;
-    if (params) gn_param_kernel<<<(p.C + 31) / 32, 256, 0, st>>>(p, g.partials);
+    if (params) gn_param_kernel<<<p.C / 8, 1024, 0, st>>>(p, g.partials);
     return launched();
 }
 

@@ -173,10 +173,10 @@ int launch_step(int d, const void* q, const void* k, const void* v, long long ld
 LinPlan linattn_plan(int B, int T, int H, int d, int roles)
 {
     // CTAs that the GPU holds at once, about, at each width
-    const long long slots = 152LL * (d == 64 ? 2 : d == 32 ? 8 : 20);
+    const long long slots = 152LL * (d == 64 ? 2 : d == 32 ? 4 : 10);
     const long long ctas = static_cast<long long>(B) * H * roles;
     const int chunks = T / d + (T % d != 0);
-    long long segments = ctas * 2 > slots ? 1 : slots / ctas;
+    long long segments = ctas * 3 > slots ? 1 : slots / ctas;
     if (segments > chunks / 8) segments = chunks / 8;   // at least 8 chunks each: the split reads two tensors again
     if (segments < 2) return {chunks > 0 ? chunks * d : d, 1};
     const int per = static_cast<int>((chunks + segments - 1) / segments);
