@@ -1,4 +1,6 @@
-"""Python binding of libsrwm.so: argument marshalling only.
+"""Python binding of libsrwm.so: argument marshalling only (ctypes; for the
+linear attention and group norm operators, whose calls can be shorter than
+that, a CPython module, _srwm_torch).
 
 Every step of the recurrence runs in the library's sm_103a kernels; this
 module checks tensor types, allocates outputs with torch when the caller does
@@ -13,14 +15,14 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libsrwm.so")
 _LIB = None
+_NATIVE = None
 
 # Status codes of include/srwm.h
 SRWM_OK = 0
 SRWM_ERR_SHAPE = 2
 SRWM_ERR_TIMEOUT = 7
 
-# enum srwm_dtype and enum srwm_activation
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+# enum srwm_activation
 _ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 
 EXPORTS = ("srwm_forward", "srwm_forward_balanced", "srwm_forward_balanced_noalloc",
@@ -383,90 +385,24 @@ def srwm_layer_forward(u, H, n_lr, softmax_input, ln1_gamma, ln1_beta, W0, ln2_g
     return out, W_final
 
 
-def _refuse(t, name, shape, dtype):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _arr(t, name, shape, dtype):
-    """The address of a contiguous CUDA tensor of this shape and type (0 when empty)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, shape, dtype)
-
-
-def _maybe(t, name, shape, dtype):
-    return None if t is None else _arr(t, name, shape, dtype)
-
-
-def _current(t):
-    """The raw handle of the current stream of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _native():
+    """The CPython module that marshals the operators below (csrc/srwm_torch.cpp)."""
+    global _NATIVE
+    if _NATIVE is None:
+        _lib()
+        try:
+            from . import _srwm_torch
+        except ImportError as e:
+            raise RuntimeError("the package's _srwm_torch module is not built. Build it with "
+                               "`python -m self_referential_weight_gb300.build` (needs nvcc).") from e
+        _srwm_torch.set_error(SrwmError)
+        _NATIVE = _srwm_torch
+    return _NATIVE
 
 
 def _on(stream):
     """A context in which `stream` is current: what a call allocates then belongs to the stream that uses it."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-
-
-def _token_rows(x, y, z, names, dtype):
-    """The addresses of three [B,T,H,d] (or [B,H,d]) tensors whose tokens lie
-    one common distance apart, and that distance in elements."""
-    shape = x.shape
-    if x.is_contiguous() and isinstance(y, torch.Tensor) and isinstance(z, torch.Tensor) and y.is_contiguous() and \
-            z.is_contiguous() and x.dtype is dtype and y.dtype is dtype and z.dtype is dtype and \
-            y.shape == shape and z.shape == shape and x.is_cuda and y.is_cuda and z.is_cuda:
-        return x.data_ptr(), y.data_ptr(), z.data_ptr(), shape[-1] * shape[-2]
-    H, d = shape[-2:]
-    ld = None
-    for t, name in zip((x, y, z), names):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype or not t.is_cuda:
-            raise ValueError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.numel() == 0:
-            continue
-        st = t.stride()
-        B, T = (shape[0], shape[1]) if t.dim() == 4 else (shape[0], 1)
-        mine = H * d if B * T == 1 else st[1] if t.dim() == 4 and T > 1 else st[0]
-        if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d) or (T > 1 and B > 1 and st[0] != T * mine):
-            raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
-        if ld is None:
-            ld = mine
-        elif ld != mine:
-            raise ValueError(f"{', '.join(names)} must have the same strides")
-    return x.data_ptr(), y.data_ptr(), z.data_ptr(), H * d if ld is None else ld
-
-
-def _scratch(workspace, need, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace
-
-
-def _dtype_code(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    return code
-
-
-def _check_lengths(lengths, B):
-    if lengths is None:
-        return None
-    if not isinstance(lengths, torch.Tensor) or lengths.dtype != torch.int32 or not lengths.is_cuda or \
-            not lengths.is_contiguous() or lengths.shape != (B,):
-        raise ValueError(f"lengths must be a contiguous int32 CUDA tensor of {B} values")
-    return lengths.data_ptr()
 
 
 def srwm_linattn_workspace_bytes(B, T, H, d) -> int:
@@ -485,23 +421,7 @@ def srwm_linattn_forward(q, k, v, log_decay, scale=None, S_init=None, lengths=No
     if stream is not None:
         with _on(stream):
             return srwm_linattn_forward(q, k, v, log_decay, scale, S_init, lengths, o, S_final, workspace)
-    code = _dtype_code(q, "q")
-    B, T, H, d = q.shape
-    pq, pk, pv, ld = _token_rows(q, k, v, ("q", "k", "v"), q.dtype)
-    if o is None:
-        o = torch.empty((B, T, H, d), dtype=q.dtype, device=q.device)
-    if S_final is None:
-        S_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-    lib = _lib()
-    workspace = _scratch(workspace, max(16, lib.srwm_linattn_workspace_bytes(B, T, H, d)), q.device)
-    rc = lib.srwm_linattn_forward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
-                                  _maybe(S_init, "S_init", (B, H, d, d), torch.float32),
-                                  _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
-                                  _arr(o, "o", (B, T, H, d), q.dtype),
-                                  _arr(S_final, "S_final", (B, H, d, d), torch.float32), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _current(q))
-    _check(rc, "srwm_linattn_forward")
-    return o, S_final
+    return (_NATIVE or _native()).linattn_forward(q, k, v, log_decay, scale, S_init, lengths, o, S_final, workspace)
 
 
 def srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale=None, o_t=None, S_out=None, stream=None):
@@ -511,19 +431,7 @@ def srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale=None, o_t=None, S_ou
     if stream is not None:
         with _on(stream):
             return srwm_linattn_step(q_t, k_t, v_t, log_decay, S_in, scale, o_t, S_out)
-    code = _dtype_code(q_t, "q_t")
-    B, H, d = q_t.shape
-    pq, pk, pv, ld = _token_rows(q_t, k_t, v_t, ("q_t", "k_t", "v_t"), q_t.dtype)
-    if o_t is None:
-        o_t = torch.empty((B, H, d), dtype=q_t.dtype, device=q_t.device)
-    if S_out is None:
-        S_out = torch.empty((B, H, d, d), dtype=torch.float32, device=q_t.device)
-    rc = _lib().srwm_linattn_step(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
-                                  _arr(S_in, "S_in", (B, H, d, d), torch.float32), code, B, H, d,
-                                  d ** -0.5 if scale is None else scale, _arr(o_t, "o_t", (B, H, d), q_t.dtype),
-                                  _arr(S_out, "S_out", (B, H, d, d), torch.float32), _current(q_t))
-    _check(rc, "srwm_linattn_step")
-    return o_t, S_out
+    return (_NATIVE or _native()).linattn_step(q_t, k_t, v_t, log_decay, S_in, scale, o_t, S_out)
 
 
 def srwm_linattn_backward_workspace_bytes(B, T, H, d) -> int:
@@ -540,30 +448,8 @@ def srwm_linattn_backward(q, k, v, log_decay, do, scale=None, S_init=None, lengt
         with _on(stream):
             return srwm_linattn_backward(q, k, v, log_decay, do, scale, S_init, lengths, dS_final, dq, dk, dv,
                                          dS_init, workspace)
-    code = _dtype_code(q, "q")
-    B, T, H, d = q.shape
-    pq, pk, pv, ld = _token_rows(q, k, v, ("q", "k", "v"), q.dtype)
-    given = (dq is not None) + (dk is not None) + (dv is not None)
-    if given == 0:
-        dq, dk, dv = (torch.empty((B, T, H, d), dtype=q.dtype, device=q.device) for _ in range(3))
-    elif given < 3:
-        raise ValueError("dq, dk and dv: give all three or none")
-    pdq, pdk, pdv, ldg = _token_rows(dq, dk, dv, ("dq", "dk", "dv"), q.dtype)
-    if dq.shape != q.shape:
-        raise ValueError(f"dq has shape {tuple(dq.shape)}, expected {tuple(q.shape)}")
-    if dS_init is None:
-        dS_init = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-    lib = _lib()
-    workspace = _scratch(workspace, max(16, lib.srwm_linattn_backward_workspace_bytes(B, T, H, d)), q.device)
-    rc = lib.srwm_linattn_backward(pq, pk, pv, ld, _arr(log_decay, "log_decay", (H,), torch.float32),
-                                   _maybe(S_init, "S_init", (B, H, d, d), torch.float32),
-                                   _check_lengths(lengths, B), code, B, T, H, d, d ** -0.5 if scale is None else scale,
-                                   _arr(do, "do", (B, T, H, d), q.dtype),
-                                   _maybe(dS_final, "dS_final", (B, H, d, d), torch.float32), pdq, pdk, pdv, ldg,
-                                   _arr(dS_init, "dS_init", (B, H, d, d), torch.float32), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _current(q))
-    _check(rc, "srwm_linattn_backward")
-    return dq, dk, dv, dS_init
+    return (_NATIVE or _native()).linattn_backward(q, k, v, log_decay, do, scale, S_init, lengths, dS_final, dq, dk, dv,
+                                                   dS_init, workspace)
 
 
 def srwm_groupnorm_workspace_bytes(N, L, C, G) -> int:
@@ -588,24 +474,8 @@ def srwm_groupnorm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", 
     if stream is not None:
         with _on(stream):
             return srwm_groupnorm_forward(x, gamma, beta, groups, eps, activation, y, mean, rstd, workspace)
-    code = _dtype_code(x, "x")
-    N, L, C = x.shape
-    if y is None:
-        y = torch.empty((N, L, C), dtype=x.dtype, device=x.device)
-    if mean is None:
-        mean = torch.empty((N, groups), dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = torch.empty((N, groups), dtype=torch.float32, device=x.device)
-    lib = _lib()
-    workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_workspace_bytes(N, L, C, groups)), x.device)
-    rc = lib.srwm_groupnorm_forward(_arr(x, "x", (N, L, C), x.dtype), _maybe(gamma, "gamma", (C,), torch.float32),
-                                    _maybe(beta, "beta", (C,), torch.float32), code, N, L, C, groups, eps,
-                                    _activation_code(activation), _arr(y, "y", (N, L, C), x.dtype),
-                                    _arr(mean, "mean", (N, groups), torch.float32),
-                                    _arr(rstd, "rstd", (N, groups), torch.float32), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _current(x))
-    _check(rc, "srwm_groupnorm_forward")
-    return y, mean, rstd
+    return (_NATIVE or _native()).groupnorm_forward(x, gamma, beta, groups, eps, _activation_code(activation), y, mean,
+                                                    rstd, workspace)
 
 
 def srwm_groupnorm_backward_workspace_bytes(N, L, C, G) -> int:
@@ -620,26 +490,8 @@ def srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation="
         with _on(stream):
             return srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation, dx, dgamma, dbeta,
                                            workspace)
-    code = _dtype_code(x, "x")
-    N, L, C = x.shape
-    if dx is None:
-        dx = torch.empty((N, L, C), dtype=x.dtype, device=x.device)
-    if dgamma is None:
-        dgamma = torch.empty((C,), dtype=torch.float32, device=x.device)
-    if dbeta is None:
-        dbeta = torch.empty((C,), dtype=torch.float32, device=x.device)
-    lib = _lib()
-    workspace = _scratch(workspace, max(16, lib.srwm_groupnorm_backward_workspace_bytes(N, L, C, groups)), x.device)
-    rc = lib.srwm_groupnorm_backward(_arr(x, "x", (N, L, C), x.dtype), _maybe(gamma, "gamma", (C,), torch.float32),
-                                     _maybe(beta, "beta", (C,), torch.float32),
-                                     _arr(mean, "mean", (N, groups), torch.float32),
-                                     _arr(rstd, "rstd", (N, groups), torch.float32), _arr(dy, "dy", (N, L, C), x.dtype),
-                                     code, N, L, C, groups, _activation_code(activation),
-                                     _arr(dx, "dx", (N, L, C), x.dtype), _arr(dgamma, "dgamma", (C,), torch.float32),
-                                     _arr(dbeta, "dbeta", (C,), torch.float32), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _current(x))
-    _check(rc, "srwm_groupnorm_backward")
-    return dx, dgamma, dbeta
+    return (_NATIVE or _native()).groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, _activation_code(activation),
+                                                     dx, dgamma, dbeta, workspace)
 
 
 def srwm_debug_set_layer_gemm(mode: int) -> None:

@@ -175,9 +175,11 @@ struct Channels {   // per-channel values of a thread's vector
     __device__ __forceinline__ Channels(const GnParams& p, int c)
     {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            gamma[k] = p.gamma ? p.gamma[c + k] : 1.f;
-            beta[k] = p.beta ? p.beta[c + k] : 0.f;
+        for (int k = 0; k < V; k += 4) {
+            const float4 g = p.gamma ? __ldg(reinterpret_cast<const float4*>(p.gamma + c + k)) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 b = p.beta ? __ldg(reinterpret_cast<const float4*>(p.beta + c + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            gamma[k] = g.x, gamma[k + 1] = g.y, gamma[k + 2] = g.z, gamma[k + 3] = g.w;
+            beta[k] = b.x, beta[k + 1] = b.y, beta[k + 2] = b.z, beta[k + 3] = b.w;
         }
     }
 };
@@ -278,7 +280,7 @@ __device__ __forceinline__ void write_partial(const GnParams& p, float* smem, co
 }
 
 template <typename E, int ACT, int U>
-__global__ void __launch_bounds__(kRowThreads, 3) gn_rows_grad_kernel(const GnParams p)
+__global__ void __launch_bounds__(kRowThreads, sizeof(E) == 4 ? 3 : 2) gn_rows_grad_kernel(const GnParams p)
 {
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
@@ -883,8 +885,8 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
         g.way = kRows;
         const int tile = std::min(cv, kRowThreads), slots = kRowThreads / tile;
         const long long blocks = (N + slots - 1) / slots;
-        // enough blocks for the GPU several times over; each keeps its channels' gamma and beta, and its sums
-        g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * 3 * (grad ? 1 : 2))));
+        // what the GPU holds at once: a block keeps its channels' gamma, beta and sums over its rows
+        g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * (grad && e == 2 ? 2 : 3))));
         g.partials = g.grid_x;
         g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
         return g;
