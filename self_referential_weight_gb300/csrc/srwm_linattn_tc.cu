@@ -1,0 +1,661 @@
+// srwm_linattn_tc.cu -- the primitive of srwm_linattn.h on the 5th-generation
+// tensor cores, for bf16 and d = 64: TMA tile loads and stores, tcgen05.mma
+// with accumulators in tensor memory, one persistent CTA per SM.
+//
+// A chunk is 128 tokens, in their natural order whichever way the recurrence
+// runs; in reverse the chunks are taken from the last one and the mask is the
+// upper triangle.  With i, j in the chunk, nc its valid tokens, g the decay:
+//   OX_i = alpha_u sum_j g^|i-j| (a_i . b_j) c_j         over the causal side
+//   OI_i = a_i X,  out_i = alpha_o (g^e(i) OI_i + OX_i)   e = i + 1, or nc - 1 - i in reverse
+//   U    = sum_j (w_j b_j) c_j^T,  X <- g^nc X + U        w_j = alpha_u g^(nc-1-j), or alpha_u g^(j+1)
+// Five products per chunk: P = a b^T (128 x 128 x 64), OX (P from tensor
+// memory, 128 x 64 x 128), OI (128 x 64 x 64), U (64 x 64 x 128).  a, b, c are
+// the bf16 inputs themselves.  P and X enter their products as bf16 (high,
+// low) pairs (2^-17), w_j b_j as three bf16 terms (2^-24), so that X, which is
+// kept in fp32 registers, is good to fp32.
+//
+// Warps: 0 issues the TMA loads (three stages of a, b, c), 1 the products;
+// 4-7 turn P into its pair (one row per thread); 8-11 write the weighted b's
+// terms (one token per thread); 12-15 hold X, add U to it, leave its pair in
+// shared memory, and write the outputs.  Every stage of a chunk's work runs
+// beside other stages of the same or the next chunk: P and X's chain meet only
+// at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
+// by warps 8-11 before anything reads them; past the tensor's end TMA fills
+// zeros.  Every wait is bounded; a timeout sets the status word and ends the CTA
+// after its copies and products in flight.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cstdint>
+#include <mutex>
+
+#include "srwm.h"
+#include "srwm_check.h"
+#include "srwm_ffgemm.h"
+#include "srwm_linattn.cuh"
+#include "srwm_linattn_tc.h"
+
+namespace srwm {
+namespace {
+
+constexpr int D = 64, C = 128, STAGES = 3;
+constexpr int kTileBytes = C * D * 2;
+constexpr int kThreads = 512;
+constexpr int kMaxDevices = 64;
+
+// tensor memory columns
+constexpr uint32_t kP32 = 0, kPH = 128, kPL = 192, kOI = 256, kOX = 320, kU = 384, kTmemCols = 512;
+
+struct TcMaps {
+    CUtensorMap a, b, c, out;
+};
+struct TcParams {
+    TcMaps map[3];
+    LinParams lin;
+    int roles, items;
+    unsigned* status;
+    unsigned long long wait_limit_ns;
+};
+
+struct __align__(1024) Smem {
+    uint8_t stage[STAGES][3][kTileBytes];   // a | b | c
+    uint8_t terms[3][kTileBytes];           // of w_j b_j
+    uint8_t state[2][D * D * 2];            // X's pair
+    uint8_t out[4][32 * D * 2];             // per output warp: 32 rows
+    float near[4][32], diag[4][64];         // per score warp: decay factors
+    uint64_t full[STAGES], empty[STAGES], u_full[2];
+    uint64_t terms_full, x_full, x_free, p32_full, p32_free, p16_full, o_full, o_free;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Shared-memory matrix descriptor of a 128-byte swizzled tile: atoms of eight
+// 128-byte rows, 1024 bytes apart.  K-major operands (rows = M or N, columns =
+// K) step 32 bytes per 16 of K inside the rows; MN-major ones (rows = K,
+// columns = 64 of M or N) step two atoms.  Bits as in the feed-forward products'
+// descriptor: address >> 4, both byte offsets >> 4, version 1, swizzle mode 2.
+__device__ __forceinline__ uint64_t desc128(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(64) << 16) |
+           (static_cast<uint64_t>(64) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// kind::f16, bf16 operands, fp32 accumulator; bits 15, 16: A, B MN-major.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+// Arrives on `bar` once every product issued before has completed.
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+#define SRWM_R32(r)                                                                                                    \
+    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),         \
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),          \
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),         \
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+#define SRWM_L32                                                                                                       \
+    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "   \
+    "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+
+// 32 columns of the warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_rows32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32(r) : "r"(addr) : "memory");
+}
+// 64 columns of the warp's first 16 lanes, as eight 16 x 8 accumulator
+// fragments: thread l holds (l / 4, 2 (l % 4)), the next column, and both eight lanes below.
+__device__ __forceinline__ void tmem_frag64(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " SRWM_L32 : SRWM_R32(r) : "r"(addr) : "memory");
+}
+// 16 columns of the warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Takes the bf16 of (x, y) out of them.
+__device__ __forceinline__ uint32_t take_bf16(float& x, float& y)
+{
+    const uint32_t h = pack_bf16(x, y);
+    x -= __uint_as_float(h << 16);
+    y -= __uint_as_float(h & 0xffff0000u);
+    return h;
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
+{
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4])
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+// The CTA's items (a stream in a role) and their chunks, as every warp walks them.
+struct Walk {
+    const TcParams& p;
+    int item, role, b, h, n, chunks, k;
+    bool rev;
+    __device__ explicit Walk(const TcParams& params) : p(params), item(static_cast<int>(blockIdx.x)) { open(); }
+    __device__ bool done() const { return item >= p.items; }
+    __device__ void open()
+    {
+        k = 0;
+        chunks = 0;
+        if (done()) return;
+        role = item % p.roles;
+        const int stream = item / p.roles;
+        b = stream / p.lin.H;
+        h = stream % p.lin.H;
+        n = p.lin.lengths ? min(max(p.lin.lengths[b], 0), p.lin.T) : p.lin.T;
+        rev = p.lin.role[role].reverse != 0;
+        chunks = (n + C - 1) / C;
+    }
+    __device__ void next_item()
+    {
+        item += static_cast<int>(gridDim.x);
+        open();
+    }
+    // The next chunk, over the ends of items; false at the end of the list.
+    __device__ bool skip_empty()
+    {
+        while (!done() && k >= chunks) next_item();
+        return !done();
+    }
+    __device__ int token() const { return (rev ? chunks - 1 - k : k) * C; }
+    __device__ int valid() const { return min(C, n - token()); }
+    // Rows that TMA fills with other tokens' values although they are not valid.
+    __device__ bool dirty() const { return valid() < C && n < p.lin.T; }
+};
+
+__global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcParams p)
+{
+    extern __shared__ unsigned char smem_raw[];
+    // the swizzled tiles start on 1024-byte boundaries
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        mbar_init(&sm.terms_full, 4);
+        mbar_init(&sm.u_full[0], 1);
+        mbar_init(&sm.u_full[1], 1);
+        mbar_init(&sm.x_full, 4);
+        mbar_init(&sm.x_free, 1);
+        mbar_init(&sm.p32_full, 1);
+        mbar_init(&sm.p32_free, 4);
+        mbar_init(&sm.p16_full, 4);
+        mbar_init(&sm.o_full, 1);
+        mbar_init(&sm.o_free, 4);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int* abort = &sm.abort;
+    // Waits for phase `phase` of `bar`; false, with the CTA marked to end, when it does not come.
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (mbar_wait_bounded(bar, phase & 1u, p.wait_limit_ns) && !*abort) return true;
+        *abort = 1;
+        atomicOr(p.status, kStatusTimeout);
+        return false;
+    };
+    // One arrival for the warp after its lanes' work.
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;   // the warp's tensor memory lanes
+    uint32_t g = 0;   // chunks so far, the same count in every warp
+
+    if (warp == 0) {
+        // ---- loads
+        if (lane == 0) {
+            int last = -1;
+            uint32_t last_phase = 0;
+            Walk w(p);
+            for (; w.skip_empty() && !*abort; ++w.k, ++g) {
+                const int s = g % STAGES;
+                if (!wait(&sm.empty[s], g / STAGES + 1)) break;
+                const TcMaps& m = p.map[w.role];
+                mbar_arrive_expect_tx(&sm.full[s], 3 * kTileBytes);
+                tma_load_4d(sm.stage[s][1], &m.b, &sm.full[s], 0, w.h, w.token(), w.b);
+                tma_load_4d(sm.stage[s][0], &m.a, &sm.full[s], 0, w.h, w.token(), w.b);
+                tma_load_4d(sm.stage[s][2], &m.c, &sm.full[s], 0, w.h, w.token(), w.b);
+                last = s;
+                last_phase = g / STAGES;
+            }
+            // the shared memory may only be given up once the last loads landed (stages complete in order)
+            if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            auto score = [&](uint32_t at) {   // P of chunk `at`
+                const uint32_t a = smem_u32(sm.stage[at % STAGES][0]), b = smem_u32(sm.stage[at % STAGES][1]);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tmem + kP32, desc128(a + 32 * k), desc128(b + 32 * k), idesc(C, C, false, false), k > 0);
+                commit(&sm.p32_full);
+            };
+            // a chunk's tiles may be read: landed, and cleaned where they need it
+            auto ready = [&](const Walk& w, uint32_t at) {
+                return wait(&sm.full[at % STAGES], at / STAGES) && (!w.dirty() || wait(&sm.terms_full, at));
+            };
+            Walk w(p);
+            bool ok = true, issued = false;
+            if (w.skip_empty()) {
+                ok = ready(w, 0);
+                if (ok) {
+                    fence_after();
+                    score(0);
+                    issued = true;
+                }
+            }
+            for (; ok && w.skip_empty(); ++g) {
+                const uint32_t a = smem_u32(sm.stage[g % STAGES][0]), c = smem_u32(sm.stage[g % STAGES][2]);
+                const uint32_t u = tmem + kU + 64 * (g & 1);
+                if (!(ok = wait(&sm.terms_full, g))) break;
+                fence_after();
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_ss(u, desc128(smem_u32(sm.terms[t]) + 2048 * k), desc128(c + 2048 * k), idesc(D, D, true, true),
+                               (t | k) > 0);
+                commit(&sm.u_full[g & 1]);
+                if (!(ok = wait(&sm.x_full, g) && wait(&sm.o_free, g + 1))) break;
+                fence_after();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + kOI, desc128(a + 32 * k), desc128(smem_u32(sm.state[t]) + 2048 * k),
+                               idesc(C, D, false, true), (t | k) > 0);
+                commit(&sm.x_free);
+                ++w.k;
+                if (w.skip_empty()) {   // the next chunk's scores, ahead of this one's output
+                    if (!(ok = ready(w, g + 1) && wait(&sm.p32_free, g))) break;
+                    fence_after();
+                    score(g + 1);
+                }
+                if (!(ok = wait(&sm.p16_full, g))) break;
+                fence_after();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_ts(tmem + kOX, tmem + (t ? kPL : kPH) + 8 * k, desc128(c + 2048 * k), idesc(C, D, false, true),
+                               (t | k) > 0);
+                commit(&sm.o_full);
+                commit(&sm.empty[g % STAGES]);
+            }
+            // Tensor memory may only be freed once the products issued have completed: after a timeout nobody
+            // else waits for them.
+            if (!ok && issued) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ---- P as a bf16 pair, one row per thread
+        const int row = 32 * (warp - 4) + lane;
+        int before = -1;   // direction whose masked blocks hold zeros
+        bool ok = true;
+        Walk w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
+            const int own = warp - 4;
+            float *near = sm.near[own], *diag = sm.diag[own];
+            __syncwarp();   // the tables of the item before are no longer read
+            near[lane] = exp2f(lg * static_cast<float>(w.rev ? lane : 31 - lane));
+            for (int x = lane; x < 64; x += 32) {   // diag[31 + l - x]: row l, column x of a diagonal block
+                const int gap = w.rev ? 31 - x : x - 31;
+                diag[x] = gap >= 0 ? au * exp2f(lg * static_cast<float>(gap)) : 0.f;
+            }
+            __syncwarp();
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                if (!(ok = wait(&sm.p32_full, g) && wait(&sm.o_full, g + 1))) break;   // the pair before has been read
+                fence_after();
+                uint32_t hi[16], lo[16];
+                if (before != w.rev) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) hi[k] = 0;
+                    for (int cb = 0; cb < 4; ++cb)
+                        if (w.rev ? cb < own : cb > own) {
+                            tmem_store16(tmem + quad + kPH + 16 * cb, hi);
+                            tmem_store16(tmem + quad + kPL + 16 * cb, hi);
+                        }
+                    before = w.rev;
+                }
+                const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
+#pragma unroll 1
+                for (int cb = c0; cb <= c1; ++cb) {
+                    uint32_t r[32];
+                    tmem_rows32(tmem + quad + kP32 + 32 * cb, r);
+                    if (cb == c1) {
+                        fence_before();
+                        arrive(&sm.p32_free);
+                    }
+                    if (cb == own) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            r[x] = __float_as_uint(__uint_as_float(r[x]) * diag[31 + lane - x]);
+                    } else {
+                        const float f = au * exp2f(lg * static_cast<float>(w.rev ? 32 * cb - row : row - 32 * cb - 31));
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(&near[x]);
+                            r[x] = __float_as_uint(__uint_as_float(r[x]) * f * t.x);
+                            r[x + 1] = __float_as_uint(__uint_as_float(r[x + 1]) * f * t.y);
+                            r[x + 2] = __float_as_uint(__uint_as_float(r[x + 2]) * f * t.z);
+                            r[x + 3] = __float_as_uint(__uint_as_float(r[x + 3]) * f * t.w);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
+                        hi[k] = take_bf16(x, y);
+                        lo[k] = pack_bf16(x, y);
+                    }
+                    tmem_store16(tmem + quad + kPH + 16 * cb, hi);
+                    tmem_store16(tmem + quad + kPL + 16 * cb, lo);
+                }
+                tmem_store_wait();
+                fence_before();
+                arrive(&sm.p16_full);
+            }
+        }
+    } else if (warp >= 8 && warp < 12) {
+        // ---- the terms of w_j b_j, one token per thread
+        const int j = 32 * (warp - 8) + lane;
+        bool ok = true;
+        Walk w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                const int s = g % STAGES, nc = w.valid();
+                const float wj = au * exp2f(lg * static_cast<float>(w.rev ? j + 1 : max(0, nc - 1 - j)));
+                // the terms before have been read
+                if (!(ok = wait(&sm.full[s], g / STAGES) && (g == 0 || wait(&sm.u_full[(g - 1) & 1], (g - 1) >> 1)))) break;
+                const uint32_t at = smem_u32(sm.stage[s][1]) + 128 * j;
+                const bool clean = j >= nc && w.dirty();
+                const uint32_t zero[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t o = static_cast<uint32_t>((q ^ (j & 7)) << 4);
+                    uint32_t v[4], t0[4], t1[4], t2[4];
+                    lds128(at + o, v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (clean) v[k] = 0;
+                        float x = __uint_as_float(v[k] << 16) * wj, y = __uint_as_float(v[k] & 0xffff0000u) * wj;
+                        t0[k] = take_bf16(x, y);
+                        t1[k] = take_bf16(x, y);
+                        t2[k] = pack_bf16(x, y);
+                    }
+                    const uint32_t to = smem_u32(sm.terms[0]) + 128 * j + o;
+                    sts128(to, t0);
+                    sts128(to + kTileBytes, t1);
+                    sts128(to + 2 * kTileBytes, t2);
+                    if (clean) {
+                        sts128(at + o, zero);
+                        sts128(at + o - kTileBytes, zero);   // a's and c's tiles lie on either side
+                        sts128(at + o + kTileBytes, zero);
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive(&sm.terms_full);
+            }
+        }
+    } else if (warp >= 12) {
+        // ---- the state and the outputs
+        const int own = warp - 12, r4 = lane >> 2, x2 = 2 * (lane & 3);
+        bool ok = true;
+        Walk w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            const size_t mat = (static_cast<size_t>(w.b) * p.lin.H + w.h) * D * D;
+            float X[8][4];   // rows 16 own + r4 (+ 8), columns 8 t + x2 (+ 1)
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
+                    X[t][k] = R.x_in ? R.x_in[mat + (R.transposed ? q * D + i : i * D + q)] : 0.f;
+                }
+            auto leave_state = [&](uint32_t at) {   // X's pair for chunk `at`
+                if (!(ok = wait(&sm.x_free, at + 1))) return;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float x = X[t][2 * k], y = X[t][2 * k + 1];
+                        const uint32_t to = state_at<D>(smem_u32(sm.state[0]), 16 * own + r4 + 8 * k, t, 0) + 2 * x2;
+                        const uint32_t hi = take_bf16(x, y), lo = pack_bf16(x, y);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + D * D * 2), "r"(lo) : "memory");
+                    }
+                fence_proxy_async_smem();
+                arrive(&sm.x_full);
+            };
+            const Decay full = decay_over(lg, C);
+            if (w.chunks > 0) leave_state(g);
+            for (; ok && w.k < w.chunks; ++w.k, ++g) {
+                const int nc = w.valid();
+                if (!(ok = wait(&sm.u_full[g & 1], g >> 1))) break;
+                fence_after();
+                {
+                    uint32_t u[32];
+                    tmem_frag64(tmem + quad + kU + 64 * (g & 1), u);
+                    fence_before();
+                    const Decay dec = nc == C ? full : decay_over(lg, nc);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            X[t][k] = fmaf(X[t][k], dec.m, fmaf(X[t][k], dec.c, __uint_as_float(u[4 * t + k])));
+                }
+                if (w.k + 1 < w.chunks) {
+                    leave_state(g + 1);
+                    if (!ok) break;
+                }
+                if (!(ok = wait(&sm.o_full, g))) break;
+                fence_after();
+                const int i = 32 * own + lane;
+                const float f = R.alpha_o * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
+                if (lane == 0) bulk_wait_read<0>();   // the rows before have left the staging buffer
+                __syncwarp();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t oi[32], ox[32];
+                    tmem_rows32(tmem + quad + kOI + 32 * half, oi);
+                    tmem_rows32(tmem + quad + kOX + 32 * half, ox);
+                    if (half == 1) {
+                        fence_before();
+                        arrive(&sm.o_free);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int x = 8 * q + 2 * k;
+                            v[k] = pack_bf16(fmaf(__uint_as_float(oi[x]), f, R.alpha_o * __uint_as_float(ox[x])),
+                                             fmaf(__uint_as_float(oi[x + 1]), f, R.alpha_o * __uint_as_float(ox[x + 1])));
+                        }
+                        sts128(smem_u32(sm.out[own]) + 128 * lane + (((4 * half + q) ^ (lane & 7)) << 4), v);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && w.token() + 32 * own < p.lin.T) {
+                    tma_store_4d(&p.map[w.role].out, sm.out[own], 0, w.h, w.token() + 32 * own, w.b);
+                    bulk_commit();
+                }
+            }
+            if (ok && R.x_out)
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
+                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k];
+                    }
+            // tokens past the last chunk
+            __nv_bfloat16* po = static_cast<__nv_bfloat16*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
+            const long long z0 = static_cast<long long>(w.chunks) * C, pieces = (p.lin.T - z0) * (D / 8);
+            for (long long q = threadIdx.x - 384; q < pieces; q += 128)
+                *reinterpret_cast<uint4*>(po + (z0 + q / (D / 8)) * R.ldo + q % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+        }
+        if (lane == 0) bulk_wait_all<0>();   // the rows in flight are written before the CTA ends
+        __syncwarp();
+    }
+
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+// {d, H, T, B} of token rows ld elements apart, boxes of `rows` tokens of one stream.
+int token_map(CUtensorMap* map, const void* base, long long ld, const LinParams& p, int rows)
+{
+    auto enc = encoder();
+    if (!enc) return SRWM_ERR_CUDA;
+    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(p.B)};
+    const cuuint64_t strides[3] = {2 * D, static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * p.T};
+    const cuuint32_t box[4] = {D, 1, static_cast<cuuint32_t>(rows), 1}, one[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SRWM_OK : SRWM_ERR_CUDA;
+}
+
+}  // namespace
+
+bool linattn_tc_takes(int dtype, int d, const LinParams& p)
+{
+    return dtype == SRWM_BF16 && d == D && p.segments == 1 && p.T >= C;
+}
+
+int linattn_tc_launch(int roles, const LinParams& lin, cudaStream_t st)
+{
+    TcParams p{};
+    p.lin = lin;
+    p.roles = roles;
+    const long long items = static_cast<long long>(lin.B) * lin.H * roles;
+    if (items > 0x7fffffffLL - 1024) return SRWM_ERR_SHAPE;
+    p.items = static_cast<int>(items);
+    int rc = device_status_ptr(&p.status);
+    if (rc != SRWM_OK) return rc;
+    p.wait_limit_ns = device_wait_limit_ns();
+    for (int i = 0; i < roles; ++i) {
+        const LinRole& r = lin.role[i];
+        if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].b, r.b, r.ldb, lin, C)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].c, r.c, r.ldc, lin, C)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].out, r.out, r.ldo, lin, 32)) != SRWM_OK)
+            return rc;
+    }
+    static std::atomic<int> sms[kMaxDevices];   // 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    constexpr int smem = static_cast<int>(sizeof(Smem)) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+    int n_sm = sms[dev].load();
+    if (n_sm == 0) {
+        if (cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(linattn_tc_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem) != cudaSuccess) {
+            cudaGetLastError();
+            return SRWM_ERR_CUDA;
+        }
+        sms[dev].store(n_sm);
+    }
+    linattn_tc_kernel<<<p.items < n_sm ? p.items : n_sm, kThreads, smem, st>>>(p);
+    return launched();
+}
+
+}  // namespace srwm
