@@ -46,8 +46,8 @@ constexpr int kTileBytes = C * D * 2;
 constexpr int kThreads = 512;
 constexpr int kMaxDevices = 64;
 
-// tensor memory columns
-constexpr uint32_t kP32 = 0, kPH = 128, kPL = 192, kOI = 256, kOX = 320, kU = 384, kTmemCols = 512;
+// tensor memory columns (the pair's high half, then its low half)
+constexpr uint32_t kP32 = 0, kPH = 128, kPL = kPH + 64, kOI = 256, kOX = 320, kU = 384, kTmemCols = 512;
 
 struct TcMaps {
     CUtensorMap a, b, c, out;
@@ -90,21 +90,32 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate)
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        "l"(a), "l"(b), "r"(id), "n"(ACC ? 1 : 0)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate)
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        "r"(a), "l"(b), "r"(id), "n"(ACC ? 1 : 0)
         : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
 }
 // Arrives on `bar` once every product issued before has completed.
 __device__ __forceinline__ void commit(uint64_t* bar)
@@ -283,73 +294,82 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---- products
-        if (lane == 0) {
-            auto score = [&](uint32_t at) {   // P of chunk `at`
-                const uint32_t a = smem_u32(sm.stage[at % STAGES][0]), b = smem_u32(sm.stage[at % STAGES][1]);
+        // ---- products.  The whole warp walks the chunks, so that descriptors stay in uniform registers; one
+        // elected lane issues.
+        constexpr uint32_t id_p = idesc(C, C, false, false), id_u = idesc(D, D, true, true), id_o = idesc(C, D, false, true);
+        const uint64_t d_terms = desc128(smem_u32(sm.terms[0])), d_state = desc128(smem_u32(sm.state[0]));
+        const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
+        constexpr uint64_t kStage = 3 * kTileBytes / 16, kTile = kTileBytes / 16;   // descriptor steps
+        auto score = [&](uint32_t at) {   // P of chunk `at`
+            const uint64_t a = d_stage + kStage * (at % STAGES), b = a + kTile;
+            if (elect()) {
+                mma_ss<false>(tmem + kP32, a, b, id_p);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + kP32, desc128(a + 32 * k), desc128(b + 32 * k), idesc(C, C, false, false), k > 0);
+                for (int k = 1; k < D / 16; ++k) mma_ss<true>(tmem + kP32, a + 2 * k, b + 2 * k, id_p);
                 commit(&sm.p32_full);
-            };
-            // a chunk's tiles may be read: landed, and cleaned where they need it
-            auto ready = [&](const Walk& w, uint32_t at) {
-                return wait(&sm.full[at % STAGES], at / STAGES) && (!w.dirty() || wait(&sm.terms_full, at));
-            };
-            Walk w(p);
-            bool ok = true, issued = false;
-            if (w.skip_empty()) {
-                ok = ready(w, 0);
-                if (ok) {
-                    fence_after();
-                    score(0);
-                    issued = true;
-                }
             }
-            for (; ok && w.skip_empty(); ++g) {
-                const uint32_t a = smem_u32(sm.stage[g % STAGES][0]), c = smem_u32(sm.stage[g % STAGES][2]);
-                const uint32_t u = tmem + kU + 64 * (g & 1);
-                if (!(ok = wait(&sm.terms_full, g))) break;
+            __syncwarp();
+        };
+        // a chunk's tiles may be read: landed, and cleaned where they need it
+        auto ready = [&](const Walk& w, uint32_t at) {
+            return wait(&sm.full[at % STAGES], at / STAGES) && (!w.dirty() || wait(&sm.terms_full, at));
+        };
+        Walk w(p);
+        bool ok = true, issued = false;
+        if (w.skip_empty()) {
+            ok = ready(w, 0);
+            if (ok) {
                 fence_after();
+                score(0);
+                issued = true;
+            }
+        }
+        for (; ok && w.skip_empty(); ++g) {
+            const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
+            const uint32_t u = tmem + kU + 64 * (g & 1);
+            if (!(ok = wait(&sm.terms_full, g))) break;
+            fence_after();
+            if (elect()) {
+                mma_ss<false>(u, d_terms, c, id_u);
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        mma_ss(u, desc128(smem_u32(sm.terms[t]) + 2048 * k), desc128(c + 2048 * k), idesc(D, D, true, true),
-                               (t | k) > 0);
+                for (int k = 1; k < 3 * C / 16; ++k)
+                    mma_ss<true>(u, d_terms + kTile * (k / 8) + 128 * (k % 8), c + 128 * (k % 8), id_u);
                 commit(&sm.u_full[g & 1]);
-                if (!(ok = wait(&sm.x_full, g) && wait(&sm.o_free, g + 1))) break;
-                fence_after();
+            }
+            __syncwarp();
+            if (!(ok = wait(&sm.x_full, g) && wait(&sm.o_free, g + 1))) break;
+            fence_after();
+            if (elect()) {
+                mma_ss<false>(tmem + kOI, a, d_state, id_o);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + kOI, desc128(a + 32 * k), desc128(smem_u32(sm.state[t]) + 2048 * k),
-                               idesc(C, D, false, true), (t | k) > 0);
+                for (int k = 1; k < 2 * D / 16; ++k)
+                    mma_ss<true>(tmem + kOI, a + 2 * (k % 4), d_state + 512 * (k / 4) + 128 * (k % 4), id_o);
                 commit(&sm.x_free);
-                ++w.k;
-                if (w.skip_empty()) {   // the next chunk's scores, ahead of this one's output
-                    if (!(ok = ready(w, g + 1) && wait(&sm.p32_free, g))) break;
-                    fence_after();
-                    score(g + 1);
-                }
-                if (!(ok = wait(&sm.p16_full, g))) break;
+            }
+            __syncwarp();
+            ++w.k;
+            if (w.skip_empty()) {   // the next chunk's scores, ahead of this one's output
+                if (!(ok = ready(w, g + 1) && wait(&sm.p32_free, g))) break;
                 fence_after();
+                score(g + 1);
+            }
+            if (!(ok = wait(&sm.p16_full, g))) break;
+            fence_after();
+            if (elect()) {
+                mma_ts<false>(tmem + kOX, tmem + kPH, c, id_o);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        mma_ts(tmem + kOX, tmem + (t ? kPL : kPH) + 8 * k, desc128(c + 2048 * k), idesc(C, D, false, true),
-                               (t | k) > 0);
+                for (int k = 1; k < 2 * C / 16; ++k)
+                    mma_ts<true>(tmem + kOX, tmem + kPH + 8 * k, c + 128 * (k % 8), id_o);
                 commit(&sm.o_full);
                 commit(&sm.empty[g % STAGES]);
             }
-            // Tensor memory may only be freed once the products issued have completed: after a timeout nobody
-            // else waits for them.
-            if (!ok && issued) {
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 1000000ull) {
-                }
+            __syncwarp();
+        }
+        // Tensor memory may only be freed once the products issued have completed: after a timeout nobody else
+        // waits for them.
+        if (!ok && issued) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000ull) {
             }
         }
         __syncwarp();
