@@ -14,10 +14,10 @@
 // low) pairs (2^-17), w_j b_j as three bf16 terms (2^-24), so that X, which is
 // kept in fp32 registers, is good to fp32.
 //
-// Warps: 0 issues the TMA loads (three stages of a, b, c), 1 the products;
-// 4-7 turn P into its pair (one row per thread); 8-11 write the weighted b's
-// terms (one token per thread); 12-15 hold X, add U to it, leave its pair in
-// shared memory, and write the outputs.  Every stage of a chunk's work runs
+// Warps: 0-7 turn P into its pair (one row per thread); 8-11 write the weighted
+// b's terms (one token per thread); 12-15 hold X, add U to it and leave its
+// pair in shared memory; 16-19 write the outputs; 20 issues the TMA loads
+// (three stages of a, b, c), 21 the products.  Every stage of a chunk's work runs
 // beside other stages of the same or the next chunk: P and X's chain meet only
 // at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
 // by warps 8-11 before anything reads them; past the tensor's end TMA fills
@@ -43,8 +43,10 @@ namespace {
 
 constexpr int D = 64, C = 128, STAGES = 3;
 constexpr int kTileBytes = C * D * 2;
-constexpr int kThreads = 512;
+constexpr int kThreads = 704;
 constexpr int kMaxDevices = 64;
+// first warps of the roles; those that read tensor memory start at multiples of four, whose lanes they own in order
+constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21;
 
 // tensor memory columns (the pair's high half, then its low half)
 constexpr uint32_t kP32 = 0, kPH = 128, kPL = kPH + 64, kOI = 256, kOX = 320, kU = 384, kTmemCols = 512;
@@ -65,7 +67,7 @@ struct __align__(1024) Smem {
     uint8_t terms[3][kTileBytes];           // of w_j b_j
     uint8_t state[2][D * D * 2];            // X's pair
     uint8_t out[4][32 * D * 2];             // per output warp: 32 rows
-    float near[4][32], diag[4][64];         // per score warp: decay factors
+    float decay[8][64];                     // per score warp: g^|column - row| of a diagonal block, by their difference
     uint64_t full[STAGES], empty[STAGES], u_full[2];
     uint64_t terms_full, x_full, x_free, p32_full, p32_free, p16_full, o_full, o_free;
     uint32_t tmem_base;
@@ -130,25 +132,41 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-#define SRWM_R32(r)                                                                                                    \
-    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),         \
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),          \
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),         \
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+// Tensor memory loads return before their registers are written; tmem_wait
+// names the registers, so that no use of them moves ahead of it.
+#define SRWM_R16(c, r)                                                                                                 \
+    c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]), c(r[10]), c(r[11]),       \
+        c(r[12]), c(r[13]), c(r[14]), c(r[15])
+#define SRWM_R32(c, r)                                                                                                 \
+    SRWM_R16(c, r), c(r[16]), c(r[17]), c(r[18]), c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), \
+        c(r[26]), c(r[27]), c(r[28]), c(r[29]), c(r[30]), c(r[31])
+#define SRWM_L16 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
 #define SRWM_L32                                                                                                       \
     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "   \
-    "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+    "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
 
-// 32 columns of the warp's 32 lanes, one lane per thread.
-__device__ __forceinline__ void tmem_rows32(uint32_t addr, uint32_t (&r)[32])
+// 16 or 32 columns of the warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32(r) : "r"(addr) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " SRWM_L16 : SRWM_R16("=r", r) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
 }
 // 64 columns of the warp's first 16 lanes, as eight 16 x 8 accumulator
 // fragments: thread l holds (l / 4, 2 (l % 4)), the next column, and both eight lanes below.
 __device__ __forceinline__ void tmem_frag64(uint32_t addr, uint32_t (&r)[32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " SRWM_L32 : SRWM_R32(r) : "r"(addr) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R16("+r", r)::"memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R32("+r", r)::"memory");
 }
 // 16 columns of the warp's 32 lanes, one lane per thread.
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
@@ -224,9 +242,12 @@ struct Walk {
 
 __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcParams p)
 {
-    extern __shared__ unsigned char smem_raw[];
-    // the swizzled tiles start on 1024-byte boundaries
-    Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    if ((smem_u32(smem_raw) & 1023u) != 0) {   // the swizzled tiles start on 1024-byte boundaries
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemBase);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -239,14 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         mbar_init(&sm.x_full, 4);
         mbar_init(&sm.x_free, 1);
         mbar_init(&sm.p32_full, 1);
-        mbar_init(&sm.p32_free, 4);
-        mbar_init(&sm.p16_full, 4);
+        mbar_init(&sm.p32_free, 8);
+        mbar_init(&sm.p16_full, 8);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.o_free, 4);
         sm.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
@@ -272,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;   // the warp's tensor memory lanes
     uint32_t g = 0;   // chunks so far, the same count in every warp
 
-    if (warp == 0) {
+    if (warp == kLoadWarp) {
         // ---- loads
         if (lane == 0) {
             int last = -1;
@@ -293,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         // ---- products.  The whole warp walks the chunks, so that descriptors stay in uniform registers; one
         // elected lane issues.
         constexpr uint32_t id_p = idesc(C, C, false, false), id_u = idesc(D, D, true, true), id_o = idesc(C, D, false, true);
@@ -373,9 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
-        // ---- P as a bf16 pair, one row per thread
-        const int row = 32 * (warp - 4) + lane;
+    } else if (warp < kTermWarp) {
+        // ---- P as a bf16 pair, one row per thread; two sets of four warps take the 32-column blocks in turn
+        const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
+        float* decay = sm.decay[warp];
         int before = -1;   // direction whose masked blocks hold zeros
         bool ok = true;
         Walk w(p);
@@ -383,70 +405,72 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
-            const int own = warp - 4;
-            float *near = sm.near[own], *diag = sm.diag[own];
-            __syncwarp();   // the tables of the item before are no longer read
-            near[lane] = exp2f(lg * static_cast<float>(w.rev ? lane : 31 - lane));
-            for (int x = lane; x < 64; x += 32) {   // diag[31 + l - x]: row l, column x of a diagonal block
-                const int gap = w.rev ? 31 - x : x - 31;
-                diag[x] = gap >= 0 ? au * exp2f(lg * static_cast<float>(gap)) : 0.f;
+            // tab[x - l]: alpha_u g^|x - l| for row l, column x on the causal side of a diagonal block, 0 on the
+            // other.  A block beside the diagonal takes the row's factor off: its columns are those of row 31 in
+            // order, of row 0 in reverse, 16-byte aligned in either case.
+            float* tab = decay + 31 + (w.rev ? 1 : 0);
+            __syncwarp();   // the table of the item before is no longer read
+            for (int i = lane; i < 63; i += 32) {
+                const int gap = w.rev ? i - 31 : 31 - i;
+                tab[i - 31] = gap >= 0 ? au * exp2f(lg * static_cast<float>(gap)) : 0.f;
             }
             __syncwarp();
+            const float4* beside = reinterpret_cast<const float4*>(w.rev ? tab : tab - 31);
+            const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
+            const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
                 if (!(ok = wait(&sm.p32_full, g) && wait(&sm.o_full, g + 1))) break;   // the pair before has been read
                 fence_after();
-                uint32_t hi[16], lo[16];
                 if (before != w.rev) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) hi[k] = 0;
-                    for (int cb = 0; cb < 4; ++cb)
-                        if (w.rev ? cb < own : cb > own) {
-                            tmem_store16(tmem + quad + kPH + 16 * cb, hi);
-                            tmem_store16(tmem + quad + kPL + 16 * cb, hi);
+                    const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                    for (int cb = set; cb < 4; cb += 2)
+                        if (cb < c0 || cb > c1) {
+                            tmem_store16(tmem + quad + kPH + 16 * cb, zero);
+                            tmem_store16(tmem + quad + kPL + 16 * cb, zero);
                         }
                     before = w.rev;
                 }
-                const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
 #pragma unroll 1
-                for (int cb = c0; cb <= c1; ++cb) {
-                    uint32_t r[32];
-                    tmem_rows32(tmem + quad + kP32 + 32 * cb, r);
-                    if (cb == c1) {
-                        fence_before();
-                        arrive(&sm.p32_free);
-                    }
+                for (int cb = first; cb <= c1; cb += 2) {
+                    uint32_t r[32], v[16];
+                    tmem_rows(tmem + quad + kP32 + 32 * cb, r);
+                    const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
+                    tmem_wait(r);
                     if (cb == own) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            r[x] = __float_as_uint(__uint_as_float(r[x]) * diag[31 + lane - x]);
+                        for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * tab[x - lane]);
                     } else {
-                        const float f = au * exp2f(lg * static_cast<float>(w.rev ? 32 * cb - row : row - 32 * cb - 31));
 #pragma unroll
                         for (int x = 0; x < 32; x += 4) {
-                            const float4 t = *reinterpret_cast<const float4*>(&near[x]);
-                            r[x] = __float_as_uint(__uint_as_float(r[x]) * f * t.x);
-                            r[x + 1] = __float_as_uint(__uint_as_float(r[x + 1]) * f * t.y);
-                            r[x + 2] = __float_as_uint(__uint_as_float(r[x + 2]) * f * t.z);
-                            r[x + 3] = __float_as_uint(__uint_as_float(r[x + 3]) * f * t.w);
+                            const float4 t = beside[x / 4];
+                            r[x] = __float_as_uint(__uint_as_float(r[x]) * (f * t.x));
+                            r[x + 1] = __float_as_uint(__uint_as_float(r[x + 1]) * (f * t.y));
+                            r[x + 2] = __float_as_uint(__uint_as_float(r[x + 2]) * (f * t.z));
+                            r[x + 3] = __float_as_uint(__uint_as_float(r[x + 3]) * (f * t.w));
                         }
                     }
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
-                        hi[k] = take_bf16(x, y);
-                        lo[k] = pack_bf16(x, y);
+                        v[k] = take_bf16(x, y);
+                        r[2 * k] = __float_as_uint(x);
+                        r[2 * k + 1] = __float_as_uint(y);
                     }
-                    tmem_store16(tmem + quad + kPH + 16 * cb, hi);
-                    tmem_store16(tmem + quad + kPL + 16 * cb, lo);
+                    tmem_store16(tmem + quad + kPH + 16 * cb, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = pack_bf16(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+                    tmem_store16(tmem + quad + kPL + 16 * cb, v);
                 }
+                fence_before();
+                arrive(&sm.p32_free);
                 tmem_store_wait();
                 fence_before();
                 arrive(&sm.p16_full);
             }
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp < kStateWarp) {
         // ---- the terms of w_j b_j, one token per thread
-        const int j = 32 * (warp - 8) + lane;
+        const int j = 32 * (warp - kTermWarp) + lane;
         bool ok = true;
         Walk w(p);
         for (; ok && !w.done(); w.next_item()) {
@@ -461,18 +485,25 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 const uint32_t at = smem_u32(sm.stage[s][1]) + 128 * j;
                 const bool clean = j >= nc && w.dirty();
                 const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll
+                uint32_t ahead[4];
+                lds128(at + static_cast<uint32_t>((j & 7) << 4), ahead);
+#pragma unroll 1
                 for (int q = 0; q < 8; ++q) {
                     const uint32_t o = static_cast<uint32_t>((q ^ (j & 7)) << 4);
-                    uint32_t v[4], t0[4], t1[4], t2[4];
-                    lds128(at + o, v);
+                    uint32_t t0[4], t1[4], t2[4];
+                    float x[4], y[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (clean) v[k] = 0;
-                        float x = __uint_as_float(v[k] << 16) * wj, y = __uint_as_float(v[k] & 0xffff0000u) * wj;
-                        t0[k] = take_bf16(x, y);
-                        t1[k] = take_bf16(x, y);
-                        t2[k] = pack_bf16(x, y);
+                        const uint32_t v = clean ? 0 : ahead[k];
+                        x[k] = __uint_as_float(v << 16) * wj;
+                        y[k] = __uint_as_float(v & 0xffff0000u) * wj;
+                    }
+                    lds128(at + static_cast<uint32_t>((((q + 1) & 7) ^ (j & 7)) << 4), ahead);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        t0[k] = take_bf16(x[k], y[k]);
+                        t1[k] = take_bf16(x[k], y[k]);
+                        t2[k] = pack_bf16(x[k], y[k]);
                     }
                     const uint32_t to = smem_u32(sm.terms[0]) + 128 * j + o;
                     sts128(to, t0);
@@ -488,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 arrive(&sm.terms_full);
             }
         }
-    } else if (warp >= 12) {
-        // ---- the state and the outputs
-        const int own = warp - 12, r4 = lane >> 2, x2 = 2 * (lane & 3);
+    } else if (warp < kOutWarp) {
+        // ---- the state
+        const int own = warp - kStateWarp, r4 = lane >> 2, x2 = 2 * (lane & 3);
         bool ok = true;
         Walk w(p);
         for (; ok && !w.done(); w.next_item()) {
@@ -529,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 {
                     uint32_t u[32];
                     tmem_frag64(tmem + quad + kU + 64 * (g & 1), u);
+                    tmem_wait(u);
                     fence_before();
                     const Decay dec = nc == C ? full : decay_over(lg, nc);
 #pragma unroll
@@ -541,17 +573,39 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     leave_state(g + 1);
                     if (!ok) break;
                 }
+            }
+            if (ok && R.x_out)
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
+                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k];
+                    }
+        }
+    } else if (warp < kLoadWarp) {
+        // ---- the outputs, one row per thread
+        const int own = warp - kOutWarp;
+        bool ok = true;
+        Walk w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                const int nc = w.valid();
                 if (!(ok = wait(&sm.o_full, g))) break;
                 fence_after();
                 const int i = 32 * own + lane;
                 const float f = R.alpha_o * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
                 if (lane == 0) bulk_wait_read<0>();   // the rows before have left the staging buffer
                 __syncwarp();
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t oi[32], ox[32];
-                    tmem_rows32(tmem + quad + kOI + 32 * half, oi);
-                    tmem_rows32(tmem + quad + kOX + 32 * half, ox);
+                    tmem_rows(tmem + quad + kOI + 32 * half, oi);
+                    tmem_rows(tmem + quad + kOX + 32 * half, ox);
+                    tmem_wait(oi);
+                    tmem_wait(ox);
                     if (half == 1) {
                         fence_before();
                         arrive(&sm.o_free);
@@ -575,18 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     bulk_commit();
                 }
             }
-            if (ok && R.x_out)
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
-                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k];
-                    }
             // tokens past the last chunk
             __nv_bfloat16* po = static_cast<__nv_bfloat16*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
             const long long z0 = static_cast<long long>(w.chunks) * C, pieces = (p.lin.T - z0) * (D / 8);
-            for (long long q = threadIdx.x - 384; q < pieces; q += 128)
+            for (long long q = threadIdx.x - 32 * kOutWarp; q < pieces; q += 128)
                 *reinterpret_cast<uint4*>(po + (z0 + q / (D / 8)) * R.ldo + q % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
         }
         if (lane == 0) bulk_wait_all<0>();   // the rows in flight are written before the CTA ends
@@ -596,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 1)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
@@ -662,7 +708,7 @@ int linattn_tc_launch(int roles, const LinParams& lin, cudaStream_t st)
         cudaGetLastError();
         return SRWM_ERR_CUDA;
     }
-    constexpr int smem = static_cast<int>(sizeof(Smem)) + 1024;
+    constexpr int smem = static_cast<int>(sizeof(Smem));
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
     int n_sm = sms[dev].load();
     if (n_sm == 0) {
