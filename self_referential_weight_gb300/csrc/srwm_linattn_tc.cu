@@ -15,9 +15,9 @@
 // kept in fp32 registers, is good to fp32.
 //
 // Warps: 0-7 turn P into its pair (one row per thread); 8-11 write the weighted
-// b's terms (one token per thread); 12-15 hold X, add U to it and leave its
+// b's terms; 12-15 hold X, add U to it and leave its
 // pair in shared memory; 16-19 write the outputs; 20 issues the TMA loads
-// (three stages of a, b, c), 21 the products.  Every stage of a chunk's work runs
+// (three stages of a, b, c), 21 and 22 the products.  Every stage of a chunk's work runs
 // beside other stages of the same or the next chunk: P and X's chain meet only
 // at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
 // by warps 8-11 before anything reads them; past the tensor's end TMA fills
@@ -43,13 +43,15 @@ namespace {
 
 constexpr int D = 64, C = 128, STAGES = 3;
 constexpr int kTileBytes = C * D * 2;
-constexpr int kThreads = 704;
+constexpr int kThreads = 736;
 constexpr int kMaxDevices = 64;
 // first warps of the roles; those that read tensor memory start at multiples of four, whose lanes they own in order
-constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kMmaWarp = 21;
+constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
+              kStateMmaWarp = 22;
 
-// tensor memory columns (the pair's high half, then its low half)
-constexpr uint32_t kP32 = 0, kPH = 128, kPL = kPH + 64, kOI = 256, kOX = 320, kU = 384, kTmemCols = 512;
+// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's pair
+// goes over it block by block: 32 columns of fp32 become 16 of high and 16 of low halves.
+constexpr uint32_t kP = 0, kOI = 256, kOX = 384, kU = 448, kTmemCols = 512;
 
 struct TcMaps {
     CUtensorMap a, b, c, out;
@@ -68,8 +70,11 @@ struct __align__(1024) Smem {
     uint8_t state[2][D * D * 2];            // X's pair
     uint8_t out[4][32 * D * 2];             // per output warp: 32 rows
     float decay[8][64];                     // per score warp: g^|column - row| of a diagonal block, by their difference
-    uint64_t full[STAGES], empty[STAGES], u_full[2];
-    uint64_t terms_full, x_full, x_free, p32_full, p32_free, p16_full, o_full, o_free;
+    // A barrier's next phase never completes before every waiter of this one has passed: where the producer
+    // may run ahead of a waiter by a chunk, there are two of them, or one for each stage.
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t terms_full[2], terms_free[2];  // of a chunk's first and second 64 tokens
+    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], clean[STAGES];
     uint32_t tmem_base;
     int abort;
 };
@@ -252,22 +257,25 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
+            mbar_init(&sm.empty[s], 2);
+            mbar_init(&sm.clean[s], 4);
         }
-        mbar_init(&sm.terms_full, 4);
-        mbar_init(&sm.u_full[0], 1);
-        mbar_init(&sm.u_full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.terms_full[i], 4);
+            mbar_init(&sm.terms_free[i], 1);
+            mbar_init(&sm.p32_full[i], 1);
+            mbar_init(&sm.p16_full[i], 8);
+            mbar_init(&sm.o_free[i], 4);
+        }
+        mbar_init(&sm.u_full, 1);
+        mbar_init(&sm.u_free, 4);
         mbar_init(&sm.x_full, 4);
         mbar_init(&sm.x_free, 1);
-        mbar_init(&sm.p32_full, 1);
-        mbar_init(&sm.p32_free, 8);
-        mbar_init(&sm.p16_full, 8);
-        mbar_init(&sm.o_full, 1);
-        mbar_init(&sm.o_free, 4);
+        mbar_init(&sm.o_full, 2);
         sm.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kStateMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
@@ -314,77 +322,91 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---- products.  The whole warp walks the chunks, so that descriptors stay in uniform registers; one
-        // elected lane issues.
+    } else if (warp >= kScoreMmaWarp) {
+        // ---- products: one warp issues P and OX, another U and OI, so that neither chain waits behind the other.
+        // The whole warp walks the chunks, which keeps the descriptors in uniform registers; an elected lane issues.
         constexpr uint32_t id_p = idesc(C, C, false, false), id_u = idesc(D, D, true, true), id_o = idesc(C, D, false, true);
-        const uint64_t d_terms = desc128(smem_u32(sm.terms[0])), d_state = desc128(smem_u32(sm.state[0]));
-        const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
         constexpr uint64_t kStage = 3 * kTileBytes / 16, kTile = kTileBytes / 16;   // descriptor steps
-        auto score = [&](uint32_t at) {   // P of chunk `at`
-            const uint64_t a = d_stage + kStage * (at % STAGES), b = a + kTile;
-            if (elect()) {
-                mma_ss<false>(tmem + kP32, a, b, id_p);
-#pragma unroll
-                for (int k = 1; k < D / 16; ++k) mma_ss<true>(tmem + kP32, a + 2 * k, b + 2 * k, id_p);
-                commit(&sm.p32_full);
-            }
-            __syncwarp();
-        };
-        // a chunk's tiles may be read: landed, and cleaned where they need it
-        auto ready = [&](const Walk& w, uint32_t at) {
-            return wait(&sm.full[at % STAGES], at / STAGES) && (!w.dirty() || wait(&sm.terms_full, at));
-        };
-        Walk w(p);
+        const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
         bool ok = true, issued = false;
-        if (w.skip_empty()) {
-            ok = ready(w, 0);
-            if (ok) {
+        Walk w(p);
+        if (warp == kScoreMmaWarp) {
+            // P of chunk `at`, once its tiles have landed and been cleaned where they need it.  Its place was last
+            // read by the product OX of chunk at - 2, issued before by this lane: products run in order.
+            auto score = [&](uint32_t at) {
+                if (!(ok = wait(&sm.full[at % STAGES], at / STAGES) &&
+                           (!w.dirty() || wait(&sm.clean[at % STAGES], at / STAGES))))
+                    return;
                 fence_after();
-                score(0);
+                const uint64_t a = d_stage + kStage * (at % STAGES), b = a + kTile;
+                const uint32_t to = tmem + kP + C * (at & 1);
+                if (elect()) {
+                    mma_ss<false>(to, a, b, id_p);
+#pragma unroll
+                    for (int k = 1; k < D / 16; ++k) mma_ss<true>(to, a + 2 * k, b + 2 * k, id_p);
+                    commit(&sm.p32_full[at & 1]);
+                }
+                __syncwarp();
                 issued = true;
-            }
-        }
-        for (; ok && w.skip_empty(); ++g) {
-            const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
-            const uint32_t u = tmem + kU + 64 * (g & 1);
-            if (!(ok = wait(&sm.terms_full, g))) break;
-            fence_after();
-            if (elect()) {
-                mma_ss<false>(u, d_terms, c, id_u);
-#pragma unroll
-                for (int k = 1; k < 3 * C / 16; ++k)
-                    mma_ss<true>(u, d_terms + kTile * (k / 8) + 128 * (k % 8), c + 128 * (k % 8), id_u);
-                commit(&sm.u_full[g & 1]);
-            }
-            __syncwarp();
-            if (!(ok = wait(&sm.x_full, g) && wait(&sm.o_free, g + 1))) break;
-            fence_after();
-            if (elect()) {
-                mma_ss<false>(tmem + kOI, a, d_state, id_o);
-#pragma unroll
-                for (int k = 1; k < 2 * D / 16; ++k)
-                    mma_ss<true>(tmem + kOI, a + 2 * (k % 4), d_state + 512 * (k / 4) + 128 * (k % 4), id_o);
-                commit(&sm.x_free);
-            }
-            __syncwarp();
-            ++w.k;
-            if (w.skip_empty()) {   // the next chunk's scores, ahead of this one's output
-                if (!(ok = ready(w, g + 1) && wait(&sm.p32_free, g))) break;
+            };
+            if (w.skip_empty()) score(0);
+            for (; ok && w.skip_empty(); ++g) {
+                const uint64_t c = d_stage + kStage * (g % STAGES) + 2 * kTile;
+                ++w.k;
+                if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
+                // the pair is there, and the outputs before have been read
+                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) && (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1)))) break;
                 fence_after();
-                score(g + 1);
-            }
-            if (!(ok = wait(&sm.p16_full, g))) break;
-            fence_after();
-            if (elect()) {
-                mma_ts<false>(tmem + kOX, tmem + kPH, c, id_o);
+                const uint32_t pair = tmem + kP + C * (g & 1);
+                if (elect()) {
+                    mma_ts<false>(tmem + kOX, pair, c, id_o);
 #pragma unroll
-                for (int k = 1; k < 2 * C / 16; ++k)
-                    mma_ts<true>(tmem + kOX, tmem + kPH + 8 * k, c + 128 * (k % 8), id_o);
-                commit(&sm.o_full);
-                commit(&sm.empty[g % STAGES]);
+                    for (int k = 1; k < 2 * C / 16; ++k)   // step k % 8 of the tokens, of the high halves, then of the low
+                        mma_ts<true>(tmem + kOX, pair + 32 * (k % 8 / 2) + 8 * (k % 2) + 16 * (k / 8), c + 128 * (k % 8), id_o);
+                    commit(&sm.o_full);
+                    commit(&sm.empty[g % STAGES]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+        } else {
+            const uint64_t d_terms = desc128(smem_u32(sm.terms[0])), d_state = desc128(smem_u32(sm.state[0]));
+            for (; ok && w.skip_empty(); ++w.k, ++g) {
+                const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
+                const uint32_t u = tmem + kU, oi = tmem + kOI + 64 * (g & 1);
+                if (!(ok = wait(&sm.full[g % STAGES], g / STAGES) && wait(&sm.u_free, g + 1))) break;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(&sm.terms_full[half], g))) break;
+                    fence_after();
+                    if (elect()) {
+                        const uint64_t t = d_terms + 512 * half, v = c + 512 * half;
+                        if (half == 0)
+                            mma_ss<false>(u, t, v, id_u);
+                        else
+                            mma_ss<true>(u, t, v, id_u);
+#pragma unroll
+                        for (int k = 1; k < 3 * 4; ++k)
+                            mma_ss<true>(u, t + kTile * (k / 4) + 128 * (k % 4), v + 128 * (k % 4), id_u);
+                        commit(&sm.terms_free[half]);
+                        if (half == 1) commit(&sm.u_full);
+                    }
+                    __syncwarp();
+                    issued = true;
+                }
+                // X's copy is there, and the outputs that used this place have been read
+                if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
+                fence_after();
+                if (elect()) {
+                    mma_ss<false>(oi, a, d_state, id_o);
+#pragma unroll
+                    for (int k = 1; k < 2 * D / 16; ++k)
+                        mma_ss<true>(oi, a + 2 * (k % 4), d_state + 512 * (k / 4) + 128 * (k % 4), id_o);
+                    commit(&sm.x_free);
+                    commit(&sm.o_full);
+                    commit(&sm.empty[g % STAGES]);
+                }
+                __syncwarp();
+            }
         }
         // Tensor memory may only be freed once the products issued have completed: after a timeout nobody else
         // waits for them.
@@ -398,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         // ---- P as a bf16 pair, one row per thread; two sets of four warps take the 32-column blocks in turn
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
         float* decay = sm.decay[warp];
-        int before = -1;   // direction whose masked blocks hold zeros
         bool ok = true;
         Walk w(p);
         for (; ok && !w.done(); w.next_item()) {
@@ -419,21 +440,19 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
             const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
-                if (!(ok = wait(&sm.p32_full, g) && wait(&sm.o_full, g + 1))) break;   // the pair before has been read
+                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1))) break;
                 fence_after();
-                if (before != w.rev) {
-                    const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                    for (int cb = set; cb < 4; cb += 2)
-                        if (cb < c0 || cb > c1) {
-                            tmem_store16(tmem + quad + kPH + 16 * cb, zero);
-                            tmem_store16(tmem + quad + kPL + 16 * cb, zero);
-                        }
-                    before = w.rev;
-                }
+                const uint32_t P = tmem + quad + kP + C * (g & 1);
+                for (int cb = set; cb < 4; cb += 2)   // the side that is masked
+                    if (cb < c0 || cb > c1) {
+                        const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                        tmem_store16(P + 32 * cb, zero);
+                        tmem_store16(P + 32 * cb + 16, zero);
+                    }
 #pragma unroll 1
                 for (int cb = first; cb <= c1; cb += 2) {
                     uint32_t r[32], v[16];
-                    tmem_rows(tmem + quad + kP32 + 32 * cb, r);
+                    tmem_rows(P + 32 * cb, r);
                     const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
                     tmem_wait(r);
                     if (cb == own) {
@@ -456,67 +475,70 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         r[2 * k] = __float_as_uint(x);
                         r[2 * k + 1] = __float_as_uint(y);
                     }
-                    tmem_store16(tmem + quad + kPH + 16 * cb, v);
+                    tmem_store16(P + 32 * cb, v);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = pack_bf16(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-                    tmem_store16(tmem + quad + kPL + 16 * cb, v);
+                    tmem_store16(P + 32 * cb + 16, v);
                 }
-                fence_before();
-                arrive(&sm.p32_free);
                 tmem_store_wait();
                 fence_before();
-                arrive(&sm.p16_full);
+                arrive(&sm.p16_full[g & 1]);
             }
         }
     } else if (warp < kStateWarp) {
-        // ---- the terms of w_j b_j, one token per thread
-        const int j = 32 * (warp - kTermWarp) + lane;
+        // ---- the terms of w_j b_j: 64 tokens at a time, so that the products of one half run while the other is
+        // written; half a token's row per thread
+        const int t = threadIdx.x - 32 * kTermWarp, q0 = t >> 6 << 2;
         bool ok = true;
         Walk w(p);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
-            for (; w.k < w.chunks; ++w.k, ++g) {
+            for (; ok && w.k < w.chunks; ++w.k, ++g) {
                 const int s = g % STAGES, nc = w.valid();
-                const float wj = au * exp2f(lg * static_cast<float>(w.rev ? j + 1 : max(0, nc - 1 - j)));
-                // the terms before have been read
-                if (!(ok = wait(&sm.full[s], g / STAGES) && (g == 0 || wait(&sm.u_full[(g - 1) & 1], (g - 1) >> 1)))) break;
-                const uint32_t at = smem_u32(sm.stage[s][1]) + 128 * j;
-                const bool clean = j >= nc && w.dirty();
-                const uint32_t zero[4] = {0, 0, 0, 0};
-                uint32_t ahead[4];
-                lds128(at + static_cast<uint32_t>((j & 7) << 4), ahead);
+                if (!(ok = wait(&sm.full[s], g / STAGES))) break;
 #pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t o = static_cast<uint32_t>((q ^ (j & 7)) << 4);
-                    uint32_t t0[4], t1[4], t2[4];
-                    float x[4], y[4];
+                for (int half = 0; half < 2; ++half) {
+                    const int j = 64 * half + (t & 63);
+                    const float wj = au * exp2f(lg * static_cast<float>(w.rev ? j + 1 : max(0, nc - 1 - j)));
+                    if (!(ok = wait(&sm.terms_free[half], g + 1))) break;   // those of the chunk before have been read
+                    const uint32_t at = smem_u32(sm.stage[s][1]) + 128 * j, to = smem_u32(sm.terms[0]) + 128 * j;
+                    const bool clean = j >= nc && w.dirty();
+                    const uint32_t zero[4] = {0, 0, 0, 0};
+                    uint32_t ahead[4];
+                    lds128(at + static_cast<uint32_t>((q0 ^ (j & 7)) << 4), ahead);
+#pragma unroll 1
+                    for (int q = q0; q < q0 + 4; ++q) {
+                        const uint32_t o = static_cast<uint32_t>((q ^ (j & 7)) << 4);
+                        uint32_t t0[4], t1[4], t2[4];
+                        float x[4], y[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t v = clean ? 0 : ahead[k];
-                        x[k] = __uint_as_float(v << 16) * wj;
-                        y[k] = __uint_as_float(v & 0xffff0000u) * wj;
-                    }
-                    lds128(at + static_cast<uint32_t>((((q + 1) & 7) ^ (j & 7)) << 4), ahead);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t v = clean ? 0 : ahead[k];
+                            x[k] = __uint_as_float(v << 16) * wj;
+                            y[k] = __uint_as_float(v & 0xffff0000u) * wj;
+                        }
+                        lds128(at + static_cast<uint32_t>((((q + 1) & 7) ^ (j & 7)) << 4), ahead);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        t0[k] = take_bf16(x[k], y[k]);
-                        t1[k] = take_bf16(x[k], y[k]);
-                        t2[k] = pack_bf16(x[k], y[k]);
+                        for (int k = 0; k < 4; ++k) {
+                            t0[k] = take_bf16(x[k], y[k]);
+                            t1[k] = take_bf16(x[k], y[k]);
+                            t2[k] = pack_bf16(x[k], y[k]);
+                        }
+                        sts128(to + o, t0);
+                        sts128(to + o + kTileBytes, t1);
+                        sts128(to + o + 2 * kTileBytes, t2);
+                        if (clean) {
+                            sts128(at + o, zero);
+                            sts128(at + o - kTileBytes, zero);   // a's and c's tiles lie on either side
+                            sts128(at + o + kTileBytes, zero);
+                        }
                     }
-                    const uint32_t to = smem_u32(sm.terms[0]) + 128 * j + o;
-                    sts128(to, t0);
-                    sts128(to + kTileBytes, t1);
-                    sts128(to + 2 * kTileBytes, t2);
-                    if (clean) {
-                        sts128(at + o, zero);
-                        sts128(at + o - kTileBytes, zero);   // a's and c's tiles lie on either side
-                        sts128(at + o + kTileBytes, zero);
-                    }
+                    fence_proxy_async_smem();
+                    arrive(&sm.terms_full[half]);
                 }
-                fence_proxy_async_smem();
-                arrive(&sm.terms_full);
+                if (ok) arrive(&sm.clean[s]);
             }
         }
     } else if (warp < kOutWarp) {
@@ -555,13 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             if (w.chunks > 0) leave_state(g);
             for (; ok && w.k < w.chunks; ++w.k, ++g) {
                 const int nc = w.valid();
-                if (!(ok = wait(&sm.u_full[g & 1], g >> 1))) break;
+                if (!(ok = wait(&sm.u_full, g))) break;
                 fence_after();
                 {
                     uint32_t u[32];
-                    tmem_frag64(tmem + quad + kU + 64 * (g & 1), u);
+                    tmem_frag64(tmem + quad + kU, u);
                     tmem_wait(u);
                     fence_before();
+                    arrive(&sm.u_free);
                     const Decay dec = nc == C ? full : decay_over(lg, nc);
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
@@ -602,13 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t oi[32], ox[32];
-                    tmem_rows(tmem + quad + kOI + 32 * half, oi);
+                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 32 * half, oi);
                     tmem_rows(tmem + quad + kOX + 32 * half, ox);
                     tmem_wait(oi);
                     tmem_wait(ox);
                     if (half == 1) {
                         fence_before();
-                        arrive(&sm.o_free);
+                        arrive(&sm.o_free[g & 1]);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -642,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kStateMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
