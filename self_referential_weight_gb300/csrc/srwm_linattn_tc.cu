@@ -245,6 +245,16 @@ struct Walk {
     __device__ bool dirty() const { return valid() < C && n < p.lin.T; }
 };
 
+// The part of a wait that spins, out of line: six kinds of warps share an
+// instruction cache, and their loops have to stay in it.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort, unsigned* status)
+{
+    if (mbar_wait_bounded(bar, parity, limit_ns) && !*abort) return true;
+    *abort = 1;
+    atomicOr(status, kStatusTimeout);
+    return false;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcParams p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -288,10 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     volatile int* abort = &sm.abort;
     // Waits for phase `phase` of `bar`; false, with the CTA marked to end, when it does not come.
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (mbar_wait_bounded(bar, phase & 1u, p.wait_limit_ns) && !*abort) return true;
-        *abort = 1;
-        atomicOr(p.status, kStatusTimeout);
-        return false;
+        return mbar_try_wait(bar, phase & 1u) || wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
     };
     // One arrival for the warp after its lanes' work.
     auto arrive = [&](uint64_t* bar) {
@@ -428,15 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
             // tab[x - l]: alpha_u g^|x - l| for row l, column x on the causal side of a diagonal block, 0 on the
             // other.  A block beside the diagonal takes the row's factor off: its columns are those of row 31 in
-            // order, of row 0 in reverse, 16-byte aligned in either case.
-            float* tab = decay + 31 + (w.rev ? 1 : 0);
+            // order, of row 0 in reverse.
+            float* tab = decay + 31;
             __syncwarp();   // the table of the item before is no longer read
             for (int i = lane; i < 63; i += 32) {
                 const int gap = w.rev ? i - 31 : 31 - i;
                 tab[i - 31] = gap >= 0 ? au * exp2f(lg * static_cast<float>(gap)) : 0.f;
             }
             __syncwarp();
-            const float4* beside = reinterpret_cast<const float4*>(w.rev ? tab : tab - 31);
+            const float* beside = w.rev ? tab : tab - 31;
             const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
             const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
@@ -454,20 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     uint32_t r[32], v[16];
                     tmem_rows(P + 32 * cb, r);
                     const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
+                    const float* col = cb == own ? tab - lane : beside;
                     tmem_wait(r);
-                    if (cb == own) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * tab[x - lane]);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 t = beside[x / 4];
-                            r[x] = __float_as_uint(__uint_as_float(r[x]) * (f * t.x));
-                            r[x + 1] = __float_as_uint(__uint_as_float(r[x + 1]) * (f * t.y));
-                            r[x + 2] = __float_as_uint(__uint_as_float(r[x + 2]) * (f * t.z));
-                            r[x + 3] = __float_as_uint(__uint_as_float(r[x + 3]) * (f * t.w));
-                        }
-                    }
+                    for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * (f * col[x]));
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
@@ -558,10 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
                     X[t][k] = R.x_in ? R.x_in[mat + (R.transposed ? q * D + i : i * D + q)] : 0.f;
                 }
-            auto leave_state = [&](uint32_t at) {   // X's pair for chunk `at`
-                if (!(ok = wait(&sm.x_free, at + 1))) return;
+            const Decay full = decay_over(lg, C);
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                if (!(ok = wait(&sm.x_free, g + 1))) break;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 8; ++t)   // X's pair
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float x = X[t][2 * k], y = X[t][2 * k + 1];
@@ -572,10 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     }
                 fence_proxy_async_smem();
                 arrive(&sm.x_full);
-            };
-            const Decay full = decay_over(lg, C);
-            if (w.chunks > 0) leave_state(g);
-            for (; ok && w.k < w.chunks; ++w.k, ++g) {
                 const int nc = w.valid();
                 if (!(ok = wait(&sm.u_full, g))) break;
                 fence_after();
@@ -591,10 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             X[t][k] = fmaf(X[t][k], dec.m, fmaf(X[t][k], dec.c, __uint_as_float(u[4 * t + k])));
-                }
-                if (w.k + 1 < w.chunks) {
-                    leave_state(g + 1);
-                    if (!ok) break;
                 }
             }
             if (ok && R.x_out)
