@@ -50,7 +50,7 @@ constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLo
               kStateMmaWarp = 22;
 
 // Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's pair
-// goes over it block by block: 32 columns of fp32 become 16 of high and 16 of low halves.
+// goes over it: 16 columns of fp32 become 8 of high and 8 of low halves.
 constexpr uint32_t kP = 0, kOI = 256, kOX = 384, kU = 448, kTmemCols = 512;
 
 struct TcMaps {
@@ -173,7 +173,13 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R32("+r", r)::"memory");
 }
-// 16 columns of the warp's 32 lanes, one lane per thread.
+// 8 or 16 columns of the warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     mma_ts<false>(tmem + kOX, pair, c, id_o);
 #pragma unroll
                     for (int k = 1; k < 2 * C / 16; ++k)   // step k % 8 of the tokens, of the high halves, then of the low
-                        mma_ts<true>(tmem + kOX, pair + 32 * (k % 8 / 2) + 8 * (k % 2) + 16 * (k / 8), c + 128 * (k % 8), id_o);
+                        mma_ts<true>(tmem + kOX, pair + 16 * (k % 8) + 8 * (k / 8), c + 128 * (k % 8), id_o);
                     commit(&sm.o_full);
                     commit(&sm.empty[g % STAGES]);
                 }
@@ -457,25 +463,22 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         tmem_store16(P + 32 * cb + 16, zero);
                     }
 #pragma unroll 1
-                for (int cb = first; cb <= c1; cb += 2) {
-                    uint32_t r[32], v[16];
-                    tmem_rows(P + 32 * cb, r);
+                for (int hb = 2 * first; hb <= 2 * c1 + 1; hb += (hb & 1) ? 3 : 1) {   // 16 columns of this set's blocks
+                    const int cb = hb >> 1, x0 = 16 * (hb & 1);
+                    uint32_t r[16], hi[8], lo[8];
+                    tmem_rows(P + 16 * hb, r);
                     const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
-                    const float* col = cb == own ? tab - lane : beside;
+                    const float* col = (cb == own ? tab - lane : beside) + x0;
                     tmem_wait(r);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * (f * col[x]));
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
-                        v[k] = take_bf16(x, y);
-                        r[2 * k] = __float_as_uint(x);
-                        r[2 * k + 1] = __float_as_uint(y);
+                    for (int k = 0; k < 8; ++k) {
+                        float x = __uint_as_float(r[2 * k]) * (f * col[2 * k]), y = __uint_as_float(r[2 * k + 1]) * (f * col[2 * k + 1]);
+                        hi[k] = take_bf16(x, y);
+                        lo[k] = pack_bf16(x, y);
                     }
-                    tmem_store16(P + 32 * cb, v);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = pack_bf16(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-                    tmem_store16(P + 32 * cb + 16, v);
+                    // 16 columns of fp32 become 8 of high and 8 of low halves
+                    tmem_store8(P + 16 * hb, hi);
+                    tmem_store8(P + 16 * hb + 8, lo);
                 }
                 tmem_store_wait();
                 fence_before();
