@@ -34,6 +34,7 @@
 
 #include "srwm.h"
 #include "srwm_check.h"
+#include "srwm_f2.cuh"
 #include "srwm_ffgemm.h"
 #include "srwm_linattn.cuh"
 #include "srwm_linattn_tc.h"
@@ -196,14 +197,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y)
     const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Takes the bf16 of (x, y) out of them.
-__device__ __forceinline__ uint32_t take_bf16(float& x, float& y)
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) { return pack_bf16(v.x, v.y); }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t v)
 {
-    const uint32_t h = pack_bf16(x, y);
-    x -= __uint_as_float(h << 16);
-    y -= __uint_as_float(h & 0xffff0000u);
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+// Takes the bf16 of both out of v.
+__device__ __forceinline__ uint32_t take_bf16(float2& v)
+{
+    const uint32_t h = pack_bf16(v);
+    v = fma2(unpack_bf16(h), both(-1.f), v);
     return h;
 }
+__device__ __forceinline__ float2 as_float2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
 {
@@ -472,9 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     tmem_wait(r);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        float x = __uint_as_float(r[2 * k]) * (f * col[2 * k]), y = __uint_as_float(r[2 * k + 1]) * (f * col[2 * k + 1]);
-                        hi[k] = take_bf16(x, y);
-                        lo[k] = pack_bf16(x, y);
+                        float2 v = mul2(as_float2(r[2 * k], r[2 * k + 1]), mul2(both(f), make_float2(col[2 * k], col[2 * k + 1])));
+                        hi[k] = take_bf16(v);
+                        lo[k] = pack_bf16(v);
                     }
                     // 16 columns of fp32 become 8 of high and 8 of low halves
                     tmem_store8(P + 16 * hb, hi);
@@ -512,19 +518,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     for (int q = q0; q < q0 + 4; ++q) {
                         const uint32_t o = static_cast<uint32_t>((q ^ (j & 7)) << 4);
                         uint32_t t0[4], t1[4], t2[4];
-                        float x[4], y[4];
+                        float2 v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t v = clean ? 0 : ahead[k];
-                            x[k] = __uint_as_float(v << 16) * wj;
-                            y[k] = __uint_as_float(v & 0xffff0000u) * wj;
-                        }
+                        for (int k = 0; k < 4; ++k) v[k] = mul2(unpack_bf16(clean ? 0 : ahead[k]), both(wj));
                         lds128(at + static_cast<uint32_t>((((q + 1) & 7) ^ (j & 7)) << 4), ahead);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            t0[k] = take_bf16(x[k], y[k]);
-                            t1[k] = take_bf16(x[k], y[k]);
-                            t2[k] = pack_bf16(x[k], y[k]);
+                            t0[k] = take_bf16(v[k]);
+                            t1[k] = take_bf16(v[k]);
+                            t2[k] = pack_bf16(v[k]);
                         }
                         sts128(to + o, t0);
                         sts128(to + o + kTileBytes, t1);
@@ -550,13 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             const size_t mat = (static_cast<size_t>(w.b) * p.lin.H + w.h) * D * D;
-            float X[8][4];   // rows 16 own + r4 (+ 8), columns 8 t + x2 (+ 1)
+            float2 X[8][2];   // rows 16 own + r4 (+ 8), columns 8 t + x2 and the next
 #pragma unroll
             for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
-                    X[t][k] = R.x_in ? R.x_in[mat + (R.transposed ? q * D + i : i * D + q)] : 0.f;
+                for (int k = 0; k < 2; ++k) {
+                    const int i = 16 * own + r4 + 8 * k, q = 8 * t + x2;
+                    X[t][k] = !R.x_in       ? both(0.f)
+                              : R.transposed ? make_float2(R.x_in[mat + q * D + i], R.x_in[mat + (q + 1) * D + i])
+                                             : *reinterpret_cast<const float2*>(R.x_in + mat + i * D + q);
                 }
             const Decay full = decay_over(lg, C);
             for (; w.k < w.chunks; ++w.k, ++g) {
@@ -565,9 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 for (int t = 0; t < 8; ++t)   // X's pair
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float x = X[t][2 * k], y = X[t][2 * k + 1];
+                        float2 v = X[t][k];
                         const uint32_t to = state_at<D>(smem_u32(sm.state[0]), 16 * own + r4 + 8 * k, t, 0) + 2 * x2;
-                        const uint32_t hi = take_bf16(x, y), lo = pack_bf16(x, y);
+                        const uint32_t hi = take_bf16(v), lo = pack_bf16(v);
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + D * D * 2), "r"(lo) : "memory");
                     }
@@ -586,17 +590,18 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            X[t][k] = fmaf(X[t][k], dec.m, fmaf(X[t][k], dec.c, __uint_as_float(u[4 * t + k])));
+                        for (int k = 0; k < 2; ++k)
+                            X[t][k] = fma2(X[t][k], both(dec.m), fma2(X[t][k], both(dec.c), as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1])));
                 }
             }
             if (ok && R.x_out)
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = 16 * own + r4 + 8 * (k >> 1), q = 8 * t + x2 + (k & 1);
-                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k];
+                    for (int k = 0; k < 2; ++k) {
+                        const int i = 16 * own + r4 + 8 * k, q = 8 * t + x2;
+                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k].x;
+                        R.x_out[mat + (R.transposed ? (q + 1) * D + i : i * D + q + 1)] = X[t][k].y;
                     }
         }
     } else if (warp < kLoadWarp) {
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (!(ok = wait(&sm.o_full, g))) break;
                 fence_after();
                 const int i = 32 * own + lane;
-                const float f = R.alpha_o * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
+                const float alpha = R.alpha_o, f = alpha * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
                 if (lane == 0) bulk_wait_read<0>();   // the rows before have left the staging buffer
                 __syncwarp();
 #pragma unroll 1
@@ -632,8 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int x = 8 * q + 2 * k;
-                            v[k] = pack_bf16(fmaf(__uint_as_float(oi[x]), f, R.alpha_o * __uint_as_float(ox[x])),
-                                             fmaf(__uint_as_float(oi[x + 1]), f, R.alpha_o * __uint_as_float(ox[x + 1])));
+                            v[k] = pack_bf16(fma2(as_float2(oi[x], oi[x + 1]), both(f), mul2(both(alpha), as_float2(ox[x], ox[x + 1]))));
                         }
                         sts128(smem_u32(sm.out[own]) + 128 * lane + (((4 * half + q) ^ (lane & 7)) << 4), v);
                     }
