@@ -621,27 +621,25 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (lane == 0) bulk_wait_read<0>();   // the rows before have left the staging buffer
                 __syncwarp();
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t oi[32], ox[32];
-                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 32 * half, oi);
-                    tmem_rows(tmem + quad + kOX + 32 * half, ox);
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t oi[16], ox[16];
+                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 16 * part, oi);
+                    tmem_rows(tmem + quad + kOX + 16 * part, ox);
                     tmem_wait(oi);
                     tmem_wait(ox);
-                    if (half == 1) {
-                        fence_before();
-                        arrive(&sm.o_free[g & 1]);
-                    }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t v[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int x = 8 * q + 2 * k;
                             v[k] = pack_bf16(fma2(as_float2(oi[x], oi[x + 1]), both(f), mul2(both(alpha), as_float2(ox[x], ox[x + 1]))));
                         }
-                        sts128(smem_u32(sm.out[own]) + 128 * lane + (((4 * half + q) ^ (lane & 7)) << 4), v);
+                        sts128(smem_u32(sm.out[own]) + 128 * lane + (((2 * part + q) ^ (lane & 7)) << 4), v);
                     }
                 }
+                fence_before();
+                arrive(&sm.o_free[g & 1]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && w.token() + 32 * own < p.lin.T) {
