@@ -10,16 +10,17 @@
 //   U    = sum_j (w_j b_j) c_j^T,  X <- g^nc X + U        w_j = alpha_u g^(nc-1-j), or alpha_u g^(j+1)
 // Five products per chunk: P = a b^T (128 x 128 x 64), OX (P from tensor
 // memory, 128 x 64 x 128), OI (128 x 64 x 64), U (64 x 64 x 128).  a, b, c are
-// the bf16 inputs themselves.  P and X enter their products as bf16 (high,
-// low) pairs (2^-17), w_j b_j as three bf16 terms (2^-24), so that X, which is
-// kept in fp32 registers, is good to fp32.
+// the bf16 inputs themselves.  P enters its product as bf16 (2^-8 of each score at
+// most, as much as the outputs' own rounding; as a pair it costs 6 % of the
+// forward pass and 9 % of the gradients for 0.0017 instead of 0.0021 of relative
+// error), X as a bf16 (high, low) pair (2^-17), w_j b_j as three bf16 terms
+// (2^-24), so that X, which is kept in fp32 registers, is good to fp32.
 //
-// Warps: 0-7 turn P into its pair (one row per thread); 8-11 write the weighted
-// b's terms; 12-15 hold X, add U to it and leave its
-// pair in shared memory; 16-19 write the outputs; 20 issues the TMA loads
-// (three stages of a, b, c), 21 and 22 the products.  Every stage of a chunk's work runs
-// beside other stages of the same or the next chunk: P and X's chain meet only
-// at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
+// Warps: 0-7 turn P into bf16 (one row per thread); 8-11 write the weighted b's
+// terms; 12-15 hold X, add U to it and leave its pair in shared memory; 16-19
+// write the outputs; 20 issues the TMA loads (three stages of a, b, c), 21 and 22
+// the products.  Every stage of a chunk's work runs beside other stages of the
+// same or the next chunk: P and X's chain meet only at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
 // by warps 8-11 before anything reads them; past the tensor's end TMA fills
 // zeros.  Every wait is bounded; a timeout sets the status word and ends the CTA
 // after its copies and products in flight.
@@ -50,8 +51,8 @@ constexpr int kMaxDevices = 64;
 constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
               kStateMmaWarp = 22;
 
-// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's pair
-// goes over it: 16 columns of fp32 become 8 of high and 8 of low halves.
+// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's bf16
+// values go over it: 16 columns of fp32 become the first 8 of them.
 constexpr uint32_t kP = 0, kOI = 256, kOX = 384, kU = 448, kTmemCols = 512;
 
 struct TcMaps {
@@ -174,21 +175,12 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R32("+r", r)::"memory");
 }
-// 8 or 16 columns of the warp's 32 lanes, one lane per thread.
+// 8 columns of the warp's 32 lanes, one lane per thread.
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-}
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -373,15 +365,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 const uint64_t c = d_stage + kStage * (g % STAGES) + 2 * kTile;
                 ++w.k;
                 if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
-                // the pair is there, and the outputs before have been read
+                // the scores are there, and the outputs before have been read
                 if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) && (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1)))) break;
                 fence_after();
-                const uint32_t pair = tmem + kP + C * (g & 1);
+                const uint32_t scores = tmem + kP + C * (g & 1);
                 if (elect()) {
-                    mma_ts<false>(tmem + kOX, pair, c, id_o);
+                    mma_ts<false>(tmem + kOX, scores, c, id_o);
 #pragma unroll
-                    for (int k = 1; k < 2 * C / 16; ++k)   // step k % 8 of the tokens, of the high halves, then of the low
-                        mma_ts<true>(tmem + kOX, pair + 16 * (k % 8) + 8 * (k / 8), c + 128 * (k % 8), id_o);
+                    for (int k = 1; k < C / 16; ++k) mma_ts<true>(tmem + kOX, scores + 16 * k, c + 128 * k, id_o);
                     commit(&sm.o_full);
                     commit(&sm.empty[g % STAGES]);
                 }
@@ -436,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         }
         __syncwarp();
     } else if (warp < kTermWarp) {
-        // ---- P as a bf16 pair, one row per thread; two sets of four warps take the 32-column blocks in turn
+        // ---- P as bf16, one row per thread; two sets of four warps take the 32-column blocks in turn
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
         float* decay = sm.decay[warp];
         bool ok = true;
@@ -464,14 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 const uint32_t P = tmem + quad + kP + C * (g & 1);
                 for (int cb = set; cb < 4; cb += 2)   // the side that is masked
                     if (cb < c0 || cb > c1) {
-                        const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                        tmem_store16(P + 32 * cb, zero);
-                        tmem_store16(P + 32 * cb + 16, zero);
+                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        tmem_store8(P + 32 * cb, zero);
+                        tmem_store8(P + 32 * cb + 16, zero);
                     }
 #pragma unroll 1
                 for (int hb = 2 * first; hb <= 2 * c1 + 1; hb += (hb & 1) ? 3 : 1) {   // 16 columns of this set's blocks
                     const int cb = hb >> 1, x0 = 16 * (hb & 1);
-                    uint32_t r[16], hi[8], lo[8];
+                    uint32_t r[16], hi[8];
                     tmem_rows(P + 16 * hb, r);
                     const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
                     const float* col = (cb == own ? tab - lane : beside) + x0;
@@ -479,12 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         float2 v = mul2(as_float2(r[2 * k], r[2 * k + 1]), mul2(both(f), make_float2(col[2 * k], col[2 * k + 1])));
-                        hi[k] = take_bf16(v);
-                        lo[k] = pack_bf16(v);
+                        hi[k] = pack_bf16(v);
                     }
-                    // 16 columns of fp32 become 8 of high and 8 of low halves
                     tmem_store8(P + 16 * hb, hi);
-                    tmem_store8(P + 16 * hb + 8, lo);
                 }
                 tmem_store_wait();
                 fence_before();

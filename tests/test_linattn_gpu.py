@@ -12,7 +12,8 @@ relative to a partial sum, and no partial sum exceeds A):
   * pairs are scaled to the largest value among 16 tokens: a floor of 2^-30 of
     the largest A of the stream covers entries far below their neighbours.
   * bf16: the score and the state enter their products as one fp16 number,
-    2^-11 each; the output rounds by 2^-8 of itself.  fp16: they enter as
+    2^-11 each, or (d = 64, T >= 128) the score as one bf16, 2^-8 of each term
+    and so of A; the output rounds by 2^-8 of itself.  fp16: they enter as
     pairs (as fp32); the output rounds by 2^-11 of itself (half the smallest
     subnormal step, 2^-25, where that is larger).
   * results below fp32's smallest normal number are multiples of 2^-149, so
@@ -38,7 +39,8 @@ def assert_near(got, ref, size, d, T, dtype, what):
     tol = (32 * 2.0 ** -24 + (d + 64 + 2 * chunks) * 2.0 ** -23) * size + 2.0 ** -30 * size.amax((-1,), keepdim=True)
     tol = tol + (d + T) * 2.0 ** -149
     if dtype == BF16:
-        tol = tol + 2 * 2.0 ** -11 * size + 2.0 ** -8 * ref.abs()
+        score = 2.0 ** -8 if d == 64 and T >= 128 else 2.0 ** -11
+        tol = tol + (2.0 ** -11 + score) * size + 2.0 ** -8 * ref.abs()
     elif dtype == F16:
         tol = tol + 2.0 ** -11 * ref.abs() + 2.0 ** -25
     over = ((got - ref).abs() - tol)
