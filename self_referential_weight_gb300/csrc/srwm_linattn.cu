@@ -186,7 +186,8 @@ LinPlan linattn_plan(int B, int T, int H, int d, int roles)
 
 int linattn_launch(int dtype, int d, int roles, int slots, const LinParams& p, cudaStream_t st)
 {
-    if (linattn_tc_takes(dtype, d, p)) return linattn_tc_launch(roles, p, st);
+    if (linattn_tc_takes(dtype, d, p))
+        return dtype == SRWM_F32 ? linattn_tc32_launch(roles, p, st) : linattn_tc_launch(roles, p, st);
     if (dtype == SRWM_F32) return by_width<float>(d, roles, slots, p, st);
     if (dtype == SRWM_BF16) return by_width<__nv_bfloat16>(d, roles, slots, p, st);
     return by_width<__half>(d, roles, slots, p, st);

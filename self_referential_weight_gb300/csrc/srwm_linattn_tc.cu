@@ -24,31 +24,22 @@
 // by warps 8-11 before anything reads them; past the tensor's end TMA fills
 // zeros.  Every wait is bounded; a timeout sets the status word and ends the CTA
 // after its copies and products in flight.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
 #include <atomic>
-#include <cstdint>
-#include <mutex>
 
-#include "srwm.h"
 #include "srwm_check.h"
-#include "srwm_f2.cuh"
 #include "srwm_ffgemm.h"
-#include "srwm_linattn.cuh"
-#include "srwm_linattn_tc.h"
+#include "srwm_linattn_tc.cuh"
 
 namespace srwm {
 namespace {
 
-constexpr int D = 64, C = 128, STAGES = 3;
+using namespace tc;
+
+constexpr int STAGES = 3;
 constexpr int kTileBytes = C * D * 2;
 constexpr int kThreads = 736;
-constexpr int kMaxDevices = 64;
-// first warps of the roles; those that read tensor memory start at multiples of four, whose lanes they own in order
-constexpr int kScoreWarp = 0, kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
+// first warps of the roles after the scores' eight; those that read tensor memory start at multiples of four, whose lanes they own in order
+constexpr int kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
               kStateMmaWarp = 22;
 
 // Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's bf16
@@ -80,184 +71,6 @@ struct __align__(1024) Smem {
     uint32_t tmem_base;
     int abort;
 };
-
-// Shared-memory matrix descriptor of a 128-byte swizzled tile: atoms of eight
-// 128-byte rows, 1024 bytes apart.  K-major operands (rows = M or N, columns =
-// K) step 32 bytes per 16 of K inside the rows; MN-major ones (rows = K,
-// columns = 64 of M or N) step two atoms.  Bits as in the feed-forward products'
-// descriptor: address >> 4, both byte offsets >> 4, version 1, swizzle mode 2.
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr)
-{
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(64) << 16) |
-           (static_cast<uint64_t>(64) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-
-// kind::f16, bf16 operands, fp32 accumulator; bits 15, 16: A, B MN-major.
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-template <bool ACC>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "n"(ACC ? 1 : 0)
-        : "memory");
-}
-template <bool ACC>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "n"(ACC ? 1 : 0)
-        : "memory");
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect()
-{
-    uint32_t yes;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(yes));
-    return yes != 0;
-}
-// Arrives on `bar` once every product issued before has completed.
-__device__ __forceinline__ void commit(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Tensor memory loads return before their registers are written; tmem_wait
-// names the registers, so that no use of them moves ahead of it.
-#define SRWM_R16(c, r)                                                                                                 \
-    c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]), c(r[10]), c(r[11]),       \
-        c(r[12]), c(r[13]), c(r[14]), c(r[15])
-#define SRWM_R32(c, r)                                                                                                 \
-    SRWM_R16(c, r), c(r[16]), c(r[17]), c(r[18]), c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), \
-        c(r[26]), c(r[27]), c(r[28]), c(r[29]), c(r[30]), c(r[31])
-#define SRWM_L16 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-#define SRWM_L32                                                                                                       \
-    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "   \
-    "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-
-// 16 or 32 columns of the warp's 32 lanes, one lane per thread.
-__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " SRWM_L16 : SRWM_R16("=r", r) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
-}
-// 64 columns of the warp's first 16 lanes, as eight 16 x 8 accumulator
-// fragments: thread l holds (l / 4, 2 (l % 4)), the next column, and both eight lanes below.
-__device__ __forceinline__ void tmem_frag64(uint32_t addr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R16("+r", r)::"memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R32("+r", r)::"memory");
-}
-// 8 columns of the warp's 32 lanes, one lane per thread.
-__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float2 v) { return pack_bf16(v.x, v.y); }
-__device__ __forceinline__ float2 unpack_bf16(uint32_t v)
-{
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-// Takes the bf16 of both out of v.
-__device__ __forceinline__ uint32_t take_bf16(float2& v)
-{
-    const uint32_t h = pack_bf16(v);
-    v = fma2(unpack_bf16(h), both(-1.f), v);
-    return h;
-}
-__device__ __forceinline__ float2 as_float2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
-
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4])
-{
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
-}
-__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4])
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-
-// The CTA's items (a stream in a role) and their chunks, as every warp walks them.
-struct Walk {
-    const TcParams& p;
-    int item, role, b, h, n, chunks, k;
-    bool rev;
-    __device__ explicit Walk(const TcParams& params) : p(params), item(static_cast<int>(blockIdx.x)) { open(); }
-    __device__ bool done() const { return item >= p.items; }
-    __device__ void open()
-    {
-        k = 0;
-        chunks = 0;
-        if (done()) return;
-        role = item % p.roles;
-        const int stream = item / p.roles;
-        b = stream / p.lin.H;
-        h = stream % p.lin.H;
-        n = p.lin.lengths ? min(max(p.lin.lengths[b], 0), p.lin.T) : p.lin.T;
-        rev = p.lin.role[role].reverse != 0;
-        chunks = (n + C - 1) / C;
-    }
-    __device__ void next_item()
-    {
-        item += static_cast<int>(gridDim.x);
-        open();
-    }
-    // The next chunk, over the ends of items; false at the end of the list.
-    __device__ bool skip_empty()
-    {
-        while (!done() && k >= chunks) next_item();
-        return !done();
-    }
-    __device__ int token() const { return (rev ? chunks - 1 - k : k) * C; }
-    __device__ int valid() const { return min(C, n - token()); }
-    // Rows that TMA fills with other tokens' values although they are not valid.
-    __device__ bool dirty() const { return valid() < C && n < p.lin.T; }
-};
-
-// The part of a wait that spins, out of line: six kinds of warps share an
-// instruction cache, and their loops have to stay in it.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort, unsigned* status)
-{
-    if (mbar_wait_bounded(bar, parity, limit_ns) && !*abort) return true;
-    *abort = 1;
-    atomicOr(status, kStatusTimeout);
-    return false;
-}
 
 __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcParams p)
 {
@@ -317,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (lane == 0) {
             int last = -1;
             uint32_t last_phase = 0;
-            Walk w(p);
+            Walk<TcParams> w(p);
             for (; w.skip_empty() && !*abort; ++w.k, ++g) {
                 const int s = g % STAGES;
                 if (!wait(&sm.empty[s], g / STAGES + 1)) break;
@@ -336,11 +149,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     } else if (warp >= kScoreMmaWarp) {
         // ---- products: one warp issues P and OX, another U and OI, so that neither chain waits behind the other.
         // The whole warp walks the chunks, which keeps the descriptors in uniform registers; an elected lane issues.
-        constexpr uint32_t id_p = idesc(C, C, false, false), id_u = idesc(D, D, true, true), id_o = idesc(C, D, false, true);
+        constexpr uint32_t id_p = idesc(true, C, C, false, false), id_u = idesc(true, D, D, true, true), id_o = idesc(true, C, D, false, true);
         constexpr uint64_t kStage = 3 * kTileBytes / 16, kTile = kTileBytes / 16;   // descriptor steps
         const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
         bool ok = true, issued = false;
-        Walk w(p);
+        Walk<TcParams> w(p);
         if (warp == kScoreMmaWarp) {
             // P of chunk `at`, once its tiles have landed and been cleaned where they need it.  Its place was last
             // read by the product OX of chunk at - 2, issued before by this lane: products run in order.
@@ -390,13 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     fence_after();
                     if (elect()) {
                         const uint64_t t = d_terms + 512 * half, v = c + 512 * half;
+                        // the small terms first, since each sum is cut off to fp32
                         if (half == 0)
-                            mma_ss<false>(u, t, v, id_u);
+                            mma_ss<false>(u, t + 2 * kTile, v, id_u);
                         else
-                            mma_ss<true>(u, t, v, id_u);
+                            mma_ss<true>(u, t + 2 * kTile, v, id_u);
 #pragma unroll
                         for (int k = 1; k < 3 * 4; ++k)
-                            mma_ss<true>(u, t + kTile * (k / 4) + 128 * (k % 4), v + 128 * (k % 4), id_u);
+                            mma_ss<true>(u, t + kTile * (2 - k / 4) + 128 * (k % 4), v + 128 * (k % 4), id_u);
                         commit(&sm.terms_free[half]);
                         if (half == 1) commit(&sm.u_full);
                     }
@@ -407,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
                 fence_after();
                 if (elect()) {
-                    mma_ss<false>(oi, a, d_state, id_o);
+                    mma_ss<false>(oi, a, d_state + 512, id_o);
 #pragma unroll
                     for (int k = 1; k < 2 * D / 16; ++k)
-                        mma_ss<true>(oi, a + 2 * (k % 4), d_state + 512 * (k / 4) + 128 * (k % 4), id_o);
+                        mma_ss<true>(oi, a + 2 * (k % 4), d_state + 512 * (k < 4) + 128 * (k % 4), id_o);
                     commit(&sm.x_free);
                     commit(&sm.o_full);
                     commit(&sm.empty[g % STAGES]);
@@ -431,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
         float* decay = sm.decay[warp];
         bool ok = true;
-        Walk w(p);
+        Walk<TcParams> w(p);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
@@ -484,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         // written; half a token's row per thread
         const int t = threadIdx.x - 32 * kTermWarp, q0 = t >> 6 << 2;
         bool ok = true;
-        Walk w(p);
+        Walk<TcParams> w(p);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
@@ -535,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         // ---- the state
         const int own = warp - kStateWarp, r4 = lane >> 2, x2 = 2 * (lane & 3);
         bool ok = true;
-        Walk w(p);
+        Walk<TcParams> w(p);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
@@ -569,17 +383,22 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (!(ok = wait(&sm.u_full, g))) break;
                 fence_after();
                 {
-                    uint32_t u[32];
-                    tmem_frag64(tmem + quad + kU, u);
-                    tmem_wait(u);
-                    fence_before();
-                    arrive(&sm.u_free);
                     const Decay dec = nc == C ? full : decay_over(lg, nc);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t u[16];
+                        tmem_frag32(tmem + quad + kU + 32 * part, u);
+                        tmem_wait(u);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            X[t][k] = fma2(X[t][k], both(dec.m), fma2(X[t][k], both(dec.c), as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1])));
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float2& x = X[4 * part + t][k];
+                                x = fma2(x, both(dec.m), fma2(x, both(dec.c), as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1])));
+                            }
+                    }
+                    fence_before();
+                    arrive(&sm.u_free);
                 }
             }
             if (ok && R.x_out)
@@ -596,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         // ---- the outputs, one row per thread
         const int own = warp - kOutWarp;
         bool ok = true;
-        Walk w(p);
+        Walk<TcParams> w(p);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
@@ -652,41 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* q = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
-            r == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
-
-// {d, H, T, B} of token rows ld elements apart, boxes of `rows` tokens of one stream.
-int token_map(CUtensorMap* map, const void* base, long long ld, const LinParams& p, int rows)
-{
-    auto enc = encoder();
-    if (!enc) return SRWM_ERR_CUDA;
-    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(p.B)};
-    const cuuint64_t strides[3] = {2 * D, static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * p.T};
-    const cuuint32_t box[4] = {D, 1, static_cast<cuuint32_t>(rows), 1}, one[4] = {1, 1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SRWM_OK : SRWM_ERR_CUDA;
-}
-
 }  // namespace
 
 bool linattn_tc_takes(int dtype, int d, const LinParams& p)
 {
-    return dtype == SRWM_BF16 && d == D && p.segments == 1 && p.T >= C;
+    return dtype != SRWM_F16 && d == D && p.segments == 1 && p.T >= C;
 }
 
 int linattn_tc_launch(int roles, const LinParams& lin, cudaStream_t st)
@@ -702,10 +491,10 @@ int linattn_tc_launch(int roles, const LinParams& lin, cudaStream_t st)
     p.wait_limit_ns = device_wait_limit_ns();
     for (int i = 0; i < roles; ++i) {
         const LinRole& r = lin.role[i];
-        if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C)) != SRWM_OK ||
-            (rc = token_map(&p.map[i].b, r.b, r.ldb, lin, C)) != SRWM_OK ||
-            (rc = token_map(&p.map[i].c, r.c, r.ldc, lin, C)) != SRWM_OK ||
-            (rc = token_map(&p.map[i].out, r.out, r.ldo, lin, 32)) != SRWM_OK)
+        if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C, false)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].b, r.b, r.ldb, lin, C, false)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].c, r.c, r.ldc, lin, C, false)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].out, r.out, r.ldo, lin, 32, false)) != SRWM_OK)
             return rc;
     }
     static std::atomic<int> sms[kMaxDevices];   // 0: not asked yet

@@ -1,5 +1,5 @@
-// srwm_linattn_tc.h -- host interface of the tcgen05 kernel of the primitive in
-// srwm_linattn.h (bf16, d = 64).
+// srwm_linattn_tc.h -- host interface of the tcgen05 kernels of the primitive in
+// srwm_linattn.h (bf16 and fp32, d = 64).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -8,8 +8,9 @@
 
 namespace srwm {
 
-// Whether a call may take it: bf16, d = 64, an unsplit axis of at least one of its chunks.
+// Whether a call may take them: an unsplit axis of at least one of their chunks.
 bool linattn_tc_takes(int dtype, int d, const LinParams& p);
-int linattn_tc_launch(int roles, const LinParams& p, cudaStream_t st);
+int linattn_tc_launch(int roles, const LinParams& p, cudaStream_t st);     // bf16
+int linattn_tc32_launch(int roles, const LinParams& p, cudaStream_t st);   // fp32
 
 }  // namespace srwm

@@ -1,0 +1,587 @@
+// srwm_linattn_tc32.cu -- the primitive of srwm_linattn.h on the 5th-generation
+// tensor cores, for fp32 and d = 64.  The chunk, its five products and the
+// pipeline are those of srwm_linattn_tc.cu; what differs is the operands'
+// precision.
+//
+// Every operand is a pair of fp16 values, x ~ (high + low) 2^e with one
+// exponent for 16 tokens (22 bits of the largest of them, see
+// srwm_linattn.cuh), and every product three: high high, high low, low high.
+// a, b, c land as fp32 in two tiles of 32 columns each, and are turned into
+// their pairs in place: a row's high halves take its 128 bytes of the first
+// tile, the low halves those of the second.  The scores of 16 columns carry
+// 2^(eb + ec) relative to the largest on the strip's causal side, the weighted
+// b's terms likewise, and X's copy the exponent of a bound on X; sums are fp32
+// throughout.
+//
+// Warps: 0-7 turn P into its pair; 8-11 write the weighted b's terms, 32 tokens
+// at a time into two buffers in turn; 12-15 hold X; 16-19 write the outputs;
+// 20-23 convert the landed tiles; 24 issues the TMA loads (two stages), 25 and
+// 26 the products.
+#include <atomic>
+
+#include "srwm_check.h"
+#include "srwm_ffgemm.h"
+#include "srwm_linattn_tc.cuh"
+
+namespace srwm {
+namespace {
+
+using namespace tc;
+
+constexpr int STAGES = 2, RING = 4;
+constexpr int kHalfTile = C * 128;   // bytes: 32 columns of fp32, or 64 of fp16
+constexpr int kThreads = 864;
+constexpr int kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kConvertWarp = 20, kLoadWarp = 24, kScoreMmaWarp = 25,
+              kStateMmaWarp = 26;
+
+// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's pair
+// goes over it: 16 columns of fp32 become 8 of high and 8 of low halves.
+constexpr uint32_t kP = 0, kOI = 256, kOX = 384, kU = 448, kTmemCols = 512;
+
+struct Tc32Maps {
+    CUtensorMap a, b, c;
+};
+struct Tc32Params {
+    Tc32Maps map[3];
+    LinParams lin;
+    int roles, items;
+    unsigned* status;
+    unsigned long long wait_limit_ns;
+};
+
+struct __align__(1024) Smem32 {
+    uint8_t stage[STAGES][3][2][kHalfTile];   // a | b | c: columns 0-31 | 32-63, then high | low halves
+    uint8_t terms[2][2][32 * 128];            // of w_j b_j for 32 tokens: high | low
+    uint8_t state[2][D * D * 2];              // X's copy: high | low
+    float decay[8][64];
+    int exps[RING][3][8];                     // of a, b, c, per 16 tokens
+    int state_exp[RING];
+    float top[2][4];                          // largest |X| of each state warp's rows at an item's start
+    uint64_t full[STAGES], empty[STAGES], ready[STAGES];
+    uint64_t terms_full[2], terms_free[2];
+    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], top_full;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// The exponent that normalises the scores of rows r0 .. r0 + 31: of the largest
+// alpha_u 2^(eb + ec) g^gap among the column groups on the causal side.
+__device__ __forceinline__ int score_exp(const int (&e)[3][8], int ue, float lg, int r0, bool rev)
+{
+    float top = -8000.f;
+#pragma unroll 1
+    for (int c = rev ? r0 / 16 : 0; c <= (rev ? 7 : r0 / 16 + 1); ++c) {
+        const int gap = max(0, rev ? 16 * c - r0 - 31 : r0 - 16 * c - 15);
+        top = fmaxf(top, fmaf(lg, static_cast<float>(gap), static_cast<float>(e[1][c] + e[2][c] + ue)));
+    }
+    return static_cast<int>(ceilf(top));
+}
+
+// The exponent that normalises the weighted b's terms: of the largest 2^(eb + ec) g^(tokens to the chunk's end).
+__device__ __forceinline__ int term_exp(const int (&e)[3][8], float lg, int nc, bool rev)
+{
+    float top = -8000.f;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        const int gap = rev ? 16 * c + 1 : max(0, nc - 16 * c - 16);
+        top = fmaxf(top, fmaf(lg, static_cast<float>(gap), static_cast<float>(e[1][c] + e[2][c])));
+    }
+    return static_cast<int>(ceilf(top));
+}
+
+__global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_constant__ Tc32Params p)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem32& sm = *reinterpret_cast<Smem32*>(smem_raw);
+    if ((smem_u32(smem_raw) & 1023u) != 0) {   // the swizzled tiles start on 1024-byte boundaries
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemBase);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 2);
+            mbar_init(&sm.ready[s], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.terms_full[i], 4);
+            mbar_init(&sm.terms_free[i], 1);
+            mbar_init(&sm.p32_full[i], 1);
+            mbar_init(&sm.p16_full[i], 8);
+            mbar_init(&sm.o_free[i], 4);
+        }
+        mbar_init(&sm.u_full, 1);
+        mbar_init(&sm.u_free, 4);
+        mbar_init(&sm.x_full, 4);
+        mbar_init(&sm.x_free, 1);
+        mbar_init(&sm.o_full, 2);
+        mbar_init(&sm.top_full, 4);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kStateMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int* abort = &sm.abort;
+    // Waits for phase `phase` of `bar`; false, with the CTA marked to end, when it does not come.
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return mbar_try_wait(bar, phase & 1u) || wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
+    };
+    // One arrival for the warp after its lanes' work.
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;   // the warp's tensor memory lanes
+    uint32_t g = 0;   // chunks so far, the same count in every warp
+
+    if (warp == kLoadWarp) {
+        // ---- loads
+        if (lane == 0) {
+            int last = -1;
+            uint32_t last_phase = 0;
+            Walk<Tc32Params> w(p);
+            for (; w.skip_empty() && !*abort; ++w.k, ++g) {
+                const int s = g % STAGES;
+                if (!wait(&sm.empty[s], g / STAGES + 1)) break;
+                const Tc32Maps& m = p.map[w.role];
+                mbar_arrive_expect_tx(&sm.full[s], 6 * kHalfTile);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    tma_load_4d(sm.stage[s][1][half], &m.b, &sm.full[s], 32 * half, w.h, w.token(), w.b);
+                    tma_load_4d(sm.stage[s][0][half], &m.a, &sm.full[s], 32 * half, w.h, w.token(), w.b);
+                    tma_load_4d(sm.stage[s][2][half], &m.c, &sm.full[s], 32 * half, w.h, w.token(), w.b);
+                }
+                last = s;
+                last_phase = g / STAGES;
+            }
+            // the shared memory may only be given up once the last loads landed (stages complete in order)
+            if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
+        }
+        __syncwarp();
+    } else if (warp >= kScoreMmaWarp) {
+        // ---- products: one warp issues P and OX, another U and OI.  The whole warp walks the chunks, which keeps
+        // the descriptors in uniform registers; an elected lane issues.
+        constexpr uint32_t id_p = idesc(false, C, C, false, false), id_u = idesc(false, D, D, true, true),
+                           id_o = idesc(false, C, D, false, true);
+        constexpr uint64_t kStage = 6 * kHalfTile / 16, kTile = 2 * kHalfTile / 16, kLow = kHalfTile / 16;
+        const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0][0]));
+        bool ok = true, issued = false;
+        Walk<Tc32Params> w(p);
+        if (warp == kScoreMmaWarp) {
+            // P of chunk `at`, once its tiles are pairs.  Its place was last read by the product OX of chunk at - 2,
+            // issued before by this lane: products run in order.
+            auto score = [&](uint32_t at) {
+                if (!(ok = wait(&sm.ready[at % STAGES], at / STAGES))) return;
+                fence_after();
+                const uint64_t a = d_stage + kStage * (at % STAGES), b = a + kTile;
+                const uint32_t to = tmem + kP + C * (at & 1);
+                if (elect()) {
+                    // low high, high low, high high: the small products first, since each sum is cut off to fp32
+                    mma_ss<false>(to, a + kLow, b, id_p);
+#pragma unroll
+                    for (int k = 1; k < 3 * 4; ++k)
+                        mma_ss<true>(to, a + (k < 4) * kLow + 2 * (k % 4), b + (k / 4 == 1) * kLow + 2 * (k % 4), id_p);
+                    commit(&sm.p32_full[at & 1]);
+                }
+                __syncwarp();
+                issued = true;
+            };
+            if (w.skip_empty()) score(0);
+            for (; ok && w.skip_empty(); ++g) {
+                const uint64_t c = d_stage + kStage * (g % STAGES) + 2 * kTile;
+                ++w.k;
+                if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
+                // the scores are there, and the outputs before have been read
+                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) && (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1)))) break;
+                fence_after();
+                const uint32_t scores = tmem + kP + C * (g & 1);
+                if (elect()) {
+                    mma_ts<false>(tmem + kOX, scores + 8, c, id_o);
+#pragma unroll
+                    for (int k = 1; k < 3 * 8; ++k)
+                        mma_ts<true>(tmem + kOX, scores + 16 * (k % 8) + 8 * (k < 8), c + (k / 8 == 1) * kLow + 128 * (k % 8), id_o);
+                    commit(&sm.o_full);
+                    commit(&sm.empty[g % STAGES]);
+                }
+                __syncwarp();
+            }
+        } else {
+            const uint64_t d_terms = desc128(smem_u32(sm.terms[0][0])), d_state = desc128(smem_u32(sm.state[0]));
+            for (; ok && w.skip_empty(); ++w.k, ++g) {
+                const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
+                const uint32_t u = tmem + kU, oi = tmem + kOI + 64 * (g & 1);
+                if (!(ok = wait(&sm.ready[g % STAGES], g / STAGES) && wait(&sm.u_free, g + 1))) break;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    if (!(ok = wait(&sm.terms_full[q & 1], 2 * g + (q >> 1)))) break;
+                    fence_after();
+                    if (elect()) {
+                        const uint64_t t = d_terms + 512 * (q & 1), v = c + 256 * q;   // 32 tokens: 4 KB of a tile
+                        if (q == 0)
+                            mma_ss<false>(u, t + 256, v, id_u);
+                        else
+                            mma_ss<true>(u, t + 256, v, id_u);
+#pragma unroll
+                        for (int k = 1; k < 3 * 2; ++k)
+                            mma_ss<true>(u, t + (k < 2) * 256 + 128 * (k % 2), v + (k / 2 == 1) * kLow + 128 * (k % 2), id_u);
+                        commit(&sm.terms_free[q & 1]);
+                        if (q == 3) commit(&sm.u_full);
+                    }
+                    __syncwarp();
+                    issued = true;
+                }
+                // X's copy is there, and the outputs that used this place have been read
+                if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
+                fence_after();
+                if (elect()) {
+                    mma_ss<false>(oi, a + kLow, d_state, id_o);
+#pragma unroll
+                    for (int k = 1; k < 3 * 4; ++k)
+                        mma_ss<true>(oi, a + (k < 4) * kLow + 2 * (k % 4), d_state + 512 * (k / 4 == 1) + 128 * (k % 4), id_o);
+                    commit(&sm.x_free);
+                    commit(&sm.o_full);
+                    commit(&sm.empty[g % STAGES]);
+                }
+                __syncwarp();
+            }
+        }
+        // Tensor memory may only be freed once the products issued have completed: after a timeout nobody else
+        // waits for them.
+        if (!ok && issued) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp < kTermWarp) {
+        // ---- P as a pair, one row per thread; two sets of four warps take the 32-column blocks in turn
+        const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
+        bool ok = true;
+        Walk<Tc32Params> w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            // tab[x - l]: alpha_u's mantissa times g^|x - l| for row l, column x on the causal side of a diagonal
+            // block, 0 on the other.  A block beside the diagonal takes the row's factor off: its columns are those
+            // of row 31 in order, of row 0 in reverse.
+            float* tab = sm.decay[warp] + 31;
+            __syncwarp();   // the table of the item before is no longer read
+            for (int i = lane; i < 63; i += 32) {
+                const int gap = w.rev ? i - 31 : 31 - i;
+                tab[i - 31] = gap >= 0 ? R.alpha_u_man * exp2f(lg * static_cast<float>(gap)) : 0.f;
+            }
+            __syncwarp();
+            const float* beside = w.rev ? tab : tab - 31;
+            const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
+            const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1))) break;
+                fence_after();
+                const int(&e)[3][8] = sm.exps[g % RING];
+                const int ef = score_exp(e, R.alpha_u_exp, lg, 32 * own, w.rev) - R.alpha_u_exp + 20;
+                const uint32_t P = tmem + quad + kP + C * (g & 1);
+                for (int cb = set; cb < 4; cb += 2)   // the side that is masked
+                    if (cb < c0 || cb > c1) {
+                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tmem_store8(P + 32 * cb + 8 * k, zero);
+                    }
+#pragma unroll 1
+                for (int hb = 2 * first; hb <= 2 * c1 + 1; hb += (hb & 1) ? 3 : 1) {   // 16 columns of this set's blocks
+                    const int cb = hb >> 1;
+                    uint32_t r[16], hi[8], lo[8];
+                    tmem_rows(P + 16 * hb, r);
+                    const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31))) *
+                                    pow2i(e[1][hb] + e[2][hb] - ef);
+                    const float* col = (cb == own ? tab - lane : beside) + 16 * (hb & 1);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        split_half2_2(mul2(as_float2(r[2 * k], r[2 * k + 1]), mul2(both(f), make_float2(col[2 * k], col[2 * k + 1]))),
+                                      hi[k], lo[k]);
+                    tmem_store8(P + 16 * hb, hi);
+                    tmem_store8(P + 16 * hb + 8, lo);
+                }
+                tmem_store_wait();
+                fence_before();
+                arrive(&sm.p16_full[g & 1]);
+            }
+        }
+    } else if (warp < kStateWarp) {
+        // ---- the terms of w_j b_j, 32 tokens at a time: one token per lane, 16 columns per warp
+        const int own = warp - kTermWarp;
+        bool ok = true;
+        Walk<Tc32Params> w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            for (; ok && w.k < w.chunks; ++w.k, ++g) {
+                const int s = g % STAGES, nc = w.valid();
+                if (!(ok = wait(&sm.ready[s], g / STAGES))) break;
+                const int(&e)[3][8] = sm.exps[g % RING];
+                const int eu = term_exp(e, lg, nc, w.rev);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    const int j = 32 * q + lane;
+                    const float wj = exp2f(lg * static_cast<float>(w.rev ? j + 1 : max(0, nc - 1 - j))) *
+                                     pow2i(e[1][j >> 4] + e[2][j >> 4] - eu);
+                    if (!(ok = wait(&sm.terms_free[q & 1], 2 * g + (q >> 1) + 1))) break;   // those before have been read
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t o = static_cast<uint32_t>(((2 * own + i) ^ (j & 7)) << 4);
+                        const uint32_t from = smem_u32(sm.stage[s][1][0]) + 128 * j + o;
+                        const uint32_t to = smem_u32(sm.terms[q & 1][0]) + 128 * lane + o;
+                        uint32_t h[4], l[4];
+                        lds128(from, h);
+                        lds128(from + kHalfTile, l);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            split_half2_2(mul2(add2(unpack_half2(h[k]), unpack_half2(l[k])), both(wj)), h[k], l[k]);
+                        sts128(to, h);
+                        sts128(to + 32 * 128, l);
+                    }
+                    fence_proxy_async_smem();
+                    arrive(&sm.terms_full[q & 1]);
+                }
+            }
+        }
+    } else if (warp < kOutWarp) {
+        // ---- the state
+        const int own = warp - kStateWarp, r4 = lane >> 2, x2 = 2 * (lane & 3);
+        uint32_t starts = 0;   // items that began with a state
+        bool ok = true;
+        Walk<Tc32Params> w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            const size_t mat = (static_cast<size_t>(w.b) * p.lin.H + w.h) * D * D;
+            float2 X[8][2];   // rows 16 own + r4 (+ 8), columns 8 t + x2 and the next
+            float bound = 0.f;   // >= every |X|, the same in every state warp
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = 16 * own + r4 + 8 * k, q = 8 * t + x2;
+                    X[t][k] = !R.x_in       ? both(0.f)
+                              : R.transposed ? make_float2(R.x_in[mat + q * D + i], R.x_in[mat + (q + 1) * D + i])
+                                             : *reinterpret_cast<const float2*>(R.x_in + mat + i * D + q);
+                    bound = fmaxf(bound, fmaxf(fabsf(X[t][k].x), fabsf(X[t][k].y)));
+                }
+            if (R.x_in && w.chunks > 0) {
+                bound = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bound)));
+                if (lane == 0) sm.top[starts & 1][own] = bound;
+                arrive(&sm.top_full);
+                if (!(ok = wait(&sm.top_full, starts))) break;
+                for (int i = 0; i < 4; ++i) bound = fmaxf(bound, sm.top[starts & 1][i]);
+                ++starts;
+            }
+            const Decay full = decay_over(lg, C);
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                if (!(ok = wait(&sm.x_free, g + 1))) break;
+                const int eb = max(static_cast<int>(__float_as_uint(bound) >> 23), 14);
+                const float sc = bound == 0.f ? 0.f : pow2i(140 - eb);   // X's copy: X * 2^-(eb - 140), at most 2^14
+                if (own == 0 && lane == 0) sm.state_exp[g % RING] = bound == 0.f ? kNoValue : eb - 140;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t to = state_at<D>(smem_u32(sm.state[0]), 16 * own + r4 + 8 * k, t, 0) + 2 * x2;
+                        uint32_t hi, lo;
+                        split_half2_2(mul2(X[t][k], both(sc)), hi, lo);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + D * D * 2), "r"(lo) : "memory");
+                    }
+                fence_proxy_async_smem();
+                arrive(&sm.x_full);
+                const int nc = w.valid();
+                if (!(ok = wait(&sm.u_full, g))) break;
+                fence_after();
+                const int eu = term_exp(sm.exps[g % RING], lg, nc, w.rev) + R.alpha_u_exp;
+                // X = g^nc X + alpha_u U 2^eu, in two factors that stay inside fp32's range
+                const float f1 = pow2i(eu / 2), f2 = R.alpha_u_man * pow2i(eu - eu / 2);
+                const Decay dec = nc == C ? full : decay_over(lg, nc);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t u[16];
+                    tmem_frag32(tmem + quad + kU + 32 * part, u);
+                    tmem_wait(u);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float2& x = X[4 * part + t][k];
+                            x = fma2(mul2(as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1]), both(f1)), both(f2),
+                                     fma2(x, both(dec.m), mul2(x, both(dec.c))));
+                        }
+                }
+                fence_before();
+                arrive(&sm.u_free);
+                // |U| < C 2^28
+                const float most = fabsf(f2) * static_cast<float>(C) * pow2i(28 + eu / 2);
+                bound = fminf(fmaf(bound, dec.m + dec.c, most) * 1.0001f, 1.7e38f);
+            }
+            if (ok && R.x_out)
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int i = 16 * own + r4 + 8 * k, q = 8 * t + x2;
+                        R.x_out[mat + (R.transposed ? q * D + i : i * D + q)] = X[t][k].x;
+                        R.x_out[mat + (R.transposed ? (q + 1) * D + i : i * D + q + 1)] = X[t][k].y;
+                    }
+        }
+    } else if (warp < kConvertWarp) {
+        // ---- the outputs, one row per thread, written from registers (32 bytes at a time)
+        const int own = warp - kOutWarp, i = 32 * own + lane;
+        bool ok = true;
+        Walk<Tc32Params> w(p);
+        for (; ok && !w.done(); w.next_item()) {
+            const LinRole& R = p.lin.role[w.role];
+            const float lg = decay_log2(p.lin.log_decay[w.h]);
+            float* po = static_cast<float*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
+            for (; w.k < w.chunks; ++w.k, ++g) {
+                const int nc = w.valid();
+                if (!(ok = wait(&sm.o_full, g))) break;
+                fence_after();
+                const int(&e)[3][8] = sm.exps[g % RING];
+                const int ea = e[0][i >> 4];
+                // out = alpha_o 2^ea (g^e 2^eX OI + 2^ef OX), each power in two factors that stay inside fp32's range
+                const int ei = ea + sm.state_exp[g % RING], ex = ea + score_exp(e, R.alpha_u_exp, lg, 32 * own, w.rev) + 20;
+                const float fi = pow2i(ei / 2), fx = pow2i(ex / 2);
+                const float gi = R.alpha_o * pow2i(ei - ei / 2) * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
+                const float gx = R.alpha_o * pow2i(ex - ex / 2);
+                const int t = w.token() + i;
+                float* row = po + static_cast<long long>(t) * R.ldo;
+#pragma unroll 1
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t oi[16], ox[16];
+                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 16 * part, oi);
+                    tmem_rows(tmem + quad + kOX + 16 * part, ox);
+                    tmem_wait(oi);
+                    tmem_wait(ox);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 v = fma2(mul2(as_float2(oi[2 * k], oi[2 * k + 1]), both(fi)), both(gi),
+                                              mul2(mul2(as_float2(ox[2 * k], ox[2 * k + 1]), both(fx)), both(gx)));
+                        oi[2 * k] = __float_as_uint(v.x);
+                        oi[2 * k + 1] = __float_as_uint(v.y);
+                    }
+                    if (t < p.lin.T) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(row + 16 * part + 4 * k) =
+                                make_uint4(oi[4 * k], oi[4 * k + 1], oi[4 * k + 2], oi[4 * k + 3]);
+                    }
+                }
+                fence_before();
+                arrive(&sm.o_free[g & 1]);
+            }
+            // tokens past the last chunk
+            const long long z0 = static_cast<long long>(w.chunks) * C, pieces = (p.lin.T - z0) * (D / 4);
+            for (long long q = threadIdx.x - 32 * kOutWarp; q < pieces; q += 128)
+                *reinterpret_cast<uint4*>(po + (z0 + q / (D / 4)) * R.ldo + q % (D / 4) * 4) = make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        // ---- fp32 tiles into pairs, in place: 16 tokens of one tensor at a time, two lanes per token
+        const int own = warp - kConvertWarp, half = lane & 1;
+        bool ok = true;
+        Walk<Tc32Params> w(p);
+        for (; ok && w.skip_empty(); ++w.k, ++g) {
+            const int s = g % STAGES, nc = w.valid();
+            if (!(ok = wait(&sm.full[s], g / STAGES))) break;
+#pragma unroll 1
+            for (int unit = 0; unit < 6; ++unit) {
+                const int tensor = unit < 2 ? 1 : unit < 4 ? 0 : 2, group = 2 * own + (unit & 1), r = 16 * group + (lane >> 1);
+                const uint32_t tile = smem_u32(sm.stage[s][tensor][0]) + 128 * r;
+                const bool valid = r < nc;
+                uint32_t v[8][4];   // piece k holds columns 4 (k ^ 4 half) .. of this lane's tile: its lanes' banks differ
+                float m = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    lds128(tile + half * kHalfTile + (((k ^ (half << 2)) ^ (r & 7)) << 4), v[k]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (!valid) v[k][i] = 0;
+                        m = fmaxf(m, fabsf(__uint_as_float(v[k][i])));
+                    }
+                }
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));   // every lane has read its row
+                const int ex = max(static_cast<int>(top >> 23), 14);                       // 2^(ex-127) <= top < 2^(ex-126)
+                const float sc = __int_as_float((267 - ex) << 23);                         // top * sc in [2^13, 2^14)
+                if (lane == 0) sm.exps[g % RING][tensor][group] = top == 0 ? kNoValue : ex - 140;
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        split_half2_2(mul2(as_float2(v[2 * k + i / 2][i % 2 * 2], v[2 * k + i / 2][i % 2 * 2 + 1]), both(sc)), hi[i],
+                                      lo[i]);
+                    const uint32_t o = static_cast<uint32_t>(((4 * half + (k ^ (half << 1))) ^ (r & 7)) << 4);
+                    sts128(tile + o, hi);
+                    sts128(tile + o + kHalfTile, lo);
+                }
+            }
+            fence_proxy_async_smem();
+            arrive(&sm.ready[s]);
+        }
+    }
+
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kStateMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+}  // namespace
+
+int linattn_tc32_launch(int roles, const LinParams& lin, cudaStream_t st)
+{
+    Tc32Params p{};
+    p.lin = lin;
+    p.roles = roles;
+    const long long items = static_cast<long long>(lin.B) * lin.H * roles;
+    if (items > 0x7fffffffLL - 1024) return SRWM_ERR_SHAPE;
+    p.items = static_cast<int>(items);
+    int rc = device_status_ptr(&p.status);
+    if (rc != SRWM_OK) return rc;
+    p.wait_limit_ns = device_wait_limit_ns();
+    for (int i = 0; i < roles; ++i) {
+        const LinRole& r = lin.role[i];
+        if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C, true)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].b, r.b, r.ldb, lin, C, true)) != SRWM_OK ||
+            (rc = token_map(&p.map[i].c, r.c, r.ldc, lin, C, true)) != SRWM_OK)
+            return rc;
+    }
+    static std::atomic<int> sms[kMaxDevices];   // 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return SRWM_ERR_CUDA;
+    }
+    constexpr int smem = static_cast<int>(sizeof(Smem32));
+    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+    int n_sm = sms[dev].load();
+    if (n_sm == 0) {
+        if (cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(linattn_tc32_kernel),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return SRWM_ERR_CUDA;
+        }
+        sms[dev].store(n_sm);
+    }
+    linattn_tc32_kernel<<<p.items < n_sm ? p.items : n_sm, kThreads, smem, st>>>(p);
+    return launched();
+}
+
+}  // namespace srwm

@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "srwm_f2.cuh"
+
 namespace srwm {
 
 // c[16x8] += a[16x16] b[16x8].  Lane l holds, with r = l / 4 and x = 2 (l % 4):
@@ -67,6 +69,14 @@ __device__ __forceinline__ void split_half2(float x, float y, uint32_t& hi, uint
     hi = pack_half2(x, y);
     const float2 h = unpack_half2(hi);
     lo = pack_half2(x - h.x, y - h.y);
+}
+
+// The same with two fp32 operations per instruction.
+__device__ __forceinline__ void split_half2_2(float2 v, uint32_t& hi, uint32_t& lo)
+{
+    hi = pack_half2(v.x, v.y);
+    const float2 rest = fma2(unpack_half2(hi), both(-1.f), v);
+    lo = pack_half2(rest.x, rest.y);
 }
 
 }  // namespace srwm
