@@ -14,8 +14,8 @@
 // throughout.
 //
 // Warps: 0-7 turn P into its pair; 8-11 write the weighted b's terms, 32 tokens
-// at a time into two buffers in turn; 12-15 hold X; 16-19 write the outputs;
-// 20-23 convert the landed tiles; 24 issues the TMA loads (two stages), 25 and
+// at a time into two buffers in turn; 12-15 hold X; 16-19 convert c and write
+// the outputs; 20-23 convert a and b; 24 issues the TMA loads (two stages), 25 and
 // 26 the products.
 #include <atomic>
 
@@ -57,7 +57,8 @@ struct __align__(1024) Smem32 {
     int exps[RING][3][8];                     // of a, b, c, per 16 tokens
     int state_exp[RING];
     float top[2][4];                          // largest |X| of each state warp's rows at an item's start
-    uint64_t full[STAGES], empty[STAGES], ready[STAGES];
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t ready_ab[STAGES], ready_c[STAGES];   // the tiles are pairs
     uint64_t terms_full[2], terms_free[2];
     uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], top_full;
     uint32_t tmem_base;
@@ -89,6 +90,42 @@ __device__ __forceinline__ int term_exp(const int (&e)[3][8], float lg, int nc, 
     return static_cast<int>(ceilf(top));
 }
 
+// Sixteen tokens of a landed fp32 tile into pairs, in place, two lanes per
+// token; tokens at and past nc become zeros.
+__device__ __noinline__ void convert_tokens(uint8_t* tiles, int group, int nc, int* exponent)
+{
+    const int lane = threadIdx.x & 31, half = lane & 1, r = 16 * group + (lane >> 1);
+    const uint32_t tile = smem_u32(tiles) + 128 * r;
+    const bool valid = r < nc;
+    uint32_t v[8][4];   // piece k holds columns 4 (k ^ 4 half) .. of this lane's tile: its lanes' banks differ
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        lds128(tile + half * kHalfTile + (((k ^ (half << 2)) ^ (r & 7)) << 4), v[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!valid) v[k][i] = 0;
+            m = fmaxf(m, fabsf(__uint_as_float(v[k][i])));
+        }
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));   // every lane has read its row
+    const int ex = max(static_cast<int>(top >> 23), 14);                       // 2^(ex-127) <= top < 2^(ex-126)
+    const float sc = __int_as_float((267 - ex) << 23);                         // top * sc in [2^13, 2^14)
+    if (lane == 0) *exponent = top == 0 ? kNoValue : ex - 140;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            split_half2_2(mul2(as_float2(v[2 * k + i / 2][i % 2 * 2], v[2 * k + i / 2][i % 2 * 2 + 1]), both(sc)), hi[i],
+                          lo[i]);
+        const uint32_t o = static_cast<uint32_t>(((4 * half + (k ^ (half << 1))) ^ (r & 7)) << 4);
+        sts128(tile + o, hi);
+        sts128(tile + o + kHalfTile, lo);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_constant__ Tc32Params p)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -102,7 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 2);
-            mbar_init(&sm.ready[s], 4);
+            mbar_init(&sm.ready_ab[s], 4);
+            mbar_init(&sm.ready_c[s], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.terms_full[i], 4);
@@ -177,10 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
         bool ok = true, issued = false;
         Walk<Tc32Params> w(p);
         if (warp == kScoreMmaWarp) {
-            // P of chunk `at`, once its tiles are pairs.  Its place was last read by the product OX of chunk at - 2,
+            // P of chunk `at`, once a and b are pairs.  Its place was last read by the product OX of chunk at - 2,
             // issued before by this lane: products run in order.
             auto score = [&](uint32_t at) {
-                if (!(ok = wait(&sm.ready[at % STAGES], at / STAGES))) return;
+                if (!(ok = wait(&sm.ready_ab[at % STAGES], at / STAGES))) return;
                 fence_after();
                 const uint64_t a = d_stage + kStage * (at % STAGES), b = a + kTile;
                 const uint32_t to = tmem + kP + C * (at & 1);
@@ -219,7 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             for (; ok && w.skip_empty(); ++w.k, ++g) {
                 const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
                 const uint32_t u = tmem + kU, oi = tmem + kOI + 64 * (g & 1);
-                if (!(ok = wait(&sm.ready[g % STAGES], g / STAGES) && wait(&sm.u_free, g + 1))) break;
+                if (!(ok = wait(&sm.ready_ab[g % STAGES], g / STAGES) && wait(&sm.ready_c[g % STAGES], g / STAGES) &&
+                           wait(&sm.u_free, g + 1)))
+                    break;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     if (!(ok = wait(&sm.terms_full[q & 1], 2 * g + (q >> 1)))) break;
@@ -284,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
             const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
-                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1))) break;
+                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1) && wait(&sm.ready_c[g % STAGES], g / STAGES))) break;
                 fence_after();
                 const int(&e)[3][8] = sm.exps[g % RING];
                 const int ef = score_exp(e, R.alpha_u_exp, lg, 32 * own, w.rev) - R.alpha_u_exp + 20;
@@ -325,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             for (; ok && w.k < w.chunks; ++w.k, ++g) {
                 const int s = g % STAGES, nc = w.valid();
-                if (!(ok = wait(&sm.ready[s], g / STAGES))) break;
+                if (!(ok = wait(&sm.ready_ab[s], g / STAGES) && wait(&sm.ready_c[s], g / STAGES))) break;
                 const int(&e)[3][8] = sm.exps[g % RING];
                 const int eu = term_exp(e, lg, nc, w.rev);
 #pragma unroll 1
@@ -439,17 +479,29 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     }
         }
     } else if (warp < kConvertWarp) {
-        // ---- the outputs, one row per thread, written from registers (32 bytes at a time)
+        // ---- the outputs, one row per thread, written from registers; and the next chunk's c into pairs before
+        // this one's outputs are there
         const int own = warp - kOutWarp, i = 32 * own + lane;
-        bool ok = true;
-        Walk<Tc32Params> w(p);
+        Walk<Tc32Params> w(p), next(p);
+        auto convert = [&](uint32_t at) {
+            const int s = at % STAGES, nc = next.valid();
+            if (!wait(&sm.full[s], at / STAGES)) return false;
+#pragma unroll 1
+            for (int group = 2 * own; group < 2 * own + 2; ++group)
+                convert_tokens(sm.stage[s][2][0], group, nc, &sm.exps[at % RING][2][group]);
+            fence_proxy_async_smem();
+            arrive(&sm.ready_c[s]);
+            ++next.k;
+            return true;
+        };
+        bool ok = !next.skip_empty() || convert(0);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             float* po = static_cast<float*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
             for (; w.k < w.chunks; ++w.k, ++g) {
                 const int nc = w.valid();
-                if (!(ok = wait(&sm.o_full, g))) break;
+                if (!(ok = (!next.skip_empty() || convert(g + 1)) && wait(&sm.o_full, g))) break;
                 fence_after();
                 const int(&e)[3][8] = sm.exps[g % RING];
                 const int ea = e[0][i >> 4];
@@ -490,48 +542,20 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 *reinterpret_cast<uint4*>(po + (z0 + q / (D / 4)) * R.ldo + q % (D / 4) * 4) = make_uint4(0, 0, 0, 0);
         }
     } else {
-        // ---- fp32 tiles into pairs, in place: 16 tokens of one tensor at a time, two lanes per token
-        const int own = warp - kConvertWarp, half = lane & 1;
+        // ---- a and b into pairs
+        const int own = warp - kConvertWarp;
         bool ok = true;
         Walk<Tc32Params> w(p);
         for (; ok && w.skip_empty(); ++w.k, ++g) {
             const int s = g % STAGES, nc = w.valid();
             if (!(ok = wait(&sm.full[s], g / STAGES))) break;
 #pragma unroll 1
-            for (int unit = 0; unit < 6; ++unit) {
-                const int tensor = unit < 2 ? 1 : unit < 4 ? 0 : 2, group = 2 * own + (unit & 1), r = 16 * group + (lane >> 1);
-                const uint32_t tile = smem_u32(sm.stage[s][tensor][0]) + 128 * r;
-                const bool valid = r < nc;
-                uint32_t v[8][4];   // piece k holds columns 4 (k ^ 4 half) .. of this lane's tile: its lanes' banks differ
-                float m = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    lds128(tile + half * kHalfTile + (((k ^ (half << 2)) ^ (r & 7)) << 4), v[k]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (!valid) v[k][i] = 0;
-                        m = fmaxf(m, fabsf(__uint_as_float(v[k][i])));
-                    }
-                }
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));   // every lane has read its row
-                const int ex = max(static_cast<int>(top >> 23), 14);                       // 2^(ex-127) <= top < 2^(ex-126)
-                const float sc = __int_as_float((267 - ex) << 23);                         // top * sc in [2^13, 2^14)
-                if (lane == 0) sm.exps[g % RING][tensor][group] = top == 0 ? kNoValue : ex - 140;
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        split_half2_2(mul2(as_float2(v[2 * k + i / 2][i % 2 * 2], v[2 * k + i / 2][i % 2 * 2 + 1]), both(sc)), hi[i],
-                                      lo[i]);
-                    const uint32_t o = static_cast<uint32_t>(((4 * half + (k ^ (half << 1))) ^ (r & 7)) << 4);
-                    sts128(tile + o, hi);
-                    sts128(tile + o + kHalfTile, lo);
-                }
+            for (int unit = 0; unit < 4; ++unit) {
+                const int tensor = unit < 2 ? 1 : 0, group = 2 * own + (unit & 1);
+                convert_tokens(sm.stage[s][tensor][0], group, nc, &sm.exps[g % RING][tensor][group]);
             }
             fence_proxy_async_smem();
-            arrive(&sm.ready[s]);
+            arrive(&sm.ready_ab[s]);
         }
     }
 
