@@ -87,12 +87,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
 #define SRWM_R32(c, r)                                                                                                 \
     SRWM_R16(c, r), c(r[16]), c(r[17]), c(r[18]), c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), \
         c(r[26]), c(r[27]), c(r[28]), c(r[29]), c(r[30]), c(r[31])
+#define SRWM_R8(c, r) c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7])
+#define SRWM_L8 "{%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
 #define SRWM_L16 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
 #define SRWM_L32                                                                                                       \
     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "   \
     "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
 
-// 16 or 32 columns of the warp's 32 lanes, one lane per thread.
+// 8, 16 or 32 columns of the warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 " SRWM_L8 : SRWM_R8("=r", r) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " SRWM_L16 : SRWM_R16("=r", r) : "r"(addr) : "memory");
@@ -101,11 +107,19 @@ __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
 }
-// 32 columns of the warp's first 16 lanes, as four 16 x 8 accumulator
+// 16 or 32 columns of the warp's first 16 lanes, as two or four 16 x 8 accumulator
 // fragments: thread l holds (l / 4, 2 (l % 4)), the next column, and both eight lanes below.
+__device__ __forceinline__ void tmem_frag16(uint32_t addr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 " SRWM_L8 : SRWM_R8("=r", r) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_frag32(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 " SRWM_L16 : SRWM_R16("=r", r) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R8("+r", r)::"memory");
 }
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
 {

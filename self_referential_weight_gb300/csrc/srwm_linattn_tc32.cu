@@ -55,44 +55,21 @@ struct __align__(1024) Smem32 {
     uint8_t state[2][D * D * 2];              // X's copy: high | low
     float decay[8][64];
     int exps[RING][3][8];                     // of a, b, c, per 16 tokens
+    int norm[RING][5];                        // the exponents that normalise four strips' scores, and the terms
     int state_exp[RING];
+    int valid[RING], total;                   // valid tokens of a chunk; chunks of this CTA
     float top[2][4];                          // largest |X| of each state warp's rows at an item's start
     uint64_t full[STAGES], empty[STAGES];
-    uint64_t ready_ab[STAGES], ready_c[STAGES];   // the tiles are pairs
+    uint64_t ready_ab[STAGES], ready_c[STAGES], norm_full[STAGES];   // the tiles are pairs, and norm is there
     uint64_t terms_full[2], terms_free[2];
     uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], top_full;
     uint32_t tmem_base;
     int abort;
 };
 
-// The exponent that normalises the scores of rows r0 .. r0 + 31: of the largest
-// alpha_u 2^(eb + ec) g^gap among the column groups on the causal side.
-__device__ __forceinline__ int score_exp(const int (&e)[3][8], int ue, float lg, int r0, bool rev)
-{
-    float top = -8000.f;
-#pragma unroll 1
-    for (int c = rev ? r0 / 16 : 0; c <= (rev ? 7 : r0 / 16 + 1); ++c) {
-        const int gap = max(0, rev ? 16 * c - r0 - 31 : r0 - 16 * c - 15);
-        top = fmaxf(top, fmaf(lg, static_cast<float>(gap), static_cast<float>(e[1][c] + e[2][c] + ue)));
-    }
-    return static_cast<int>(ceilf(top));
-}
-
-// The exponent that normalises the weighted b's terms: of the largest 2^(eb + ec) g^(tokens to the chunk's end).
-__device__ __forceinline__ int term_exp(const int (&e)[3][8], float lg, int nc, bool rev)
-{
-    float top = -8000.f;
-#pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-        const int gap = rev ? 16 * c + 1 : max(0, nc - 16 * c - 16);
-        top = fmaxf(top, fmaf(lg, static_cast<float>(gap), static_cast<float>(e[1][c] + e[2][c])));
-    }
-    return static_cast<int>(ceilf(top));
-}
-
 // Sixteen tokens of a landed fp32 tile into pairs, in place, two lanes per
 // token; tokens at and past nc become zeros.
-__device__ __noinline__ void convert_tokens(uint8_t* tiles, int group, int nc, int* exponent)
+__device__ __forceinline__ void convert_tokens(uint8_t* tiles, int group, int nc, int* exponent)
 {
     const int lane = threadIdx.x & 31, half = lane & 1, r = 16 * group + (lane >> 1);
     const uint32_t tile = smem_u32(tiles) + 128 * r;
@@ -141,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             mbar_init(&sm.empty[s], 2);
             mbar_init(&sm.ready_ab[s], 4);
             mbar_init(&sm.ready_c[s], 4);
+            mbar_init(&sm.norm_full[s], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.terms_full[i], 4);
@@ -157,6 +135,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
         mbar_init(&sm.top_full, 4);
         sm.abort = 0;
         fence_mbar_init();
+    }
+    if (warp == kLoadWarp) {
+        int total = 0;
+        for (int item = blockIdx.x + gridDim.x * lane; item < p.items; item += 32 * gridDim.x) {
+            const int n = p.lin.lengths ? min(max(p.lin.lengths[item / p.roles / p.lin.H], 0), p.lin.T) : p.lin.T;
+            total += (n + C - 1) / C;
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        if (lane == 0) sm.total = total;
     }
     if (warp == kStateMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
@@ -191,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 const int s = g % STAGES;
                 if (!wait(&sm.empty[s], g / STAGES + 1)) break;
                 const Tc32Maps& m = p.map[w.role];
+                sm.valid[g % RING] = w.valid();
                 mbar_arrive_expect_tx(&sm.full[s], 6 * kHalfTile);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -324,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
             const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
-                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1) && wait(&sm.ready_c[g % STAGES], g / STAGES))) break;
+                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1) && wait(&sm.norm_full[g % STAGES], g / STAGES))) break;
                 fence_after();
                 const int(&e)[3][8] = sm.exps[g % RING];
-                const int ef = score_exp(e, R.alpha_u_exp, lg, 32 * own, w.rev) - R.alpha_u_exp + 20;
+                const int ef = sm.norm[g % RING][own] + 20;
                 const uint32_t P = tmem + quad + kP + C * (g & 1);
                 for (int cb = set; cb < 4; cb += 2)   // the side that is masked
                     if (cb < c0 || cb > c1) {
@@ -367,7 +355,29 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 const int s = g % STAGES, nc = w.valid();
                 if (!(ok = wait(&sm.ready_ab[s], g / STAGES) && wait(&sm.ready_c[s], g / STAGES))) break;
                 const int(&e)[3][8] = sm.exps[g % RING];
-                const int eu = term_exp(e, lg, nc, w.rev);
+                // The largest 2^(eb + ec) g^gap among the column groups on the causal side of 32 rows, and among all
+                // with their distance to the chunk's end: what the scores and the terms are relative to.
+                int eu;
+                {
+                    const int c = lane & 7, r0 = 32 * own;
+                    const float ec = static_cast<float>(e[1][c] + e[2][c]);
+                    const int gap = w.rev ? 16 * c - r0 - 31 : r0 - 16 * c - 15;
+                    const int end = w.rev ? 16 * c + 1 : max(0, nc - 16 * c - 16);
+                    const bool causal = w.rev ? 16 * c >= r0 : 16 * c < r0 + 32;
+                    float top = causal ? fmaf(lg, static_cast<float>(max(0, gap)), ec) : -8000.f;
+                    float last = fmaf(lg, static_cast<float>(end), ec);
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        last = fmaxf(last, __shfl_xor_sync(0xffffffffu, last, o));
+                    }
+                    eu = static_cast<int>(ceilf(fmaxf(last, -8000.f)));
+                    if (lane == 0) {
+                        sm.norm[g % RING][own] = static_cast<int>(ceilf(fmaxf(top, -8000.f)));
+                        if (own == 0) sm.norm[g % RING][4] = eu;
+                    }
+                    arrive(&sm.norm_full[s]);
+                }
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     const int j = 32 * q + lane;
@@ -444,20 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 const int nc = w.valid();
                 if (!(ok = wait(&sm.u_full, g))) break;
                 fence_after();
-                const int eu = term_exp(sm.exps[g % RING], lg, nc, w.rev) + R.alpha_u_exp;
+                const int eu = sm.norm[g % RING][4] + R.alpha_u_exp;
                 // X = g^nc X + alpha_u U 2^eu, in two factors that stay inside fp32's range
                 const float f1 = pow2i(eu / 2), f2 = R.alpha_u_man * pow2i(eu - eu / 2);
                 const Decay dec = nc == C ? full : decay_over(lg, nc);
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t u[16];
-                    tmem_frag32(tmem + quad + kU + 32 * part, u);
+                for (int part = 0; part < 4; ++part) {
+                    uint32_t u[8];
+                    tmem_frag16(tmem + quad + kU + 16 * part, u);
                     tmem_wait(u);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            float2& x = X[4 * part + t][k];
+                            float2& x = X[2 * part + t][k];
                             x = fma2(mul2(as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1]), both(f1)), both(f2),
                                      fma2(x, both(dec.m), mul2(x, both(dec.c))));
                         }
@@ -482,45 +492,41 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
         // ---- the outputs, one row per thread, written from registers; and the next chunk's c into pairs before
         // this one's outputs are there
         const int own = warp - kOutWarp, i = 32 * own + lane;
-        Walk<Tc32Params> w(p), next(p);
+        Walk<Tc32Params> w(p);
         auto convert = [&](uint32_t at) {
-            const int s = at % STAGES, nc = next.valid();
+            const int s = at % STAGES;
             if (!wait(&sm.full[s], at / STAGES)) return false;
 #pragma unroll 1
             for (int group = 2 * own; group < 2 * own + 2; ++group)
-                convert_tokens(sm.stage[s][2][0], group, nc, &sm.exps[at % RING][2][group]);
+                convert_tokens(sm.stage[s][2][0], group, sm.valid[at % RING], &sm.exps[at % RING][2][group]);
             fence_proxy_async_smem();
             arrive(&sm.ready_c[s]);
-            ++next.k;
             return true;
         };
-        bool ok = !next.skip_empty() || convert(0);
+        bool ok = sm.total == 0 || convert(0);
         for (; ok && !w.done(); w.next_item()) {
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
-            float* po = static_cast<float*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
             for (; w.k < w.chunks; ++w.k, ++g) {
-                const int nc = w.valid();
-                if (!(ok = (!next.skip_empty() || convert(g + 1)) && wait(&sm.o_full, g))) break;
+                if (!(ok = (static_cast<int>(g) + 1 == sm.total || convert(g + 1)) && wait(&sm.o_full, g))) break;
                 fence_after();
-                const int(&e)[3][8] = sm.exps[g % RING];
-                const int ea = e[0][i >> 4];
+                const int ea = sm.exps[g % RING][0][i >> 4];
                 // out = alpha_o 2^ea (g^e 2^eX OI + 2^ef OX), each power in two factors that stay inside fp32's range
-                const int ei = ea + sm.state_exp[g % RING], ex = ea + score_exp(e, R.alpha_u_exp, lg, 32 * own, w.rev) + 20;
+                const int ei = ea + sm.state_exp[g % RING], ex = ea + sm.norm[g % RING][own] + R.alpha_u_exp + 20;
                 const float fi = pow2i(ei / 2), fx = pow2i(ex / 2);
-                const float gi = R.alpha_o * pow2i(ei - ei / 2) * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
+                const float gi = R.alpha_o * pow2i(ei - ei / 2) * exp2f(lg * static_cast<float>(w.rev ? max(0, w.valid() - 1 - i) : i + 1));
                 const float gx = R.alpha_o * pow2i(ex - ex / 2);
                 const int t = w.token() + i;
-                float* row = po + static_cast<long long>(t) * R.ldo;
+                float* row = static_cast<float*>(R.out) + (static_cast<long long>(w.b) * p.lin.T + t) * R.ldo + w.h * D;
 #pragma unroll 1
-                for (int part = 0; part < 4; ++part) {
-                    uint32_t oi[16], ox[16];
-                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 16 * part, oi);
-                    tmem_rows(tmem + quad + kOX + 16 * part, ox);
+                for (int part = 0; part < 8; ++part) {
+                    uint32_t oi[8], ox[8];
+                    tmem_rows(tmem + quad + kOI + 64 * (g & 1) + 8 * part, oi);
+                    tmem_rows(tmem + quad + kOX + 8 * part, ox);
                     tmem_wait(oi);
                     tmem_wait(ox);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const float2 v = fma2(mul2(as_float2(oi[2 * k], oi[2 * k + 1]), both(fi)), both(gi),
                                               mul2(mul2(as_float2(ox[2 * k], ox[2 * k + 1]), both(fx)), both(gx)));
                         oi[2 * k] = __float_as_uint(v.x);
@@ -528,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     }
                     if (t < p.lin.T) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4*>(row + 16 * part + 4 * k) =
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<uint4*>(row + 8 * part + 4 * k) =
                                 make_uint4(oi[4 * k], oi[4 * k + 1], oi[4 * k + 2], oi[4 * k + 3]);
                     }
                 }
@@ -537,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 arrive(&sm.o_free[g & 1]);
             }
             // tokens past the last chunk
+            float* po = static_cast<float*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
             const long long z0 = static_cast<long long>(w.chunks) * C, pieces = (p.lin.T - z0) * (D / 4);
             for (long long q = threadIdx.x - 32 * kOutWarp; q < pieces; q += 128)
                 *reinterpret_cast<uint4*>(po + (z0 + q / (D / 4)) * R.ldo + q % (D / 4) * 4) = make_uint4(0, 0, 0, 0);
