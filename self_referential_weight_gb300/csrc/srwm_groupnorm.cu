@@ -31,6 +31,7 @@
 #include "srwm.h"
 #include "srwm_check.h"
 #include "srwm_elem.cuh"
+#include "srwm_f2.cuh"
 #include "srwm_groupnorm.h"
 #include "srwm_mma.cuh"
 #include "srwm_ptx.cuh"
@@ -117,6 +118,20 @@ __device__ __forceinline__ float act(float z)
     if constexpr (ACT == SRWM_ACT_SILU) return z * sigmoid(z);
     if constexpr (ACT == SRWM_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
     return z;
+}
+
+// Two activations at once.
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 z)
+{
+    if constexpr (ACT == SRWM_ACT_SILU) {
+        float2 e = mul2(both(-1.4426950408889634f), z);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+        e = add2(both(1.f), e);
+        return mul2(z, make_float2(rcp_approx(e.x), rcp_approx(e.y)));
+    }
+    return make_float2(act<ACT>(z.x), act<ACT>(z.y));
 }
 
 // Slope of the activation at z = (x - mean) rstd g + b.
@@ -220,22 +235,27 @@ __global__ void __launch_bounds__(kRowThreads, 3) gn_rows_kernel(const GnParams 
             unpack(on && row < p.N ? load_vec<E>(p.x, static_cast<size_t>(row) * p.C + c) : make_uint4(0, 0, 0, 0), x[u],
                    E{});
         }
+        auto pair = [&x](int u, int k) { return make_float2(x[u][k], x[u][k + 1]); };
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            sum[u] = 0.f;
+            float2 s = pair(u, 0);
 #pragma unroll
-            for (int k = 0; k < V; ++k) sum[u] += x[u][k];
+            for (int k = 2; k < V; k += 2) s = add2(s, pair(u, k));
+            sum[u] = s.x + s.y;
         }
         lanes_sum(sum, rt.lanes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             sum[u] *= inv;
-            sq[u] = 0.f;
+            float2 q = both(0.f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                x[u][k] -= sum[u];
-                sq[u] = fmaf(x[u][k], x[u][k], sq[u]);
+            for (int k = 0; k < V; k += 2) {
+                const float2 d = add2(pair(u, k), both(-sum[u]));
+                q = fma2(d, d, q);
+                x[u][k] = d.x;
+                x[u][k + 1] = d.y;
             }
+            sq[u] = q.x + q.y;
         }
         lanes_sum(sq, rt.lanes);
 #pragma unroll
@@ -244,7 +264,12 @@ __global__ void __launch_bounds__(kRowThreads, 3) gn_rows_kernel(const GnParams 
             const float rstd = rsqrtf(fmaf(sq[u], inv, p.eps));
             if (on && row < p.N) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) x[u][k] = act<ACT>(fmaf(x[u][k] * rstd, ch.gamma[k], ch.beta[k]));
+                for (int k = 0; k < V; k += 2) {
+                    const float2 y = act2<ACT>(fma2(mul2(pair(u, k), both(rstd)), make_float2(ch.gamma[k], ch.gamma[k + 1]),
+                                                    make_float2(ch.beta[k], ch.beta[k + 1])));
+                    x[u][k] = y.x;
+                    x[u][k + 1] = y.y;
+                }
                 store_vec<E>(p.y, static_cast<size_t>(row) * p.C + c, pack(x[u], E{}));
                 if ((threadIdx.x & (rt.lanes - 1)) == 0) {
                     const size_t g = static_cast<size_t>(row) * p.G + group;
@@ -587,7 +612,12 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
                 float x[V];
                 unpack(sx[threadIdx.x + i * stride], x, E{});
 #pragma unroll
-                for (int k = 0; k < V; ++k) x[k] = act<ACT>(fmaf(x[k] - mean[k], rstd[k], ch.beta[k]));
+                for (int k = 0; k < V; k += 2) {
+                    const float2 d = add2(make_float2(x[k], x[k + 1]), make_float2(-mean[k], -mean[k + 1]));
+                    const float2 y = act2<ACT>(fma2(d, make_float2(rstd[k], rstd[k + 1]), make_float2(ch.beta[k], ch.beta[k + 1])));
+                    x[k] = y.x;
+                    x[k + 1] = y.y;
+                }
                 store_vec<E>(p.y, at0 + static_cast<size_t>(i) * slots * p.C, pack(x, E{}));
             }
         } else {
