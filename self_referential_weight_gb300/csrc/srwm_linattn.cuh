@@ -202,8 +202,8 @@ __device__ __forceinline__ int convert_group(uint32_t group)
         for (int q = 0; q < L::kPieces; ++q) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 f = pair_to_f(v[q][k], E{});
-                v[q][k] = pack_half2(f.x * sc, f.y * sc);
+                const float2 f = mul2(pair_to_f(v[q][k], E{}), both(sc));
+                v[q][k] = pack_half2(f.x, f.y);
             }
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at[q]), "r"(v[q][0]), "r"(v[q][1]),
                          "r"(v[q][2]), "r"(v[q][3])
@@ -390,7 +390,7 @@ __device__ __forceinline__ void state_warp(const LinWork<E, D, STATE_ONLY>& W, i
                     v.x += lo.x;
                     v.y += lo.y;
                 }
-                split_half2(v.x * wt[2 * (k >> 1)], v.y * wt[2 * (k >> 1) + 1], bh[k], bl[k]);
+                split_half2_2(mul2(v, make_float2(wt[2 * (k >> 1)], wt[2 * (k >> 1) + 1])), bh[k], bl[k]);
             }
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
