@@ -928,22 +928,28 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
         g.scratch = grad ? static_cast<size_t>(g.partials) * 2 * C : 0;
         return g;
     }
-    // The slab: as few CTAs per sample as hold it well; more of them, then fewer
-    // channels each (at least 64 bytes of a position), while a CTA holds too
-    // much or the GPU is not filled.
+    // The slab: as few CTAs per sample as hold it well; more of them, or fewer
+    // channels each, while a CTA holds too much or the GPU is not filled.  Large
+    // inputs are split by positions first, and by channels only down to 64 bytes
+    // of a position (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7
+    // by channels; 208 x 1764 x 64 in fp32 forward: 41 and 55): a cluster's
+    // exchange costs a small call more than short pieces of memory do.
     SlabPlan s{};
     s.cluster = 1;
     s.groups = G;
     const long long copies = grad ? 2 : 1;
+    const bool small = copies * N * L * C * e < (48 << 20);
     auto bytes = [&] { return copies * ((L + s.cluster - 1) / s.cluster) * s.groups * width * e; };
     auto can_halve = [&] {
-        return s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0 && (s.groups / 2 * width * e) >= 64;
+        return s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0 && s.groups / 2 * width * e >= (small ? 32 : 64);
     };
     while (s.groups * width / V > 256 && s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0) s.groups /= 2;
     for (;;) {
         const bool full = N * s.cluster * (G / s.groups) >= 2 * kSms;
         if (bytes() <= kSlabGood && (full || bytes() <= 8192)) break;
-        if (s.cluster < kMaxCluster && L >= 2 * s.cluster)
+        if (small && can_halve())
+            s.groups /= 2;
+        else if (s.cluster < kMaxCluster && L >= 2 * s.cluster)
             s.cluster *= 2;
         else if (can_halve())
             s.groups /= 2;
