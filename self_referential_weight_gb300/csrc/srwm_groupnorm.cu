@@ -9,8 +9,8 @@
 // Everything here is bound by memory: x (and dy) is to be read once and y (dx)
 // written once.  What differs with the shape is where a group's values wait for
 // their statistics, so there are four ways (gn_plan):
-//   rows   L = 1 and a group of a power of two of 16-byte vectors, up to a
-//          warp's 32: one vector per thread in registers, statistics by shuffles.
+//   rows   L = 1 and a group of up to 32 whole 16-byte vectors: one vector per
+//          thread in registers, statistics by shuffles.
 //   line   L = 1 otherwise: one warp per group, its values re-read from L1.
 //   slab   a cluster of up to 8 CTAs holds a sample (or some of its groups) in
 //          shared memory, a range of positions each; statistics are exchanged
@@ -203,16 +203,18 @@ struct Channels {   // per-channel values of a thread's vector
 // Block of kRowThreads: `slots` rows of `tile` vectors.  A thread's rows are
 // `slots` * gridDim.x apart; U of them are in flight at once.
 struct RowTile {
-    int tile, slots, lanes;   // lanes: of one group
+    int tile, slots, lanes, vecs;   // lanes of one group, and the vectors that they hold (idle lanes fill up to a power of two)
 };
 template <typename E>
 __host__ __device__ RowTile row_tile(int C, int G)
 {
-    const int cv = C / vec<E>;
     RowTile t;
+    t.vecs = C / G / vec<E>;
+    t.lanes = 1;
+    while (t.lanes < t.vecs) t.lanes *= 2;
+    const int cv = G * t.lanes;
     t.tile = cv < kRowThreads ? cv : kRowThreads;
     t.slots = kRowThreads / t.tile;
-    t.lanes = C / G / vec<E>;
     return t;
 }
 
@@ -221,11 +223,11 @@ __global__ void __launch_bounds__(kRowThreads, 3) gn_rows_kernel(const GnParams 
 {
     constexpr int V = vec<E>;
     const RowTile rt = row_tile<E>(p.C, p.G);
-    const int slot = threadIdx.x / rt.tile, c = (blockIdx.y * kRowThreads + threadIdx.x % rt.tile) * V;
-    const bool on = slot < rt.slots && c < p.C;
+    const int slot = threadIdx.x / rt.tile, v = blockIdx.y * kRowThreads + threadIdx.x % rt.tile;
+    const int group = v / rt.lanes, c = (group * rt.vecs + v % rt.lanes) * V;
+    const bool on = slot < rt.slots && group < p.G && v % rt.lanes < rt.vecs;
     const Channels<V> ch(p, on ? c : 0);
-    const float inv = 1.f / static_cast<float>(rt.lanes * V);
-    const int group = c / (rt.lanes * V);
+    const float inv = 1.f / static_cast<float>(rt.vecs * V);
     const long long step = static_cast<long long>(gridDim.x) * rt.slots;
     for (long long base = static_cast<long long>(blockIdx.x) * rt.slots; base < p.N; base += step * U) {
         float x[U][V], sum[U], sq[U];
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) gn_rows_kernel(const GnParams 
                 x[u][k] = d.x;
                 x[u][k + 1] = d.y;
             }
-            sq[u] = q.x + q.y;
+            sq[u] = on ? q.x + q.y : 0.f;   // the lanes that fill a group up hold no values
         }
         lanes_sum(sq, rt.lanes);
 #pragma unroll
@@ -310,11 +312,12 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(E) == 4 ? 3 : 2) gn_rows_g
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
     const RowTile rt = row_tile<E>(p.C, p.G);
-    const int slot = threadIdx.x / rt.tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % rt.tile * V;
-    const bool on = slot < rt.slots && c < p.C;
+    const int slot = threadIdx.x / rt.tile, v = blockIdx.y * kRowThreads + threadIdx.x % rt.tile;
+    const int group = v / rt.lanes, c = (group * rt.vecs + v % rt.lanes) * V;
+    const int c0 = blockIdx.y * (kRowThreads / rt.lanes) * rt.vecs * V;   // the block's first channel
+    const bool on = slot < rt.slots && group < p.G && v % rt.lanes < rt.vecs;
     const Channels<V> ch(p, on ? c : 0);
-    const float inv = 1.f / static_cast<float>(rt.lanes * V);
-    const int group = c / (rt.lanes * V);
+    const float inv = 1.f / static_cast<float>(rt.vecs * V);
     const long long step = static_cast<long long>(gridDim.x) * rt.slots;
     float A[V], B[V];
 #pragma unroll
@@ -363,7 +366,8 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(E) == 4 ? 3 : 2) gn_rows_g
             }
         }
     }
-    if (p.dgamma || p.dbeta) write_partial<V>(p, s_part, A, B, slot, rt.slots, rt.tile, c, c0, on, blockIdx.x);
+    if (p.dgamma || p.dbeta)
+        write_partial<V>(p, s_part, A, B, slot, rt.slots, rt.tile / rt.lanes * rt.vecs, c, c0, on, blockIdx.x);
 }
 
 // dbeta, dgamma: the partials' sums over their index, in a fixed order.  Eight
@@ -526,8 +530,7 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
         if ((per & (per - 1)) == 0 && per <= 32) {
             for (int i = lane / per; i < slots; i += 32 / per) s += s_part[i * units + g * per + (lane & (per - 1))];
         } else {
-            for (int i = 0; i < slots; ++i)
-                for (int c = lane; c < per; c += 32) s += s_part[i * units + g * per + c];
+            for (int i = lane; i < slots * per; i += 32) s += s_part[i / per * units + g * per + i % per];
         }
         return warp_sum(s);
     };
@@ -811,30 +814,38 @@ __global__ void __launch_bounds__(kRowThreads) gn_split_kernel(const GnParams p,
     }
 }
 
-// One CTA per sample and group: its ranges' and channels' values together.
+// One CTA per sample and group: its ranges' and channels' values together.  A
+// thread keeps one channel (or steps over channels where the group is wider
+// than the block), so that its loads of several ranges are in flight at once.
+constexpr int kMergeThreads = 1024;
+
 template <bool GRAD>
-__global__ void __launch_bounds__(128) gn_merge_kernel(const GnParams p, const SplitPlan sp)
+__global__ void __launch_bounds__(kMergeThreads) gn_merge_kernel(const GnParams p, const SplitPlan sp)
 {
-    __shared__ float s0[128], s1[128], s2[128];
+    __shared__ float s0[kMergeThreads], s1[kMergeThreads], s2[kMergeThreads];
     const long long n = blockIdx.x / p.G;
     const int g = blockIdx.x % p.G, width = p.C / p.G, t = threadIdx.x;
+    const int across = min(width, kMergeThreads), deep = kMergeThreads / across;   // channels, ranges at a time
     const float* in = p.part + static_cast<size_t>(n) * sp.ranges * 2 * p.C + g * width;
-    const long long items = static_cast<long long>(sp.ranges) * width;
     Stat s{0.f, 0.f, 0.f};
-    for (long long i = t; i < items; i += 128) {
-        const long long range = i / width;
-        const int c = static_cast<int>(i % width);
-        const float u = in[range * 2 * p.C + c], w = in[range * 2 * p.C + p.C + c];
-        if constexpr (GRAD) {
-            const float ga = p.gamma ? p.gamma[g * width + c] : 1.f;
-            s.mean = fmaf(ga, u, s.mean);
-            s.m2 = fmaf(ga, w, s.m2);
-        } else {
-            s = merge(s, Stat{static_cast<float>(min(static_cast<long long>(sp.rows), p.L - range * sp.rows)), u, w});
+    if (t < across * deep)
+        for (int c = t % across; c < width; c += across) {
+            const float ga = GRAD && p.gamma ? p.gamma[g * width + c] : 1.f;
+#pragma unroll 4
+            for (int range = t / across; range < sp.ranges; range += deep) {
+                const float* at = in + static_cast<size_t>(range) * 2 * p.C + c;
+                const float u = at[0], w = at[p.C];
+                if constexpr (GRAD) {
+                    s.mean = fmaf(ga, u, s.mean);
+                    s.m2 = fmaf(ga, w, s.m2);
+                } else {
+                    const long long rows = min(static_cast<long long>(sp.rows), p.L - static_cast<long long>(range) * sp.rows);
+                    s = merge(s, Stat{static_cast<float>(rows), u, w});
+                }
+            }
         }
-    }
     s0[t] = s.n, s1[t] = s.mean, s2[t] = s.m2;
-    for (int o = 64; o > 0; o >>= 1) {
+    for (int o = kMergeThreads / 2; o > 0; o >>= 1) {
         __syncthreads();
         if (t < o) {
             if constexpr (GRAD) {
@@ -910,10 +921,11 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     GnPlan g{};
     const int V = 16 / e, cv = C / V, width = C / G;
     g.grid_y = (cv + kRowThreads - 1) / kRowThreads;
-    const int lanes = width / V;
-    if (L == 1 && width % V == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0) {
+    if (L == 1 && width % V == 0 && width / V <= 32) {
         g.way = kRows;
-        const int tile = std::min(cv, kRowThreads), slots = kRowThreads / tile;
+        const RowTile rt = e == 4 ? row_tile<float>(C, G) : row_tile<__half>(C, G);
+        const int slots = rt.slots;
+        g.grid_y = (G * rt.lanes + kRowThreads - 1) / kRowThreads;
         const long long blocks = (N + slots - 1) / slots;
         // what the GPU holds at once: a block keeps its channels' gamma, beta and sums over its rows
         g.grid_x = static_cast<int>(std::max(1LL, std::min(blocks, static_cast<long long>(kSms) * (grad && e == 2 ? 2 : 3))));
@@ -930,8 +942,8 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     }
     // The slab: as few CTAs per sample as hold it well; more of them, or fewer
     // channels each, while a CTA holds too much or the GPU is not filled.  Large
-    // inputs are split by positions first, and by channels only down to 64 bytes
-    // of a position (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7
+    // inputs are split by channels down to 256 bytes of a position, then by
+    // positions, then by channels down to 64 bytes, small ones by channels first (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7
     // by channels; 208 x 1764 x 64 in fp32 forward: 41 and 55): a cluster's
     // exchange costs a small call more than short pieces of memory do.
     SlabPlan s{};
@@ -940,18 +952,18 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     const long long copies = grad ? 2 : 1;
     const bool small = copies * N * L * C * e < (48 << 20);
     auto bytes = [&] { return copies * ((L + s.cluster - 1) / s.cluster) * s.groups * width * e; };
-    auto can_halve = [&] {
-        return s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0 && s.groups / 2 * width * e >= (small ? 32 : 64);
+    auto can_halve = [&](int least) {   // to pieces of at least so many bytes of a position
+        return s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0 && s.groups / 2 * width * e >= least;
     };
     while (s.groups * width / V > 256 && s.groups % 2 == 0 && (s.groups / 2 * width) % V == 0) s.groups /= 2;
     for (;;) {
         const bool full = N * s.cluster * (G / s.groups) >= 2 * kSms;
         if (bytes() <= kSlabGood && (full || bytes() <= 8192)) break;
-        if (small && can_halve())
+        if (can_halve(small ? 32 : 256))
             s.groups /= 2;
         else if (s.cluster < kMaxCluster && L >= 2 * s.cluster)
             s.cluster *= 2;
-        else if (can_halve())
+        else if (can_halve(64))
             s.groups /= 2;
         else
             break;
@@ -960,7 +972,8 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     const int tile = s.cblk / V;
     s.rows = static_cast<int>((L + s.cluster - 1) / s.cluster);
     const long long vectors = static_cast<long long>(s.rows) * tile;
-    s.threads = vectors >= 8192 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
+    // fewer threads per sum to exchange; more where one or two CTAs have an SM to themselves
+    s.threads = bytes() > 80 * 1024 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
     while (s.threads < tile) s.threads *= 2;
     if (tile <= 256 && slab_smem(s, e, grad) <= kSmemMost) {
         g.way = kSlab;
@@ -1039,7 +1052,7 @@ int forward(const GnParams& p, cudaStream_t st)
         return launch_slab<E, ACT, false>(p, g, st);
     else {
         gn_split_kernel<E, ACT, false, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
-        gn_merge_kernel<false><<<static_cast<unsigned>(p.N * p.G), 128, 0, st>>>(p, g.split);
+        gn_merge_kernel<false><<<static_cast<unsigned>(p.N * p.G), kMergeThreads, 0, st>>>(p, g.split);
         gn_split_kernel<E, ACT, false, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
     }
     return launched();
@@ -1064,7 +1077,7 @@ int backward(const GnParams& p, cudaStream_t st)
         rc = launch_slab<E, ACT, true>(p, g, st);
     else {
         gn_split_kernel<E, ACT, true, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
-        gn_merge_kernel<true><<<static_cast<unsigned>(p.N * p.G), 128, 0, st>>>(p, g.split);
+        gn_merge_kernel<true><<<static_cast<unsigned>(p.N * p.G), kMergeThreads, 0, st>>>(p, g.split);
         gn_split_kernel<E, ACT, true, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
     }
     if (rc != SRWM_OK) return rc;
