@@ -171,15 +171,26 @@ int launch_step(int d, const void* q, const void* k, const void* v, long long ld
 
 }  // namespace
 
-LinPlan linattn_plan(int B, int T, int H, int d, int roles)
+LinPlan linattn_plan(int dtype, int B, int T, int H, int d, int roles)
 {
     // CTAs that the GPU holds at once, about, at each width
     const long long slots = 152LL * (d == 64 ? 2 : d == 32 ? 4 : 10);
     const long long ctas = static_cast<long long>(B) * H * roles;
     const int chunks = T / d + (T % d != 0);
+    const LinPlan whole{chunks > 0 ? chunks * d : d, 1};
+    // Splitting fills the GPU when there are few streams, for a second pass over two of the three tensors.
     long long segments = ctas * 3 > slots ? 1 : slots / ctas;
-    if (segments > chunks / 8) segments = chunks / 8;   // at least 8 chunks each: the split reads two tensors again
-    if (segments < 2) return {chunks > 0 ? chunks * d : d, 1};
+    if (segments > chunks / 8) segments = chunks / 8;   // at least 8 chunks each
+    if (segments < 2) return whole;
+    if (d == 64 && dtype != SRWM_F16) {
+        // The tcgen05 kernels take an unsplit stream's 128 tokens in 1.45 us (bf16) or 4.9 us (fp32) however few
+        // streams there are; the split takes about 32 or 45 us, and 2.0 or 3.6 us for each stream's 8192 tokens
+        // (bf16, T = 8192: 8 streams 41 us split and 95 whole, 32 streams 85 and 99, 64 streams 161 and 98; fp32:
+        // 58 and 307, 133 and 313, 266 and 316, and 349 and 322 at 96; at T = 1024 whole streams are faster).
+        const bool wide = dtype == SRWM_F32;
+        const double split = (wide ? 45.0 : 32.0) + static_cast<double>(ctas) * T * (wide ? 3.6 : 2.0) / 8192;
+        if (split >= 5.0 + T / 128.0 * (wide ? 4.9 : 1.45)) return whole;
+    }
     const int per = static_cast<int>((chunks + segments - 1) / segments);
     return {per * d, (chunks + per - 1) / per};
 }

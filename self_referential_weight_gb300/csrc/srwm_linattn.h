@@ -54,7 +54,7 @@ struct LinParams {
 struct LinPlan {
     int seg_len, segments;
 };
-LinPlan linattn_plan(int B, int T, int H, int d, int roles);
+LinPlan linattn_plan(int dtype, int B, int T, int H, int d, int roles);
 
 int linattn_launch(int dtype, int d, int roles, int slots, const LinParams& p, cudaStream_t st);
 int linattn_step_launch(int dtype, int d, const void* q, const void* k, const void* v, long long ld,

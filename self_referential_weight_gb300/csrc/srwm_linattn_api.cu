@@ -50,17 +50,21 @@ int check_align(std::initializer_list<const void*> ptrs)
     return SRWM_OK;
 }
 
-// Segment states (none when the axis is not split).
+// Segment states, enough for any type (none when the axis is not split).
 size_t scratch(int B, int T, int H, int d, int roles, int slots)
 {
-    const srwm::LinPlan plan = srwm::linattn_plan(B, T, H, d, roles);
-    if (plan.segments == 1) return 256;
-    return srwm::round256(static_cast<size_t>(slots) * plan.segments * B * H * d * d * 4);
+    size_t most = 256;
+    for (int dtype : {SRWM_F32, SRWM_BF16, SRWM_F16}) {
+        const srwm::LinPlan plan = srwm::linattn_plan(dtype, B, T, H, d, roles);
+        const size_t need = static_cast<size_t>(slots) * plan.segments * B * H * d * d * 4;
+        if (plan.segments > 1 && need > most) most = srwm::round256(need);
+    }
+    return most;
 }
 
-void set_plan(srwm::LinParams& p, int d, int roles, void* workspace)
+void set_plan(srwm::LinParams& p, int dtype, int d, int roles, void* workspace)
 {
-    const srwm::LinPlan plan = srwm::linattn_plan(p.B, p.T, p.H, d, roles);
+    const srwm::LinPlan plan = srwm::linattn_plan(dtype, p.B, p.T, p.H, d, roles);
     p.seg_len = plan.seg_len;
     p.segments = plan.segments;
     p.seg_state = static_cast<float*>(workspace);
@@ -111,7 +115,7 @@ int srwm_linattn_forward(const void* q, const void* k, const void* v, long long 
     p.B = B, p.T = T, p.H = H;
     p.role[0] = {q, k, v, ld, ld, ld, o, static_cast<long long>(H) * d, S_init, S_final, 0, 0, 1.f, 0, scale, 0, 0};
     p.state_role[0] = 0;
-    set_plan(p, d, 1, workspace);
+    set_plan(p, dtype, d, 1, workspace);
     return srwm::linattn_launch(dtype, d, 1, 1, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -179,7 +183,7 @@ int srwm_linattn_backward(const void* q, const void* k, const void* v, long long
     p.role[2] = {v, do_, q, ld, hd, ld, dk, ld_grad, dS_final, nullptr, 1, 1, man, ex - 1, 1.f, 1, 1};
     p.state_role[0] = 0;
     p.state_role[1] = 1;
-    set_plan(p, d, 3, workspace);
+    set_plan(p, dtype, d, 3, workspace);
     return srwm::linattn_launch(dtype, d, 3, 2, p,static_cast<cudaStream_t>(stream));
 }
 
