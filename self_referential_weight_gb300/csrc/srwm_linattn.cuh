@@ -51,10 +51,10 @@ __device__ __forceinline__ float pow2i(int e)
     return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23);
 }
 
-// log2 of the decay per token: <= 0 and finite, so that multiples of it are.
+// log2 of the decay per token: <= 0 and finite, so that multiples of it are; NaN stays NaN.
 __device__ __forceinline__ float decay_log2(float log_decay)
 {
-    return fmaxf(fminf(log_decay, 0.f) * 1.4426950408889634f, -16384.f);
+    return isnan(log_decay) ? log_decay : fmaxf(fminf(log_decay, 0.f) * 1.4426950408889634f, -16384.f);
 }
 
 // g^n as X -> m X + c X: with c = 1 and m = g^n - 1 where g^n is near 1, so

@@ -67,7 +67,7 @@ struct __align__(1024) Smem {
     // may run ahead of a waiter by a chunk, there are two of them, or one for each stage.
     uint64_t full[STAGES], empty[STAGES];
     uint64_t terms_full[2], terms_free[2];  // of a chunk's first and second 64 tokens
-    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], clean[STAGES];
+    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full[2], o_free[2], clean[STAGES];
     uint32_t tmem_base;
     int abort;
 };
@@ -92,13 +92,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             mbar_init(&sm.terms_free[i], 1);
             mbar_init(&sm.p32_full[i], 1);
             mbar_init(&sm.p16_full[i], 8);
+            mbar_init(&sm.o_full[i], 2);   // OX and OI, of which OI may be a chunk ahead
             mbar_init(&sm.o_free[i], 4);
         }
         mbar_init(&sm.u_full, 1);
         mbar_init(&sm.u_free, 4);
         mbar_init(&sm.x_full, 4);
         mbar_init(&sm.x_free, 1);
-        mbar_init(&sm.o_full, 2);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     mma_ts<false>(tmem + kOX, scores, c, id_o);
 #pragma unroll
                     for (int k = 1; k < C / 16; ++k) mma_ts<true>(tmem + kOX, scores + 16 * k, c + 128 * k, id_o);
-                    commit(&sm.o_full);
+                    commit(&sm.o_full[g & 1]);
                     commit(&sm.empty[g % STAGES]);
                 }
                 __syncwarp();
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     for (int k = 1; k < 2 * D / 16; ++k)
                         mma_ss<true>(oi, a + 2 * (k % 4), d_state + 512 * (k < 4) + 128 * (k % 4), id_o);
                     commit(&sm.x_free);
-                    commit(&sm.o_full);
+                    commit(&sm.o_full[g & 1]);
                     commit(&sm.empty[g % STAGES]);
                 }
                 __syncwarp();
@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         }
                     }
                     fence_proxy_async_smem();
+                    if (half == 1) arrive(&sm.clean[s]);   // first: this phase ends before the stage is given up
                     arrive(&sm.terms_full[half]);
                 }
-                if (ok) arrive(&sm.clean[s]);
             }
         }
     } else if (warp < kOutWarp) {
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             for (; w.k < w.chunks; ++w.k, ++g) {
                 const int nc = w.valid();
-                if (!(ok = wait(&sm.o_full, g))) break;
+                if (!(ok = wait(&sm.o_full[g & 1], g >> 1))) break;
                 fence_after();
                 const int i = 32 * own + lane;
                 const float alpha = R.alpha_o, f = alpha * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         for (int k = 0; k < 4; ++k) {
                             const int x = 8 * q + 2 * k;
                             v[k] = pack_bf16(fma2(as_float2(oi[x], oi[x + 1]), both(f), mul2(both(alpha), as_float2(ox[x], ox[x + 1]))));
+                            if (i >= nc) v[k] = 0;   // 0 times what is not finite
                         }
                         sts128(smem_u32(sm.out[own]) + 128 * lane + (((2 * part + q) ^ (lane & 7)) << 4), v);
                     }

@@ -62,7 +62,7 @@ struct __align__(1024) Smem32 {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t ready_ab[STAGES], ready_c[STAGES], norm_full[STAGES];   // the tiles are pairs, and norm is there
     uint64_t terms_full[2], terms_free[2];
-    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full, o_free[2], top_full;
+    uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full[2], o_free[2], top_full;
     uint32_t tmem_base;
     int abort;
 };
@@ -125,13 +125,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             mbar_init(&sm.terms_free[i], 1);
             mbar_init(&sm.p32_full[i], 1);
             mbar_init(&sm.p16_full[i], 8);
+            mbar_init(&sm.o_full[i], 2);   // OX and OI, of which OI may be a chunk ahead
             mbar_init(&sm.o_free[i], 4);
         }
         mbar_init(&sm.u_full, 1);
         mbar_init(&sm.u_free, 4);
         mbar_init(&sm.x_full, 4);
         mbar_init(&sm.x_free, 1);
-        mbar_init(&sm.o_full, 2);
         mbar_init(&sm.top_full, 4);
         sm.abort = 0;
         fence_mbar_init();
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
 #pragma unroll
                     for (int k = 1; k < 3 * 8; ++k)
                         mma_ts<true>(tmem + kOX, scores + 16 * (k % 8) + 8 * (k < 8), c + (k / 8 == 1) * kLow + 128 * (k % 8), id_o);
-                    commit(&sm.o_full);
+                    commit(&sm.o_full[g & 1]);
                     commit(&sm.empty[g % STAGES]);
                 }
                 __syncwarp();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     for (int k = 1; k < 3 * 4; ++k)
                         mma_ss<true>(oi, a + (k < 4) * kLow + 2 * (k % 4), d_state + 512 * (k / 4 == 1) + 128 * (k % 4), id_o);
                     commit(&sm.x_free);
-                    commit(&sm.o_full);
+                    commit(&sm.o_full[g & 1]);
                     commit(&sm.empty[g % STAGES]);
                 }
                 __syncwarp();
@@ -508,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const LinRole& R = p.lin.role[w.role];
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             for (; w.k < w.chunks; ++w.k, ++g) {
-                if (!(ok = (static_cast<int>(g) + 1 == sm.total || convert(g + 1)) && wait(&sm.o_full, g))) break;
+                if (!(ok = (static_cast<int>(g) + 1 == sm.total || convert(g + 1)) && wait(&sm.o_full[g & 1], g >> 1))) break;
                 fence_after();
-                const int ea = sm.exps[g % RING][0][i >> 4];
+                const int ea = sm.exps[g % RING][0][i >> 4], nc = w.valid();
                 // out = alpha_o 2^ea (g^e 2^eX OI + 2^ef OX), each power in two factors that stay inside fp32's range
                 const int ei = ea + sm.state_exp[g % RING], ex = ea + sm.norm[g % RING][own] + R.alpha_u_exp + 20;
                 const float fi = pow2i(ei / 2), fx = pow2i(ex / 2);
-                const float gi = R.alpha_o * pow2i(ei - ei / 2) * exp2f(lg * static_cast<float>(w.rev ? max(0, w.valid() - 1 - i) : i + 1));
+                const float gi = R.alpha_o * pow2i(ei - ei / 2) * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
                 const float gx = R.alpha_o * pow2i(ex - ex / 2);
                 const int t = w.token() + i;
                 float* row = static_cast<float*>(R.out) + (static_cast<long long>(w.b) * p.lin.T + t) * R.ldo + w.h * D;
@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     for (int k = 0; k < 4; ++k) {
                         const float2 v = fma2(mul2(as_float2(oi[2 * k], oi[2 * k + 1]), both(fi)), both(gi),
                                               mul2(mul2(as_float2(ox[2 * k], ox[2 * k + 1]), both(fx)), both(gx)));
-                        oi[2 * k] = __float_as_uint(v.x);
-                        oi[2 * k + 1] = __float_as_uint(v.y);
+                        oi[2 * k] = i < nc ? __float_as_uint(v.x) : 0u;   // not 0 times what is not finite
+                        oi[2 * k + 1] = i < nc ? __float_as_uint(v.y) : 0u;
                     }
                     if (t < p.lin.T) {
 #pragma unroll

@@ -11,6 +11,13 @@ relative to a partial sum, and no partial sum exceeds A):
     2^-23 (the tensor cores truncate): (d + 64 + 2 * chunks) * 2^-23 covers it.
   * pairs are scaled to the largest value among 16 tokens: a floor of 2^-30 of
     the largest A of the stream covers entries far below their neighbours.
+    Where tokens of zeros follow others under a strong decay, A itself falls
+    below that: a term g^i x y is an fp16 pair whose scale is set by its 16
+    tokens' largest values at the nearest of the 16 positions, and at most 31
+    rows away, so its error is up to half the pair's smallest step, 2^-25, of
+    2^14: 2^-39 of max|x| max|y| (times d for a score), whatever g^i is.  At
+    most 2 * 128 of them meet in a chunk's sums and what older chunks left
+    decays no slower than their terms: 2^-31 max|x| max|y| (`floor`).
   * bf16: the score and the state enter their products as one fp16 number,
     2^-11 each, or (d = 64, T >= 128) the score as one bf16, 2^-8 of each term
     and so of A; the output rounds by 2^-8 of itself.  fp16: they enter as
@@ -32,12 +39,12 @@ DEV = "cuda:0"
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 
 
-def assert_near(got, ref, size, d, T, dtype, what):
+def assert_near(got, ref, size, d, T, dtype, what, floor=0.0):
     got = got.double()
     assert torch.isfinite(got).all(), f"{what}: not finite"
     chunks = -(-T // d)
     tol = (32 * 2.0 ** -24 + (d + 64 + 2 * chunks) * 2.0 ** -23) * size + 2.0 ** -30 * size.amax((-1,), keepdim=True)
-    tol = tol + (d + T) * 2.0 ** -149
+    tol = tol + (d + T) * 2.0 ** -149 + floor
     if dtype == BF16:
         score = 2.0 ** -8 if d == 64 and T >= 128 else 2.0 ** -11
         tol = tol + (2.0 ** -11 + score) * size + 2.0 ** -8 * ref.abs()
@@ -380,3 +387,155 @@ def test_binding_refuses():
         with pytest.raises(binding.SrwmError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T", [127, 128, 129, 255, 256, 257, 390])
+def test_lengths_around_wide_chunks(T, dtype):
+    """d = 64 around multiples of 128 tokens, views of packed arrays."""
+    q, k, v, lg, S0, do, dS = make(T, 2, T, 3, 64, dtype, packed=True)
+    check_forward(q, k, v, lg, S0)
+    check_backward(q, k, v, lg, do, S0, None, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_streams_than_the_gpu_holds(dtype):
+    """Several streams for each CTA, their lengths from nothing to T, masked
+    rows NaN."""
+    T, lens = 300, [0, 300, 1, 128, 0, -3, 127, 129, 256, 299, 300, 17, 0, 257, 255, 64]
+    lengths = torch.tensor(lens * 3, dtype=torch.int32, device=DEV)
+    B = len(lengths)
+    q, k, v, lg, S0, do, dS = make(3, B, T, 9, 64, dtype)
+    rows = torch.arange(T, device=DEV) >= lengths[:, None]
+    for x in (q, k, v, do):
+        x[rows] = float("nan")
+    o, _ = check_forward(q, k, v, lg, S0, lengths)
+    assert (o[rows] == 0).all()
+    for x in check_backward(q, k, v, lg, do, S0, lengths, dS)[:3]:
+        assert (x[rows] == 0).all()
+    check_forward(q, k, v, lg, None, lengths)
+    for x in (q, k, v, do):
+        x[rows] = 0
+    o, S = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0)      # all T tokens, zeros among them
+    sc = 64 ** -0.5
+    (ro, rS), (ao, aS) = oracle.forward(q, k, v, lg, sc, S0), oracle.sizes(q, k, v, lg, sc, S0)
+    top = [float(x.abs().max()) for x in (q, k, v, do)]
+    assert_near(o, ro, ao, 64, T, dtype, "o", 2.0 ** -31 * sc * 64 * top[0] * top[1] * top[2])
+    assert_near(S, rS, aS, 64, T, F32, "S_final", 2.0 ** -31 * top[1] * top[2])
+    got = binding.srwm_linattn_backward(q, k, v, lg, do)
+    ref, size = oracle.grads(q, k, v, lg, sc, do), oracle.grad_sizes(q, k, v, lg, sc, do)
+    for name, x, r, a, i in zip(("dq", "dk", "dv"), got, ref, size, range(3)):
+        floor = 2.0 ** -31 * sc * 64 * top[0] * top[1] * top[2] * top[3] / top[i]
+        assert_near(x, r, a, 64, T, dtype, name, floor)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+def test_padding_stays_zero_beside_values_that_are_not_finite(d, dtype):
+    T = 300
+    lengths = torch.tensor([290, 130, 5], dtype=torch.int32, device=DEV)
+    q, k, v, lg, S0, do, dS = make(29 + d, 3, T, 2, d, dtype)
+    for x, t in ((k, 3), (v, 4), (do, 2)):
+        x[:, t, 0, 5] = float("inf")
+        x[:, t, 1, 5] = float("nan")
+    rows = torch.arange(T, device=DEV) >= lengths[:, None]
+    o, S = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0, lengths=lengths)
+    assert (o[rows] == 0).all() and not torch.isfinite(S).flatten(2).all(-1).any()
+    for x in binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, lengths=lengths, dS_final=dS)[:3]:
+        assert (x[rows] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [100, 300])
+def test_not_finite_inputs_stay_in_their_stream_at_width_64(T, dtype):
+    q, k, v, lg, S0, _, _ = make(14, 60, T, 4, 64, dtype)
+    o, S = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0)
+    k[1, T - 10, 2, 5] = float("nan")
+    v[2, 50, 0, 3] = float("inf")
+    o2, S2 = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0)
+    touched = torch.zeros(60, 4, dtype=torch.bool, device=DEV)
+    touched[1, 2] = touched[2, 0] = True
+    assert torch.equal(S[~touched], S2[~touched])
+    assert torch.equal(o.transpose(1, 2)[~touched], o2.transpose(1, 2)[~touched])
+    assert not torch.isfinite(S2[1, 2]).all() and not torch.isfinite(S2[2, 0]).all()
+    before = (T - 10) // 128 * 128 if T >= 128 else (T - 10) // 64 * 64
+    assert torch.equal(o[1, :before, 2], o2[1, :before, 2])
+    assert torch.isnan(o2[1, T - 10:, 2]).any(-1).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [16, 64])
+def test_a_decay_that_is_nan_is_not_hidden(d, dtype):
+    q, k, v, lg, S0, _, _ = make(6, 2, 200, 3, d, dtype)
+    o, S = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0)
+    o1, S1 = binding.srwm_linattn_step(q[:, 0], k[:, 0], v[:, 0], lg, S0)
+    lg[1] = float("nan")
+    o2, S2 = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0)
+    o3, S3 = binding.srwm_linattn_step(q[:, 0], k[:, 0], v[:, 0], lg, S0)
+    for x in (S2, S3, o2.transpose(1, 2), o3):
+        assert torch.isnan(x[:, 1]).all()
+    for x, y in ((S, S2), (S1, S3), (o.transpose(1, 2), o2.transpose(1, 2)), (o1, o3)):
+        assert torch.equal(x[:, ::2], y[:, ::2])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_streams_at_once(dtype):
+    """Calls that run beside one another on two CUDA streams give what each
+    gives alone, and no wait runs out."""
+    sets = [make(s, 60, 400, 4, 64, dtype) for s in (50, 51)]
+    alone = [binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, dS_final=dS) for q, k, v, lg, S0, do, dS in sets]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in sets]
+    both = [[], []]
+    for _ in range(4):
+        for i, (q, k, v, lg, S0, do, dS) in enumerate(sets):
+            with torch.cuda.stream(side[i]):
+                both[i] = binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, dS_final=dS)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert binding.srwm_last_device_status() == 0
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured into a graph."""
+    code = """
+import torch
+from self_referential_weight_gb300 import binding
+q = torch.randn(2, 200, 3, 64, device="cuda")
+lg = torch.full((3,), -0.1, device="cuda")
+x = [t for dt in (torch.float32, torch.bfloat16) for t in (q.to(dt),)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = [binding.srwm_linattn_forward(t, t, t, lg)[0] for t in x]
+g.replay()
+torch.cuda.synchronize()
+want = [binding.srwm_linattn_forward(t, t, t, lg)[0] for t in x]
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+"""
+    import pathlib
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parent.parent, capture_output=True, text=True,
+                       timeout=200)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+def test_repeats_give_the_same_bits(d, dtype):
+    """Ragged batches of more streams than the GPU holds, where the kernels'
+    warps meet in changing orders."""
+    T, lens = 300, [0, 300, 1, 128, 0, 257, 127, 129, 256, 299, 300, 17, 0, 257, 255, 64]
+    lengths = torch.tensor(lens * 5, dtype=torch.int32, device=DEV)
+    q, k, v, lg, S0, do, dS = make(71, len(lengths), T, 9, d, dtype)
+
+    def run():
+        return binding.srwm_linattn_forward(q, k, v, lg, S_init=S0, lengths=lengths) + \
+            binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, lengths=lengths, dS_final=dS)
+
+    first = run()
+    for _ in range(25):
+        assert all(torch.equal(x, y) for x, y in zip(first, run()))
