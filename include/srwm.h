@@ -327,7 +327,7 @@ int srwm_debug_set_layer_gemm(int mode);
  * g = exp(log_decay[h]),
  *   S_t = g S_{t-1} + k_t v_t^T          (S_0 = S_init[b,h], or 0)
  *   o_t = scale * S_t^T q_t
- * for t = 1 .. n_b, n_b the sequence's length.  Computed in chunks of d tokens:
+ * for t = 1 .. n_b, n_b the sequence's length.  Computed in chunks of tokens:
  * inside a chunk as a masked product, from earlier chunks through the state.
  *
  *   q, k, v    [B, T, H, d] of `dtype`; token (b, t) starts at element
@@ -338,7 +338,7 @@ int srwm_debug_set_layer_gemm(int mode);
  *              H * d, a multiple of 16 bytes
  *   log_decay  [H] fp32, log g <= 0; 0 keeps everything (the sum over all
  *              tokens), -infinity keeps the current token alone.  Values above
- *              0 are taken as 0.
+ *              0 are taken as 0; a NaN makes its head's results NaN.
  *   S_init     [B, H, d, d] fp32 (row = index of k, column = index of v), or
  *              NULL for zero
  *   lengths    [B] int32 on the device (4-byte aligned), the valid tokens of
@@ -357,11 +357,23 @@ int srwm_debug_set_layer_gemm(int mode);
  *
  * Supported: d in {16, 32, 64}; T = 0 is valid (q, k, v, o may be NULL then).
  * States are fp32 and every sum is accumulated in fp32.  The products run on
- * the tensor cores in fp16 after scaling by powers of two: fp32 inputs as
- * (high, low) pairs, which keeps about 22 bits relative to the largest
- * magnitude among 16 neighbouring tokens of a head.  Inputs must be finite:
- * an infinity or NaN in a valid token reaches every output of its sequence
- * and head from its chunk on, and of no other.
+ * the tensor cores:
+ *   fp32, fp16  values as (high, low) pairs of fp16 after scaling by powers of
+ *         two (an fp16 input is one of them): about 22 bits relative to the
+ *         largest magnitude among 16 neighbouring tokens of a head, and never
+ *         finer than 2^-39 of what that magnitude would give at the nearest of
+ *         the 16 positions, so that what a strong decay leaves of a token
+ *         followed by zeros may be lost below that.
+ *   bf16  inputs as they are, or as one fp16 scaled in the same way; a score
+ *         enters its product as one bf16 (2^-8 of it) where d = 64 and
+ *         T >= 128, else as one fp16 (2^-11), the state its product with 2^-11
+ *         or better.  S_final is good to fp32.
+ * Inputs must be finite: an infinity or NaN in a valid token reaches every
+ * output of its sequence and head from its chunk on (the tokens from the last
+ * multiple of d before it, or of 128 at d = 64), and of no other; rows past
+ * the length stay zero.
+ * At d = 64 the kernels wait for their own copies with a limit; a call that ran
+ * into it is reported by srwm_last_device_status.
  */
 size_t srwm_linattn_workspace_bytes(int B, int T, int H, int d);
 int srwm_linattn_forward(const void* q, const void* k, const void* v, long long ld, const float* log_decay,
@@ -392,6 +404,8 @@ int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld,
  *   dq_t = scale * S_t do_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t,
  *   dS_init = g D_1 (dS_final for an empty sequence).
  * The decay is a constant of the head: it gets no gradient.
+ * dv and dk run from the last token to the first: a value that is not finite
+ * reaches them from its chunk on towards the first token.
  *
  *   do_        [B, T, H, d] of `dtype`, contiguous: dL/do (not read at and
  *              past a sequence's length)
@@ -459,8 +473,9 @@ const char* srwm_status_string(int status);
 /*
  * srwm_last_device_status -- synchronise `stream`, then read and clear the
  * device status word that kernels set when a bounded wait gives up (a TMA
- * transfer that never arrived).  Returns SRWM_OK, SRWM_ERR_TIMEOUT, or
- * SRWM_ERR_CUDA if the synchronisation itself failed.
+ * transfer, or a product on the tensor cores, that never arrived).  Returns
+ * SRWM_OK, SRWM_ERR_TIMEOUT, or SRWM_ERR_CUDA if the synchronisation itself
+ * failed.
  */
 int srwm_last_device_status(void* stream);
 

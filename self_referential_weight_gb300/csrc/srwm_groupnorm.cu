@@ -943,9 +943,10 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     // The slab: as few CTAs per sample as hold it well; more of them, or fewer
     // channels each, while a CTA holds too much or the GPU is not filled.  Large
     // inputs are split by channels down to 256 bytes of a position, then by
-    // positions, then by channels down to 64 bytes, small ones by channels first (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7
-    // by channels; 208 x 1764 x 64 in fp32 forward: 41 and 55): a cluster's
-    // exchange costs a small call more than short pieces of memory do.
+    // positions, then by channels down to 64 bytes, small ones by channels first
+    // (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7 by channels;
+    // 208 x 1764 x 64 in fp32 forward: 41 and 55): a cluster's exchange costs a
+    // small call more than short pieces of memory do.
     SlabPlan s{};
     s.cluster = 1;
     s.groups = G;

@@ -14,12 +14,17 @@
 // then the column groups below the diagonal, where the decay is a product of a
 // row's, a group's and a column's factor, then the diagonal 16 x 16 block.
 // Blocks above the diagonal are not computed.
-// Per token that is 4 D^2 multiply-adds by the state and about 1.25 D^2 inside
-// the chunk, whatever T is.
+// Per token that is 2 D^2 multiply-adds by the state and about 1.25 D^2 inside
+// the chunk, whatever T is; a warp's share of every matrix is a 16-row strip.
 //
 // The products run on the tensor cores in fp16 (mma.sync), with fp32 sums.
-// Chunk of D tokens: the work per token is about 4 D^2 + 2.5 D^2 multiply-adds
-// whatever T is, and a warp's share of every matrix is a 16-row strip.
+// mma.sync rather than tcgen05.mma at D = 16 and 32, whose strips would fill an
+// eighth or a quarter of a 128-row product; D = 64 comes here where the axis is
+// split, in fp16, and below 128 tokens (srwm_linattn_tc.cu takes the rest).
+// What bounds it is instruction issue: 2048 ragged streams of up to 512 tokens
+// in bf16 at D = 32 (184 MB) take 55 us, 0.49 of the copy rate, with 59 % of
+// the issue slots busy over the whole launch, its uneven end included; 2048
+// streams of 26 tokens in fp32 at D = 16 take 6.9 us, gradients 17.4.
 //
 // Range and precision.  Each group of 16 tokens of a, b and c is scaled by a
 // power of two that puts its largest magnitude into [2^13, 2^14), exactly; all

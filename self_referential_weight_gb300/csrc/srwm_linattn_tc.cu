@@ -20,10 +20,19 @@
 // terms; 12-15 hold X, add U to it and leave its pair in shared memory; 16-19
 // write the outputs; 20 issues the TMA loads (three stages of a, b, c), 21 and 22
 // the products.  Every stage of a chunk's work runs beside other stages of the
-// same or the next chunk: P and X's chain meet only at the output.  Invalid tokens of a ragged chunk are zeroed in shared memory
-// by warps 8-11 before anything reads them; past the tensor's end TMA fills
-// zeros.  Every wait is bounded; a timeout sets the status word and ends the CTA
-// after its copies and products in flight.
+// same or the next chunk: P and X's chain meet only at the output.  Invalid
+// tokens of a ragged chunk are zeroed in shared memory by warps 8-11 before
+// anything reads them; past the tensor's end TMA fills zeros.  Every wait is
+// bounded; a timeout sets the status word and ends the CTA after its copies and
+// products in flight.
+//
+// What bounds it: 512 streams of 1024 tokens (268 MB in and out) take 60.6 us,
+// 4.4 TB/s or 0.67 of the copy rate, their gradients 148 us; the chunked
+// mma.sync kernel (srwm_linattn.cuh) takes 105 and 281 us.  A full chunk takes
+// 1.45 us: the products keep the tensor pipe 43 % busy, and the six kinds of
+// warps' loops share the instruction cache (their fetches at 61 % of its rate),
+// which is why they are rolled and the waits' slow part is out of line.  512
+// streams on 152 SMs also leave the last of four rounds a third full.
 #include <atomic>
 
 #include "srwm_check.h"
@@ -38,7 +47,8 @@ using namespace tc;
 constexpr int STAGES = 3;
 constexpr int kTileBytes = C * D * 2;
 constexpr int kThreads = 736;
-// first warps of the roles after the scores' eight; those that read tensor memory start at multiples of four, whose lanes they own in order
+// First warps of the roles after the scores' eight; those that read tensor memory start at multiples of four, whose
+// lanes they own in order.
 constexpr int kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
               kStateMmaWarp = 22;
 
@@ -63,8 +73,9 @@ struct __align__(1024) Smem {
     uint8_t state[2][D * D * 2];            // X's pair
     uint8_t out[4][32 * D * 2];             // per output warp: 32 rows
     float decay[8][64];                     // per score warp: g^|column - row| of a diagonal block, by their difference
-    // A barrier's next phase never completes before every waiter of this one has passed: where the producer
-    // may run ahead of a waiter by a chunk, there are two of them, or one for each stage.
+    // A barrier's next phase never completes before every waiter of this one has passed, nor does an arrival for
+    // it come before this one completes: where a producer may run a chunk ahead of a waiter or of another
+    // producer, there are two of them, or one for each stage.
     uint64_t full[STAGES], empty[STAGES];
     uint64_t terms_full[2], terms_free[2];  // of a chunk's first and second 64 tokens
     uint64_t u_full, u_free, x_full, x_free, p32_full[2], p16_full[2], o_full[2], o_free[2], clean[STAGES];
@@ -149,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     } else if (warp >= kScoreMmaWarp) {
         // ---- products: one warp issues P and OX, another U and OI, so that neither chain waits behind the other.
         // The whole warp walks the chunks, which keeps the descriptors in uniform registers; an elected lane issues.
-        constexpr uint32_t id_p = idesc(true, C, C, false, false), id_u = idesc(true, D, D, true, true), id_o = idesc(true, C, D, false, true);
+        constexpr uint32_t id_p = idesc(true, C, C, false, false), id_u = idesc(true, D, D, true, true),
+                           id_o = idesc(true, C, D, false, true);
         constexpr uint64_t kStage = 3 * kTileBytes / 16, kTile = kTileBytes / 16;   // descriptor steps
         const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
         bool ok = true, issued = false;
@@ -179,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 ++w.k;
                 if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
                 // the scores are there, and the outputs before have been read
-                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) && (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1)))) break;
+                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) &&
+                                  (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1))))
+                    break;
                 fence_after();
                 const uint32_t scores = tmem + kP + C * (g & 1);
                 if (elect()) {
@@ -278,13 +292,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     const int cb = hb >> 1, x0 = 16 * (hb & 1);
                     uint32_t r[16], hi[8];
                     tmem_rows(P + 16 * hb, r);
-                    const float f = exp2f(lg * static_cast<float>(w.rev ? max(0, 32 * cb - row) : max(0, row - 32 * cb - 31)));
+                    const int beyond = w.rev ? 32 * cb - row : row - 32 * cb - 31;
+                    const float f = exp2f(lg * static_cast<float>(max(0, beyond)));
                     const float* col = (cb == own ? tab - lane : beside) + x0;
                     tmem_wait(r);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        float2 v = mul2(as_float2(r[2 * k], r[2 * k + 1]), mul2(both(f), make_float2(col[2 * k], col[2 * k + 1])));
-                        hi[k] = pack_bf16(v);
+                        const float2 w = mul2(both(f), make_float2(col[2 * k], col[2 * k + 1]));
+                        hi[k] = pack_bf16(mul2(as_float2(r[2 * k], r[2 * k + 1]), w));
                     }
                     tmem_store8(P + 16 * hb, hi);
                 }
@@ -394,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 float2& x = X[4 * part + t][k];
-                                x = fma2(x, both(dec.m), fma2(x, both(dec.c), as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1])));
+                                const float2 add = as_float2(u[4 * t + 2 * k], u[4 * t + 2 * k + 1]);
+                                x = fma2(x, both(dec.m), fma2(x, both(dec.c), add));
                             }
                     }
                     fence_before();
@@ -424,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (!(ok = wait(&sm.o_full[g & 1], g >> 1))) break;
                 fence_after();
                 const int i = 32 * own + lane;
-                const float alpha = R.alpha_o, f = alpha * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
+                const float alpha = R.alpha_o;
+                const float f = alpha * exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));
                 if (lane == 0) bulk_wait_read<0>();   // the rows before have left the staging buffer
                 __syncwarp();
 #pragma unroll 1
@@ -440,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int x = 8 * q + 2 * k;
-                            v[k] = pack_bf16(fma2(as_float2(oi[x], oi[x + 1]), both(f), mul2(both(alpha), as_float2(ox[x], ox[x + 1]))));
+                            v[k] = pack_bf16(fma2(as_float2(oi[x], oi[x + 1]), both(f),
+                                                  mul2(both(alpha), as_float2(ox[x], ox[x + 1]))));
                             if (i >= nc) v[k] = 0;   // 0 times what is not finite
                         }
                         sts128(smem_u32(sm.out[own]) + 128 * lane + (((2 * part + q) ^ (lane & 7)) << 4), v);
@@ -456,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 }
             }
             // tokens past the last chunk
-            __nv_bfloat16* po = static_cast<__nv_bfloat16*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
+            __nv_bfloat16* po =
+                static_cast<__nv_bfloat16*>(R.out) + static_cast<long long>(w.b) * p.lin.T * R.ldo + w.h * D;
             const long long z0 = static_cast<long long>(w.chunks) * C, pieces = (p.lin.T - z0) * (D / 8);
             for (long long q = threadIdx.x - 32 * kOutWarp; q < pieces; q += 128)
                 *reinterpret_cast<uint4*>(po + (z0 + q / (D / 8)) * R.ldo + q % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
@@ -474,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 
 }  // namespace
 
+// fp16 stays with the other kernel: its scores would have to enter as pairs, as in fp32.
 bool linattn_tc_takes(int dtype, int d, const LinParams& p)
 {
     return dtype != SRWM_F16 && d == D && p.segments == 1 && p.T >= C;

@@ -84,17 +84,11 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
 #define SRWM_R16(c, r)                                                                                                 \
     c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]), c(r[10]), c(r[11]),       \
         c(r[12]), c(r[13]), c(r[14]), c(r[15])
-#define SRWM_R32(c, r)                                                                                                 \
-    SRWM_R16(c, r), c(r[16]), c(r[17]), c(r[18]), c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), \
-        c(r[26]), c(r[27]), c(r[28]), c(r[29]), c(r[30]), c(r[31])
 #define SRWM_R8(c, r) c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7])
 #define SRWM_L8 "{%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
 #define SRWM_L16 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-#define SRWM_L32                                                                                                       \
-    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "   \
-    "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
 
-// 8, 16 or 32 columns of the warp's 32 lanes, one lane per thread.
+// 8 or 16 columns of the warp's 32 lanes, one lane per thread.
 __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 " SRWM_L8 : SRWM_R8("=r", r) : "r"(addr) : "memory");
@@ -102,10 +96,6 @@ __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[8])
 __device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " SRWM_L16 : SRWM_R16("=r", r) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_rows(uint32_t addr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " SRWM_L32 : SRWM_R32("=r", r) : "r"(addr) : "memory");
 }
 // 16 or 32 columns of the warp's first 16 lanes, as two or four 16 x 8 accumulator
 // fragments: thread l holds (l / 4, 2 (l % 4)), the next column, and both eight lanes below.
@@ -124,10 +114,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[8])
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R16("+r", r)::"memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : SRWM_R32("+r", r)::"memory");
 }
 // 8 columns of the warp's 32 lanes, one lane per thread.
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8])
@@ -239,8 +225,9 @@ inline int token_map(CUtensorMap* map, const void* base, long long ld, const Lin
     const cuuint64_t e = fp32 ? 4 : 2;
     const cuuint64_t strides[3] = {e * D, static_cast<cuuint64_t>(ld) * e, static_cast<cuuint64_t>(ld) * e * p.T};
     const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / e), 1, static_cast<cuuint32_t>(rows), 1}, one[4] = {1, 1, 1, 1};
-    const CUresult r = enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+    const CUresult r = enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SRWM_OK : SRWM_ERR_CUDA;
 }

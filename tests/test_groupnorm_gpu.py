@@ -283,3 +283,26 @@ def test_linear_attention_with_its_head_norm(dtype):
     for name, a, b in zip(("z", "dq", "dk", "dv", "dgamma", "dbeta"), (z,) + grads[:3] + (dg, db), want):
         off = float((a.double() - b.detach().view_as(a)).norm() / b.detach().norm())
         assert off <= 8 * HALF_STEP[dtype] + 2.0 ** -16, (name, off)
+
+
+@pytest.mark.parametrize("shape", [(700, 1, 128, 4), (101, 441, 64, 16), (5, 1764, 64, 8), (3, 40001, 64, 4), (50, 25, 72, 3)],
+                         ids=str)
+def test_repeats_beside_another_stream_give_the_same_bits(shape):
+    N, L, C, G = shape
+    sets = [make(s, N, L, C, BF16) for s in (3, 4)]
+
+    def run(x, gamma, beta, dy):
+        y, mean, rstd = binding.srwm_groupnorm_forward(x, gamma, beta, G, activation="silu")
+        return (y, mean, rstd) + binding.srwm_groupnorm_backward(x, gamma, beta, G, mean, rstd, dy, activation="silu")
+
+    first = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in sets]
+    for _ in range(10):
+        got = []
+        for s, st in zip(sets, side):
+            with torch.cuda.stream(st):
+                got.append(run(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(first, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
