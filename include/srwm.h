@@ -458,8 +458,8 @@ int srwm_groupnorm_forward(const void* x, const float* gamma, const float* beta,
  *   dx        [N, L, C] of `dtype`, written
  *   dgamma, dbeta  [C] fp32, written (zeros for N = 0): sums over all samples
  *             and positions in a fixed order; or NULL, both or either
- * ReLU's slope is taken at the sign of its argument evaluated in fp64 where
- * fp32 cannot tell it.
+ * ReLU's slope is taken at the sign of its argument, evaluated in pairs of
+ * fp32 where one cannot tell it.
  */
 size_t srwm_groupnorm_backward_workspace_bytes(long long N, long long L, int C, int G);
 int srwm_groupnorm_backward(const void* x, const float* gamma, const float* beta, const float* mean,

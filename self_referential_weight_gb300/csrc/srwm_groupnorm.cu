@@ -134,6 +134,20 @@ __device__ __forceinline__ float2 act2(float2 z)
     return make_float2(act<ACT>(z.x), act<ACT>(z.y));
 }
 
+// (x - mean) rstd g + b in pairs of fp32: each rounding's error is kept as a second number.
+__device__ __noinline__ float border(float x, float mean, float rstd, float g, float b)
+{
+    auto sum = [](float u, float v, float& err) {
+        const float s = __fadd_rn(u, v), w = __fsub_rn(s, u);
+        err = __fadd_rn(__fsub_rn(u, __fsub_rn(s, w)), __fsub_rn(v, w));
+        return s;
+    };
+    float dl, sl;
+    const float d = sum(x, -mean, dl), r = __fmul_rn(rstd, g), rl = __fmaf_rn(rstd, g, -r);
+    const float m = __fmul_rn(d, r), ml = __fmaf_rn(d, r, -m), s = sum(m, b, sl);
+    return __fadd_rn(s, __fadd_rn(sl, __fadd_rn(ml, __fmaf_rn(d, rl, __fmul_rn(dl, r)))));
+}
+
 // Slope of the activation at z = (x - mean) rstd g + b.
 template <int ACT>
 __device__ __forceinline__ float slope(float x, float mean, float rstd, float g, float b, float xh)
@@ -144,13 +158,12 @@ __device__ __forceinline__ float slope(float x, float mean, float rstd, float g,
         return e * fmaf(z, 1.f - e, 1.f);
     }
     if constexpr (ACT == SRWM_ACT_RELU) {
-        const float z = fmaf(xh, g, b);
-        // the side of the border decides a whole term of the gradient: within
-        // fp32's error of it (a few roundings of both terms) it is taken in fp64
-        if (fabsf(z) <= 1e-6f * (fabsf(x * rstd * g) + fabsf(mean * rstd * g) + fabsf(b))) {
-            const double zd = (static_cast<double>(x) - mean) * rstd * g + b;
-            return zd > 0.0 ? 1.f : 0.f;
-        }
+        float z = fmaf(xh, g, b);
+        // the side of the border decides a whole term of the gradient: within fp32's error of it (a few roundings of
+        // both terms) z is taken again from exact differences and products, good to 2^-45 of its terms.  fp64 would
+        // do, but the compiler computes both sides of a condition this short, and fp64 is slow: 31.7M values of
+        // fp16 took 717 us.
+        if (fabsf(z) <= 1e-6f * (fabsf(x * rstd * g) + fabsf(mean * rstd * g) + fabsf(b))) z = border(x, mean, rstd, g, b);
         return z > 0.f ? 1.f : 0.f;
     }
     return 1.f;
@@ -494,7 +507,6 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
     float* s_own = s_stat;                     // [groups][2]: this CTA's, read by the cluster
     float* s_all = s_stat + 2 * sp.groups;     // [groups][2]: the sample's
     const uint32_t ax = smem_u32(sx + threadIdx.x), ad = smem_u32(sd + threadIdx.x);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = sp.threads >> 5;
     const Channels<V> ch(p, c0 + cl);
     int gl[V];   // the local group of each channel
     gl[0] = cl / width;
@@ -525,14 +537,26 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
             for (int k = 0; k < V; ++k) s_part[slot * units + cl + k] = v[k];
         }
     };
-    auto group_sum = [&](int g) {
-        float s = 0.f;
-        if ((per & (per - 1)) == 0 && per <= 32) {
-            for (int i = lane / per; i < slots; i += 32 / per) s += s_part[i * units + g * per + (lane & (per - 1))];
-        } else {
-            for (int i = lane; i < slots * per; i += 32) s += s_part[i / per * units + g * per + i % per];
+    // Sums of each group, by `sub` neighbouring lanes: as many as make the groups fill the block (a warp for each
+    // of 32 groups in turn took 22.6 us for 29 samples of 3 x 96).
+    int sub = 32;
+    while (sub > 1 && sp.groups * sub > sp.threads) sub >>= 1;
+    const int sl = threadIdx.x & (sub - 1);
+    auto each_group = [&](auto&& terms, auto&& done) {
+        for (int g0 = 0; g0 < sp.groups; g0 += sp.threads / sub) {
+            const int g = g0 + static_cast<int>(threadIdx.x) / sub;
+            float v[2] = {0.f, 0.f};
+            if (g < sp.groups) terms(g, v);
+            lanes_sum(v, sub);
+            if (sl == 0 && g < sp.groups) done(g, v);
         }
-        return warp_sum(s);
+    };
+    auto slots_of = [&](int g, float (&v)[2]) {   // the group's units over all slots
+        if ((per & (per - 1)) == 0 && per <= sub) {
+            for (int i = sl / per; i < slots; i += sub / per) v[0] += s_part[i * units + g * per + (sl & (per - 1))];
+        } else {
+            for (int i = sl; i < slots * per; i += sub) v[0] += s_part[i / per * units + g * per + i % per];
+        }
     };
 
     const long long clusters = gridDim.x / sp.cluster;
@@ -566,10 +590,7 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
             }
             put(a);
             __syncthreads();
-            for (int g = warp; g < sp.groups; g += warps) {
-                const float s = group_sum(g);
-                if (lane == 0) s_own[2 * g] = rows > 0 ? s / count : 0.f;
-            }
+            each_group(slots_of, [&](int g, const float (&v)[2]) { s_own[2 * g] = rows > 0 ? v[0] / count : 0.f; });
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < V; ++k) mean[k] = s_own[2 * gl[k]];
@@ -584,10 +605,7 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
             }
             put(b);
             __syncthreads();
-            for (int g = warp; g < sp.groups; g += warps) {
-                const float s = group_sum(g);
-                if (lane == 0) s_own[2 * g + 1] = s;
-            }
+            each_group(slots_of, [&](int g, const float (&v)[2]) { s_own[2 * g + 1] = v[0]; });
             if (sp.cluster > 1) cluster.sync(); else __syncthreads();
             for (int g = threadIdx.x; g < sp.groups; g += sp.threads) {
                 Stat s{0.f, 0.f, 0.f};
@@ -634,7 +652,10 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
                     const float dz = d[k] * slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
                     a[k] += dz;
                     b[k] = fmaf(dz, xh, b[k]);
+                    d[k] = dz;
                 }
+                // dy or 0: kept, so that the second pass does not ask for the slope again
+                if constexpr (ACT == SRWM_ACT_RELU) sd[threadIdx.x + i * stride] = pack(d, E{});
             }
             if (on)
 #pragma unroll
@@ -655,20 +676,18 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
                 s_part2[c] = sb;
             }
             __syncthreads();
-            for (int g = warp; g < sp.groups; g += warps) {
-                float u = 0.f, w = 0.f;
-                for (int i = lane; i < width; i += 32) {
-                    const float ga = p.gamma ? p.gamma[c0 + g * width + i] : 1.f;
-                    u = fmaf(ga, s_part[g * width + i], u);
-                    w = fmaf(ga, s_part2[g * width + i], w);
-                }
-                u = warp_sum(u);
-                w = warp_sum(w);
-                if (lane == 0) {
-                    s_own[2 * g] = u;
-                    s_own[2 * g + 1] = w;
-                }
-            }
+            each_group(
+                [&](int g, float (&v)[2]) {
+                    for (int i = sl; i < width; i += sub) {
+                        const float ga = p.gamma ? p.gamma[c0 + g * width + i] : 1.f;
+                        v[0] = fmaf(ga, s_part[g * width + i], v[0]);
+                        v[1] = fmaf(ga, s_part2[g * width + i], v[1]);
+                    }
+                },
+                [&](int g, const float (&v)[2]) {
+                    s_own[2 * g] = v[0];
+                    s_own[2 * g + 1] = v[1];
+                });
             if (sp.cluster > 1) cluster.sync(); else __syncthreads();
             for (int g = threadIdx.x; g < sp.groups; g += sp.threads) {
                 float u = 0.f, w = 0.f;
@@ -694,7 +713,9 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const float xh = (x[k] - mean[k]) * rstd[k];
-                    const float dz = d[k] * slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
+                    float dz = d[k];
+                    if constexpr (ACT != SRWM_ACT_RELU)
+                        dz *= slope<ACT>(x[k], mean[k], rstd[k], ch.gamma[k], ch.beta[k], xh);
                     x[k] = rstd[k] * (dz * ch.gamma[k] - fmaf(xh, m2[k], m1[k]));
                 }
                 store_vec<E>(p.dx, at0 + static_cast<size_t>(i) * slots * p.C, pack(x, E{}));

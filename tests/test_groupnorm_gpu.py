@@ -306,3 +306,20 @@ def test_repeats_beside_another_stream_give_the_same_bits(shape):
         torch.cuda.synchronize()
         for a, b in zip(first, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_relu_border_over_positions():
+    """As for rows: one position's arguments within a rounding of 0, groups over positions."""
+    N, L, C = 128, 6, 64
+    x, gamma, _, dy = make(15, N, L, C, F32)
+    _, rm, rr = oracle.forward(x, gamma, None, 1, 1e-5, "none")
+    mean, rstd = rm.float(), rr.float()
+    beta = -((x[0, 0] - mean[0]) * rstd[0] * gamma)
+    wide = [v.double()[:, :, None] for v in (mean, rstd)]
+    xh = (x.double() - wide[0]) * wide[1]
+    dx, dg, db = binding.srwm_groupnorm_backward(x, gamma, beta, 1, mean, rstd, dy, activation="relu")
+    dz = dy.double() * (xh * gamma.double() + beta.double() > 0)
+    dh = dz * gamma.double()
+    want = wide[1] * (dh - dh.mean((1, 2), keepdim=True) - xh * (dh * xh).mean((1, 2), keepdim=True))
+    assert ((dx.double() - want).abs() <= 2.0 ** -16 * wide[1] * (1 + want.abs().amax())).all()
+    assert ((db.double() - dz.sum((0, 1))).abs() <= 2.0 ** -14 * dz.abs().sum((0, 1))).all()
