@@ -356,8 +356,9 @@ int srwm_debug_set_layer_gemm(int mode);
  *              others until the work on `stream` ends
  *
  * Supported: d in {16, 32, 64}; T = 0 is valid (q, k, v, o may be NULL then).
- * States are fp32 and every sum is accumulated in fp32.  The products run on
- * the tensor cores:
+ * States are fp32 and every sum is accumulated in fp32.  Short sequences (a few
+ * tens of tokens) run token by token in fp32; the products of longer ones run
+ * on the tensor cores:
  *   fp32, fp16  values as (high, low) pairs of fp16 after scaling by powers of
  *         two (an fp16 input is one of them): about 22 bits relative to the
  *         largest magnitude among 16 neighbouring tokens of a head, and never

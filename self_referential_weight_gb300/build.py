@@ -27,7 +27,7 @@ MODULE_SOURCE = "srwm_torch.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["srwm_api.cu", "srwm_d16.cu", "srwm_d32.cu", "srwm_d64.cu", "srwm_probe.cu", "srwm_noalloc.cu", "srwm_bwd.cu",
          "srwm_layer.cu", "srwm_ffgemm.cu", "srwm_linattn.cu", "srwm_linattn_tc.cu",
-         "srwm_linattn_tc32.cu", "srwm_linattn_api.cu", "srwm_groupnorm.cu",
+         "srwm_linattn_tc32.cu", "srwm_linattn_scan.cu", "srwm_linattn_api.cu", "srwm_groupnorm.cu",
          "srwm_groupnorm_api.cu"]
 
 

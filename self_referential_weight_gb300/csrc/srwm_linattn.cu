@@ -7,6 +7,7 @@
 #include "srwm.h"
 #include "srwm_check.h"
 #include "srwm_linattn.cuh"
+#include "srwm_linattn_scan.h"
 #include "srwm_linattn_tc.h"
 
 namespace srwm {
@@ -199,6 +200,7 @@ LinPlan linattn_plan(int dtype, int B, int T, int H, int d, int roles)
 
 int linattn_launch(int dtype, int d, int roles, int slots, const LinParams& p, cudaStream_t st)
 {
+    if (linattn_scan_takes(dtype, d, roles, p)) return linattn_scan_launch(dtype, d, roles, p, st);
     if (linattn_tc_takes(dtype, d, p))
         return dtype == SRWM_F32 ? linattn_tc32_launch(roles, p, st) : linattn_tc_launch(roles, p, st);
     if (dtype == SRWM_F32) return by_width<float>(d, roles, slots, p, st);

@@ -20,11 +20,11 @@
 // The products run on the tensor cores in fp16 (mma.sync), with fp32 sums.
 // mma.sync rather than tcgen05.mma at D = 16 and 32, whose strips would fill an
 // eighth or a quarter of a 128-row product; D = 64 comes here where the axis is
-// split, in fp16, and below 128 tokens (srwm_linattn_tc.cu takes the rest).
+// split, in fp16, and below 128 tokens (srwm_linattn_tc.cu takes the rest).  The
+// shortest sequences run token by token (srwm_linattn_scan.cu).
 // What bounds it is instruction issue: 2048 ragged streams of up to 512 tokens
 // in bf16 at D = 32 (184 MB) take 55 us, 0.49 of the copy rate, with 59 % of
-// the issue slots busy over the whole launch, its uneven end included; 2048
-// streams of 26 tokens in fp32 at D = 16 take 6.9 us, gradients 17.4.
+// the issue slots busy over the whole launch, its uneven end included.
 //
 // Range and precision.  Each group of 16 tokens of a, b and c is scaled by a
 // power of two that puts its largest magnitude into [2^13, 2^14), exactly; all

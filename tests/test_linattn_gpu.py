@@ -539,3 +539,21 @@ def test_repeats_give_the_same_bits(d, dtype):
     first = run()
     for _ in range(25):
         assert all(torch.equal(x, y) for x, y in zip(first, run()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("T,B,H", [(3, 2, 3), (8, 1, 1), (9, 401, 5), (17, 331, 7), (19, 601, 3), (27, 301, 7), (40, 303, 5)])
+def test_short_sequences(T, B, H, d, dtype):
+    """Few and many streams of a few tokens, whole and ragged, views of packed arrays."""
+    q, k, v, lg, S0, do, dS = make(T + d, B, T, H, d, dtype, packed=True)
+    check_forward(q, k, v, lg, S0)
+    check_backward(q, k, v, lg, do, S0, None, dS)
+    lengths = (torch.arange(B, device=DEV) * 7 % (T + 3) - 1).int()
+    rows = torch.arange(T, device=DEV) >= lengths[:, None]
+    for x in (q, k, v, do):
+        x[rows] = float("nan")
+    o, _ = check_forward(q, k, v, lg, None, lengths, scale=-0.3)
+    assert (o[rows] == 0).all()
+    for x in check_backward(q, k, v, lg, do, None, lengths, scale=-0.3)[:3]:
+        assert (x[rows] == 0).all()
