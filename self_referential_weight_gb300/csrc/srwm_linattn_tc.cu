@@ -12,7 +12,7 @@
 // memory, 128 x 64 x 128), OI (128 x 64 x 64), U (64 x 64 x 128).  a, b, c are
 // the bf16 inputs themselves.  P enters its product as bf16 (2^-8 of each score at
 // most, as much as the outputs' own rounding; as a pair it costs 6 % of the
-// forward pass and 9 % of the gradients for 0.0017 instead of 0.0021 of relative
+// forward pass and 9 % of the gradients for 0.0017 instead of 0.0018 of relative
 // error), X as a bf16 (high, low) pair (2^-17), w_j b_j as three bf16 terms
 // (2^-24), so that X, which is kept in fp32 registers, is good to fp32.
 //
