@@ -67,6 +67,26 @@ inline int check_device_memory(std::initializer_list<const void*> ptrs)
     return SRWM_OK;
 }
 
+// Launches a kernel that calls griddep_wait() (srwm_ptx.cuh) behind one that calls griddep_launch(): its CTAs may be
+// placed while the last of the other's still run, instead of some 2 us after them.
+template <typename... P, typename... A>
+int launch_behind(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return SRWM_OK;
+    cudaGetLastError();
+    return SRWM_ERR_CUDA;
+}
+
 inline int launched() { return cudaGetLastError() == cudaSuccess ? SRWM_OK : SRWM_ERR_CUDA; }
 
 }  // namespace srwm

@@ -48,6 +48,11 @@ constexpr int kRowThreads = 256;
 constexpr int kSmemMost = 227 * 1024;    // of a CTA
 constexpr int kSlabGood = 48 * 1024;     // with this many, four CTAs share an SM and their loads overlap
 
+// The kernels of one call follow each other closely (launch_behind): each lets the next be placed as soon as all of its
+// own CTAs are, and waits for the one before to have completed.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- values
 template <typename E>
 constexpr int vec = 16 / static_cast<int>(sizeof(E));
@@ -324,6 +329,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(E) == 4 ? 3 : 2) gn_rows_g
 {
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
+    griddep_launch();
     const RowTile rt = row_tile<E>(p.C, p.G);
     const int slot = threadIdx.x / rt.tile, v = blockIdx.y * kRowThreads + threadIdx.x % rt.tile;
     const int group = v / rt.lanes, c = (group * rt.vecs + v % rt.lanes) * V;
@@ -388,6 +394,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(E) == 4 ? 3 : 2) gn_rows_g
 __global__ void __launch_bounds__(1024) gn_param_kernel(const GnParams p, long long partials)
 {
     __shared__ float s[2][128][9];
+    griddep_wait();
     const int t = threadIdx.x & 7, w = threadIdx.x >> 3, c = blockIdx.x * 8 + t;
     float a = 0.f, b = 0.f;
 #pragma unroll 8
@@ -488,6 +495,7 @@ __global__ void __launch_bounds__(256) gn_slab_kernel(const GnParams p, const Sl
 {
     constexpr int V = vec<E>;
     extern __shared__ __align__(128) unsigned char smem[];
+    if constexpr (GRAD) griddep_launch();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = sp.cluster > 1 ? static_cast<int>(cluster.block_rank()) : 0;
     const int tile = sp.cblk / V, slots = sp.threads / tile, width = p.C / p.G;
@@ -753,6 +761,8 @@ __global__ void __launch_bounds__(kRowThreads) gn_split_kernel(const GnParams p,
 {
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
+    griddep_launch();
+    if constexpr (STAGE == 1) griddep_wait();
     const int cv = p.C / V, tile = min(cv, kRowThreads), slots = kRowThreads / tile, width = p.C / p.G;
     const int slot = threadIdx.x / tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % tile * V;
     const bool on = slot < slots && c < p.C;
@@ -844,6 +854,8 @@ template <bool GRAD>
 __global__ void __launch_bounds__(kMergeThreads) gn_merge_kernel(const GnParams p, const SplitPlan sp)
 {
     __shared__ float s0[kMergeThreads], s1[kMergeThreads], s2[kMergeThreads];
+    griddep_launch();
+    griddep_wait();
     const long long n = blockIdx.x / p.G;
     const int g = blockIdx.x % p.G, width = p.C / p.G, t = threadIdx.x;
     const int across = min(width, kMergeThreads), deep = kMergeThreads / across;   // channels, ranges at a time
@@ -900,6 +912,7 @@ __global__ void __launch_bounds__(kRowThreads) gn_line_param_kernel(const GnPara
 {
     constexpr int V = vec<E>;
     __shared__ float s_part[kRowThreads * V];
+    griddep_launch();
     const int tile = min(p.C / V, kRowThreads), slots = kRowThreads / tile, width = p.C / p.G;
     const int slot = threadIdx.x / tile, c0 = blockIdx.y * kRowThreads * V, c = c0 + threadIdx.x % tile * V;
     const bool on = slot < slots && c < p.C;
@@ -1073,9 +1086,12 @@ int forward(const GnParams& p, cudaStream_t st)
     else if (g.way == kSlab)
         return launch_slab<E, ACT, false>(p, g, st);
     else {
-        gn_split_kernel<E, ACT, false, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
-        gn_merge_kernel<false><<<static_cast<unsigned>(p.N * p.G), kMergeThreads, 0, st>>>(p, g.split);
-        gn_split_kernel<E, ACT, false, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+        const dim3 grid(g.grid_x, g.grid_y);
+        gn_split_kernel<E, ACT, false, 0><<<grid, kRowThreads, 0, st>>>(p, g.split);
+        int rc = launched();
+        if (rc == SRWM_OK)
+            rc = launch_behind(gn_merge_kernel<false>, dim3(static_cast<unsigned>(p.N * p.G)), kMergeThreads, 0, st, p, g.split);
+        return rc == SRWM_OK ? launch_behind(gn_split_kernel<E, ACT, false, 1>, grid, kRowThreads, 0, st, p, g.split) : rc;
     }
     return launched();
 }
@@ -1098,13 +1114,16 @@ int backward(const GnParams& p, cudaStream_t st)
     } else if (g.way == kSlab)
         rc = launch_slab<E, ACT, true>(p, g, st);
     else {
-        gn_split_kernel<E, ACT, true, 0><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
-        gn_merge_kernel<true><<<static_cast<unsigned>(p.N * p.G), kMergeThreads, 0, st>>>(p, g.split);
-        gn_split_kernel<E, ACT, true, 1><<<dim3(g.grid_x, g.grid_y), kRowThreads, 0, st>>>(p, g.split);
+        const dim3 grid(g.grid_x, g.grid_y);
+        gn_split_kernel<E, ACT, true, 0><<<grid, kRowThreads, 0, st>>>(p, g.split);
+        rc = launched();
+        if (rc == SRWM_OK)
+            rc = launch_behind(gn_merge_kernel<true>, dim3(static_cast<unsigned>(p.N * p.G)), kMergeThreads, 0, st, p, g.split);
+        if (rc == SRWM_OK) rc = launch_behind(gn_split_kernel<E, ACT, true, 1>, grid, kRowThreads, 0, st, p, g.split);
     }
+    if (rc == SRWM_OK) rc = launched();
     if (rc != SRWM_OK) return rc;
-    if (params) gn_param_kernel<<<p.C / 8, 1024, 0, st>>>(p, g.partials);
-    return launched();
+    return params ? launch_behind(gn_param_kernel, dim3(p.C / 8), 1024, 0, st, p, g.partials) : SRWM_OK;
 }
 
 template <typename E>
