@@ -46,6 +46,7 @@ constexpr int kSms = 152;
 constexpr int kMaxCluster = 8;
 constexpr int kRowThreads = 256;
 constexpr int kSmemMost = 227 * 1024;    // of a CTA
+constexpr int kSmemPair = 112 * 1024;    // of each of two
 constexpr int kSlabGood = 48 * 1024;     // with this many, four CTAs share an SM and their loads overlap
 
 // The kernels of one call follow each other closely (launch_behind): each lets the next be placed as soon as all of its
@@ -1010,7 +1011,10 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     // fewer threads per sum to exchange; more where one or two CTAs have an SM to themselves
     s.threads = bytes() > 80 * 1024 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
     while (s.threads < tile) s.threads *= 2;
-    if (tile <= 256 && slab_smem(s, e, grad) <= kSmemMost) {
+    // fp32 gradients leave room for a second CTA on the SM, or the split way is faster though it reads x and dy twice
+    // (76 x 1718 x 256: 175 us with one CTA, 122 split; 64 x 3136 x 64: 66 and 58).  In bf16 the slab keeps its lead
+    // (32 x 9447 x 64: 87 and 102), and so does the forward pass (1 x 8000 x 512 in bf16: 13 and 28).
+    if (tile <= 256 && slab_smem(s, e, grad) <= (grad && e == 4 ? kSmemPair : kSmemMost)) {
         g.way = kSlab;
         g.grid_y = G / s.groups;
         // the backward pass keeps its channel sums over several samples: fewer partials
