@@ -67,7 +67,7 @@ inline int check_device_memory(std::initializer_list<const void*> ptrs)
     return SRWM_OK;
 }
 
-// Launches a kernel that calls griddep_wait() (srwm_ptx.cuh) behind one that calls griddep_launch(): its CTAs may be
+// Launches a kernel that calls griddep_wait() (srwm_mma.cuh) behind one that calls griddep_launch(): its CTAs may be
 // placed while the last of the other's still run, instead of some 2 us after them.
 template <typename... P, typename... A>
 int launch_behind(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args)

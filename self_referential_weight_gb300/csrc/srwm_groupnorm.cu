@@ -49,11 +49,6 @@ constexpr int kSmemMost = 227 * 1024;    // of a CTA
 constexpr int kSmemPair = 112 * 1024;    // of each of two
 constexpr int kSlabGood = 48 * 1024;     // with this many, four CTAs share an SM and their loads overlap
 
-// The kernels of one call follow each other closely (launch_behind): each lets the next be placed as soon as all of its
-// own CTAs are, and waits for the one before to have completed.
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ---------------------------------------------------------------- values
 template <typename E>
 constexpr int vec = 16 / static_cast<int>(sizeof(E));

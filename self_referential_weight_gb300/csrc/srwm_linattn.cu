@@ -33,6 +33,7 @@ template <typename E, int D>
 __global__ void __launch_bounds__(LinTile<E, D>::kThreads, blocks_per_sm<E, D>())
     linattn_state_kernel(const __grid_constant__ LinParams p)
 {
+    griddep_launch();
     linattn_body<E, D, true>(p);
 }
 
@@ -142,6 +143,10 @@ int launch(int roles, int slots, const LinParams& p, cudaStream_t st)
         rc = allow_smem(reinterpret_cast<const void*>(linattn_state_kernel<E, D>), L::kSmemState, state_ok);
         if (rc != SRWM_OK) return rc;
         linattn_state_kernel<E, D><<<dim3(streams * (p.segments - 1), slots), L::kThreads, L::kSmemState, st>>>(p);
+        rc = launched();
+        return rc != SRWM_OK ? rc
+                             : launch_behind(linattn_kernel<E, D>, dim3(streams * p.segments, roles), L::kThreads,
+                                             static_cast<int>(L::kSmem), st, p);
     }
     linattn_kernel<E, D><<<dim3(streams * p.segments, roles), L::kThreads, L::kSmem, st>>>(p);
     return launched();

@@ -304,6 +304,7 @@ __device__ __forceinline__ void state_warp(const LinWork<E, D, STATE_ONLY>& W, i
     };
     float bound = 0.f;   // >= every |X|, the same in every state warp
     if constexpr (!STATE_ONLY) {
+        if (p.segments > 1) griddep_wait();   // the earlier segments' states come from the kernel before
         if (R.x_in) add_state(R.x_in + mat, R.transposed, W.gpow(min(W.first, W.n)));
         for (int s = 0; s < W.seg; ++s)   // what the earlier segments left, in their order
             add_state(p.seg_state + ((static_cast<size_t>(R.state_slot) * p.segments + s) * p.B * p.H + W.stream) * D * D,

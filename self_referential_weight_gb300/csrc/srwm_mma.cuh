@@ -1,6 +1,6 @@
 // srwm_mma.cuh -- warp-level fp16 matrix products with fp32 accumulation
-// (mma.sync m16n8k16), the loads of their fragments, and 16-byte asynchronous
-// copies, as inline PTX.
+// (mma.sync m16n8k16), the loads of their fragments, 16-byte asynchronous
+// copies, and the order of a call's kernels, as inline PTX.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -78,5 +78,10 @@ __device__ __forceinline__ void split_half2_2(float2 v, uint32_t& hi, uint32_t& 
     const float2 rest = fma2(unpack_half2(hi), both(-1.f), v);
     lo = pack_half2(rest.x, rest.y);
 }
+
+// For the kernels of one call that follow each other closely (launch_behind in srwm_check.h): a kernel lets the next be
+// placed as soon as all of its own CTAs are; the next waits for it to have completed.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace srwm
