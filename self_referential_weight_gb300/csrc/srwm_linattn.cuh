@@ -275,7 +275,7 @@ template <typename E, int D, bool STATE_ONLY>
 __device__ __forceinline__ void state_warp(const LinWork<E, D, STATE_ONLY>& W, int warp)
 {
     using L = LinTile<E, D>;
-    constexpr int NI = L::NI, NM = L::NM, NT = D / 8;
+    constexpr int NI = L::NI, NM = L::NM, NT = D / 8, UNROLL = 128 / D;
     const LinParams& p = W.p;
     const LinRole& R = W.R;
     const int lane = threadIdx.x & 31, r4 = lane >> 2, x2 = 2 * (lane & 3);
@@ -297,18 +297,24 @@ __device__ __forceinline__ void state_warp(const LinWork<E, D, STATE_ONLY>& W, i
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = 16 * warp + r4 + 8 * (k >> 1), j = 8 * t + x2 + (k & 1);
-                X[t][k] = fmaf(f, transposed ? m[j * D + i] : m[i * D + j], X[t][k]);
+            for (int k = 0; k < 4; k += 2) {
+                const int i = 16 * warp + r4 + 4 * k, j = 8 * t + x2;
+                const float2 v = transposed ? make_float2(m[j * D + i], m[(j + 1) * D + i])
+                                            : *reinterpret_cast<const float2*>(m + i * D + j);
+                X[t][k] = fmaf(f, v.x, X[t][k]);
+                X[t][k + 1] = fmaf(f, v.y, X[t][k + 1]);
             }
     };
     float bound = 0.f;   // >= every |X|, the same in every state warp
     if constexpr (!STATE_ONLY) {
         if (p.segments > 1) griddep_wait();   // the earlier segments' states come from the kernel before
         if (R.x_in) add_state(R.x_in + mat, R.transposed, W.gpow(min(W.first, W.n)));
-        for (int s = 0; s < W.seg; ++s)   // what the earlier segments left, in their order
-            add_state(p.seg_state + ((static_cast<size_t>(R.state_slot) * p.segments + s) * p.B * p.H + W.stream) * D * D,
-                      R.state_transposed, W.gpow(min(W.first, W.n) - min((s + 1) * p.seg_len, W.n)));
+        // what the earlier segments left, in their order; several of their loads in flight at once
+        const float* left = p.seg_state + (static_cast<size_t>(R.state_slot) * p.segments * p.B * p.H + W.stream) * D * D;
+#pragma unroll UNROLL
+        for (int s = 0; s < W.seg; ++s)
+            add_state(left + static_cast<size_t>(s) * p.B * p.H * D * D, R.state_transposed,
+                      W.gpow(min(W.first, W.n) - min((s + 1) * p.seg_len, W.n)));
         float m = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
