@@ -2,7 +2,9 @@
 // the chunked kernel (srwm_linattn.cuh), and the single-token kernel.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "srwm.h"
 #include "srwm_check.h"
@@ -186,17 +188,21 @@ LinPlan linattn_plan(int dtype, int B, int T, int H, int d, int roles)
     const long long ctas = static_cast<long long>(B) * H * roles;
     const int chunks = T / d + (T % d != 0);
     const LinPlan whole{chunks > 0 ? chunks * d : d, 1};
-    // Splitting fills the GPU when there are few streams, for a second pass over two of the three tensors.
+    // Splitting fills the GPU when there are few streams, for a second pass over two of the three tensors.  A segment's
+    // chunks and the states before it, which it adds up, both run one after another: 2 sqrt(chunks) segments are near
+    // the best of both (16 streams of 1200 tokens, fp32, d = 32: 16.6 us with 19 segments, 21.5 with 4; 4 streams of
+    // 8192, bf16, d = 16: 20.7 with 32, 23.7 with 64, 35.5 with 128).
+    const double root = std::sqrt(static_cast<double>(chunks));
     long long segments = ctas * 3 > slots ? 1 : slots / ctas;
-    if (segments > chunks / 8) segments = chunks / 8;   // at least 8 chunks each
-    if (segments < 2) return whole;
+    segments = std::min(segments, static_cast<long long>(2 * root));
+    if (segments < 2 || chunks < 8) return whole;   // below, the second launch costs what it saves
     if (d == 64 && dtype != SRWM_F16) {
-        // The tcgen05 kernels take an unsplit stream's 128 tokens in 1.45 us (bf16) or 4.9 us (fp32) however few
-        // streams there are; the split takes about 32 or 45 us, and 2.0 or 3.6 us for each stream's 8192 tokens
-        // (bf16, T = 8192: 8 streams 41 us split and 95 whole, 32 streams 85 and 99, 64 streams 161 and 98; fp32:
-        // 58 and 307, 133 and 313, 266 and 316, and 349 and 322 at 96; at T = 1024 whole streams are faster).
+        // Against that, the tcgen05 kernels take a whole stream's 128 tokens in 1.45 us (bf16) or 4.9 us (fp32) however
+        // few streams there are; the split takes a time with the root of the chunks, and 2.0 or 3.6 us for each
+        // stream's 8192 tokens (split and whole, fp32: 10 streams of 1200 24 and 51 us, 64 of 2500 91 and 104; bf16: 3 of
+        // 1200 17 and 19, 16 of 2500 27 and 34, 32 of 8192 81 and 98).
         const bool wide = dtype == SRWM_F32;
-        const double split = (wide ? 45.0 : 32.0) + static_cast<double>(ctas) * T * (wide ? 3.6 : 2.0) / 8192;
+        const double split = 6 + root * (wide ? 3.0 : 2.0) + static_cast<double>(ctas) * T * (wide ? 3.6 : 2.0) / 8192;
         if (split >= 5.0 + T / 128.0 * (wide ? 4.9 : 1.45)) return whole;
     }
     const int per = static_cast<int>((chunks + segments - 1) / segments);
