@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
         const float* x = R.x_in + mat + (R.transposed ? col * D : col);
 #pragma unroll
         for (int i = 0; i < D / 2; i += 2) {
+            const float* y = x + 2 * i * D;
             const float4 v = R.transposed ? *reinterpret_cast<const float4*>(x + 2 * i)
-                                          : make_float4(x[2 * i * D], x[(2 * i + 1) * D], x[(2 * i + 2) * D], x[(2 * i + 3) * D]);
+                                          : make_float4(y[0], y[D], y[2 * D], y[3 * D]);
             X[i] = make_float2(v.x, v.y);
             X[i + 1] = make_float2(v.z, v.w);
         }
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const float2 x = pair_to_f(v[2 * half], E{}), y = pair_to_f(v[2 * half + 1], E{});
-                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at + piece * 32 + 16 * half), "f"(x.x), "f"(x.y),
-                                 "f"(y.x), "f"(y.y)
+                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at + piece * 32 + 16 * half), "f"(x.x),
+                                 "f"(x.y), "f"(y.x), "f"(y.y)
                                  : "memory");
                 }
             }

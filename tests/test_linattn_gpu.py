@@ -557,3 +557,15 @@ def test_short_sequences(T, B, H, d, dtype):
     assert (o[rows] == 0).all()
     for x in check_backward(q, k, v, lg, do, None, lengths, scale=-0.3)[:3]:
         assert (x[rows] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,d", [(128, 16), (255, 32), (449, 64), (1201, 64)])
+def test_a_few_streams_of_some_hundred_tokens(T, d, dtype):
+    """The shortest axes that are split, whole and with lengths that end inside, at and before a segment."""
+    q, k, v, lg, S0, do, dS = make(T + d, 4, T, 1, d, dtype)
+    check_forward(q, k, v, lg, S0)
+    check_backward(q, k, v, lg, do, S0, None, dS)
+    lengths = torch.tensor([T // 2, 0, T - 1, 2 * d], dtype=torch.int32, device=DEV)
+    check_forward(q, k, v, lg, S0, lengths)
+    check_backward(q, k, v, lg, do, S0, lengths, dS)
