@@ -9,9 +9,9 @@
 // a, b, c land as fp32 in two tiles of 32 columns each, and are turned into
 // their pairs in place: a row's high halves take its 128 bytes of the first
 // tile, the low halves those of the second.  The scores of 16 columns carry
-// 2^(eb + ec) relative to the largest on the strip's causal side, the weighted
-// b's terms likewise, and X's copy the exponent of a bound on X; sums are fp32
-// throughout.
+// 2^(eb + ec) relative to the largest that their 16 rows see, the weighted b's
+// terms relative to the chunk's largest, and X's copy the exponent of a bound
+// on X; sums are fp32 throughout.
 //
 // Warps: 0-7 turn P into its pair; 8-11 write the weighted b's terms, 32 tokens
 // at a time into two buffers in turn; 12-15 hold X; 16-19 convert c and write
@@ -64,7 +64,7 @@ struct __align__(1024) Smem32 {
     uint8_t state[2][D * D * 2];              // X's copy: high | low
     float decay[8][64];
     int exps[RING][3][8];                     // of a, b, c, per 16 tokens
-    int norm[RING][5];                        // the exponents that normalise four strips' scores, and the terms
+    int norm[RING][9];                        // the exponents that normalise the scores of 16 rows each, and the terms
     int state_exp[RING];
     int valid[RING], total;                   // valid tokens of a chunk; chunks of this CTA
     float top[2][4];                          // largest |X| of each state warp's rows at an item's start
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 if (!(ok = wait(&sm.p32_full[g & 1], g >> 1) && wait(&sm.norm_full[g % STAGES], g / STAGES))) break;
                 fence_after();
                 const int(&e)[3][8] = sm.exps[g % RING];
-                const int ef = sm.norm[g % RING][own] + 20;
+                const int ef = sm.norm[g % RING][row >> 4] + 20;
                 const uint32_t P = tmem + quad + kP + C * (g & 1);
                 for (int cb = set; cb < 4; cb += 2)   // the side that is masked
                     if (cb < c0 || cb > c1) {
@@ -370,15 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 const int s = g % STAGES, nc = w.valid();
                 if (!(ok = wait(&sm.ready_ab[s], g / STAGES) && wait(&sm.ready_c[s], g / STAGES))) break;
                 const int(&e)[3][8] = sm.exps[g % RING];
-                // The largest 2^(eb + ec) g^gap among the column groups on the causal side of 32 rows, and among all
-                // with their distance to the chunk's end: what the scores and the terms are relative to.
+                // The largest 2^(eb + ec) g^gap among the column groups on the causal side of 16 rows (lanes 0-7 the
+                // first of this warp's, 8-15 the others: a group that no row sees must not cost them their bits), and
+                // among all with their distance to the chunk's end: what the scores and the terms are relative to.
                 int eu;
                 {
-                    const int c = lane & 7, r0 = 32 * own;
+                    const int c = lane & 7, strip = 2 * own + ((lane >> 3) & 1), r0 = 16 * strip;
                     const float ec = static_cast<float>(e[1][c] + e[2][c]);
-                    const int gap = w.rev ? 16 * c - r0 - 31 : r0 - 16 * c - 15;
+                    const int gap = w.rev ? 16 * c - r0 - 15 : r0 - 16 * c - 15;
                     const int end = w.rev ? 16 * c + 1 : max(0, nc - 16 * c - 16);
-                    const bool causal = w.rev ? 16 * c >= r0 : 16 * c < r0 + 32;
+                    const bool causal = w.rev ? c >= strip : c <= strip;
                     float top = causal ? fmaf(lg, static_cast<float>(max(0, gap)), ec) : -8000.f;
                     float last = fmaf(lg, static_cast<float>(end), ec);
 #pragma unroll
@@ -387,10 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                         last = fmaxf(last, __shfl_xor_sync(0xffffffffu, last, o));
                     }
                     eu = static_cast<int>(ceilf(fmaxf(last, -8000.f)));
-                    if (lane == 0) {
-                        sm.norm[g % RING][own] = static_cast<int>(ceilf(fmaxf(top, -8000.f)));
-                        if (own == 0) sm.norm[g % RING][4] = eu;
-                    }
+                    if (lane < 16 && c == 0) sm.norm[g % RING][strip] = static_cast<int>(ceilf(fmaxf(top, -8000.f)));
+                    if (own == 0 && lane == 0) sm.norm[g % RING][8] = eu;
                     arrive(&sm.norm_full[s]);
                 }
 #pragma unroll 1
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 const int nc = w.valid();
                 if (!(ok = wait(&sm.u_full, g))) break;
                 fence_after();
-                const int eu = sm.norm[g % RING][4] + R.alpha_u_exp;
+                const int eu = sm.norm[g % RING][8] + R.alpha_u_exp;
                 // X = g^nc X + alpha_u U 2^eu, in two factors that stay inside fp32's range
                 const float f1 = pow2i(eu / 2), f2 = R.alpha_u_man * pow2i(eu - eu / 2);
                 const Decay dec = nc == C ? full : decay_over(lg, nc);
@@ -527,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 fence_after();
                 const int ea = sm.exps[g % RING][0][i >> 4], nc = w.valid();
                 // out = alpha_o 2^ea (g^e 2^eX OI + 2^ef OX), each power in two factors that stay inside fp32's range
-                const int ei = ea + sm.state_exp[g % RING], ex = ea + sm.norm[g % RING][own] + R.alpha_u_exp + 20;
+                const int ei = ea + sm.state_exp[g % RING], ex = ea + sm.norm[g % RING][i >> 4] + R.alpha_u_exp + 20;
                 const float fi = pow2i(ei / 2), fx = pow2i(ex / 2);
                 const float gi = R.alpha_o * pow2i(ei - ei / 2) *
                                  exp2f(lg * static_cast<float>(w.rev ? max(0, nc - 1 - i) : i + 1));

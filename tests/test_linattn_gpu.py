@@ -569,3 +569,30 @@ def test_a_few_streams_of_some_hundred_tokens(T, d, dtype):
     lengths = torch.tensor([T // 2, 0, T - 1, 2 * d], dtype=torch.int32, device=DEV)
     check_forward(q, k, v, lg, S0, lengths)
     check_backward(q, k, v, lg, do, S0, lengths, dS)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("decay", [0.0, -0.3])
+@pytest.mark.parametrize("by", [10, 15])
+@pytest.mark.parametrize("at", [16, 112, 176])
+def test_later_tokens_do_not_cost_earlier_ones_their_bits(at, by, decay, dtype):
+    """Sixteen tokens far above their neighbours, which do not see them: in
+    order tokens at .. at + 15 for the sixteen before, in reverse at - 16 ..
+    at - 1 for the sixteen behind.  No state, so that those rows stay small;
+    each row's tolerance is that of the tokens it sees."""
+    T, d = 200, 64
+    q, k, v, lg, _, do, _ = make(at + by, 2, T, 3, d, dtype, decay)
+    if dtype == F16:
+        by //= 3      # values and outputs stay below 65504
+    big = torch.ones(T, 1, 1, device=DEV)
+    big[at:at + 16] = 2.0 ** by
+    check_forward(q, (k.float() * big).to(dtype), (v.float() * big).to(dtype), lg)
+    dq = binding.srwm_linattn_backward(q, (k.float() * big).to(dtype), (v.float() * big).to(dtype), lg, do)[0]
+    args = (q, (k.float() * big).to(dtype), (v.float() * big).to(dtype), lg, d ** -0.5, do)
+    assert_near(dq, oracle.grads(*args)[0], oracle.grad_sizes(*args)[0], d, T, dtype, "dq")
+    big = torch.ones(T, 1, 1, device=DEV)
+    big[at - 16:at] = 2.0 ** by
+    args = ((q.float() * big).to(dtype), k, v, lg, d ** -0.5, (do.float() * big).to(dtype))
+    got = binding.srwm_linattn_backward(args[0], k, v, lg, args[5])
+    for name, x, r, a in list(zip(("dq", "dk", "dv"), got, oracle.grads(*args), oracle.grad_sizes(*args)))[1:]:
+        assert_near(x, r, a, d, T, dtype, name)
