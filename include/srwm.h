@@ -338,7 +338,8 @@ int srwm_debug_set_layer_gemm(int mode);
  *              H * d, a multiple of 16 bytes
  *   log_decay  [H] fp32, log g <= 0; 0 keeps everything (the sum over all
  *              tokens), -infinity keeps the current token alone.  Values above
- *              0 are taken as 0; a NaN makes its head's results NaN.
+ *              0 are taken as 0; a NaN makes its head's results NaN (an empty
+ *              sequence still passes its state on).
  *   S_init     [B, H, d, d] fp32 (row = index of k, column = index of v), or
  *              NULL for zero
  *   lengths    [B] int32 on the device (4-byte aligned), the valid tokens of

@@ -308,13 +308,15 @@ __device__ __forceinline__ void state_warp(const LinWork<E, D, STATE_ONLY>& W, i
     float bound = 0.f;   // >= every |X|, the same in every state warp
     if constexpr (!STATE_ONLY) {
         if (p.segments > 1) griddep_wait();   // the earlier segments' states come from the kernel before
-        if (R.x_in) add_state(R.x_in + mat, R.transposed, W.gpow(min(W.first, W.n)));
-        // what the earlier segments left, in their order; several of their loads in flight at once
+        const int before = min(W.first, W.n);
+        if (R.x_in) add_state(R.x_in + mat, R.transposed, before > 0 ? W.gpow(before) : 1.f);   // as it is, whatever g
+        // what the earlier segments with tokens left, in their order; several of their loads in flight at once
+        const int filled = min(W.seg, (W.n + p.seg_len - 1) / p.seg_len);
         const float* left = p.seg_state + (static_cast<size_t>(R.state_slot) * p.segments * p.B * p.H + W.stream) * D * D;
 #pragma unroll UNROLL
-        for (int s = 0; s < W.seg; ++s)
+        for (int s = 0; s < filled; ++s)
             add_state(left + static_cast<size_t>(s) * p.B * p.H * D * D, R.state_transposed,
-                      W.gpow(min(W.first, W.n) - min((s + 1) * p.seg_len, W.n)));
+                      W.gpow(before - min((s + 1) * p.seg_len, W.n)));
         float m = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)

@@ -596,3 +596,18 @@ def test_later_tokens_do_not_cost_earlier_ones_their_bits(at, by, decay, dtype):
     got = binding.srwm_linattn_backward(args[0], k, v, lg, args[5])
     for name, x, r, a in list(zip(("dq", "dk", "dv"), got, oracle.grads(*args), oracle.grad_sizes(*args)))[1:]:
         assert_near(x, r, a, d, T, dtype, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("T", [8, 26, 100, 300, 1201])
+def test_an_empty_sequence_passes_its_state_on_whatever_the_decay(T, d, dtype):
+    """No token, no decay: also of a head whose decay is NaN, beside sequences that have tokens."""
+    q, k, v, lg, S0, do, dS = make(T + d, 3, T, 3, d, dtype)
+    lg[1] = float("nan")
+    lengths = torch.tensor([T, 0, (T + 1) // 2], dtype=torch.int32, device=DEV)
+    o, S = binding.srwm_linattn_forward(q, k, v, lg, S_init=S0, lengths=lengths)
+    got = binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, lengths=lengths, dS_final=dS)
+    assert torch.equal(S[1], S0[1]) and torch.equal(got[3][1], dS[1])
+    assert all((x[1] == 0).all() for x in (o,) + tuple(got[:3]))
+    assert torch.isnan(S[::2, 1]).all() and torch.isnan(got[3][::2, 1]).all()
