@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
     const Decay dec = decay_over(decay_log2(p.log_decay[h]), 1);
     float off = 0.f;
     const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
+    const float undecayed = n > 0 ? fmaf(0.f, dec.m, 1.f) : 1.f;   // 1, or NaN under a decay that is NaN
     E* const out = static_cast<E*>(R.out) + token0 * R.ldo + h * D + col;
     E* to = out + (rev ? (n - 1) * R.ldo : 0);
     const long long step = rev ? -R.ldo : R.ldo;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
             const int i = TT * tile + r;
             const float4* a = reinterpret_cast<const float4*>(rows + r * D);
             const float4* k = a + TT * D / 4;
-            float g = 1.f;
+            float g = undecayed;
             if (i < n && !(rev && i == 0)) {
                 g = dec.c + (dec.m - off);
                 off += (g - dec.c) - dec.m;

@@ -611,3 +611,24 @@ def test_an_empty_sequence_passes_its_state_on_whatever_the_decay(T, d, dtype):
     assert torch.equal(S[1], S0[1]) and torch.equal(got[3][1], dS[1])
     assert all((x[1] == 0).all() for x in (o,) + tuple(got[:3]))
     assert torch.isnan(S[::2, 1]).all() and torch.isnan(got[3][::2, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("T", [1, 8, 26, 100, 200])
+def test_gradients_under_a_decay_that_is_nan(T, d, dtype):
+    """All of that head's gradients are NaN, whichever kernel a length takes;
+    the other heads' are as they were."""
+    q, k, v, lg, S0, do, dS = make(T + d, 3, T, 3, d, dtype)
+    lengths = torch.tensor([T, 1, (T + 1) // 2], dtype=torch.int32, device=DEV)
+    run = lambda: binding.srwm_linattn_backward(q, k, v, lg, do, S_init=S0, lengths=lengths, dS_final=dS)  # noqa: E731
+    was = run()
+    lg[1] = float("nan")
+    got = run()
+    for b, n in enumerate(lengths.tolist()):
+        for x in got[:3]:
+            assert torch.isnan(x[b, :n, 1]).all() and (x[b, n:, 1] == 0).all()
+        assert torch.isnan(got[3][b, 1]).all()
+    for x, y in zip(got, was):
+        heads = (lambda t: t[:, ::2]) if x is got[3] else (lambda t: t[:, :, ::2])
+        assert torch.equal(heads(x), heads(y))
