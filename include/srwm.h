@@ -483,16 +483,18 @@ int srwm_last_device_status(void* stream);
 
 /*
  * srwm_set_wait_limit_ns -- the time after which a kernel's wait on an
- * asynchronous copy gives up (default 1 s).  Values < 1000 are clamped to
- * 1000.  Applies to launches made after the call, from any thread.
+ * asynchronous copy, or on a product on the tensor cores, gives up (default
+ * 1 s).  Values < 1000 are clamped to 1000.  Applies to launches made after the
+ * call, from any thread.
  */
 int srwm_set_wait_limit_ns(long long limit_ns);
 
 /*
  * srwm_debug_skip_x_chunk -- fault injection for tests: the next launches do
  * not issue the TMA load of input chunk `chunk` (a chunk is a fixed number of
- * consecutive steps) so the kernel's bounded wait on it runs out; -1 turns
- * injection off.  The kernel then stops early, waits for its other copies,
+ * consecutive steps; in the linear attention kernels that load by TMA, d = 64
+ * in fp32 and bf16 from 128 tokens on, 128 of them, and no later chunk is loaded either)
+ * so the kernel's bounded wait on it runs out; -1 turns injection off.  The kernel then stops early, waits for its other copies,
  * writes no further outputs, and sets the status word read by
  * srwm_last_device_status.  Not for production use.
  */

@@ -463,6 +463,8 @@ namespace srwm {
 int device_status_ptr(unsigned** out) { return status_ptr(out); }
 unsigned long long device_wait_limit_ns() { return static_cast<unsigned long long>(g_wait_limit_ns.load()); }
 
+int debug_skip_chunk() { return g_skip_chunk.load(); }
+
 }  // namespace srwm
 
 extern "C" {

@@ -18,9 +18,10 @@ struct GemmArgs {
     unsigned long long wait_limit_ns;
 };
 
-// The library's device status word and bounded-wait limit (srwm_api.cu).
+// The library's device status word, bounded-wait limit and chunk that is not loaded (-1: none) (srwm_api.cu).
 int device_status_ptr(unsigned** out);
 unsigned long long device_wait_limit_ns();
+int debug_skip_chunk();
 
 // fp32 [n] -> bf16 hi and lo parts (x ~ hi + lo)
 int ff_split(const float* src, void* hi, void* lo, long long n, cudaStream_t st);

@@ -65,6 +65,7 @@ struct TcParams {
     int roles, items;
     unsigned* status;
     unsigned long long wait_limit_ns;
+    int skip_chunk;   // fault injection: where the loads of a stream end (-1: nowhere)
 };
 
 struct __align__(1024) Smem {
@@ -139,22 +140,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     if (warp == kLoadWarp) {
         // ---- loads
         if (lane == 0) {
-            int last = -1;
-            uint32_t last_phase = 0;
             Walk<TcParams> w(p);
             for (; w.skip_empty() && !*abort; ++w.k, ++g) {
                 const int s = g % STAGES;
-                if (!wait(&sm.empty[s], g / STAGES + 1)) break;
+                if (w.k == p.skip_chunk || !wait(&sm.empty[s], g / STAGES + 1)) break;
                 const TcMaps& m = p.map[w.role];
                 mbar_arrive_expect_tx(&sm.full[s], 3 * kTileBytes);
                 tma_load_4d(sm.stage[s][1], &m.b, &sm.full[s], 0, w.h, w.token(), w.b);
                 tma_load_4d(sm.stage[s][0], &m.a, &sm.full[s], 0, w.h, w.token(), w.b);
                 tma_load_4d(sm.stage[s][2], &m.c, &sm.full[s], 0, w.h, w.token(), w.b);
-                last = s;
-                last_phase = g / STAGES;
             }
-            // the shared memory may only be given up once the last loads landed (stages complete in order)
-            if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
+            drain_loads(sm.full, g);
         }
         __syncwarp();
     } else if (warp >= kScoreMmaWarp) {
@@ -510,6 +506,7 @@ int linattn_tc_launch(int roles, const LinParams& lin, cudaStream_t st)
     int rc = device_status_ptr(&p.status);
     if (rc != SRWM_OK) return rc;
     p.wait_limit_ns = device_wait_limit_ns();
+    p.skip_chunk = debug_skip_chunk();
     for (int i = 0; i < roles; ++i) {
         const LinRole& r = lin.role[i];
         if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C, false)) != SRWM_OK ||

@@ -200,6 +200,17 @@ static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, ui
     return false;
 }
 
+// What a CTA's last copies may take, whatever limit its other waits have.
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+
+// The loader's end, after `chunks` loads into the stages in turn: the shared memory may only be given up once those
+// that may still be in flight have landed, whose order is not given.
+template <int N>
+__device__ __forceinline__ void drain_loads(uint64_t (&full)[N], uint32_t chunks)
+{
+    for (uint32_t c = chunks > N ? chunks - N : 0; c < chunks; ++c) mbar_wait_bounded(&full[c % N], (c / N) & 1u, kDrainLimitNs);
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

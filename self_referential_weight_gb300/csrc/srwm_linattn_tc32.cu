@@ -56,6 +56,7 @@ struct Tc32Params {
     int roles, items;
     unsigned* status;
     unsigned long long wait_limit_ns;
+    int skip_chunk;   // fault injection: where the loads of a stream end (-1: nowhere)
 };
 
 struct __align__(1024) Smem32 {
@@ -180,12 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
     if (warp == kLoadWarp) {
         // ---- loads
         if (lane == 0) {
-            int last = -1;
-            uint32_t last_phase = 0;
             Walk<Tc32Params> w(p);
             for (; w.skip_empty() && !*abort; ++w.k, ++g) {
                 const int s = g % STAGES;
-                if (!wait(&sm.empty[s], g / STAGES + 1)) break;
+                if (w.k == p.skip_chunk || !wait(&sm.empty[s], g / STAGES + 1)) break;
                 const Tc32Maps& m = p.map[w.role];
                 sm.valid[g % RING] = w.valid();
                 mbar_arrive_expect_tx(&sm.full[s], 6 * kHalfTile);
@@ -195,11 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     tma_load_4d(sm.stage[s][0][half], &m.a, &sm.full[s], 32 * half, w.h, w.token(), w.b);
                     tma_load_4d(sm.stage[s][2][half], &m.c, &sm.full[s], 32 * half, w.h, w.token(), w.b);
                 }
-                last = s;
-                last_phase = g / STAGES;
             }
-            // the shared memory may only be given up once the last loads landed (stages complete in order)
-            if (last >= 0) mbar_wait_bounded(&sm.full[last], last_phase & 1u, p.wait_limit_ns);
+            drain_loads(sm.full, g);
         }
         __syncwarp();
     } else if (warp >= kScoreMmaWarp) {
@@ -601,6 +597,7 @@ int linattn_tc32_launch(int roles, const LinParams& lin, cudaStream_t st)
     int rc = device_status_ptr(&p.status);
     if (rc != SRWM_OK) return rc;
     p.wait_limit_ns = device_wait_limit_ns();
+    p.skip_chunk = debug_skip_chunk();
     for (int i = 0; i < roles; ++i) {
         const LinRole& r = lin.role[i];
         if ((rc = token_map(&p.map[i].a, r.a, r.lda, lin, C, true)) != SRWM_OK ||

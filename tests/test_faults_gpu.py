@@ -74,3 +74,34 @@ def test_missing_chunk_wrap_schedule(short_waits, d, H, slots_per_sm):
         yo, Wo = oracle.forward(x[b:b + 1], W0, 1, True)
         assert np.abs(y[b].cpu().numpy() - yo[0]).max() / np.abs(yo).max() <= 1e-4
         assert np.abs(Wf[b].cpu().numpy() - Wo[0]).max() / np.abs(Wo).max() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B", [2, 90])
+def test_missing_chunk_of_linear_attention(short_waits, B, dtype):
+    """The kernels on 128-token chunks, a stream or several per SM (the first
+    stream that has a second chunk ends its CTA), forward and backward: the
+    timeout status, then calls that are right again."""
+    T, H, d = 300, 5, 64
+    g = torch.Generator(device=DEV).manual_seed(B)
+    q, k, v, do = (torch.randn(B, T, H, d, generator=g, device=DEV).to(dtype) for _ in range(4))
+    lg = torch.full((H,), -0.05, device=DEV)
+    assert binding.srwm_last_device_status() == 0
+    o, S = binding.srwm_linattn_forward(q, k, v, lg)
+    grads = binding.srwm_linattn_backward(q, k, v, lg, do)
+    assert binding.srwm_last_device_status() == 0
+    for call in (lambda: binding.srwm_linattn_forward(q, k, v, lg), lambda: binding.srwm_linattn_backward(q, k, v, lg, do)):
+        binding.srwm_debug_skip_x_chunk(1)
+        call()
+        assert binding.srwm_last_device_status() == binding.SRWM_ERR_TIMEOUT
+        assert binding.srwm_last_device_status() == 0
+        binding.srwm_debug_skip_x_chunk(-1)
+        o2, S2 = binding.srwm_linattn_forward(q, k, v, lg)
+        again = binding.srwm_linattn_backward(q, k, v, lg, do)
+        assert binding.srwm_last_device_status() == 0
+        assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(x, y) for x, y in zip(grads, again))
+    short = torch.full((B,), 128, dtype=torch.int32, device=DEV)      # no sequence has a second chunk
+    want = binding.srwm_linattn_forward(q, k, v, lg, lengths=short)
+    binding.srwm_debug_skip_x_chunk(1)
+    got = binding.srwm_linattn_forward(q, k, v, lg, lengths=short)
+    assert binding.srwm_last_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(want, got))
