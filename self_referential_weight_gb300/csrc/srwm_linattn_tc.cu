@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                            id_o = idesc(true, C, D, false, true);
         constexpr uint64_t kStage = 3 * kTileBytes / 16, kTile = kTileBytes / 16;   // descriptor steps
         const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0]));
-        bool ok = true, issued = false;
+        bool ok = true;
         Walk<TcParams> w(p);
         if (warp == kScoreMmaWarp) {
             // P of chunk `at`, once its tiles have landed and been cleaned where they need it.  Its place was last
@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     commit(&sm.p32_full[at & 1]);
                 }
                 __syncwarp();
-                issued = true;
             };
             if (w.skip_empty()) score(0);
             for (; ok && w.skip_empty(); ++g) {
@@ -225,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         if (half == 1) commit(&sm.u_full);
                     }
                     __syncwarp();
-                    issued = true;
                 }
                 // X's copy is there, and the outputs that used this place have been read
                 if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
@@ -242,14 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 __syncwarp();
             }
         }
-        // Tensor memory may only be freed once the products issued have completed: after a timeout nobody else
-        // waits for them.
-        if (!ok && issued) {
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 1000000ull) {
-            }
-        }
-        __syncwarp();
     } else if (warp < kTermWarp) {
         // ---- P as bf16, one row per thread; two sets of four warps take the 32-column blocks in turn
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
@@ -483,8 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kStateMmaWarp)
+    if (warp == kStateMmaWarp) {
+        if (*abort) let_products_end();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
 }
 
 }  // namespace

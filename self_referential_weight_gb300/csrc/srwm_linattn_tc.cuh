@@ -211,6 +211,16 @@ __device__ __forceinline__ void drain_loads(uint64_t (&full)[N], uint32_t chunks
     for (uint32_t c = chunks > N ? chunks - N : 0; c < chunks; ++c) mbar_wait_bounded(&full[c % N], (c / N) & 1u, kDrainLimitNs);
 }
 
+// Tensor memory and the operands' shared memory may only be given up once the products issued have completed.  After a
+// timeout, of whichever warp, nobody has waited for the last of them: some microseconds' work, given a millisecond.
+static __device__ __noinline__ void let_products_end()
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+    __syncwarp();
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                            id_o = idesc(false, C, D, false, true);
         constexpr uint64_t kStage = 6 * kHalfTile / 16, kTile = 2 * kHalfTile / 16, kLow = kHalfTile / 16;
         const uint64_t d_stage = desc128(smem_u32(sm.stage[0][0][0]));
-        bool ok = true, issued = false;
+        bool ok = true;
         Walk<Tc32Params> w(p);
         if (warp == kScoreMmaWarp) {
             // P of chunk `at`, once a and b are pairs.  Its place was last read by the product OX of chunk at - 2,
@@ -224,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     commit(&sm.p32_full[at & 1]);
                 }
                 __syncwarp();
-                issued = true;
             };
             if (w.skip_empty()) score(0);
             for (; ok && w.skip_empty(); ++g) {
@@ -274,7 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                         if (q == 3) commit(&sm.u_full);
                     }
                     __syncwarp();
-                    issued = true;
                 }
                 // X's copy is there, and the outputs that used this place have been read
                 if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
@@ -292,14 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 __syncwarp();
             }
         }
-        // Tensor memory may only be freed once the products issued have completed: after a timeout nobody else
-        // waits for them.
-        if (!ok && issued) {
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 1000000ull) {
-            }
-        }
-        __syncwarp();
     } else if (warp < kTermWarp) {
         // ---- P as a pair, one row per thread; two sets of four warps take the 32-column blocks in turn
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
@@ -580,8 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kStateMmaWarp)
+    if (warp == kStateMmaWarp) {
+        if (*abort) let_products_end();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
 }
 
 }  // namespace
