@@ -125,9 +125,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     fence_after();
     const uint32_t tmem = sm.tmem_base;
     volatile int* abort = &sm.abort;
-    // Waits for phase `phase` of `bar`; false, with the CTA marked to end, when it does not come.
+    // A warp's wait for phase `phase` of `bar`: the same answer for all of its lanes.
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-        return mbar_try_wait(bar, phase & 1u) || wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1u)) ||
+               wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
+    };
+    // For two of them at once.
+    auto wait2 = [&](uint64_t* bar, uint32_t phase, uint64_t* bar2, uint32_t phase2) {
+        const bool here = mbar_try_wait(bar, phase & 1u), here2 = mbar_try_wait(bar2, phase2 & 1u);
+        return __all_sync(0xffffffffu, here && here2) ||
+               (wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status) &&
+                wait_slow(bar2, phase2 & 1u, p.wait_limit_ns, abort, p.status));
     };
     // One arrival for the warp after its lanes' work.
     auto arrive = [&](uint64_t* bar) {
@@ -143,7 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             Walk<TcParams> w(p);
             for (; w.skip_empty() && !*abort; ++w.k, ++g) {
                 const int s = g % STAGES;
-                if (w.k == p.skip_chunk || !wait(&sm.empty[s], g / STAGES + 1)) break;
+                if (w.k == p.skip_chunk ||
+                    !wait_bounded(&sm.empty[s], (g / STAGES + 1) & 1u, p.wait_limit_ns, abort, p.status))
+                    break;
                 const TcMaps& m = p.map[w.role];
                 mbar_arrive_expect_tx(&sm.full[s], 3 * kTileBytes);
                 tma_load_4d(sm.stage[s][1], &m.b, &sm.full[s], 0, w.h, w.token(), w.b);
@@ -186,9 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 ++w.k;
                 if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
                 // the scores are there, and the outputs before have been read
-                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) &&
-                                  (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1))))
-                    break;
+                if (!ok || !(ok = wait2(&sm.p16_full[g & 1], g >> 1, &sm.o_free[(g - 1) & 1], (g - 1) >> 1))) break;
                 fence_after();
                 const uint32_t scores = tmem + kP + C * (g & 1);
                 if (elect()) {
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             for (; ok && w.skip_empty(); ++w.k, ++g) {
                 const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
                 const uint32_t u = tmem + kU, oi = tmem + kOI + 64 * (g & 1);
-                if (!(ok = wait(&sm.full[g % STAGES], g / STAGES) && wait(&sm.u_free, g + 1))) break;
+                if (!(ok = wait2(&sm.full[g % STAGES], g / STAGES, &sm.u_free, g + 1))) break;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = wait(&sm.terms_full[half], g))) break;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                     __syncwarp();
                 }
                 // X's copy is there, and the outputs that used this place have been read
-                if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
+                if (!ok || !(ok = wait2(&sm.x_full, g, &sm.o_free[g & 1], (g - 2) >> 1))) break;
                 fence_after();
                 if (elect()) {
                     mma_ss<false>(oi, a, d_state + 512, id_o);

@@ -190,14 +190,23 @@ struct Walk {
     __device__ bool dirty() const { return valid() < C && n < p.lin.T; }
 };
 
-// The part of a wait that spins, out of line: six kinds of warps share an
-// instruction cache, and their loops have to stay in it.
-static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort, unsigned* status)
+// Waits for phase `parity` of `bar`; false, with the CTA marked to end, when it does not come.
+static __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort,
+                                                    unsigned* status)
 {
     if (mbar_wait_bounded(bar, parity, limit_ns) && !*abort) return true;
     *abort = 1;
     atomicOr(status, kStatusTimeout);
     return false;
+}
+
+// The part of a warp's wait that spins, out of line: six kinds of warps share an
+// instruction cache, and their loops have to stay in it.  All of its lanes get one
+// answer: a phase that ends just at the limit must not part them, since the
+// products and the tensor memory accesses that follow take whole warps.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort, unsigned* status)
+{
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, limit_ns, abort, status));
 }
 
 // What a CTA's last copies may take, whatever limit its other waits have.

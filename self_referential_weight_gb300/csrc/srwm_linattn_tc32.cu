@@ -166,9 +166,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
     fence_after();
     const uint32_t tmem = sm.tmem_base;
     volatile int* abort = &sm.abort;
-    // Waits for phase `phase` of `bar`; false, with the CTA marked to end, when it does not come.
+    // A warp's wait for phase `phase` of `bar`: the same answer for all of its lanes.
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-        return mbar_try_wait(bar, phase & 1u) || wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1u)) ||
+               wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status);
+    };
+    // For two of them at once.
+    auto wait2 = [&](uint64_t* bar, uint32_t phase, uint64_t* bar2, uint32_t phase2) {
+        const bool here = mbar_try_wait(bar, phase & 1u), here2 = mbar_try_wait(bar2, phase2 & 1u);
+        return __all_sync(0xffffffffu, here && here2) ||
+               (wait_slow(bar, phase & 1u, p.wait_limit_ns, abort, p.status) &&
+                wait_slow(bar2, phase2 & 1u, p.wait_limit_ns, abort, p.status));
     };
     // One arrival for the warp after its lanes' work.
     auto arrive = [&](uint64_t* bar) {
@@ -184,7 +192,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             Walk<Tc32Params> w(p);
             for (; w.skip_empty() && !*abort; ++w.k, ++g) {
                 const int s = g % STAGES;
-                if (w.k == p.skip_chunk || !wait(&sm.empty[s], g / STAGES + 1)) break;
+                if (w.k == p.skip_chunk ||
+                    !wait_bounded(&sm.empty[s], (g / STAGES + 1) & 1u, p.wait_limit_ns, abort, p.status))
+                    break;
                 const Tc32Maps& m = p.map[w.role];
                 sm.valid[g % RING] = w.valid();
                 mbar_arrive_expect_tx(&sm.full[s], 6 * kHalfTile);
@@ -231,9 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                 ++w.k;
                 if (w.skip_empty()) score(g + 1);   // the next chunk's, ahead of this one's output
                 // the scores are there, and the outputs before have been read
-                if (!ok || !(ok = wait(&sm.p16_full[g & 1], g >> 1) &&
-                                  (g == 0 || wait(&sm.o_free[(g - 1) & 1], (g - 1) >> 1))))
-                    break;
+                if (!ok || !(ok = wait2(&sm.p16_full[g & 1], g >> 1, &sm.o_free[(g - 1) & 1], (g - 1) >> 1))) break;
                 fence_after();
                 const uint32_t scores = tmem + kP + C * (g & 1);
                 if (elect()) {
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             for (; ok && w.skip_empty(); ++w.k, ++g) {
                 const uint64_t a = d_stage + kStage * (g % STAGES), c = a + 2 * kTile;
                 const uint32_t u = tmem + kU, oi = tmem + kOI + 64 * (g & 1);
-                if (!(ok = wait(&sm.ready_ab[g % STAGES], g / STAGES) && wait(&sm.ready_c[g % STAGES], g / STAGES) &&
+                if (!(ok = wait2(&sm.ready_ab[g % STAGES], g / STAGES, &sm.ready_c[g % STAGES], g / STAGES) &&
                            wait(&sm.u_free, g + 1)))
                     break;
 #pragma unroll 1
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
                     __syncwarp();
                 }
                 // X's copy is there, and the outputs that used this place have been read
-                if (!ok || !(ok = wait(&sm.x_full, g) && (g < 2 || wait(&sm.o_free[g & 1], (g - 2) >> 1)))) break;
+                if (!ok || !(ok = wait2(&sm.x_full, g, &sm.o_free[g & 1], (g - 2) >> 1))) break;
                 fence_after();
                 if (elect()) {
                     mma_ss<false>(oi, a + kLow, d_state, id_o);
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const int c0 = w.rev ? own : 0, c1 = w.rev ? 3 : own;
             const int first = c0 + ((c0 ^ set) & 1);   // this set's first block on the causal side
             for (; w.k < w.chunks; ++w.k, ++g) {
-                if (!(ok = wait(&sm.p32_full[g & 1], g >> 1) && wait(&sm.norm_full[g % STAGES], g / STAGES))) break;
+                if (!(ok = wait2(&sm.p32_full[g & 1], g >> 1, &sm.norm_full[g % STAGES], g / STAGES))) break;
                 fence_after();
                 const int(&e)[3][8] = sm.exps[g % RING];
                 const int ef = sm.norm[g % RING][row >> 4] + 20;
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc32_kernel(const __grid_
             const float lg = decay_log2(p.lin.log_decay[w.h]);
             for (; ok && w.k < w.chunks; ++w.k, ++g) {
                 const int s = g % STAGES, nc = w.valid();
-                if (!(ok = wait(&sm.ready_ab[s], g / STAGES) && wait(&sm.ready_c[s], g / STAGES))) break;
+                if (!(ok = wait2(&sm.ready_ab[s], g / STAGES, &sm.ready_c[s], g / STAGES))) break;
                 const int(&e)[3][8] = sm.exps[g % RING];
                 // The largest 2^(eb + ec) g^gap among the column groups on the causal side of 16 rows (lanes 0-7 the
                 // first of this warp's, 8-15 the others: a group that no row sees must not cost them their bits), and

@@ -105,3 +105,30 @@ def test_missing_chunk_of_linear_attention(short_waits, B, dtype):
     binding.srwm_debug_skip_x_chunk(1)
     got = binding.srwm_linattn_forward(q, k, v, lg, lengths=short)
     assert binding.srwm_last_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_attention_under_the_shortest_limit(short_waits, dtype):
+    """Waits that run out anywhere, at or beside the end of what they wait for:
+    each call ends, says so or is right, and the next ones are right."""
+    B, T, H, d = 60, 400, 5, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    q, k, v, do = (torch.randn(B, T, H, d, generator=g, device=DEV).to(dtype) for _ in range(4))
+    lg = torch.full((H,), -0.05, device=DEV)
+    lengths = (torch.arange(B, device=DEV) * 37 % (T + 1)).int()
+
+    def run():
+        return (binding.srwm_linattn_forward(q, k, v, lg, lengths=lengths) +
+                binding.srwm_linattn_backward(q, k, v, lg, do, lengths=lengths))
+
+    want = run()
+    assert binding.srwm_last_device_status() == 0
+    for limit in (1000, 1500, 2500, 5000, 20000):
+        binding.srwm_set_wait_limit_ns(limit)
+        got = run()
+        status = binding.srwm_last_device_status()
+        assert status in (0, binding.SRWM_ERR_TIMEOUT)
+        assert status or all(torch.equal(x, y) for x, y in zip(want, got))
+    binding.srwm_set_wait_limit_ns(50_000_000)
+    got = run()
+    assert binding.srwm_last_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(want, got))
