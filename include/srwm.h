@@ -367,9 +367,9 @@ int srwm_debug_set_layer_gemm(int mode);
  *         the 16 positions, so that what a strong decay leaves of a token
  *         followed by zeros may be lost below that.
  *   bf16  inputs as they are, or as one fp16 scaled in the same way; a score
- *         enters its product as one bf16 (2^-8 of it) where d = 64 and
- *         T >= 128, else as one fp16 (2^-11), the state its product with 2^-11
- *         or better.  S_final is good to fp32.
+ *         and the state enter their products as pairs of bf16 (2^-16) where
+ *         d = 64, T >= 128 and the axis is not split, else as one fp16 (2^-11).
+ *         S_final is good to fp32.
  * Inputs must be finite: an infinity or NaN in a valid token reaches every
  * output of its sequence and head from its chunk on (the tokens from the last
  * multiple of d before it, or of 128 at d = 64), and of no other; rows past

@@ -34,7 +34,8 @@
 // fp16 values are one fp16 exactly.  The weighted rows of b always enter the
 // state as pairs, so the state is good to fp32 for every type.  The score P
 // and the state's copy enter their products as pairs for fp32 and fp16, and as
-// one fp16 (2^-11 of each value) for bf16, whose outputs round by 2^-8.
+// one fp16 (2^-11 of each value) for bf16, whose outputs round by 2^-8: as pairs
+// the batch above takes 64.6 us, for the same relative error but for 0.6 % of it.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -10,13 +10,13 @@
 //   U    = sum_j (w_j b_j) c_j^T,  X <- g^nc X + U        w_j = alpha_u g^(nc-1-j), or alpha_u g^(j+1)
 // Five products per chunk: P = a b^T (128 x 128 x 64), OX (P from tensor
 // memory, 128 x 64 x 128), OI (128 x 64 x 64), U (64 x 64 x 128).  a, b, c are
-// the bf16 inputs themselves.  P enters its product as bf16 (2^-8 of each score at
-// most, as much as the outputs' own rounding; as a pair it costs 6 % of the
-// forward pass and 9 % of the gradients for 0.0017 instead of 0.0018 of relative
-// error), X as a bf16 (high, low) pair (2^-17), w_j b_j as three bf16 terms
-// (2^-24), so that X, which is kept in fp32 registers, is good to fp32.
+// the bf16 inputs themselves.  P and X enter their products as bf16 (high, low)
+// pairs (2^-16), w_j b_j as three bf16 terms (2^-24), so that X, which is kept in
+// fp32 registers, is good to fp32.  P as one bf16 took 63.7 instead of 67.3 us for the
+// prompt below and 150 instead of 162 for its gradients, for a relative error of
+// 0.00185 instead of the 0.00166 that the outputs' own rounding leaves.
 //
-// Warps: 0-7 turn P into bf16 (one row per thread); 8-11 write the weighted b's
+// Warps: 0-7 turn P into its pair (one row per thread); 8-11 write the weighted b's
 // terms; 12-15 hold X, add U to it and leave its pair in shared memory; 16-19
 // write the outputs; 20 issues the TMA loads (three stages of a, b, c), 21 and 22
 // the products.  Every stage of a chunk's work runs beside other stages of the
@@ -52,8 +52,8 @@ constexpr int kThreads = 736;
 constexpr int kTermWarp = 8, kStateWarp = 12, kOutWarp = 16, kLoadWarp = 20, kScoreMmaWarp = 21,
               kStateMmaWarp = 22;
 
-// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's bf16
-// values go over it: 16 columns of fp32 become the first 8 of them.
+// Tensor memory columns: P of two chunks, OI of two chunks, OX, U.  P's pair
+// goes over it: 16 columns of fp32 become 8 of high and 8 of low halves.
 constexpr uint32_t kP = 0, kOI = 256, kOX = 384, kU = 448, kTmemCols = 512;
 
 struct TcMaps {
@@ -200,9 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 fence_after();
                 const uint32_t scores = tmem + kP + C * (g & 1);
                 if (elect()) {
-                    mma_ts<false>(tmem + kOX, scores, c, id_o);
+                    // low halves first, since each sum is cut off to fp32
+                    mma_ts<false>(tmem + kOX, scores + 8, c, id_o);
 #pragma unroll
-                    for (int k = 1; k < C / 16; ++k) mma_ts<true>(tmem + kOX, scores + 16 * k, c + 128 * k, id_o);
+                    for (int k = 1; k < 2 * C / 16; ++k)
+                        mma_ts<true>(tmem + kOX, scores + 16 * (k % 8) + 8 * (k < 8), c + 128 * (k % 8), id_o);
                     commit(&sm.o_full[g & 1]);
                     commit(&sm.empty[g % STAGES]);
                 }
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
         }
     } else if (warp < kTermWarp) {
-        // ---- P as bf16, one row per thread; two sets of four warps take the 32-column blocks in turn
+        // ---- P as a pair, one row per thread; two sets of four warps take the 32-column blocks in turn
         const int own = warp & 3, set = warp >> 2, row = 32 * own + lane;
         float* decay = sm.decay[warp];
         bool ok = true;
@@ -278,13 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 for (int cb = set; cb < 4; cb += 2)   // the side that is masked
                     if (cb < c0 || cb > c1) {
                         const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        tmem_store8(P + 32 * cb, zero);
-                        tmem_store8(P + 32 * cb + 16, zero);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tmem_store8(P + 32 * cb + 8 * k, zero);
                     }
 #pragma unroll 1
                 for (int hb = 2 * first; hb <= 2 * c1 + 1; hb += (hb & 1) ? 3 : 1) {   // 16 columns of this set's blocks
                     const int cb = hb >> 1, x0 = 16 * (hb & 1);
-                    uint32_t r[16], hi[8];
+                    uint32_t r[16], hi[8], lo[8];
                     tmem_rows(P + 16 * hb, r);
                     const int beyond = w.rev ? 32 * cb - row : row - 32 * cb - 31;
                     const float f = exp2f(lg * static_cast<float>(max(0, beyond)));
@@ -293,9 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float2 w = mul2(both(f), make_float2(col[2 * k], col[2 * k + 1]));
-                        hi[k] = pack_bf16(mul2(as_float2(r[2 * k], r[2 * k + 1]), w));
+                        float2 v = mul2(as_float2(r[2 * k], r[2 * k + 1]), w);
+                        hi[k] = take_bf16(v);
+                        lo[k] = pack_bf16(v);
                     }
                     tmem_store8(P + 16 * hb, hi);
+                    tmem_store8(P + 16 * hb + 8, lo);
                 }
                 tmem_store_wait();
                 fence_before();

@@ -632,3 +632,24 @@ def test_gradients_under_a_decay_that_is_nan(T, d, dtype):
     for x, y in zip(got, was):
         heads = (lambda t: t[:, ::2]) if x is got[3] else (lambda t: t[:, :, ::2])
         assert torch.equal(heads(x), heads(y))
+
+
+@pytest.mark.parametrize("T", [128, 200, 390])
+def test_scores_of_wide_chunks_keep_their_bits(T):
+    """bf16, d = 64, T >= 128: the score and the state enter their products as
+    pairs of bf16, off by half a step of a half step, 2^-16 each; sums and
+    weighted rows as in fp32 (see above); the output rounds by 2^-8 of itself."""
+    d, q, k, v, lg, S0, do, dS = 64, *make(T, 3, T, 5, 64, BF16)
+    tol = 2 * 2.0 ** -16 + (d + 64 + 2 * -(-T // d)) * 2.0 ** -23 + 32 * 2.0 ** -24
+
+    def near(x, ref, size):
+        room = (1 + 2.0 ** -7) * tol * size + 2.0 ** -8 * ref.abs() + (d + T) * 2.0 ** -133
+        assert ((x.double() - ref).abs() <= room).all(), float(((x.double() - ref).abs() / room).max())
+
+    for S, D in ((S0, dS), (None, None)):
+        args = (q, k, v, lg, d ** -0.5)
+        near(binding.srwm_linattn_forward(*args[:4], S_init=S)[0], oracle.forward(*args, S)[0],
+             oracle.sizes(*(x.float() for x in args[:3]), *args[3:], S)[0])
+        got = binding.srwm_linattn_backward(*args[:4], do, S_init=S, dS_final=D)
+        for x, r, a in list(zip(got, oracle.grads(*args, do, S, None, D), oracle.grad_sizes(*args, do, S, None, D)))[:3]:
+            near(x, r, a)
