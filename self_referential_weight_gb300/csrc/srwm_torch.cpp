@@ -112,12 +112,16 @@ const int* lengths_address(PyObject* o, int64_t B)
     return static_cast<const int*>(data(t));
 }
 
-float scale_of(PyObject* o, int64_t d)
+float number(PyObject* o)
 {
-    if (o == Py_None) return static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return static_cast<float>(v);
+}
+
+float scale_of(PyObject* o, int64_t d)
+{
+    return o == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : number(o);
 }
 
 long long integer(PyObject* o)
@@ -239,6 +243,7 @@ PyObject* groupnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t na)
 {
     HANDLE_TH_ERRORS
     count(na, 10);
+    const float eps = number(a[4]);
     const at::Tensor& x = tensor(a[0], "x");
     const int code = dtype_code(x, "x");
     four(x, "x", 3);
@@ -252,7 +257,7 @@ PyObject* groupnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t na)
     const int rc = srwm_groupnorm_forward(
         px, static_cast<const float*>(optional(a[1], "gamma", channels, at::kFloat)),
         static_cast<const float*>(optional(a[2], "beta", channels, at::kFloat)), code, N, L, as_int(C), as_int(G),
-        scale_of(a[4], 1), static_cast<int>(integer(a[5])), data(y), static_cast<float*>(data(mean)),
+        eps, static_cast<int>(integer(a[5])), data(y), static_cast<float*>(data(mean)),
         static_cast<float*>(data(rstd)), ws.data_ptr(), ws.nbytes(), stream_of(x));
     return finish(rc, "srwm_groupnorm_forward", {y, mean, rstd});
     END_HANDLE_TH_ERRORS

@@ -8,6 +8,7 @@ import torch
 
 from oracle import groupnorm as gn_oracle
 from oracle import linattn as la_oracle
+from self_referential_weight_gb300 import binding
 from self_referential_weight_gb300 import build as lib_build
 
 A = 0x100000  # fake, 16-byte aligned "device" addresses: never dereferenced
@@ -176,3 +177,13 @@ def test_groupnorm_oracle_against_torch_and_differences(act):
         up[i], dn[i] = base[i] + h * u, base[i] - h * u
         f = lambda a: float((gn_oracle.forward(a[0], a[1], a[2], 2, 1e-5, act)[0] * dy).sum())  # noqa: E731
         assert abs((f(up) - f(dn)) / (2 * h) - float((gr * u).sum())) < 1e-6 * (1 + abs(float((gr * u).sum())))
+
+
+def test_groupnorm_wants_an_eps():
+    """None is no eps (it was taken as 1)."""
+    x = torch.zeros(2, 3, 16)
+    for eps in (None, "small"):
+        with pytest.raises(TypeError):
+            binding.srwm_groupnorm_forward(x, None, None, 2, eps=eps)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.srwm_groupnorm_forward(x, None, None, 2)
