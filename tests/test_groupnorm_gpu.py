@@ -323,3 +323,21 @@ def test_relu_border_over_positions():
     want = wide[1] * (dh - dh.mean((1, 2), keepdim=True) - xh * (dh * xh).mean((1, 2), keepdim=True))
     assert ((dx.double() - want).abs() <= 2.0 ** -16 * wide[1] * (1 + want.abs().amax())).all()
     assert ((db.double() - dz.sum((0, 1))).abs() <= 2.0 ** -14 * dz.abs().sum((0, 1))).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(70000, 1, 64, 2), (9000, 1, 96, 3), (9001, 1, 520, 1), (301, 1, 24, 8), (300, 50, 64, 8),
+                                   (1000, 7, 64, 64), (5, 900, 512, 16), (1, 120001, 64, 1), (3, 40000, 256, 8)], ids=str)
+def test_parameter_gradients_count_every_position_once(shape, dtype):
+    """Whole numbers, mean 0 and rstd 1: every product is at most 32 and every
+    partial sum below 2^24, so the sums are exact in any order, and one
+    position or range left out or taken twice changes them."""
+    N, L, C, G = shape
+    assert 32 * N * L < 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(N + L)
+    x = torch.randint(-4, 5, (N, L, C), generator=g, device=DEV).to(dtype)
+    dy = torch.randint(-8, 9, (N, L, C), generator=g, device=DEV).to(dtype)
+    mean, rstd = torch.zeros(N, G, device=DEV), torch.ones(N, G, device=DEV)
+    _, dg, db = binding.srwm_groupnorm_backward(x, None, None, G, mean, rstd, dy)
+    assert torch.equal(db.double(), dy.double().sum((0, 1)))
+    assert torch.equal(dg.double(), (dy.double() * x.double()).sum((0, 1)))
