@@ -104,8 +104,8 @@ __device__ __forceinline__ void store_vec(void* p, size_t element, const uint4& 
 }
 
 // ---------------------------------------------------------------- activation
-// sigmoid(z), good to a few units of 2^-23: exp underflows to 0 and overflows to
-// infinity, whose reciprocal is 0.
+// sigmoid(z), good to about (|z| + 3) 2^-23 of itself for z < 0, where the rounding of exp's argument grows with it,
+// and to 3 * 2^-23 above: exp underflows to 0 and overflows to infinity, whose reciprocal is 0.
 __device__ __forceinline__ float sigmoid(float z)
 {
     float e;
