@@ -344,8 +344,8 @@ int srwm_debug_set_layer_gemm(int mode);
  *              NULL for zero
  *   lengths    [B] int32 on the device (4-byte aligned), the valid tokens of
  *              each sequence (its first ones), or NULL for T each; a value below 0 counts as 0,
- *              one above T as T.  Rows of q, k, v at and past the length are
- *              not read, so they may hold anything.
+ *              one above T as T.  Rows of q, k, v at and past the length do
+ *              not count, so they may hold anything; they may be read.
  *   dtype      enum srwm_dtype of q, k, v and o
  *   scale      factor on o, e.g. 1 / sqrt(d)
  *   o          [B, T, H, d] of `dtype`, contiguous, written; rows at and past
@@ -362,13 +362,19 @@ int srwm_debug_set_layer_gemm(int mode);
  * on the tensor cores:
  *   fp32, fp16  values as (high, low) pairs of fp16 after scaling by powers of
  *         two (an fp16 input is one of them): about 22 bits relative to the
- *         largest magnitude among 16 neighbouring tokens of a head, and never
- *         finer than 2^-39 of what that magnitude would give at the nearest of
- *         the 16 positions, so that what a strong decay leaves of a token
- *         followed by zeros may be lost below that.
+ *         largest magnitude among 16 neighbouring tokens of a head.  Scores,
+ *         weighted keys and the state enter their products as such pairs too,
+ *         never finer than 2^-39 of the largest product of two such magnitudes
+ *         that takes part: for the scores of 16 tokens among the tokens of
+ *         their chunk that they see, each decayed as the nearest of its 16, and
+ *         the state; for the state's update among the chunk's tokens; for the
+ *         state itself the sum of these over all earlier tokens.  So what lies
+ *         that far below may be lost: what a strong decay leaves of a token
+ *         followed by zeros, or a key's column far below its other columns.
  *   bf16  inputs as they are, or as one fp16 scaled in the same way; a score
  *         and the state enter their products as pairs of bf16 (2^-16) where
  *         d = 64, T >= 128 and the axis is not split, else as one fp16 (2^-11).
+ *         In the former case q.k itself must stay within fp32's range.
  *         S_final is good to fp32.
  * Inputs must be finite: an infinity or NaN in a valid token reaches every
  * output of its sequence and head from its chunk on (the tokens from the last
@@ -409,7 +415,7 @@ int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld,
  * dv and dk run from the last token to the first: a value that is not finite
  * reaches them from its chunk on towards the first token.
  *
- *   do_        [B, T, H, d] of `dtype`, contiguous: dL/do (not read at and
+ *   do_        [B, T, H, d] of `dtype`, contiguous: dL/do (does not count at and
  *              past a sequence's length)
  *   dS_final   [B, H, d, d] fp32: dL/dS_final, or NULL for zero
  *   dq, dk, dv [B, T, H, d] of `dtype`, token rows ld_grad elements apart

@@ -653,3 +653,12 @@ def test_scores_of_wide_chunks_keep_their_bits(T):
         got = binding.srwm_linattn_backward(*args[:4], do, S_init=S, dS_final=D)
         for x, r, a in list(zip(got, oracle.grads(*args, do, S, None, D), oracle.grad_sizes(*args, do, S, None, D)))[:3]:
             near(x, r, a)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_values_in_wide_chunks(dtype):
+    """d = 64, T >= 128: scores and states far from 1, in fp32's range."""
+    q, k, v, lg, S0, do, dS = make(5, 2, 200, 2, 64, dtype, -0.5)
+    for a, b, c in ((1e-6, 1e15, 1e-4), (1e12, 1e-3, 1e8), (1e-12, 1e-9, 1e5)):
+        check_forward(*((x.float() * s).to(dtype) for x, s in ((q, a), (k, b), (v, c))), lg)
+        check_backward(*((x.float() * s).to(dtype) for x, s in ((q, a), (k, b), (v, c))), lg, (do.float() / a).to(dtype))
