@@ -8,9 +8,10 @@
 // fp32 operations a token, against a whole chunk of D (or 128) tokens in the
 // chunked kernels however few of them there are.
 //
-// What bounds it: at D = 64 the fp32 operations (2048 streams, gradients, T = 40:
-// 146 us, 28 TFLOP/s of fp32) and below T = 10 the states, read and written once
-// (T = 1: 34 us for 134 MB); at D = 16 a token's latency, about 0.1 us.  Several
+// What bounds it: at D = 64 shared memory, from which every warp loads a token's a
+// and b in full (2048 streams, gradients, T = 40: 130 us, with L1 at 86 % of its rate, the
+// fp32 pipe at 62 % and three warps on a scheduler), and below T = 10 the states,
+// read and written once (T = 1: 34 us for 134 MB); at D = 16 a token's latency, about 0.1 us.  Several
 // tokens are unrolled so that one's loads run under another's sums (d = 16, 2048
 // streams of 26 tokens in fp32: 7.5 us one by one, 6.4 by four).
 #include <cuda_runtime.h>
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
     // and are by 1.5e-7 now).
     const Decay dec = decay_over(decay_log2(p.log_decay[h]), 1);
     float off = 0.f;
-    const float au = R.alpha_u_man * pow2i(R.alpha_u_exp);
-    const float undecayed = n > 0 ? fmaf(0.f, dec.m, 1.f) : 1.f;   // 1, or NaN under a decay that is NaN
+    // NaN under a decay that is NaN, which the first token in reverse would not show otherwise
+    const float au = R.alpha_u_man * pow2i(R.alpha_u_exp) + (n > 0 ? 0.f * dec.m : 0.f);
     E* const out = static_cast<E*>(R.out) + token0 * R.ldo + h * D + col;
     E* to = out + (rev ? (n - 1) * R.ldo : 0);
     const long long step = rev ? -R.ldo : R.ldo;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_con
             const int i = TT * tile + r;
             const float4* a = reinterpret_cast<const float4*>(rows + r * D);
             const float4* k = a + TT * D / 4;
-            float g = undecayed;
+            float g = 1.f;
             if (i < n && !(rev && i == 0)) {
                 g = dec.c + (dec.m - off);
                 off += (g - dec.c) - dec.m;
