@@ -197,13 +197,13 @@ LinPlan linattn_plan(int dtype, int B, int T, int H, int d, int roles)
     segments = std::min(segments, static_cast<long long>(2 * root));
     if (segments < 2 || chunks < 8) return whole;   // below, the second launch costs what it saves
     if (d == 64 && dtype != SRWM_F16) {
-        // Against that, the tcgen05 kernels take a whole stream's 128 tokens in 1.45 us (bf16) or 4.9 us (fp32) however
-        // few streams there are; the split takes a time with the root of the chunks, and 2.0 or 3.6 us for each
-        // stream's 8192 tokens (split and whole, fp32: 10 streams of 1200 24 and 51 us, 64 of 2500 91 and 104; bf16: 3 of
-        // 1200 17 and 19, 16 of 2500 27 and 34, 32 of 8192 81 and 98).
+        // Against that, the tcgen05 kernels take a whole stream's 128 tokens in 1.55 us (bf16) or 4.6 to 4.9 us (fp32)
+        // however few streams there are; the split takes a time with the root of the chunks, and 2.0 or 3.6 us for each
+        // stream's 8192 tokens (split and whole, fp32: 10 streams of 1200 23 and 50 us, 64 of 2500 89 and 96; bf16: 3 of
+        // 1200 16 and 20, 16 of 2500 26 and 36, 32 of 8192 79 and 104).
         const bool wide = dtype == SRWM_F32;
         const double split = 6 + root * (wide ? 3.0 : 2.0) + static_cast<double>(ctas) * T * (wide ? 3.6 : 2.0) / 8192;
-        if (split >= 5.0 + T / 128.0 * (wide ? 4.9 : 1.45)) return whole;
+        if (split >= 5.0 + T / 128.0 * (wide ? 4.9 : 1.55)) return whole;
     }
     const int per = static_cast<int>((chunks + segments - 1) / segments);
     return {per * d, (chunks + per - 1) / per};
