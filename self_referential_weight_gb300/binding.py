@@ -93,25 +93,14 @@ def _lib():
         lib.srwm_layer_workspace_bytes.restype = SZ
         lib.srwm_debug_set_layer_gemm.argtypes = [I]
         lib.srwm_debug_set_layer_gemm.restype = I
-        F = ctypes.c_float
         lib.srwm_linattn_workspace_bytes.argtypes = [I, I, I, I]
         lib.srwm_linattn_workspace_bytes.restype = SZ
-        lib.srwm_linattn_forward.argtypes = [P, P, P, LL, P, P, P, I, I, I, I, I, F, P, P, P, SZ, P]
-        lib.srwm_linattn_forward.restype = I
-        lib.srwm_linattn_step.argtypes = [P, P, P, LL, P, P, I, I, I, I, F, P, P, P]
-        lib.srwm_linattn_step.restype = I
         lib.srwm_linattn_backward_workspace_bytes.argtypes = [I, I, I, I]
         lib.srwm_linattn_backward_workspace_bytes.restype = SZ
-        lib.srwm_linattn_backward.argtypes = [P, P, P, LL, P, P, P, I, I, I, I, I, F, P, P, P, P, P, LL, P, P, SZ, P]
-        lib.srwm_linattn_backward.restype = I
         lib.srwm_groupnorm_workspace_bytes.argtypes = [LL, LL, I, I]
         lib.srwm_groupnorm_workspace_bytes.restype = SZ
-        lib.srwm_groupnorm_forward.argtypes = [P, P, P, I, LL, LL, I, I, F, I, P, P, P, P, SZ, P]
-        lib.srwm_groupnorm_forward.restype = I
         lib.srwm_groupnorm_backward_workspace_bytes.argtypes = [LL, LL, I, I]
         lib.srwm_groupnorm_backward_workspace_bytes.restype = SZ
-        lib.srwm_groupnorm_backward.argtypes = [P, P, P, P, P, P, I, LL, LL, I, I, I, P, P, P, P, SZ, P]
-        lib.srwm_groupnorm_backward.restype = I
         lib.srwm_status_string.argtypes = [I]
         lib.srwm_status_string.restype = ctypes.c_char_p
         lib.srwm_last_device_status.argtypes = [P]
