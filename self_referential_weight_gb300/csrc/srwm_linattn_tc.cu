@@ -26,11 +26,11 @@
 // bounded; a timeout sets the status word and ends the CTA after its copies and
 // products in flight.
 //
-// What bounds it: 512 streams of 1024 tokens (268 MB in and out) take 60.6 us,
-// 4.4 TB/s or 0.67 of the copy rate, their gradients 148 us; the chunked
+// What bounds it: 512 streams of 1024 tokens (268 MB in and out) take 64.6 us,
+// 4.3 TB/s or 0.63 of the copy rate, their gradients 159 us; the chunked
 // mma.sync kernel (srwm_linattn.cuh) takes 105 and 281 us.  A full chunk takes
-// 1.45 us: the products keep the tensor pipe 43 % busy, and the six kinds of
-// warps' loops share the instruction cache (their fetches at 61 % of its rate),
+// 1.55 us: the products keep the tensor pipe 47 % busy, and the six kinds of
+// warps' loops share the instruction cache (their fetches at 54 % of its rate),
 // which is why they are rolled and the waits' slow part is out of line.  512
 // streams on 152 SMs also leave the last of four rounds a third full.
 #include <atomic>

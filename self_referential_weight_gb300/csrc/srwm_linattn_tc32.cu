@@ -18,14 +18,14 @@
 // the outputs; 20-23 convert a and b; 24 issues the TMA loads (two stages), 25 and
 // 26 the products.
 //
-// What bounds it: 128 streams of 8192 tokens (1.08 GB in and out) take 330 us,
-// 0.48 of the copy rate; the chunked mma.sync kernel (srwm_linattn.cuh) takes
-// 505 us split over the axis and 547 unsplit.  A chunk takes 4.9 us, of which
-// its three products per product keep the tensor pipe 25 % busy and the
-// conversions, the terms and the scores' pairs their warps: 38 % of the issue
-// slots, with the instruction cache at 56 % of its rate.  Two stages of 96 KB
-// leave no room for a third; a stage released tensor by tensor measured 327 us
-// here and 245 instead of 226 us for gradients of 512 streams of 512 tokens.
+// What bounds it: 128 streams of 8192 tokens (1.08 GB in and out) take 316 us,
+// 0.50 of the copy rate; the chunked mma.sync kernel (srwm_linattn.cuh) takes
+// 505 us split over the axis and 547 unsplit.  A chunk takes 4.6 us, of which
+// its three products per product keep the tensor pipe 26 % busy and the
+// conversions, the terms and the scores' pairs their warps: 41 % of the issue
+// slots, with the instruction cache at 51 % of its rate.  Two stages of 96 KB
+// leave no room for a third; a stage released tensor by tensor gained 1 % here
+// and cost 8 % in gradients of 512 streams of 512 tokens, which take 217 us.
 #include <atomic>
 
 #include "srwm_check.h"
