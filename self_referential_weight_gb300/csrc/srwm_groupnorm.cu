@@ -975,8 +975,11 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     // inputs are split by channels down to 256 bytes of a position, then by
     // positions, then by channels down to 64 bytes, small ones by channels first
     // (101 x 441 x 64 in bf16 backward: 13.3 us by positions, 11.7 by channels;
-    // 208 x 1764 x 64 in fp32 forward: 41 and 55): a cluster's exchange costs a
-    // small call more than short pieces of memory do.
+    // 208 x 1764 x 64 in fp32 forward: 44 and 68): a cluster's exchange costs a
+    // small call more than short pieces of memory do.  48 MB lie between the two;
+    // more positions move the border down (700 x 441 x 64 in bf16 forward, 38 MB:
+    // 28.0 by positions, 25.3 by channels; 110 x 1764 x 64 in bf16, 24 MB: 20.0 and
+    // 22.2, in fp32, 47 MB: 24.3 and 31.4), which the rule does not follow.
     SlabPlan s{};
     s.cluster = 1;
     s.groups = G;
@@ -1003,7 +1006,8 @@ GnPlan gn_plan(int e, long long N, long long L, int C, int G, bool grad)
     const int tile = s.cblk / V;
     s.rows = static_cast<int>((L + s.cluster - 1) / s.cluster);
     const long long vectors = static_cast<long long>(s.rows) * tile;
-    // fewer threads per sum to exchange; more where one or two CTAs have an SM to themselves
+    // fewer threads per sum to exchange; more where one or two CTAs have an SM to themselves (gradients in bf16 with 256 and
+    // 128 threads: 300 x 7000 x 64 517 and 586 us, 600 x 1200 x 64 154 and 110)
     s.threads = bytes() > 80 * 1024 ? 256 : vectors >= 512 ? 128 : vectors >= 128 ? 64 : 32;
     while (s.threads < tile) s.threads *= 2;
     // fp32 gradients leave room for a second CTA on the SM, or the split way is faster though it reads x and dy twice
