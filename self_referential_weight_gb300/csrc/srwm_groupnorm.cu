@@ -135,7 +135,8 @@ __device__ __forceinline__ float2 act2(float2 z)
     return make_float2(act<ACT>(z.x), act<ACT>(z.y));
 }
 
-// (x - mean) rstd g + b in pairs of fp32: each rounding's error is kept as a second number.
+// (x - mean) rstd g + b in pairs of fp32: each rounding's error is kept as a second number (Knuth's sum of two
+// numbers with its error; a product's error by fma).
 __device__ __noinline__ float border(float x, float mean, float rstd, float g, float b)
 {
     auto sum = [](float u, float v, float& err) {
