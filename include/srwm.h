@@ -24,8 +24,8 @@
  *     16-byte aligned, unless an entry point says otherwise.  The caller owns
  *     all buffers.  srwm_forward, srwm_forward_balanced,
  *     srwm_forward_balanced_noalloc, srwm_forward_from, srwm_step,
- *     srwm_backward and the srwm_linattn_* and srwm_groupnorm_* entry points
- *     make no device allocation.
+ *     srwm_backward and the srwm_linattn_*, srwm_groupnorm_*, srwm_conv_*,
+ *     srwm_ssm_* and srwm_rmsnorm_* entry points make no device allocation.
  *   - State the library keeps, per device, for the life of the process:
  *       * the device status word (srwm_last_device_status), a file-scope
  *         __device__ variable, present once the library is loaded; its device
@@ -47,9 +47,10 @@
  *     stream) and the call returns without waiting.  Argument errors are
  *     returned before anything is enqueued; nothing is written then.
  *   - Supported: d in {16, 32, 64}, n_lr in {1, 4}, softmax_input in {0, 1}.
- *   - Outputs must not overlap inputs or each other (srwm_step and
- *     srwm_linattn_step alone allow the state's output to be its input
- *     exactly, for an in-place update).
+ *   - Outputs must not overlap inputs or each other (srwm_step,
+ *     srwm_linattn_step, srwm_conv_step and srwm_ssm_step alone allow the
+ *     state's output to be its input exactly, for an in-place update, and
+ *     srwm_rmsnorm_forward the residual's).
  *   - Results are deterministic: the same inputs give the same bits.
  */
 #ifndef SRWM_H
@@ -74,18 +75,24 @@ enum srwm_status {
     SRWM_ERR_NOT_DEVICE = 8   /* a pointer is not device-accessible CUDA memory           */
 };
 
-/* Element types of the operators that take more than fp32 (linear attention, group norm). */
+/* Element types of the operators that take more than fp32 (linear attention, group norm, and those after them). */
 enum srwm_dtype {
     SRWM_F32 = 0,
     SRWM_BF16 = 1,
     SRWM_F16 = 2
 };
 
-/* Activations of srwm_groupnorm_forward and srwm_groupnorm_backward. */
+/* Activations of the srwm_groupnorm_* and srwm_conv_* entry points (the latter take no ReLU). */
 enum srwm_activation {
     SRWM_ACT_NONE = 0,
     SRWM_ACT_SILU = 1,   /* z * sigmoid(z) */
     SRWM_ACT_RELU = 2    /* max(z, 0); slope 0 at z <= 0 */
+};
+
+/* What srwm_rmsnorm_forward writes. */
+enum srwm_out {
+    SRWM_OUT_SAME = 0,   /* the input's type */
+    SRWM_OUT_E4M3 = 1    /* 8 bits (4 of exponent, 3 of mantissa, no infinity) and scales */
 };
 
 /*
@@ -474,6 +481,214 @@ int srwm_groupnorm_backward(const void* x, const float* gamma, const float* beta
                             const float* rstd, const void* dy, int dtype, long long N, long long L, int C, int G,
                             int activation, void* dx, float* dgamma, float* dbeta, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/*
+ * srwm_conv_forward -- the short causal convolution of each channel over its
+ * last W tokens with an activation, which stands in front of a selective scan:
+ *   y_t[c] = act(bias[c] + sum_j weight[c,j] x_{t-W+1+j}[c]),  j = 0 .. W-1.
+ * Inputs before the first token come from a state of W - 1 rows (its last row
+ * is token -1), or are 0; the state that goes out holds the last W - 1 inputs.
+ *
+ *   x          [B, T, D] of `dtype`; token (b, t) starts at element
+ *              (b * T + t) * ld, its D values are contiguous: contiguous
+ *              (ld = D) or a slice of a packed projection
+ *   ld         elements between two tokens' rows: at least D, a multiple of 16 bytes
+ *   weight     [D, W] fp32
+ *   bias       [D] fp32, or NULL for zeros
+ *   state_init [B, W-1, D] of `dtype`, contiguous, or NULL for zeros
+ *   lengths    [B] int32 on the device (4-byte aligned), the valid tokens of
+ *              each sequence (its first ones), or NULL for T each; a value
+ *              below 0 counts as 0, one above T as T.  Rows of x at and past
+ *              the length are not read.
+ *   activation SRWM_ACT_NONE or SRWM_ACT_SILU
+ *   y          [B, T, D] of `dtype`, contiguous, written; rows at and past a
+ *              sequence's length get zeros
+ *   state_final [B, W-1, D] of `dtype`, contiguous, written: the last W - 1 of
+ *              the state's rows and the valid tokens, copied; or NULL
+ *
+ * Supported: W in {2, 3, 4}, D a multiple of 8; T = 0 is valid (x and y may be
+ * NULL then).  Sums are fp32 and rounded once.  An infinity or NaN reaches the
+ * W outputs that see it.
+ */
+int srwm_conv_forward(const void* x, long long ld, const float* weight, const float* bias, const void* state_init,
+                      const int* lengths, int dtype, int B, int T, int D, int W, int activation, void* y,
+                      void* state_final, void* stream);
+
+/*
+ * srwm_conv_step -- one token of the same convolution for every sequence
+ * (decoding).  Feeding state_out back as state_in token by token reproduces
+ * srwm_conv_forward.
+ *
+ *   x          [B, D] of `dtype`, sequence b at element b * ld (as above)
+ *   state_in   [B, W-1, D] of `dtype`
+ *   y          [B, D] of `dtype`, contiguous, written
+ *   state_out  [B, W-1, D] of `dtype`, written: state_in's later rows and x;
+ *              may be the same pointer as state_in (in place) but must not
+ *              partially overlap it
+ */
+int srwm_conv_step(const void* x, long long ld, const float* weight, const float* bias, const void* state_in, int dtype,
+                   int B, int D, int W, int activation, void* y, void* state_out, void* stream);
+
+/*
+ * srwm_conv_backward -- gradients through srwm_conv_forward, from dy = dL/dy
+ * and (optionally) dstate_final = dL/dstate_final, for the same other arguments.
+ *
+ *   dy         [B, T, D] of `dtype`, contiguous (rows at and past a sequence's
+ *              length are not read)
+ *   dstate_final [B, W-1, D] of `dtype`, or NULL for zero
+ *   dx         [B, T, D] of `dtype`, token rows ld_grad elements apart (same
+ *              rules as ld), written; rows at and past the length get zeros
+ *   dweight    [D, W] fp32, written; or NULL
+ *   dbias      [D] fp32, written; or NULL
+ *   dstate_init [B, W-1, D] of `dtype`, written; or NULL
+ *   workspace  device scratch of srwm_conv_backward_workspace_bytes(...)
+ *              bytes, 16-byte aligned, contents irrelevant on entry, untouched
+ *              by others until the work on `stream` ends
+ * The parameters' gradients are summed in an order that depends on the sizes alone.
+ */
+size_t srwm_conv_backward_workspace_bytes(int B, int T, int D, int W);
+int srwm_conv_backward(const void* x, long long ld, const float* weight, const float* bias, const void* state_init,
+                       const int* lengths, int dtype, int B, int T, int D, int W, int activation, const void* dy,
+                       const void* dstate_final, void* dx, long long ld_grad, float* dweight, float* dbias,
+                       void* dstate_init, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * srwm_ssm_forward -- the selective state space scan over whole sequences (a
+ * prompt, or a training batch's forward pass): a memory of N states per channel
+ * whose decay and input each token sets.  Per sequence b, channel c, state n,
+ * with group g = c / (D / G) and s = softplus(dt + dt_bias), or dt + dt_bias:
+ *   h_t[c,n] = exp(s_t[c] A[c,n]) h_{t-1}[c,n] + s_t[c] u_t[c] B_t[g,n]
+ *   y_t[c]   = (sum_n C_t[g,n] h_t[c,n] + skip[c] u_t[c]) * silu(z_t[c])
+ * for t = 1 .. n_b, n_b the sequence's length, from h_0 = h_init[b], or 0.
+ *
+ *   u, dt      [B, T, D] of `dtype`, token rows ld_u and ld_dt elements apart
+ *              (each at least D, a multiple of 16 bytes)
+ *   A          [D, N] fp32, negative for states that decay
+ *   Bt, Ct     [B, T, G, N] of `dtype`, token rows ld_bc elements apart (at
+ *              least G * N, a multiple of 16 bytes): contiguous, or slices of
+ *              one packed projection
+ *   skip       [D] fp32, or NULL for zeros
+ *   z          [B, T, D] of `dtype`, token rows ld_z elements apart, or NULL
+ *              for no gate
+ *   dt_bias    [D] fp32, or NULL for zeros
+ *   softplus   1, or 0: the step is dt + dt_bias itself
+ *   h_init     [B, D, N] fp32, or NULL for zero
+ *   lengths    [B] int32 as in srwm_conv_forward.  Rows at and past the length
+ *              do not count and are not read.
+ *   y          [B, T, D] of `dtype`, contiguous, written; rows at and past a
+ *              sequence's length get zeros
+ *   h_final    [B, D, N] fp32, written: the states at the sequence's end
+ *              (h_init, or 0, for an empty one); or NULL
+ *   workspace  device scratch of srwm_ssm_workspace_bytes(...) bytes, 16-byte
+ *              aligned, contents irrelevant on entry, untouched by others
+ *              until the work on `stream` ends
+ *
+ * Supported: N in {16, 32, 64}, G divides D, D / G a multiple of 8; T = 0 is
+ * valid (u, dt, Bt, Ct and y may be NULL then).  States, steps and sums are
+ * fp32; y is rounded once.  An infinity or NaN in a valid token stays within
+ * its sequence, and within its channel where it stands in u, dt or z.
+ */
+size_t srwm_ssm_workspace_bytes(int B, int T, int D, int N, int G);
+int srwm_ssm_forward(const void* u, long long ld_u, const void* dt, long long ld_dt, const float* A, const void* Bt,
+                     const void* Ct, long long ld_bc, const float* skip, const void* z, long long ld_z,
+                     const float* dt_bias, int softplus, const float* h_init, const int* lengths, int dtype, int B, int T,
+                     int D, int N, int G, void* y, float* h_final, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * srwm_ssm_step -- one token of the same scan for every sequence (decoding).
+ * Feeding h_out back as h_in token by token reproduces srwm_ssm_forward.
+ *
+ *   u, dt, z   [B, D] of `dtype`, sequence b at element b * ld_u, ld_dt, ld_z
+ *   Bt, Ct     [B, G, N] of `dtype`, sequence b at element b * ld_bc
+ *   h_in       [B, D, N] fp32
+ *   y          [B, D] of `dtype`, contiguous, written
+ *   h_out      [B, D, N] fp32, written; may be the same pointer as h_in (in
+ *              place) but must not partially overlap it
+ */
+int srwm_ssm_step(const void* u, long long ld_u, const void* dt, long long ld_dt, const float* A, const void* Bt,
+                  const void* Ct, long long ld_bc, const float* skip, const void* z, long long ld_z, const float* dt_bias,
+                  int softplus, const float* h_in, int dtype, int B, int D, int N, int G, void* y, float* h_out, void* stream);
+
+/*
+ * srwm_ssm_backward -- gradients through srwm_ssm_forward, from dy = dL/dy and
+ * (optionally) dh_final = dL/dh_final, for the same other arguments.  The
+ * states are computed again; nothing of the forward pass is read.
+ *
+ *   dy         [B, T, D] of `dtype`, contiguous (rows at and past a sequence's
+ *              length are not read)
+ *   dh_final   [B, D, N] fp32, or NULL for zero
+ *   du, ddt    [B, T, D] of `dtype`, contiguous, written
+ *   dA         [D, N] fp32, written
+ *   dB, dC     [B, T, G, N] of `dtype`, token rows ld_dbc elements apart (same
+ *              rules as ld_bc), written: sums over a group's channels
+ *   dskip      [D] fp32, written; or NULL
+ *   dz         [B, T, D] of `dtype`, token rows ld_dz elements apart, written;
+ *              not used where z is NULL
+ *   ddt_bias   [D] fp32, written; or NULL
+ *   dh_init    [B, D, N] fp32, written; or NULL
+ *   workspace  device scratch of srwm_ssm_backward_workspace_bytes(...) bytes:
+ *              mostly the states of every eighth token, N / 2 bytes for each
+ *              token and channel
+ * Rows at and past a sequence's length get zeros.  All sums run in fp32 in an
+ * order that depends on the sizes alone.
+ */
+size_t srwm_ssm_backward_workspace_bytes(int B, int T, int D, int N, int G);
+int srwm_ssm_backward(const void* u, long long ld_u, const void* dt, long long ld_dt, const float* A, const void* Bt,
+                      const void* Ct, long long ld_bc, const float* skip, const void* z, long long ld_z,
+                      const float* dt_bias, int softplus, const float* h_init, const int* lengths, int dtype, int B, int T,
+                      int D, int N, int G, const void* dy, const float* dh_final, void* du, void* ddt, float* dA, void* dB,
+                      void* dC, long long ld_dbc, float* dskip, void* dz, long long ld_dz, float* ddt_bias, float* dh_init,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * srwm_rmsnorm_forward -- root-mean-square norm of each row after the
+ * residual's addition: with h = x + residual,
+ *   rstd = 1 / sqrt(mean(h^2) + eps),   y = h * rstd * gamma.
+ * h enters the norm as the fp32 sum; `total` is that sum in `dtype`.
+ *
+ *   x         [N, C] of `dtype`, contiguous
+ *   residual  [N, C] of `dtype`, contiguous, or NULL for zero
+ *   gamma     [C] fp32, or NULL for ones
+ *   eps       > 0
+ *   out       enum srwm_out: y in `dtype`, or in 8 bits with scales
+ *   block     with SRWM_OUT_E4M3 the channels of one scale: 0 for a whole row,
+ *             or 128 (C a multiple of it); else 0
+ *   y         [N, C] of `dtype`, written; with SRWM_OUT_E4M3 [N, C] bytes of
+ *             e4m3: the result over its block's scale, to the nearest (ties to even)
+ *   scale     [N, C / block] fp32 ([N, 1] for a whole row), written with
+ *             SRWM_OUT_E4M3: the block's largest magnitude over 448, so
+ *             y * scale is the result; 0 for a block of zeros, NaN for one
+ *             with a NaN.  Else not used.
+ *   total     [N, C] of `dtype`, written: x + residual, rounded; may be the
+ *             same pointer as residual (the residual stream updated in place)
+ *             but must not partially overlap it; or NULL
+ *   rstd      [N] fp32, written (srwm_rmsnorm_backward reads it); or NULL
+ *
+ * Supported: C a multiple of 8 and at most 8192, N >= 0 below 2^31 (N = 0 does
+ * nothing; x, y and scale may be NULL then).
+ */
+int srwm_rmsnorm_forward(const void* x, const void* residual, const float* gamma, int dtype, long long N, int C, float eps,
+                         int out, int block, void* y, float* scale, void* total, float* rstd, void* stream);
+
+/*
+ * srwm_rmsnorm_backward -- gradients through srwm_rmsnorm_forward, from
+ * dy = dL/dy and (optionally) dtotal, what reaches the sum by other ways (the
+ * residual stream).  The rounding to 8 bits is taken as the identity.
+ *
+ *   total     [N, C] of `dtype`: the forward pass's sum (x where it had no residual)
+ *   rstd      [N] fp32: the forward pass's (its derivative is part of dx)
+ *   dy        [N, C] of `dtype`, contiguous
+ *   dtotal    [N, C] of `dtype`, or NULL for zero
+ *   dx        [N, C] of `dtype`, written: the gradient of x and of the residual
+ *   dgamma    [C] fp32, written (zeros for N = 0): the sum over all rows in an
+ *             order that depends on the sizes alone; or NULL
+ *   workspace device scratch of srwm_rmsnorm_backward_workspace_bytes(...)
+ *             bytes, 16-byte aligned, untouched by others until the work ends
+ */
+size_t srwm_rmsnorm_backward_workspace_bytes(long long N, int C);
+int srwm_rmsnorm_backward(const void* total, const float* gamma, const float* rstd, const void* dy, const void* dtotal,
+                          int dtype, long long N, int C, void* dx, float* dgamma, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* srwm_status_string(int status);

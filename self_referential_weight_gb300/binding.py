@@ -1,6 +1,6 @@
 """Python binding of libsrwm.so: argument marshalling only (ctypes; for the
-linear attention and group norm operators, whose calls can be shorter than
-that, a CPython module, _srwm_torch).
+operators from linear attention on, whose calls can be shorter than that, a
+CPython module, _srwm_torch).
 
 Every step of the recurrence runs in the library's sm_103a kernels; this
 module checks tensor types, allocates outputs with torch when the caller does
@@ -25,6 +25,9 @@ SRWM_ERR_TIMEOUT = 7
 # enum srwm_activation
 _ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 
+# enum srwm_out
+_OUTS = {"same": 0, "e4m3": 1}
+
 EXPORTS = ("srwm_forward", "srwm_forward_balanced", "srwm_forward_balanced_noalloc",
            "srwm_forward_workspace_bytes", "srwm_forward_from", "srwm_forward_host",
            "srwm_forward_host_workspace_bytes",
@@ -32,7 +35,12 @@ EXPORTS = ("srwm_forward", "srwm_forward_balanced", "srwm_forward_balanced_noall
            "srwm_layer_forward", "srwm_layer_workspace_bytes", "srwm_debug_set_layer_gemm",
            "srwm_linattn_forward", "srwm_linattn_workspace_bytes", "srwm_linattn_step", "srwm_linattn_backward",
            "srwm_linattn_backward_workspace_bytes", "srwm_groupnorm_forward", "srwm_groupnorm_workspace_bytes",
-           "srwm_groupnorm_backward", "srwm_groupnorm_backward_workspace_bytes", "srwm_status_string", "srwm_last_device_status", "srwm_set_wait_limit_ns",
+           "srwm_groupnorm_backward", "srwm_groupnorm_backward_workspace_bytes",
+           "srwm_conv_forward", "srwm_conv_step", "srwm_conv_backward", "srwm_conv_backward_workspace_bytes",
+           "srwm_ssm_forward", "srwm_ssm_workspace_bytes", "srwm_ssm_step", "srwm_ssm_backward",
+           "srwm_ssm_backward_workspace_bytes", "srwm_rmsnorm_forward", "srwm_rmsnorm_backward",
+           "srwm_rmsnorm_backward_workspace_bytes",
+           "srwm_status_string", "srwm_last_device_status", "srwm_set_wait_limit_ns",
            "srwm_debug_skip_x_chunk", "srwm_debug_set_segment_len", "srwm_debug_wrap_len",
            "srwm_debug_wrap_pieces", "srwm_debug_chunk_plan", "srwm_probe_fma")
 
@@ -111,6 +119,13 @@ def _lib():
         lib.srwm_debug_skip_x_chunk.restype = I
         lib.srwm_probe_fma.argtypes = [I, I, I, I, P, P]
         lib.srwm_probe_fma.restype = I
+        lib.srwm_conv_backward_workspace_bytes.argtypes = [I, I, I, I]
+        lib.srwm_conv_backward_workspace_bytes.restype = SZ
+        for name in ("srwm_ssm_workspace_bytes", "srwm_ssm_backward_workspace_bytes"):
+            getattr(lib, name).argtypes = [I, I, I, I, I]
+            getattr(lib, name).restype = SZ
+        lib.srwm_rmsnorm_backward_workspace_bytes.argtypes = [LL, I]
+        lib.srwm_rmsnorm_backward_workspace_bytes.restype = SZ
         _LIB = lib
     return _LIB
 
@@ -481,6 +496,139 @@ def srwm_groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, activation="
                                            workspace)
     return (_NATIVE or _native()).groupnorm_backward(x, gamma, beta, groups, mean, rstd, dy, _activation_code(activation),
                                                      dx, dgamma, dbeta, workspace)
+
+
+def srwm_conv_forward(x, weight, bias=None, activation="silu", state_init=None, lengths=None, y=None, state_final=None,
+                      stream=None):
+    """Short causal convolution with an activation: y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}).
+
+    x [B,T,D] is a float32, bfloat16 or float16 CUDA tensor, contiguous or a
+    slice of a packed projection; weight [D,W] (W 2 to 4) and bias [D] are
+    float32; state_init [B,W-1,D] (None: zeros) holds the inputs before the
+    first token, lengths [B] int32 counts each sequence's valid tokens (None:
+    T); activation is "silu" or "none".  Returns (y [B,T,D], state_final)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_conv_forward(x, weight, bias, activation, state_init, lengths, y, state_final)
+    return (_NATIVE or _native()).conv_forward(x, weight, bias, _activation_code(activation), state_init, lengths, y,
+                                               state_final)
+
+
+def srwm_conv_step(x_t, weight, bias, state_in, activation="silu", y_t=None, state_out=None, stream=None):
+    """One token of srwm_conv_forward from per-sequence states: x_t [B,D] -> (y_t [B,D], state_out [B,W-1,D]).
+
+    state_out may be state_in itself (in-place update)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_conv_step(x_t, weight, bias, state_in, activation, y_t, state_out)
+    return (_NATIVE or _native()).conv_step(x_t, weight, bias, state_in, _activation_code(activation), y_t, state_out)
+
+
+def srwm_conv_backward_workspace_bytes(B, T, D, W) -> int:
+    return int(_lib().srwm_conv_backward_workspace_bytes(int(B), int(T), int(D), int(W)))
+
+
+def srwm_conv_backward(x, weight, bias, dy, activation="silu", state_init=None, lengths=None, dstate_final=None, dx=None,
+                       dweight=None, dbias=None, dstate_init=None, workspace=None, stream=None):
+    """Gradients through srwm_conv_forward from dy [B,T,D] and dstate_final [B,W-1,D] (None: zero).
+
+    dx may be a slice of a packed array.  Returns (dx, dweight [D,W], dbias
+    [D], dstate_init [B,W-1,D]); the last two are None where there is no bias
+    or no state_init."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_conv_backward(x, weight, bias, dy, activation, state_init, lengths, dstate_final, dx, dweight,
+                                      dbias, dstate_init, workspace)
+    return (_NATIVE or _native()).conv_backward(x, weight, bias, dy, _activation_code(activation), state_init, lengths,
+                                                dstate_final, dx, dweight, dbias, dstate_init, workspace)
+
+
+def srwm_ssm_workspace_bytes(B, T, D, N, G) -> int:
+    return int(_lib().srwm_ssm_workspace_bytes(int(B), int(T), int(D), int(N), int(G)))
+
+
+def srwm_ssm_forward(u, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, softplus=True, h_init=None, lengths=None, y=None,
+                     h_final=None, workspace=None, stream=None):
+    """Selective state space scan: h_t = exp(s_t A) h_{t-1} + s_t u_t B_t, y_t = (C_t . h_t + skip u_t) silu(z_t),
+    with s = softplus(dt + dt_bias), or dt + dt_bias where softplus is False.
+
+    u, dt and z [B,T,D] and Bt and Ct [B,T,G,N] (N 16, 32 or 64; a group serves
+    D/G channels) are float32, bfloat16 or float16 CUDA tensors, contiguous or
+    slices of packed projections; A [D,N], skip [D], dt_bias [D], h_init
+    [B,D,N] (None: zero) and h_final [B,D,N] are float32; z None is no gate;
+    lengths [B] int32 counts each sequence's valid tokens (None: T).  Returns
+    (y [B,T,D], h_final)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_ssm_forward(u, dt, A, Bt, Ct, skip, z, dt_bias, softplus, h_init, lengths, y, h_final, workspace)
+    return (_NATIVE or _native()).ssm_forward(u, dt, A, Bt, Ct, skip, z, dt_bias, bool(softplus), h_init, lengths, y, h_final,
+                                              workspace)
+
+
+def srwm_ssm_step(u_t, dt_t, A, B_t, C_t, h_in, skip=None, z_t=None, dt_bias=None, softplus=True, y_t=None, h_out=None,
+                  stream=None):
+    """One token of srwm_ssm_forward from per-sequence states: u_t, dt_t, z_t [B,D], B_t, C_t [B,G,N] ->
+    (y_t [B,D], h_out [B,D,N]).
+
+    h_out may be h_in itself (in-place update)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_ssm_step(u_t, dt_t, A, B_t, C_t, h_in, skip, z_t, dt_bias, softplus, y_t, h_out)
+    return (_NATIVE or _native()).ssm_step(u_t, dt_t, A, B_t, C_t, h_in, skip, z_t, dt_bias, bool(softplus), y_t, h_out)
+
+
+def srwm_ssm_backward_workspace_bytes(B, T, D, N, G) -> int:
+    return int(_lib().srwm_ssm_backward_workspace_bytes(int(B), int(T), int(D), int(N), int(G)))
+
+
+def srwm_ssm_backward(u, dt, A, Bt, Ct, dy, skip=None, z=None, dt_bias=None, softplus=True, h_init=None, lengths=None,
+                      dh_final=None, du=None, ddt=None, dA=None, dB=None, dC=None, dskip=None, dz=None, ddt_bias=None,
+                      dh_init=None, workspace=None, stream=None):
+    """Gradients through srwm_ssm_forward from dy [B,T,D] and dh_final [B,D,N] (None: zero).
+
+    dB and dC, and dz, may be slices of packed arrays.  Returns (du, ddt, dA,
+    dB, dC, dskip, dz, ddt_bias, dh_init), with None for what was not given
+    (skip, z, dt_bias, h_init)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_ssm_backward(u, dt, A, Bt, Ct, dy, skip, z, dt_bias, softplus, h_init, lengths, dh_final, du, ddt, dA,
+                                     dB, dC, dskip, dz, ddt_bias, dh_init, workspace)
+    return (_NATIVE or _native()).ssm_backward(u, dt, A, Bt, Ct, dy, skip, z, dt_bias, bool(softplus), h_init, lengths, dh_final,
+                                               du, ddt, dA, dB, dC, dskip, dz, ddt_bias, dh_init, workspace)
+
+
+def srwm_rmsnorm_forward(x, gamma, residual=None, eps=1e-5, out="same", block=0, y=None, scale=None, total=None, rstd=None,
+                         stream=None):
+    """Root-mean-square norm after the residual's addition: h = x + residual, y = h / sqrt(mean(h^2) + eps) * gamma.
+
+    x and residual [N,C] are contiguous float32, bfloat16 or float16 CUDA
+    tensors, gamma [C] is float32 or None (ones).  out="e4m3" gives y as
+    torch.float8_e4m3fn with scales [N,C/block], block 128 or 0 for a scale per
+    row ([N,1]).  Returns (y, scale, total, rstd [N]): scale is None unless out
+    is "e4m3"; total = x + residual is None without a residual, and may be
+    given as the residual itself (updated in place)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_rmsnorm_forward(x, gamma, residual, eps, out, block, y, scale, total, rstd)
+    code = _OUTS.get(out)
+    if code is None:
+        raise ValueError(f"out must be one of {', '.join(_OUTS)}")
+    return (_NATIVE or _native()).rmsnorm_forward(x, gamma, residual, eps, code, block, y, scale, total, rstd)
+
+
+def srwm_rmsnorm_backward_workspace_bytes(N, C) -> int:
+    return int(_lib().srwm_rmsnorm_backward_workspace_bytes(int(N), int(C)))
+
+
+def srwm_rmsnorm_backward(total, gamma, rstd, dy, dtotal=None, dx=None, dgamma=None, workspace=None, stream=None):
+    """Gradients through srwm_rmsnorm_forward from dy [N,C] and what reaches total by other ways (dtotal, None: zero).
+
+    total is the forward pass's sum (x where it had no residual), rstd its rstd.
+    Returns (dx [N,C], the gradient of x and of the residual; dgamma [C], None without gamma)."""
+    if stream is not None:
+        with _on(stream):
+            return srwm_rmsnorm_backward(total, gamma, rstd, dy, dtotal, dx, dgamma, workspace)
+    return (_NATIVE or _native()).rmsnorm_backward(total, gamma, rstd, dy, dtotal, dx, dgamma, workspace)
 
 
 def srwm_debug_set_layer_gemm(mode: int) -> None:

@@ -1,6 +1,7 @@
 """Build libsrwm.so (the sm_103a CUDA library) in-tree with nvcc, and beside it
 _srwm_torch.so, the CPython module that marshals PyTorch tensors for the
-linear attention and group norm entry points.
+operators' entry points (linear attention, group norm, short convolution,
+selective scan, RMS norm).
 
 Each translation unit under csrc/ compiles in parallel with
 `-gencode arch=compute_103a,code=sm_103a`; the objects link into
@@ -28,7 +29,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["srwm_api.cu", "srwm_d16.cu", "srwm_d32.cu", "srwm_d64.cu", "srwm_probe.cu", "srwm_noalloc.cu", "srwm_bwd.cu",
          "srwm_layer.cu", "srwm_ffgemm.cu", "srwm_linattn.cu", "srwm_linattn_tc.cu",
          "srwm_linattn_tc32.cu", "srwm_linattn_scan.cu", "srwm_linattn_api.cu", "srwm_groupnorm.cu",
-         "srwm_groupnorm_api.cu"]
+         "srwm_groupnorm_api.cu", "srwm_sum.cu", "srwm_conv.cu", "srwm_conv_api.cu", "srwm_ssm.cu", "srwm_ssm_bwd.cu",
+         "srwm_ssm_api.cu", "srwm_rmsnorm.cu", "srwm_rmsnorm_api.cu"]
 
 
 def _nvcc() -> str:

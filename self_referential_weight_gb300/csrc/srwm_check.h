@@ -1,5 +1,5 @@
 // srwm_check.h -- host-side argument checks shared by the operator entry
-// points (linear attention, group norm).
+// points (linear attention, group norm, short convolution, selective scan, RMS norm).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -46,6 +46,25 @@ inline bool overlap(const Region& a, const Region& b)
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// No output overlaps an input or another output.
+inline int check_alias(std::initializer_list<Region> outs, std::initializer_list<Region> ins)
+{
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Region& i : ins)
+            if (overlap(*o, i)) return SRWM_ERR_ALIAS;
+        for (auto q = o + 1; q != outs.end(); ++q)
+            if (overlap(*o, *q)) return SRWM_ERR_ALIAS;
+    }
+    return SRWM_OK;
+}
+
+inline int check_align(std::initializer_list<const void*> ptrs)
+{
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return SRWM_ERR_ALIGN;
+    return SRWM_OK;
+}
+
 // Device memory of the current device, or managed memory?
 inline int check_device_memory(std::initializer_list<const void*> ptrs)
 {
@@ -70,11 +89,11 @@ inline int check_device_memory(std::initializer_list<const void*> ptrs)
 // Launches a kernel that calls griddep_wait() (srwm_mma.cuh) behind one that calls griddep_launch(): its CTAs may be
 // placed while the last of the other's still run, instead of some 2 us after them.
 template <typename... P, typename... A>
-int launch_behind(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args)
+int launch_behind(void (*kernel)(P...), dim3 grid, dim3 threads, int smem, cudaStream_t st, const A&... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     cudaLaunchAttribute attr{};

@@ -31,25 +31,6 @@ Region rows_of(const void* p, long long n, long long ld, long long H, long long 
     return {p, static_cast<size_t>(H * d) * e, static_cast<size_t>(ld) * e, n};
 }
 
-// No output overlaps an input or another output.
-int check_alias(std::initializer_list<Region> outs, std::initializer_list<Region> ins)
-{
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (const Region& i : ins)
-            if (srwm::overlap(*o, i)) return SRWM_ERR_ALIAS;
-        for (auto q = o + 1; q != outs.end(); ++q)
-            if (srwm::overlap(*o, *q)) return SRWM_ERR_ALIAS;
-    }
-    return SRWM_OK;
-}
-
-int check_align(std::initializer_list<const void*> ptrs)
-{
-    for (const void* p : ptrs)
-        if (!srwm::aligned16(p)) return SRWM_ERR_ALIGN;
-    return SRWM_OK;
-}
-
 // Segment states, enough for any type (none when the axis is not split).
 size_t scratch(int B, int T, int H, int d, int roles, int slots)
 {
@@ -95,12 +76,12 @@ int srwm_linattn_forward(const void* q, const void* k, const void* v, long long 
     if (!supported(d) || e == 0) return SRWM_ERR_UNSUPPORTED;
     const size_t need = srwm_linattn_workspace_bytes(B, T, H, d);
     if (!ld_ok(ld, H, d, e) || workspace_bytes < need || !std::isfinite(scale)) return SRWM_ERR_SHAPE;
-    int rc = check_align({q, k, v, log_decay, S_init, o, S_final, workspace});
+    int rc = srwm::check_align({q, k, v, log_decay, S_init, o, S_final, workspace});
     if (rc != SRWM_OK) return rc;
     if (reinterpret_cast<uintptr_t>(lengths) % 4 != 0) return SRWM_ERR_ALIGN;
     const long long n = static_cast<long long>(B) * T;
     const size_t state = static_cast<size_t>(B) * H * d * d * 4;
-    rc = check_alias({rows_of(o, n, static_cast<long long>(H) * d, H, d, e), srwm::flat(S_final, state),
+    rc = srwm::check_alias({rows_of(o, n, static_cast<long long>(H) * d, H, d, e), srwm::flat(S_final, state),
                       srwm::flat(workspace, need)},
                      {rows_of(q, n, ld, H, d, e), rows_of(k, n, ld, H, d, e), rows_of(v, n, ld, H, d, e),
                       srwm::flat(log_decay, static_cast<size_t>(H) * 4), srwm::flat(S_init, state),
@@ -128,11 +109,11 @@ int srwm_linattn_step(const void* q, const void* k, const void* v, long long ld,
     const size_t e = srwm::dtype_bytes(dtype);
     if (!supported(d) || e == 0) return SRWM_ERR_UNSUPPORTED;
     if (!ld_ok(ld, H, d, e) || !std::isfinite(scale)) return SRWM_ERR_SHAPE;
-    int rc = check_align({q, k, v, log_decay, S_in, o, S_out});
+    int rc = srwm::check_align({q, k, v, log_decay, S_in, o, S_out});
     if (rc != SRWM_OK) return rc;
     const size_t state = static_cast<size_t>(B) * H * d * d * 4;
     const Region si = srwm::flat(S_out == S_in ? nullptr : S_in, state);   // exactly in place is allowed
-    rc = check_alias({rows_of(o, B, static_cast<long long>(H) * d, H, d, e), srwm::flat(S_out, state)},
+    rc = srwm::check_alias({rows_of(o, B, static_cast<long long>(H) * d, H, d, e), srwm::flat(S_out, state)},
                      {rows_of(q, B, ld, H, d, e), rows_of(k, B, ld, H, d, e), rows_of(v, B, ld, H, d, e),
                       srwm::flat(log_decay, static_cast<size_t>(H) * 4), si});
     if (rc != SRWM_OK) return rc;
@@ -155,12 +136,12 @@ int srwm_linattn_backward(const void* q, const void* k, const void* v, long long
     const size_t need = srwm_linattn_backward_workspace_bytes(B, T, H, d);
     if (!ld_ok(ld, H, d, e) || !ld_ok(ld_grad, H, d, e) || workspace_bytes < need || !std::isfinite(scale))
         return SRWM_ERR_SHAPE;
-    int rc = check_align({q, k, v, log_decay, S_init, do_, dS_final, dq, dk, dv, dS_init, workspace});
+    int rc = srwm::check_align({q, k, v, log_decay, S_init, do_, dS_final, dq, dk, dv, dS_init, workspace});
     if (rc != SRWM_OK) return rc;
     if (reinterpret_cast<uintptr_t>(lengths) % 4 != 0) return SRWM_ERR_ALIGN;
     const long long n = static_cast<long long>(B) * T, hd = static_cast<long long>(H) * d;
     const size_t state = static_cast<size_t>(B) * H * d * d * 4;
-    rc = check_alias({rows_of(dq, n, ld_grad, H, d, e), rows_of(dk, n, ld_grad, H, d, e),
+    rc = srwm::check_alias({rows_of(dq, n, ld_grad, H, d, e), rows_of(dk, n, ld_grad, H, d, e),
                       rows_of(dv, n, ld_grad, H, d, e), srwm::flat(dS_init, state), srwm::flat(workspace, need)},
                      {rows_of(q, n, ld, H, d, e), rows_of(k, n, ld, H, d, e), rows_of(v, n, ld, H, d, e),
                       rows_of(do_, n, hd, H, d, e), srwm::flat(log_decay, static_cast<size_t>(H) * 4),

@@ -1,0 +1,126 @@
+// srwm_ssm.cuh -- what the selective scan's kernels share: the layout of a
+// warp's states, its sums over lanes, and the step's softplus.
+//
+// A lane holds four states of each of four channels.  The N / 4 lanes of a
+// channel quad follow each other, so a warp holds 128 / (N / 4) channels.  A
+// token costs it, per state, two products, two sums of products and one
+// exponential; a token's step and input come as one 16-byte load for four
+// channels, B and C for four states, and y leaves through three or more
+// shuffles for all four channels.
+#pragma once
+
+#include "srwm_ssm.h"
+#include "srwm_vec.cuh"
+
+namespace srwm {
+namespace ssm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+
+template <int N>
+struct Lay {
+    static constexpr int kLanes = N / 4;              // of a channel quad
+    static constexpr int kWarpCh = 4 * 32 / kLanes;   // channels of a warp
+    static constexpr int kCh = kWarps * kWarpCh;      // of a CTA
+};
+
+__device__ __forceinline__ float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]: by the series of artanh, log1p(e) = 2 artanh(s),
+// s = e / (2 + e) <= 1/3, whose terms past s^13 are below 2^-26 of the sum.  exp's argument is carried with its
+// rounding error, so a far negative v keeps its relative precision.  NaN gives NaN.
+__device__ __forceinline__ float softplus(float v)
+{
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v)), "f"(100.f));
+    const float hi = -m * kLog2e;
+    const float lo = fmaf(-m, kLog2e, -hi);
+    float e = ex2(hi);
+    e = fmaf(e, lo * kLn2, e);
+    const float s = e * rcp_approx(2.f + e), q = s * s;
+    float r = fmaf(q, 1.f / 13, 1.f / 11);
+    r = fmaf(r, q, 1.f / 9);
+    r = fmaf(r, q, 1.f / 7);
+    r = fmaf(r, q, 1.f / 5);
+    r = fmaf(r, q, 1.f / 3);
+    r = fmaf(r, q, 1.f);
+    return fmaf(2.f * s, r, fmaxf(v, 0.f));
+}
+
+// Four values, one per channel, summed over a quad's LANES lanes: every lane gets one channel's, quad_channel's.
+template <int LANES>
+__device__ __forceinline__ float quad_sum(float v0, float v1, float v2, float v3)
+{
+    const bool up = threadIdx.x & (LANES / 2), odd = threadIdx.x & (LANES / 4);
+    const float a = (up ? v2 : v0) + __shfl_xor_sync(0xffffffffu, up ? v0 : v2, LANES / 2);
+    const float b = (up ? v3 : v1) + __shfl_xor_sync(0xffffffffu, up ? v1 : v3, LANES / 2);
+    float r = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, LANES / 4);
+#pragma unroll
+    for (int o = LANES / 8; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    return r;
+}
+template <int LANES>
+__device__ __forceinline__ int quad_channel() { return (threadIdx.x & (LANES / 2) ? 2 : 0) + (threadIdx.x & (LANES / 4) ? 1 : 0); }
+// One of the lanes that hold a channel's sum.
+template <int LANES>
+__device__ __forceinline__ bool quad_leader() { return (threadIdx.x & (LANES / 4 - 1)) == 0; }
+
+__device__ __forceinline__ int valid_tokens(const int* lengths, int b, int T)
+{
+    return lengths ? min(max(__ldg(lengths + b), 0), T) : T;
+}
+
+// A CTA's place: a segment of a sequence and a range of a group's channels.
+struct Place {
+    int b, group, first, count, segment;   // channels first .. first + count - 1 of D
+};
+template <int CH>
+__device__ __forceinline__ Place place_of(const SsmParams& p)
+{
+    const int dg = p.D / p.G, tiles = (dg + CH - 1) / CH;
+    unsigned i = blockIdx.x;
+    Place w;
+    const int tile = static_cast<int>(i % tiles);
+    i /= tiles;
+    w.group = static_cast<int>(i % p.G);
+    i /= p.G;
+    w.b = static_cast<int>(i % p.B);
+    w.segment = static_cast<int>(i / p.B);
+    w.first = w.group * dg + tile * CH;
+    w.count = min(CH, dg - tile * CH);
+    return w;
+}
+
+// Four states of each of four channels, [.., D, N] from channel c and state n on: pairs are of channels.
+__device__ __forceinline__ void load_states(const float* from, int N, bool on, float2 (&h)[2][4])
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = on ? *reinterpret_cast<const float4*>(from + (2 * k) * N) : zero;
+        const float4 b = on ? *reinterpret_cast<const float4*>(from + (2 * k + 1) * N) : zero;
+        h[k][0] = make_float2(a.x, b.x), h[k][1] = make_float2(a.y, b.y);
+        h[k][2] = make_float2(a.z, b.z), h[k][3] = make_float2(a.w, b.w);
+    }
+}
+__device__ __forceinline__ void store_states(float* to, int N, const float2 (&h)[2][4])
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        *reinterpret_cast<float4*>(to + (2 * k) * N) = make_float4(h[k][0].x, h[k][1].x, h[k][2].x, h[k][3].x);
+        *reinterpret_cast<float4*>(to + (2 * k + 1) * N) = make_float4(h[k][0].y, h[k][1].y, h[k][2].y, h[k][3].y);
+    }
+}
+
+}  // namespace ssm
+}  // namespace srwm
