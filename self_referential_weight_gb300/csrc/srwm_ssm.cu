@@ -3,7 +3,7 @@
 //   s_t = softplus(dt_t + dt_bias),  h_t = exp(s_t A) h_{t-1} + s_t u_t B_t,
 //   y_t = (C_t . h_t + skip u_t) silu(z_t)
 // per channel, with N states each.  A CTA takes a range of channels of one
-// sequence (or of a segment of it) in tiles of TT tokens: u, dt, z, B and C come
+// sequence (or of a segment of it) in tiles of tokens: u, dt, z, B and C come
 // by asynchronous copies a tile ahead; each warp forms its channels' steps and
 // inputs in fp32, runs its states (in registers throughout) over the tile, and
 // gates and stores the outputs.  Past a sequence's end a token's step is 0, which
@@ -24,53 +24,100 @@ namespace {
 
 using namespace ssm;
 
-constexpr int TT = 16;   // tokens of a tile
 constexpr int kSms = 152;
+constexpr int kWhole = 16;   // segments are multiples of this many tokens, whole tiles of either size
+constexpr int kLaneCh = 2;
+constexpr int kPromptWarps = 2;
+constexpr int kPromptThreads = 32 * kPromptWarps;
 
+// A lane holds eight states of each of kLaneCh channels; the N / 8 lanes of these channels lie as far apart as the warp
+// has such sets, so a load of states is the same address for neighbouring lanes.
 template <typename E, int N>
 struct Tile {
-    using L = Lay<N>;
-    static constexpr int kCh = L::kCh;
+    static constexpr int TT = sizeof(E) == 4 ? 8 : 16;                        // tokens
+    static constexpr int kLanes = N / 8, kSets = 32 / kLanes;
+    static constexpr int kWarpCh = kLaneCh * kSets, kCh = kPromptWarps * kWarpCh;
     static constexpr int kRow = kCh * static_cast<int>(sizeof(E));            // bytes of a token's channels
     static constexpr int kBc = N * static_cast<int>(sizeof(E));               // and of its B (or C)
     static constexpr int kStage = TT * (3 * kRow + 2 * kBc);                  // u | dt | z | B | C as they land
-    static constexpr int kWide = TT * (2 * kCh + 2 * N) * 4;                  // steps | inputs (then outputs) | B | C in fp32
-    static constexpr int kSmem = 2 * kStage + kWide + 2 * kCh * 4;            // and dt_bias | skip
+    static constexpr int kPitch = kCh + 4;                                    // floats of a token's steps: other banks than the next's
+    static constexpr int kWideBc = sizeof(E) == 4 ? 0 : TT * 2 * N * 4;
+    static constexpr int kSmem = 2 * kStage + TT * 2 * kPitch * 4 + kWideBc;  // steps | inputs (then outputs) | B | C in fp32
+};
+
+// The eight states of a channel from `from` on, as pairs.
+__device__ __forceinline__ void load8(const float* from, bool on, float2 (&h)[4])
+{
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 a = on ? *reinterpret_cast<const float4*>(from) : zero, b = on ? *reinterpret_cast<const float4*>(from + 4) : zero;
+    h[0] = make_float2(a.x, a.y), h[1] = make_float2(a.z, a.w), h[2] = make_float2(b.x, b.y), h[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void store8(float* to, const float2 (&h)[4])
+{
+    *reinterpret_cast<float4*>(to) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    *reinterpret_cast<float4*>(to + 4) = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
+}
+
+// kLaneCh neighbouring floats.
+__device__ __forceinline__ void load_ch(const float* from, float (&v)[kLaneCh])
+{
+    if constexpr (kLaneCh == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(from);
+        v[0] = q.x, v[1] = q.y, v[kLaneCh - 2] = q.z, v[kLaneCh - 1] = q.w;
+    } else {
+        const float2 q = *reinterpret_cast<const float2*>(from);
+        v[0] = q.x, v[1] = q.y;
+    }
+}
+
+// What one token takes from shared memory.
+template <bool OUT>
+struct Token {
+    float d[kLaneCh], x[kLaneCh];
+    float2 b[4], c[4];
+
+    __device__ __forceinline__ void load(const float* step, const float* input, const float* B, const float* C)
+    {
+        load_ch(step, d);
+        load_ch(input, x);
+        load8(B, true, b);
+        if (OUT) load8(C, true, c);
+    }
 };
 
 template <typename E, int N, bool OUT>
-__global__ void __launch_bounds__(kThreads) ssm_kernel(const __grid_constant__ SsmParams p)
+__global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_constant__ SsmParams p)
 {
     using S = Tile<E, N>;
-    using L = Lay<N>;
-    constexpr int V = vec<E>, CH = S::kCh, WCH = L::kWarpCh;
+    constexpr int V = vec<E>, TT = S::TT, WCH = S::kWarpCh;
     constexpr int PIECES = TT * WCH / V;   // of a warp's tile
     extern __shared__ __align__(128) unsigned char smem[];
     float* const steps = reinterpret_cast<float*>(smem + 2 * S::kStage);
-    float* const xs = steps + TT * CH;
-    float* const Bf = xs + TT * CH;
-    float* const Cf = Bf + TT * N;
-    float* const bias = Cf + TT * N;
-    float* const skip = bias + CH;
+    float* const xs = steps + TT * S::kPitch;
+    float* const bcs = xs + TT * S::kPitch;   // B and C in fp32 (of 16 bits)
 
-    const Place w = place_of<CH>(p);
+    const Place w = place_of<S::kCh>(p);
     const int n = valid_tokens(p.lengths, w.b, p.T);
     const int t0 = w.segment * p.seg_len, t1 = min(p.T, t0 + p.seg_len), live = min(n, t1);
     const int last = n > 0 ? (n - 1) / p.seg_len : 0;   // the segment at whose end the sequence ends
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp * WCH + lane / L::kLanes * 4, n4 = lane % L::kLanes * 4;   // this lane's channels and states
-    const bool on = quad < w.count;
+    const int own = warp * WCH + lane % S::kSets * kLaneCh, n8 = lane / S::kSets * 8;   // this lane's channels and states
+    const bool on = own < w.count;
     if (!OUT && w.segment >= last) return;   // nothing comes after it
 
     E* const y = static_cast<E*>(p.y) + static_cast<size_t>(w.b) * p.T * p.D + w.first;
     if constexpr (OUT)   // rows past the end
-        for (int i = threadIdx.x; i < (t1 - max(t0, live)) * (w.count / V); i += kThreads)
+        for (int i = threadIdx.x; i < (t1 - max(t0, live)) * (w.count / V); i += kPromptThreads)
             store_vec<E>(y, static_cast<size_t>(max(t0, live) + i / (w.count / V)) * p.D + i % (w.count / V) * V, make_uint4(0, 0, 0, 0));
     if (w.segment > last) return;
 
-    for (int i = threadIdx.x; i < CH; i += kThreads) {
-        bias[i] = i < w.count && p.dt_bias ? p.dt_bias[w.first + i] : 0.f;
-        skip[i] = i < w.count && p.skip ? p.skip[w.first + i] : 0.f;
+    // the channels that this lane widens and stores, in every tile
+    const int mine = warp * WCH + lane % (WCH / V) * V;
+    float bias[V], skip[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        bias[k] = mine < w.count && p.dt_bias ? p.dt_bias[w.first + mine + k] * kLog2e : 0.f;
+        skip[k] = mine < w.count && p.skip ? p.skip[w.first + mine + k] : 0.f;
     }
     const size_t tokens = static_cast<size_t>(w.b) * p.T;
     const E* const rows[3] = {static_cast<const E*>(p.u) + tokens * p.ld_u + w.first,
@@ -80,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(const __grid_constant__ S
     const E* const bc[2] = {static_cast<const E*>(p.Bt) + tokens * p.ld_bc + w.group * N,
                             static_cast<const E*>(p.Ct) + tokens * p.ld_bc + w.group * N};
     const bool gated = OUT && p.z;
-    auto load = [&](int tile) {
+    auto load = [&](int tile) {   // zeros past the end and past the channels
         const uint32_t to = smem_u32(smem) + (tile & 1) * S::kStage;
         const int first = t0 + tile * TT;
 #pragma unroll
@@ -98,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(const __grid_constant__ S
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k == 1 && !OUT) continue;
-            for (int i = threadIdx.x; i < TT * N / V; i += kThreads) {
+            for (int i = threadIdx.x; i < TT * N / V; i += kPromptThreads) {
                 const int r = i / (N / V), c = i % (N / V) * V;
                 const bool ok = first + r < live;
                 cp_async16(to + 3 * TT * S::kRow + (k * TT + r) * S::kBc + c * static_cast<int>(sizeof(E)),
@@ -110,130 +157,157 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(const __grid_constant__ S
     if (tiles > 0) load(0);
     cp_async_commit();
 
-    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + quad) * N + n4, all = static_cast<size_t>(p.B) * p.D * N;
-    float2 A[2][4], h[2][4];
-    load_states(p.A + static_cast<size_t>(w.first + quad) * N + n4, N, on, A);
-    load_states(p.h_in + mat, N, OUT && on && p.h_in, h);
+    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + own) * N + n8, all = static_cast<size_t>(p.B) * p.D * N;
+    float2 A[kLaneCh][4], h[kLaneCh][4];
+#pragma unroll
+    for (int c = 0; c < kLaneCh; ++c) {
+        load8(p.A + static_cast<size_t>(w.first + own + c) * N + n8, on, A[c]);
+        load8(p.h_in + mat + c * N, OUT && on && p.h_in, h[c]);
+    }
     if (OUT && w.segment > 0) {
         griddep_wait();
         for (int j = 0; j < w.segment; ++j) {
-            float2 own[2][4];
-            load_states(p.seg_state + j * all + mat, N, on, own);
-            const float4 d = on ? *reinterpret_cast<const float4*>(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + quad)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float2 sum[2] = {make_float2(d.x, d.y), make_float2(d.z, d.w)};
+            float sum[kLaneCh] = {};
+            if (on) load_ch(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + own, sum);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int c = 0; c < kLaneCh; ++c) {
+                float2 part[4];
+                load8(p.seg_state + j * all + mat + c * N, on, part);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) h[k][s] = fma2(ex2_2(mul2(sum[k], A[k][s])), h[k][s], own[k][s]);
+                for (int s = 0; s < 4; ++s) h[c][s] = fma2(ex2_2(mul2(both(sum[c]), A[c][s])), h[c][s], part[s]);
+            }
         }
     }
-    float2 total[2] = {both(0.f), both(0.f)};   // steps so far
+    float total[kLaneCh] = {};   // steps so far
 
     for (int tile = 0; tile < tiles; ++tile) {
+        cp_async_wait<0>();
+        __syncthreads();   // the tile has landed, and all warps are done with the one before
         if (tile + 1 < tiles) load(tile + 1);
         cp_async_commit();
-        cp_async_wait<1>();
-        __syncthreads();   // the tile has landed, and all warps are done with the one before
         const unsigned char* const raw = smem + (tile & 1) * S::kStage;
         const int first = t0 + tile * TT, count = min(TT, live - first);
 #pragma unroll
         for (int i = 0; i < PIECES; i += 32) {
-            const int piece = i + lane, r = piece / (WCH / V), c = warp * WCH + piece % (WCH / V) * V;
+            const int piece = i + lane, r = piece / (WCH / V);
             if (piece < PIECES) {
                 float uu[V], dd[V];
-                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + c * sizeof(E));
+                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
                 unpack(at[0], uu, E{});
                 unpack(at[TT * S::kRow / 16], dd, E{});
-                const bool ok = r < count && c < w.count;
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float v = dd[k] + bias[c + k];
-                    dd[k] = ok ? p.softplus ? softplus(v) : v : 0.f;
-                    uu[k] = ok ? dd[k] * uu[k] : 0.f;
-                    dd[k] *= kLog2e;
-                }
 #pragma unroll
                 for (int k = 0; k < V; k += 4) {
-                    *reinterpret_cast<float4*>(steps + r * CH + c + k) = make_float4(dd[k], dd[k + 1], dd[k + 2], dd[k + 3]);
-                    *reinterpret_cast<float4*>(xs + r * CH + c + k) = make_float4(uu[k], uu[k + 1], uu[k + 2], uu[k + 3]);
+                    float2 s0 = fma2(make_float2(dd[k], dd[k + 1]), both(kLog2e), make_float2(bias[k], bias[k + 1]));
+                    float2 s1 = fma2(make_float2(dd[k + 2], dd[k + 3]), both(kLog2e), make_float2(bias[k + 2], bias[k + 3]));
+                    if (p.softplus) s0 = softplus2(s0), s1 = softplus2(s1);
+                    if (r >= count) s0 = s1 = both(0.f);
+                    float2 x0 = mul2(s0, make_float2(uu[k], uu[k + 1])), x1 = mul2(s1, make_float2(uu[k + 2], uu[k + 3]));
+                    if (sizeof(E) == 4) x0 = mul2(x0, both(kLn2)), x1 = mul2(x1, both(kLn2));   // else B has the factor
+                    *reinterpret_cast<float4*>(steps + r * S::kPitch + mine + k) = make_float4(s0.x, s0.y, s1.x, s1.y);
+                    *reinterpret_cast<float4*>(xs + r * S::kPitch + mine + k) = make_float4(x0.x, x0.y, x1.x, x1.y);
                 }
             }
         }
-        for (int i = threadIdx.x; i < (OUT ? 2 : 1) * TT * N / V; i += kThreads) {   // B, then C
-            float v[V];
-            unpack(reinterpret_cast<const uint4*>(raw + 3 * TT * S::kRow)[i], v, E{});
+        if constexpr (sizeof(E) == 2) {
+            for (int i = threadIdx.x; i < (OUT ? 2 : 1) * TT * N / V; i += kPromptThreads) {
+                float v[V];
+                unpack(reinterpret_cast<const uint4*>(raw + 3 * TT * S::kRow)[i], v, E{});
+                if (i < TT * N / V)
 #pragma unroll
-            for (int k = 0; k < V; k += 4)
-                *reinterpret_cast<float4*>(Bf + i * V + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    for (int k = 0; k < V; ++k) v[k] *= kLn2;
+#pragma unroll
+                for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(bcs + i * V + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            }
+            __syncthreads();
+        } else {
+            __syncwarp();
         }
-        __syncthreads();
-        for (int r = 0; r < count; r += 4) {
-            float out[4];
+        const float* const B8 = (sizeof(E) == 4 ? reinterpret_cast<const float*>(raw + 3 * TT * S::kRow) : bcs) + n8;
+        const float* const C8 = B8 + TT * N;
+        Token<OUT> now, next;
+        now.load(steps + own, xs + own, B8, C8);
+        auto token = [&](int r, int ahead) {
+            next.load(steps + ahead * S::kPitch + own, xs + ahead * S::kPitch + own, B8 + ahead * N, C8 + ahead * N);
+            float o[kLaneCh];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 d = *reinterpret_cast<const float4*>(steps + (r + q) * CH + quad);
-                const float4 x = *reinterpret_cast<const float4*>(xs + (r + q) * CH + quad);
-                const float4 b = *reinterpret_cast<const float4*>(Bf + (r + q) * N + n4);
-                const float2 dd[2] = {make_float2(d.x, d.y), make_float2(d.z, d.w)};
-                const float2 xx[2] = {make_float2(x.x, x.y), make_float2(x.z, x.w)};
-                const float2 bb[4] = {both(b.x), both(b.y), both(b.z), both(b.w)};
+            for (int c = 0; c < kLaneCh; ++c) {
+                const float2 d = both(now.d[c]), x = both(now.x[c]);
+                float2 sum;
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int s = 0; s < 4; ++s) {
+                    h[c][s] = fma2(ex2_2(mul2(d, A[c][s])), h[c][s], mul2(x, now.b[s]));
+                    if (OUT) sum = s ? fma2(now.c[s], h[c][s], sum) : mul2(now.c[s], h[c][s]);
+                }
+                if (OUT) o[c] = sum.x + sum.y;
+                if (!OUT) total[c] += now.d[c];
+            }
+            if constexpr (OUT) {   // the channels' sums over their lanes: each half of these takes half of the channels
+                const bool up = lane & 16;
+                float v[kLaneCh / 2];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) h[k][s] = fma2(ex2_2(mul2(dd[k], A[k][s])), h[k][s], mul2(xx[k], bb[s]));
-                if constexpr (OUT) {
-                    const float4 c = *reinterpret_cast<const float4*>(Cf + (r + q) * N + n4);
-                    const float2 cc[4] = {both(c.x), both(c.y), both(c.z), both(c.w)};
-                    float2 o[2];
+                for (int c = 0; c < kLaneCh / 2; ++c) {
+                    v[c] = (up ? o[kLaneCh / 2 + c] : o[c]) + __shfl_xor_sync(0xffffffffu, up ? o[c] : o[kLaneCh / 2 + c], 16);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        o[k] = mul2(cc[0], h[k][0]);
-#pragma unroll
-                        for (int s = 1; s < 4; ++s) o[k] = fma2(cc[s], h[k][s], o[k]);
-                    }
-                    out[q] = quad_sum<L::kLanes>(o[0].x, o[0].y, o[1].x, o[1].y);
-                } else {
-                    total[0] = add2(total[0], dd[0]);
-                    total[1] = add2(total[1], dd[1]);
+                    for (int k = 8; k >= S::kSets; k >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], k);
+                }
+                // in their inputs' place, which all lanes have read
+                if (S::kSets == 16 || (lane & 15) < S::kSets) {
+                    float* const to = xs + r * S::kPitch + own + (up ? kLaneCh / 2 : 0);
+                    if constexpr (kLaneCh == 4)
+                        *reinterpret_cast<float2*>(to) = make_float2(v[0], v[kLaneCh / 2 - 1]);
+                    else
+                        *to = v[0];
                 }
             }
-            if constexpr (OUT) {
-                __syncwarp();   // the outputs take their inputs' place
-                if (quad_leader<L::kLanes>())
+            now = next;
+        };
+        if (count == TT) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) xs[(r + q) * CH + quad + quad_channel<L::kLanes>()] = out[q];
-            }
+            for (int r = 0; r < TT; ++r) token(r, r + 1 < TT ? r + 1 : r);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < count; ++r) token(r, min(r + 1, TT - 1));
         }
         if constexpr (OUT) {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < PIECES; i += 32) {
-                const int piece = i + lane, r = piece / (WCH / V), c = warp * WCH + piece % (WCH / V) * V;
-                if (piece < PIECES && r < count && c < w.count) {
+                const int piece = i + lane, r = piece / (WCH / V);
+                if (piece < PIECES && r < count && mine < w.count) {
                     float uu[V], out[V];
-                    const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + c * sizeof(E));
+                    const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
                     unpack(at[0], uu, E{});
 #pragma unroll
-                    for (int k = 0; k < V; ++k) out[k] = fmaf(skip[c + k], uu[k], xs[r * CH + c + k]);
+                    for (int k = 0; k < V; k += 4) {
+                        const float4 o = *reinterpret_cast<const float4*>(xs + r * S::kPitch + mine + k);
+                        const float2 v0 = fma2(make_float2(skip[k], skip[k + 1]), make_float2(uu[k], uu[k + 1]), make_float2(o.x, o.y));
+                        const float2 v1 = fma2(make_float2(skip[k + 2], skip[k + 3]), make_float2(uu[k + 2], uu[k + 3]), make_float2(o.z, o.w));
+                        out[k] = v0.x, out[k + 1] = v0.y, out[k + 2] = v1.x, out[k + 3] = v1.y;
+                    }
                     if (gated) {
                         unpack(at[2 * TT * S::kRow / 16], uu, E{});
 #pragma unroll
-                        for (int k = 0; k < V; ++k) out[k] *= uu[k] * sigmoid(uu[k]);
+                        for (int k = 0; k < V; k += 2) {
+                            const float2 v = mul2(silu(make_float2(uu[k], uu[k + 1])), make_float2(out[k], out[k + 1]));
+                            out[k] = v.x, out[k + 1] = v.y;
+                        }
                     }
-                    store_vec<E>(y, static_cast<size_t>(first + r) * p.D + c, pack(out, E{}));
+                    store_vec<E>(y, static_cast<size_t>(first + r) * p.D + mine, pack(out, E{}));
                 }
             }
             __syncwarp();
         }
     }
     if constexpr (OUT) {
-        if (w.segment == last && on && p.h_out) store_states(p.h_out + mat, N, h);
+        if (w.segment == last && on && p.h_out)
+#pragma unroll
+            for (int c = 0; c < kLaneCh; ++c) store8(p.h_out + mat + c * N, h[c]);
     } else if (on) {
-        store_states(p.seg_state + w.segment * all + mat, N, h);
-        if (n4 == 0)
-            *reinterpret_cast<float4*>(p.seg_dt + (static_cast<size_t>(w.segment) * p.B + w.b) * p.D + w.first + quad) =
-                make_float4(total[0].x, total[0].y, total[1].x, total[1].y);
+#pragma unroll
+        for (int c = 0; c < kLaneCh; ++c) store8(p.seg_state + w.segment * all + mat + c * N, h[c]);
+        if (n8 == 0)
+#pragma unroll
+            for (int c = 0; c < kLaneCh; ++c) p.seg_dt[(static_cast<size_t>(w.segment) * p.B + w.b) * p.D + w.first + own + c] = total[c];
     }
     cp_async_wait<0>();
 }
@@ -255,8 +329,8 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constan
     const E* const Bt = static_cast<const E*>(p.Bt) + b * p.ld_bc + group * N + n4;
     const E* const Ct = static_cast<const E*>(p.Ct) + b * p.ld_bc + group * N + n4;
     const float u = to_f(static_cast<const E*>(p.u)[b * p.ld_u + c]);
-    const float v = to_f(static_cast<const E*>(p.dt)[b * p.ld_dt + c]) + (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f);
-    const float s = p.softplus ? softplus(v) : v, x = s * u, d = s * kLog2e;
+    const float v = fmaf(to_f(static_cast<const E*>(p.dt)[b * p.ld_dt + c]), kLog2e, p.dt_bias ? __ldg(p.dt_bias + c) * kLog2e : 0.f);
+    const float d = p.softplus ? softplus2(both(v)).x : v, x = d * kLn2 * u;
     float4 g;
     g.x = fmaf(ex2(d * A.x), h.x, x * to_f(Bt[0]));
     g.y = fmaf(ex2(d * A.y), h.y, x * to_f(Bt[1]));
@@ -283,13 +357,13 @@ struct Plan {
 // Segments of whole tiles, where whole sequences would leave most of the SMs idle.
 Plan plan_of(int B, int T, int D, int N, int G)
 {
-    const int ch = kWarps * 128 / (N / 4), dg = D / G;
+    const int ch = kPromptWarps * kLaneCh * 256 / N, dg = D / G;
     const long long ctas = static_cast<long long>(B) * G * ((dg + ch - 1) / ch);
-    const int most = std::max(1, T / (4 * TT));
-    const int segments = ctas >= 2 * kSms ? 1 : static_cast<int>(std::min<long long>(most, std::min<long long>(64, (4 * kSms + ctas - 1) / ctas)));
+    const int most = std::max(1, T / (4 * kWhole));
+    const int segments = ctas >= 4 * kSms ? 1 : static_cast<int>(std::min<long long>(most, std::min<long long>(64, (8 * kSms + ctas - 1) / ctas)));
     if (segments <= 1) return {1, std::max(1, T)};
-    const int tiles = (T + TT - 1) / TT, per = (tiles + segments - 1) / segments;
-    return {(tiles + per - 1) / per, per * TT};
+    const int tiles = (T + kWhole - 1) / kWhole, per = (tiles + segments - 1) / segments;
+    return {(tiles + per - 1) / per, per * kWhole};
 }
 
 template <typename E, int N>
@@ -304,11 +378,11 @@ int forward(const SsmParams& p, cudaStream_t st)
         return SRWM_ERR_CUDA;
     }
     if (p.segments > 1) {
-        ssm_kernel<E, N, false><<<grid * (p.segments - 1), kThreads, S::kSmem, st>>>(p);
+        ssm_kernel<E, N, false><<<grid * (p.segments - 1), kPromptThreads, S::kSmem, st>>>(p);
         const int rc = launched();
         if (rc != SRWM_OK) return rc;
     }
-    ssm_kernel<E, N, true><<<grid * p.segments, kThreads, S::kSmem, st>>>(p);
+    ssm_kernel<E, N, true><<<grid * p.segments, kPromptThreads, S::kSmem, st>>>(p);
     return launched();
 }
 

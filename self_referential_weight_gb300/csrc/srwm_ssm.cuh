@@ -36,25 +36,27 @@ __device__ __forceinline__ float ex2(float v)
 
 __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]: by the series of artanh, log1p(e) = 2 artanh(s),
-// s = e / (2 + e) <= 1/3, whose terms past s^13 are below 2^-26 of the sum.  exp's argument is carried with its
-// rounding error, so a far negative v keeps its relative precision.  NaN gives NaN.
-__device__ __forceinline__ float softplus(float v)
+// A step in units of log 2, log2(1 + 2^v) of its argument in these units: max(v, 0) + log2(1 + e), e = 2^-|v| in (0, 1].
+// log(1 + e) = 2 artanh(e / (2 + e)), and artanh(s) / s is a polynomial in s^2 <= 1/9 (minimax over that range by Remez'
+// exchange: within 4e-9 of itself), here in w = (2 s)^2 and times log2 e.  Far negative arguments keep the relative
+// precision that their own rounding leaves.  NaN gives NaN.
+__device__ __forceinline__ float2 softplus2(float2 v)
 {
-    float m;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(v)), "f"(100.f));
-    const float hi = -m * kLog2e;
-    const float lo = fmaf(-m, kLog2e, -hi);
-    float e = ex2(hi);
-    e = fmaf(e, lo * kLn2, e);
-    const float s = e * rcp_approx(2.f + e), q = s * s;
-    float r = fmaf(q, 1.f / 13, 1.f / 11);
-    r = fmaf(r, q, 1.f / 9);
-    r = fmaf(r, q, 1.f / 7);
-    r = fmaf(r, q, 1.f / 5);
-    r = fmaf(r, q, 1.f / 3);
-    r = fmaf(r, q, 1.f);
-    return fmaf(2.f * s, r, fmaxf(v, 0.f));
+    const float2 e = make_float2(ex2(-fabsf(v.x)), ex2(-fabsf(v.y)));
+    const float2 d = fma2(e, both(0.5f), both(1.f));
+    const float2 s = mul2(e, make_float2(rcp_approx(d.x), rcp_approx(d.y))), w = mul2(s, s);
+    float2 r = fma2(w, both(7.9437119647e-04f), both(3.1511238925e-03f));
+    r = fma2(r, w, both(1.8045010607e-02f));
+    r = fma2(r, w, both(1.2022394380e-01f));
+    r = fma2(r, w, both(1.4426950409e+00f));
+    return fma2(s, r, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
+// z sigmoid(z), twice.
+__device__ __forceinline__ float2 silu(float2 z)
+{
+    const float2 e = add2(ex2_2(mul2(z, both(-kLog2e))), both(1.f));
+    return mul2(z, make_float2(rcp_approx(e.x), rcp_approx(e.y)));
 }
 
 // Four values, one per channel, summed over a quad's LANES lanes: every lane gets one channel's, quad_channel's.

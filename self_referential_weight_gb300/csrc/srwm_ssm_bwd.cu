@@ -129,10 +129,9 @@ __device__ __forceinline__ void widen(const SsmParams& p, const Rows<E, N>& R, c
             const bool ok = r < count && c < R.w.count;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const float v = dd[k] + bias[c + k];
-                dd[k] = ok ? p.softplus ? softplus(v) : v : 0.f;
-                uu[k] = ok ? dd[k] * uu[k] : 0.f;
-                dd[k] *= kLog2e;
+                const float v = fmaf(dd[k], kLog2e, bias[c + k] * kLog2e);
+                dd[k] = ok ? p.softplus ? softplus2(both(v)).x : v : 0.f;
+                uu[k] = ok ? dd[k] * kLn2 * uu[k] : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < V; k += 4) {
