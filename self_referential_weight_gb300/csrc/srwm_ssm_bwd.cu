@@ -27,7 +27,8 @@ namespace {
 
 using namespace ssm;
 
-constexpr int TT = 8;    // tokens of a tile
+constexpr int TT = 8;           // tokens of a tile
+constexpr int kBlock = 32;      // tiles after which the parameters' sums go out: short chains of additions
 constexpr int kSms = 152;
 
 enum Row { kU, kDt, kZ, kDy };
@@ -36,28 +37,29 @@ template <typename E, int N>
 struct Tile {
     using L = Lay<N>;
     static constexpr int kCh = L::kCh;
+    static constexpr int kPitch = kCh + 4;                            // floats of a token's channels: other banks than the next's
     static constexpr int kRow = kCh * static_cast<int>(sizeof(E));
     static constexpr int kBc = N * static_cast<int>(sizeof(E));
     static constexpr int kStage = TT * (4 * kRow + 2 * kBc);          // u | dt | z | dy | B | C as they land
-    static constexpr int kWide = TT * (5 * kCh + 2 * N) * 4;          // steps | inputs, e | p | sum q A | C . h | B | C
-    static constexpr int kPart = kWarps * TT * 2 * N * 4;             // each warp's dB | dC
-    static constexpr int kStates = TT * kThreads * 64;                // states before each token
-    static constexpr int kFixed = 2 * kCh * 4;                        // dt_bias | skip
-    static constexpr int kStages = sizeof(E) == 4 ? 1 : 2;
-    static constexpr int kSmem = kStages * kStage + kWide + kPart + kStates + kFixed;
-    static constexpr int kSmemLocal = 2 * kStage + TT * (3 * kCh + 2 * N) * 4 + kFixed;
+    static constexpr int kWide = TT * kPitch * 4;                     // a token's channels in fp32
+    static constexpr int kWideBc = TT * 2 * N * 4;                    // B | C in fp32
+    static constexpr int kStates = TT / 2 * kThreads * 64;            // states before every other token
+    static constexpr int kSmem = kStates + 2 * kStage + 4 * kWide + kWideBc;
+    static constexpr int kSmemLocal = 2 * kStage + 3 * kWide + kWideBc;
 };
 
-// What both kernels have of their place and its rows.
+// What both kernels have of their place, its rows and the channels that a lane widens and stores.
 template <typename E, int N>
 struct Rows {
+    static constexpr int V = vec<E>, WCH = Lay<N>::kWarpCh, PER = WCH / V, PIECES = TT * PER;
     Place w;
-    int n, t0, t1, live, last;
+    int n, t0, t1, live, last, mine, tiles;
     const E* row[4];
     long long ld[4];
     const E* bc[2];
     long long ld_bc;
-    bool gated;
+    bool gated, softplus;
+    float2 bias[V / 2];   // in units of log 2
 
     __device__ __forceinline__ explicit Rows(const SsmParams& p) : w(place_of<Lay<N>::kCh>(p))
     {
@@ -66,8 +68,11 @@ struct Rows {
         t1 = min(p.T, t0 + p.seg_len);
         live = min(n, t1);
         last = n > 0 ? (n - 1) / p.seg_len : 0;
+        tiles = live > t0 ? (live - t0 + TT - 1) / TT : 0;
+        mine = (threadIdx.x >> 5) * WCH + (threadIdx.x & 31) % PER * V;
         const size_t tokens = static_cast<size_t>(w.b) * p.T;
         gated = p.z != nullptr;
+        softplus = p.softplus != 0;
         row[kU] = static_cast<const E*>(p.u) + tokens * p.ld_u + w.first;
         row[kDt] = static_cast<const E*>(p.dt) + tokens * p.ld_dt + w.first;
         row[kZ] = static_cast<const E*>(p.z) + (gated ? tokens * p.ld_z + w.first : 0);
@@ -76,26 +81,27 @@ struct Rows {
         bc[0] = static_cast<const E*>(p.Bt) + tokens * p.ld_bc + w.group * N;
         bc[1] = static_cast<const E*>(p.Ct) + tokens * p.ld_bc + w.group * N;
         ld_bc = p.ld_bc;
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k)
+            bias[k] = mine < w.count && p.dt_bias ? mul2(*reinterpret_cast<const float2*>(p.dt_bias + w.first + mine + 2 * k), both(kLog2e)) : both(0.f);
     }
 
-    // Tile `tile`'s rows to shared memory at `to`; WHOLE: all of them, else u, dt and B.  Zeros past the end.
+    // Tile `tile`'s rows to shared memory at `to`; WHOLE: all of them, else u, dt and B.  Zeros past the end and the channels.
     template <bool WHOLE>
     __device__ __forceinline__ void load(int tile, uint32_t to) const
     {
         using S = Tile<E, N>;
-        using L = Lay<N>;
-        constexpr int V = vec<E>, PIECES = TT * L::kWarpCh / V;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = t0 + tile * TT;
+        const int lane = threadIdx.x & 31, first = t0 + tile * TT;
 #pragma unroll
         for (int k = 0; k < (WHOLE ? 4 : 2); ++k) {
             if (k == kZ && !gated) continue;
 #pragma unroll
             for (int i = 0; i < PIECES; i += 32) {   // a warp's own channels
-                const int piece = i + lane, r = piece / (L::kWarpCh / V), c = warp * L::kWarpCh + piece % (L::kWarpCh / V) * V;
-                const bool ok = piece < PIECES && first + r < live && c < w.count;
+                const int piece = i + lane, r = piece / PER;
+                const bool ok = piece < PIECES && first + r < live && mine < w.count;
                 if (piece < PIECES)
-                    cp_async16(to + k * TT * S::kRow + r * S::kRow + c * static_cast<int>(sizeof(E)),
-                               row[k] + (ok ? static_cast<long long>(first + r) * ld[k] + c : 0), ok);
+                    cp_async16(to + k * TT * S::kRow + r * S::kRow + mine * static_cast<int>(sizeof(E)),
+                               row[k] + (ok ? static_cast<long long>(first + r) * ld[k] + mine : 0), ok);
             }
         }
 #pragma unroll
@@ -107,68 +113,85 @@ struct Rows {
                            bc[k] + (ok ? static_cast<long long>(first + r) * ld_bc + c : 0), ok);
             }
     }
-};
 
-// A landed tile in fp32: steps (times log2 e) and inputs, and with WHOLE p; B, and with WHOLE C.
-template <typename E, int N, bool WHOLE>
-__device__ __forceinline__ void widen(const SsmParams& p, const Rows<E, N>& R, const unsigned char* raw, int count, const float* bias,
-                                      float* steps, float* xs, float* ps, float* Bf)
-{
-    using S = Tile<E, N>;
-    using L = Lay<N>;
-    constexpr int V = vec<E>, PIECES = TT * L::kWarpCh / V, CH = S::kCh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // A landed tile in fp32: steps (in units of log 2) and inputs (times 1 / log 2: B has the factor), and with WHOLE p; B
+    // times log 2, and with WHOLE C.  Steps are 0 past the end.
+    template <bool WHOLE>
+    __device__ __forceinline__ void widen(int tile, const unsigned char* raw, float* steps, float* xs, float* ps, float* Bf) const
+    {
+        using S = Tile<E, N>;
+        const int lane = threadIdx.x & 31, count = live - t0 - tile * TT;
 #pragma unroll
-    for (int i = 0; i < PIECES; i += 32) {
-        const int piece = i + lane, r = piece / (L::kWarpCh / V), c = warp * L::kWarpCh + piece % (L::kWarpCh / V) * V;
-        if (piece < PIECES) {
-            float uu[V], dd[V];
-            const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + c * sizeof(E));
-            unpack(at[kU * TT * S::kRow / 16], uu, E{});
-            unpack(at[kDt * TT * S::kRow / 16], dd, E{});
-            const bool ok = r < count && c < R.w.count;
+        for (int i = 0; i < PIECES; i += 32) {
+            const int piece = i + lane, r = piece / PER;
+            if (piece < PIECES) {
+                float uu[V], dd[V];
+                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
+                const int to = r * S::kPitch + mine;
+                unpack(at[kU * TT * S::kRow / 16], uu, E{});
+                unpack(at[kDt * TT * S::kRow / 16], dd, E{});
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float v = fmaf(dd[k], kLog2e, bias[c + k] * kLog2e);
-                dd[k] = ok ? p.softplus ? softplus2(both(v)).x : v : 0.f;
-                uu[k] = ok ? dd[k] * kLn2 * uu[k] : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < V; k += 4) {
-                *reinterpret_cast<float4*>(steps + r * CH + c + k) = make_float4(dd[k], dd[k + 1], dd[k + 2], dd[k + 3]);
-                *reinterpret_cast<float4*>(xs + r * CH + c + k) = make_float4(uu[k], uu[k + 1], uu[k + 2], uu[k + 3]);
-            }
-            if constexpr (WHOLE) {
-                unpack(at[kDy * TT * S::kRow / 16], uu, E{});
-                if (R.gated) {
-                    unpack(at[kZ * TT * S::kRow / 16], dd, E{});
-#pragma unroll
-                    for (int k = 0; k < V; ++k) uu[k] *= dd[k] * sigmoid(dd[k]);
+                for (int k = 0; k < V; k += 4) {
+                    float2 s0 = fma2(make_float2(dd[k], dd[k + 1]), both(kLog2e), bias[k / 2]);
+                    float2 s1 = fma2(make_float2(dd[k + 2], dd[k + 3]), both(kLog2e), bias[k / 2 + 1]);
+                    if (softplus) s0 = softplus2(s0), s1 = softplus2(s1);
+                    if (r >= count) s0 = s1 = both(0.f);
+                    const float2 x0 = mul2(s0, make_float2(uu[k], uu[k + 1])), x1 = mul2(s1, make_float2(uu[k + 2], uu[k + 3]));
+                    *reinterpret_cast<float4*>(steps + to + k) = make_float4(s0.x, s0.y, s1.x, s1.y);
+                    *reinterpret_cast<float4*>(xs + to + k) = make_float4(x0.x, x0.y, x1.x, x1.y);
                 }
+                if constexpr (WHOLE) {   // rows past the end came as zeros
+                    unpack(at[kDy * TT * S::kRow / 16], uu, E{});
+                    if (gated) {
+                        unpack(at[kZ * TT * S::kRow / 16], dd, E{});
 #pragma unroll
-                for (int k = 0; k < V; k += 4)   // rows past the end came as zeros
-                    *reinterpret_cast<float4*>(ps + r * CH + c + k) = make_float4(uu[k], uu[k + 1], uu[k + 2], uu[k + 3]);
+                        for (int k = 0; k < V; k += 2) {
+                            const float2 v = mul2(silu(make_float2(dd[k], dd[k + 1])), make_float2(uu[k], uu[k + 1]));
+                            uu[k] = v.x, uu[k + 1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(ps + to + k) = make_float4(uu[k], uu[k + 1], uu[k + 2], uu[k + 3]);
+                }
             }
         }
-    }
-    for (int i = threadIdx.x; i < (WHOLE ? 2 : 1) * TT * N / V; i += kThreads) {
-        float v[V];
-        unpack(reinterpret_cast<const uint4*>(raw + 4 * TT * S::kRow)[i], v, E{});
+        for (int i = threadIdx.x; i < (WHOLE ? 2 : 1) * TT * N / V; i += kThreads) {
+            float v[V];
+            unpack(reinterpret_cast<const uint4*>(raw + 4 * TT * S::kRow)[i], v, E{});
+            if (i < TT * N / V)
 #pragma unroll
-        for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(Bf + i * V + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                for (int k = 0; k < V; ++k) v[k] *= kLn2;
+#pragma unroll
+            for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(Bf + i * V + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
     }
+};
+
+__device__ __forceinline__ void pairs(const float* from, float2 (&r)[2])
+{
+    const float4 v = *reinterpret_cast<const float4*>(from);
+    r[0] = make_float2(v.x, v.y), r[1] = make_float2(v.z, v.w);
+}
+__device__ __forceinline__ void spread(const float* from, float2 (&r)[4])
+{
+    const float4 v = *reinterpret_cast<const float4*>(from);
+    r[0] = both(v.x), r[1] = both(v.y), r[2] = both(v.z), r[3] = both(v.w);
 }
 
-__device__ __forceinline__ void pairs(const float4& v, float2 (&r)[2]) { r[0] = make_float2(v.x, v.y), r[1] = make_float2(v.z, v.w); }
-__device__ __forceinline__ void spread(const float4& v, float2 (&r)[4]) { r[0] = both(v.x), r[1] = both(v.y), r[2] = both(v.z), r[3] = both(v.w); }
-
-// h = a h + x B
-__device__ __forceinline__ void advance(const float2 (&dd)[2], const float2 (&xx)[2], const float2 (&bb)[4], const float2 (&A)[2][4], float2 (&h)[2][4])
+// A token's decays, and h = a h + x B.
+__device__ __forceinline__ void decays(const float2 (&dd)[2], const float2 (&A)[2][4], float2 (&a)[2][4])
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) h[k][s] = fma2(ex2_2(mul2(dd[k], A[k][s])), h[k][s], mul2(xx[k], bb[s]));
+        for (int s = 0; s < 4; ++s) a[k][s] = ex2_2(mul2(dd[k], A[k][s]));
+}
+__device__ __forceinline__ void advance(const float2 (&a)[2][4], const float2 (&xx)[2], const float2 (&bb)[4], const float2 (&from)[2][4], float2 (&h)[2][4])
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[k][s] = fma2(a[k][s], from[k][s], mul2(xx[k], bb[s]));
 }
 
 // Each segment by itself: its states' end from zero, the sum of its steps, and its gradient towards its start.
@@ -177,19 +200,15 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
 {
     using S = Tile<E, N>;
     using L = Lay<N>;
-    constexpr int CH = S::kCh;
     extern __shared__ __align__(128) unsigned char smem[];
     float* const steps = reinterpret_cast<float*>(smem + 2 * S::kStage);
-    float *const xs = steps + TT * CH, *const ps = xs + TT * CH, *const Bf = ps + TT * CH, *const Cf = Bf + TT * N;
-    float* const bias = Cf + TT * N;
+    float *const xs = steps + S::kWide / 4, *const ps = xs + S::kWide / 4, *const Bf = ps + S::kWide / 4, *const Cf = Bf + TT * N;
     const Rows<E, N> R(p);
     if (R.w.segment > R.last) return;
-    for (int i = threadIdx.x; i < CH; i += kThreads) bias[i] = i < R.w.count && p.dt_bias ? p.dt_bias[R.w.first + i] : 0.f;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp * L::kWarpCh + lane / L::kLanes * 4, n4 = lane % L::kLanes * 4;
     const bool on = quad < R.w.count;
-    const int tiles = R.live > R.t0 ? (R.live - R.t0 + TT - 1) / TT : 0;
-    if (tiles > 0) R.template load<true>(0, smem_u32(smem));
+    if (R.tiles > 0) R.template load<true>(0, smem_u32(smem));
     cp_async_commit();
     float2 A[2][4], h[2][4], g[2][4], far[2][4], total[2] = {both(0.f), both(0.f)};
     load_states(p.A + static_cast<size_t>(R.w.first + quad) * N + n4, N, on, A);
@@ -197,29 +216,29 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int s = 0; s < 4; ++s) h[k][s] = g[k][s] = both(0.f), far[k][s] = both(1.f);
-    for (int tile = 0; tile < tiles; ++tile) {
-        if (tile + 1 < tiles) R.template load<true>(tile + 1, smem_u32(smem) + ((tile + 1) & 1) * S::kStage);
+    for (int tile = 0; tile < R.tiles; ++tile) {
+        cp_async_wait<0>();
+        __syncthreads();   // the tile has landed, and all warps are done with the one before
+        if (tile + 1 < R.tiles) R.template load<true>(tile + 1, smem_u32(smem) + ((tile + 1) & 1) * S::kStage);
         cp_async_commit();
-        cp_async_wait<1>();
+        R.template widen<true>(tile, smem + (tile & 1) * S::kStage, steps, xs, ps, Bf);
         __syncthreads();
-        const int count = min(TT, R.live - R.t0 - tile * TT);
-        widen<E, N, true>(p, R, smem + (tile & 1) * S::kStage, count, bias, steps, xs, ps, Bf);
-        __syncthreads();
-        for (int r = 0; r < count; ++r) {
-            float2 dd[2], xx[2], pp[2], bb[4], cc[4];
-            pairs(*reinterpret_cast<const float4*>(steps + r * CH + quad), dd);
-            pairs(*reinterpret_cast<const float4*>(xs + r * CH + quad), xx);
-            pairs(*reinterpret_cast<const float4*>(ps + r * CH + quad), pp);
-            spread(*reinterpret_cast<const float4*>(Bf + r * N + n4), bb);
-            spread(*reinterpret_cast<const float4*>(Cf + r * N + n4), cc);
+#pragma unroll 2
+        for (int r = 0; r < TT; ++r) {
+            float2 dd[2], xx[2], pp[2], bb[4], cc[4], a[2][4];
+            pairs(steps + r * S::kPitch + quad, dd);
+            pairs(xs + r * S::kPitch + quad, xx);
+            pairs(ps + r * S::kPitch + quad, pp);
+            spread(Bf + r * N + n4, bb);
+            spread(Cf + r * N + n4, cc);
+            decays(dd, A, a);
+            advance(a, xx, bb, h, h);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 total[k] = add2(total[k], dd[k]);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const float2 a = ex2_2(mul2(dd[k], A[k][s]));
-                    h[k][s] = fma2(a, h[k][s], mul2(xx[k], bb[s]));
-                    far[k][s] = mul2(far[k][s], a);
+                    far[k][s] = mul2(far[k][s], a[k][s]);
                     g[k][s] = fma2(far[k][s], mul2(cc[s], pp[k]), g[k][s]);
                 }
             }
@@ -233,44 +252,24 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
     if (n4 == 0) *reinterpret_cast<float4*>(p.seg_dt + at) = make_float4(total[0].x, total[0].y, total[1].x, total[1].y);
 }
 
-// dB and dC of one token: eight values of each lane, summed over the warp's channel quads.  Lane l ends with the
-// 8 LANES / 32 values that start at result (l / LANES) * that, of [dB of the four states, dC of the four states].
-template <int LANES>
-__device__ __forceinline__ void quads_sum(float (&v)[8])
-{
-    int width = 8;
-#pragma unroll
-    for (int o = 16; o >= LANES; o >>= 1) {
-        width >>= 1;
-        const bool up = threadIdx.x & o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < width) {
-                const float keep = up ? v[width + i] : v[i], give = up ? v[i] : v[width + i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
-    }
-}
-
 template <typename E, int N>
-__global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const __grid_constant__ SsmParams p)
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_kernel(const __grid_constant__ SsmParams p, int blocks)
 {
     using S = Tile<E, N>;
     using L = Lay<N>;
-    constexpr int V = vec<E>, CH = S::kCh, WCH = L::kWarpCh, PIECES = TT * WCH / V;
+    constexpr int V = vec<E>, PER = Rows<E, N>::PER, PIECES = Rows<E, N>::PIECES, LANES = L::kLanes;
     extern __shared__ __align__(128) unsigned char smem[];
-    float4* const hs = reinterpret_cast<float4*>(smem) + threadIdx.x;   // [TT][4][threads]: this lane's states before each token
+    // [TT / 2][4][threads]: this lane's states before every other token; then, in their place, two tokens' parts of dB and dC
+    float4* const hs = reinterpret_cast<float4*>(smem) + threadIdx.x;
     unsigned char* const stages = smem + S::kStates;
-    float* const steps = reinterpret_cast<float*>(stages + S::kStages * S::kStage);
-    float *const xs = steps + TT * CH, *const ps = xs + TT * CH, *const qs = ps + TT * CH, *const ys = qs + TT * CH;
-    float *const Bf = ys + TT * CH, *const Cf = Bf + TT * N;
-    float* const part = Cf + TT * N;   // [warps][TT][2 N]
-    float *const bias = part + kWarps * TT * 2 * N, *const skip = bias + CH;
+    float* const steps = reinterpret_cast<float*>(stages + 2 * S::kStage);
+    float *const xs = steps + S::kWide / 4, *const ps = xs + S::kWide / 4, *const ys = ps + S::kWide / 4;
+    float *const Bf = ys + S::kWide / 4, *const Cf = Bf + TT * N;
 
     const Rows<E, N> R(p);
     const Place& w = R.w;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp * WCH + lane / L::kLanes * 4, n4 = lane % L::kLanes * 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tiles = R.tiles, mine = R.mine;
+    const int quad = warp * L::kWarpCh + lane / LANES * 4, n4 = lane % LANES * 4;
     const bool on = quad < w.count;
     const size_t tokens = static_cast<size_t>(w.b) * p.T;
     E* const du = static_cast<E*>(p.du) + tokens * p.D + w.first;
@@ -283,28 +282,23 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const __grid_constan
         store_vec<E>(ddt, t * p.D + c, make_uint4(0, 0, 0, 0));
         if (R.gated) store_vec<E>(dz, t * p.ld_dz + c, make_uint4(0, 0, 0, 0));
     }
-    for (int i = threadIdx.x; i < CH; i += kThreads) {
-        bias[i] = i < w.count && p.dt_bias ? p.dt_bias[w.first + i] : 0.f;
-        skip[i] = i < w.count && p.skip ? p.skip[w.first + i] : 0.f;
-    }
-    const int tiles = R.live > R.t0 ? (R.live - R.t0 + TT - 1) / TT : 0;
+    float2 skip[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+        skip[k] = mine < w.count && p.skip ? *reinterpret_cast<const float2*>(p.skip + w.first + mine + 2 * k) : both(0.f);
     const uint32_t stage0 = smem_u32(stages);
     const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + quad) * N + n4, all = static_cast<size_t>(p.B) * p.D * N;
-    float2 A[2][4], h[2][4], g[2][4], dA[2][4];
+    float2 A[2][4], h[2][4], g[2][4];
     load_states(p.A + static_cast<size_t>(w.first + quad) * N + n4, N, on, A);
     load_states(p.h_in + mat, N, on && p.h_in, h);
     load_states(p.dh_out + mat, N, on && p.dh_out, g);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) dA[k][s] = both(0.f);
     if (p.segments > 1 && w.segment <= R.last) {
         griddep_wait();
         auto join = [&](int j, const float* from, float2 (&v)[2][4]) {   // v = own + exp(A sum of steps) v
             float2 own[2][4], sum[2];
             load_states(from + j * all + mat, N, on, own);
-            pairs(on ? *reinterpret_cast<const float4*>(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + quad)
-                     : make_float4(0.f, 0.f, 0.f, 0.f), sum);
+            sum[0] = sum[1] = both(0.f);
+            if (on) pairs(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + quad, sum);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -313,187 +307,227 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(const __grid_constan
         for (int j = 0; j < w.segment; ++j) join(j, p.seg_state, h);
         for (int j = R.last; j > w.segment; --j) join(j, p.seg_grad, g);
     }
-    // forwards: the states at every tile's start
+    // forwards: the states at every tile's start, and at the end
     float* const check = p.check + (static_cast<size_t>(w.b) * ((p.T + TT - 1) / TT) + R.t0 / TT) * p.D * N +
                          static_cast<size_t>(w.first + quad) * N + n4;
     const size_t check_step = static_cast<size_t>(p.D) * N;
-    for (int tile = 0; tile + 1 < tiles; ++tile) {
-        __syncthreads();
-        R.template load<false>(tile, stage0);
-        cp_async_commit();
+    if (tiles > 0) R.template load<false>(0, stage0);
+    cp_async_commit();
+    for (int tile = 0; tile < tiles; ++tile) {
         cp_async_wait<0>();
-        __syncthreads();
-        widen<E, N, false>(p, R, stages, TT, bias, steps, xs, ps, Bf);
+        __syncthreads();   // the tile has landed, and all warps are done with the one before
+        if (tile + 1 < tiles)
+            R.template load<false>(tile + 1, stage0 + ((tile + 1) & 1) * S::kStage);
+        cp_async_commit();
+        R.template widen<false>(tile, stages + (tile & 1) * S::kStage, steps, xs, ps, Bf);
         __syncthreads();
         if (on) store_states(check + tile * check_step, N, h);
+#pragma unroll 2
         for (int r = 0; r < TT; ++r) {
-            float2 dd[2], xx[2], bb[4];
-            pairs(*reinterpret_cast<const float4*>(steps + r * CH + quad), dd);
-            pairs(*reinterpret_cast<const float4*>(xs + r * CH + quad), xx);
-            spread(*reinterpret_cast<const float4*>(Bf + r * N + n4), bb);
-            advance(dd, xx, bb, A, h);
+            float2 dd[2], xx[2], bb[4], a[2][4];
+            pairs(steps + r * S::kPitch + quad, dd);
+            pairs(xs + r * S::kPitch + quad, xx);
+            spread(Bf + r * N + n4, bb);
+            decays(dd, A, a);
+            advance(a, xx, bb, h, h);
         }
     }
-    // backwards
-    float dskip[V], dbias[V];
+    // backwards; h: the states after the tile
+    __syncthreads();
+    if (tiles > 0) R.template load<true>(tiles - 1, stage0 + ((tiles - 1) & 1) * S::kStage);
+    cp_async_commit();
+    float* const params = p.part + (static_cast<size_t>(w.segment) * p.B + w.b) * blocks * p.D * (N + 2);
+    const size_t param_step = static_cast<size_t>(p.D) * (N + 2);
+    float2 dA[2][4], dskip[V / 2], dbias[V / 2];
+    auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < V; ++k) dskip[k] = dbias[k] = 0.f;
-    float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / CH) * p.B * p.T + tokens) * p.G + w.group) * 2 * N;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) dA[k][s] = both(0.f);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) dskip[k] = dbias[k] = both(0.f);
+    };
+    auto flush = [&](int block) {   // a block's sums to its row of the partials
+        float* const to = params + block * param_step;
+        if (on) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) dA[k][s] = mul2(dA[k][s], both(kLn2));
+            store_states(to + static_cast<size_t>(w.first + quad) * N + n4, N, dA);
+        }
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {   // lanes l, l + PER, ... have the same channels
+#pragma unroll
+            for (int o = 16; o >= PER; o >>= 1) {
+                dskip[k].x += __shfl_xor_sync(0xffffffffu, dskip[k].x, o), dskip[k].y += __shfl_xor_sync(0xffffffffu, dskip[k].y, o);
+                dbias[k].x += __shfl_xor_sync(0xffffffffu, dbias[k].x, o), dbias[k].y += __shfl_xor_sync(0xffffffffu, dbias[k].y, o);
+            }
+            if (lane < PER && mine < w.count) {
+                *reinterpret_cast<float2*>(to + static_cast<size_t>(p.D) * N + w.first + mine + 2 * k) = dskip[k];
+                *reinterpret_cast<float2*>(to + static_cast<size_t>(p.D) * (N + 1) + w.first + mine + 2 * k) = dbias[k];
+            }
+        }
+        clear();
+    };
+    clear();
+    for (int block = blocks - 1; block >= 0 && block * kBlock >= tiles; --block) flush(block);
+    float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / S::kCh) * p.B * p.T + tokens) * p.G + w.group) * 2 * N;
     for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int count = min(TT, R.live - R.t0 - tile * TT);
-        __syncthreads();
-        R.template load<true>(tile, stage0);
-        cp_async_commit();
-        if (tile + 1 < tiles) load_states(check + tile * check_step, N, on, h);
+        const int first = R.t0 + tile * TT, count = min(TT, R.live - first);
+        const unsigned char* const raw = stages + (tile & 1) * S::kStage;
         cp_async_wait<0>();
         __syncthreads();
-        widen<E, N, true>(p, R, stages, count, bias, steps, xs, ps, Bf);
+        if (tile > 0) R.template load<true>(tile - 1, stage0 + ((tile - 1) & 1) * S::kStage);
+        cp_async_commit();
+        float2 start[2][4];
+        load_states(check + tile * check_step, N, on, start);
+        R.template widen<true>(tile, raw, steps, xs, ps, Bf);
         __syncthreads();
-        for (int r = 0; r < count; ++r) {
-            float2 dd[2], xx[2], bb[4], cc[4];
-            pairs(*reinterpret_cast<const float4*>(steps + r * CH + quad), dd);
-            pairs(*reinterpret_cast<const float4*>(xs + r * CH + quad), xx);
-            spread(*reinterpret_cast<const float4*>(Bf + r * N + n4), bb);
-            spread(*reinterpret_cast<const float4*>(Cf + r * N + n4), cc);
+#pragma unroll
+        for (int j = 0; j < TT / 2; ++j) {   // forwards: the states before tokens 0, 2, ..
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int s = 0; s < 4; s += 2)
-                    hs[(r * 4 + k * 2 + s / 2) * kThreads] = make_float4(h[k][s].x, h[k][s].y, h[k][s + 1].x, h[k][s + 1].y);
-            advance(dd, xx, bb, A, h);
-            if (R.gated) {
-                float2 o[2];
+                    hs[(j * 4 + k * 2 + s / 2) * kThreads] = make_float4(start[k][s].x, start[k][s].y, start[k][s + 1].x, start[k][s + 1].y);
+            if (j == TT / 2 - 1) break;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    o[k] = mul2(cc[0], h[k][0]);
-#pragma unroll
-                    for (int s = 1; s < 4; ++s) o[k] = fma2(cc[s], h[k][s], o[k]);
-                }
-                const float v = quad_sum<L::kLanes>(o[0].x, o[0].y, o[1].x, o[1].y);
-                if (quad_leader<L::kLanes>()) ys[r * CH + quad + quad_channel<L::kLanes>()] = v;
+            for (int r = 2 * j; r < 2 * j + 2; ++r) {
+                float2 dd[2], xx[2], bb[4], a[2][4];
+                pairs(steps + r * S::kPitch + quad, dd);
+                pairs(xs + r * S::kPitch + quad, xx);
+                spread(Bf + r * N + n4, bb);
+                decays(dd, A, a);
+                advance(a, xx, bb, start, start);
             }
         }
-        for (int r = count - 1; r >= 0; --r) {
-            float2 dd[2], xx[2], pp[2], bb[4], cc[4], e[2], qa[2];
-            pairs(*reinterpret_cast<const float4*>(steps + r * CH + quad), dd);
-            pairs(*reinterpret_cast<const float4*>(xs + r * CH + quad), xx);
-            pairs(*reinterpret_cast<const float4*>(ps + r * CH + quad), pp);
-            spread(*reinterpret_cast<const float4*>(Bf + r * N + n4), bb);
-            spread(*reinterpret_cast<const float4*>(Cf + r * N + n4), cc);
-            float2 before[2][4], db[4], dc[4];
+#pragma unroll 1
+        for (int j = TT / 2 - 1; j >= 0; --j) {   // backwards, two tokens at a time
+            const int r = 2 * j;
+            float2 before[2][4], between[2][4], a[2][4], dd[2], xx[2], bb[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int s = 0; s < 4; s += 2) {
-                    const float4 v = hs[(r * 4 + k * 2 + s / 2) * kThreads];
+                    const float4 v = hs[(j * 4 + k * 2 + s / 2) * kThreads];
                     before[k][s] = make_float2(v.x, v.y), before[k][s + 1] = make_float2(v.z, v.w);
                 }
+            pairs(steps + r * S::kPitch + quad, dd);
+            pairs(xs + r * S::kPitch + quad, xx);
+            spread(Bf + r * N + n4, bb);
+            decays(dd, A, a);
+            advance(a, xx, bb, before, between);
+            // one token backwards: `a` its decays, from and h the states before and after it
+            auto back = [&](int t, const float2 (&da)[2][4], const float2 (&d)[2], const float2 (&x)[2], const float2 (&b)[4],
+                            const float2 (&from)[2][4], const float2 (&after)[2][4], int slot) {
+                float2 pp[2], cc[4], e[2], qa[2], o[2], db[4], dc[4];
+                pairs(ps + t * S::kPitch + quad, pp);
+                spread(Cf + t * N + n4, cc);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const float2 here = fma2(cc[s], pp[k], g[k][s]);
+                        g[k][s] = mul2(da[k][s], here);
+                        const float2 q = mul2(g[k][s], from[k][s]);
+                        dA[k][s] = fma2(q, d[k], dA[k][s]);
+                        qa[k] = s ? fma2(q, A[k][s], qa[k]) : mul2(q, A[k][s]);
+                        e[k] = s ? fma2(here, b[s], e[k]) : mul2(here, b[s]);
+                        o[k] = s ? fma2(after[k][s], cc[s], o[k]) : mul2(after[k][s], cc[s]);
+                        db[s] = k ? fma2(here, x[k], db[s]) : mul2(here, x[k]);
+                        dc[s] = k ? fma2(after[k][s], pp[k], dc[s]) : mul2(after[k][s], pp[k]);
+                    }
+                hs[(j * 4 + slot * 2) * kThreads] = make_float4(db[0].x + db[0].y, db[1].x + db[1].y, db[2].x + db[2].y, db[3].x + db[3].y);
+                hs[(j * 4 + slot * 2 + 1) * kThreads] = make_float4(dc[0].x + dc[0].y, dc[1].x + dc[1].y, dc[2].x + dc[2].y, dc[3].x + dc[3].y);
+                const float es = quad_sum<LANES>(e[0].x, e[0].y, e[1].x, e[1].y);
+                const float qq = quad_sum<LANES>(qa[0].x, qa[0].y, qa[1].x, qa[1].y);
+                const float oo = R.gated ? quad_sum<LANES>(o[0].x, o[0].y, o[1].x, o[1].y) : 0.f;
+                __syncwarp();   // all lanes have read what these replace
+                if (quad_leader<LANES>()) {
+                    const int at = t * S::kPitch + quad + quad_channel<LANES>();
+                    xs[at] = es;
+                    ps[at] = qq;
+                    ys[at] = oo;
+                }
+            };
+            {
+                float2 d1[2], x1[2], b1[4], a1[2][4];
+                pairs(steps + (r + 1) * S::kPitch + quad, d1);
+                pairs(xs + (r + 1) * S::kPitch + quad, x1);
+                spread(Bf + (r + 1) * N + n4, b1);
+                decays(d1, A, a1);
+                back(r + 1, a1, d1, x1, b1, between, h, 1);
+            }
+            back(r, a, dd, xx, bb, before, between, 0);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float2 a = ex2_2(mul2(dd[k], A[k][s]));
-                    const float2 here = fma2(cc[s], pp[k], g[k][s]);
-                    g[k][s] = mul2(a, here);
-                    const float2 q = mul2(g[k][s], before[k][s]);
-                    dA[k][s] = fma2(q, dd[k], dA[k][s]);
-                    qa[k] = s ? fma2(q, A[k][s], qa[k]) : mul2(q, A[k][s]);
-                    e[k] = s ? fma2(here, bb[s], e[k]) : mul2(here, bb[s]);
-                    db[s] = k ? fma2(here, xx[k], db[s]) : mul2(here, xx[k]);
-                    dc[s] = k ? fma2(h[k][s], pp[k], dc[s]) : mul2(h[k][s], pp[k]);
-                    h[k][s] = before[k][s];
-                }
-            float v[8];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) v[s] = db[s].x + db[s].y, v[4 + s] = dc[s].x + dc[s].y;
-            quads_sum<L::kLanes>(v);
-            constexpr int WIDTH = L::kLanes / 4;   // values of a lane
-            const int result = lane / L::kLanes * WIDTH;
-#pragma unroll
-            for (int i = 0; i < WIDTH; ++i) {
-                const int j = result + i;   // of dB's four states, then dC's
-                part[(warp * TT + r) * 2 * N + (j >= 4 ? N : 0) + n4 + j % 4] = v[i];
-            }
-            const float es = quad_sum<L::kLanes>(e[0].x, e[0].y, e[1].x, e[1].y);
-            const float qq = quad_sum<L::kLanes>(qa[0].x, qa[0].y, qa[1].x, qa[1].y);
-            __syncwarp();
-            if (quad_leader<L::kLanes>()) {
-                xs[r * CH + quad + quad_channel<L::kLanes>()] = es;
-                qs[r * CH + quad + quad_channel<L::kLanes>()] = qq;
-            }
+                for (int s = 0; s < 4; ++s) h[k][s] = before[k][s];
         }
         __syncthreads();
-        const int first = R.t0 + tile * TT;
+        // dB and dC of the tile: each of a token's 2 N sums runs over the CTA's channel quads
+        const float* const parts = reinterpret_cast<const float*>(smem);
         for (int i = threadIdx.x; i < count * 2 * N; i += kThreads) {
-            const int r = i / (2 * N), j = i % (2 * N);
-            float a = part[r * 2 * N + j];
+            const int r = i / (2 * N), c = i % (2 * N) / N, n = i % N;   // B's, then C's
+            const float* const from = parts + ((r / 2 * 4 + r % 2 * 2 + c) * kThreads + n / 4) * 4 + n % 4;
+            float sum = 0.f;
+            if (N == 16) {   // C's lanes one quad ahead: other banks
 #pragma unroll
-            for (int k = 1; k < kWarps; ++k) a += part[(k * TT + r) * 2 * N + j];
-            bc_part[static_cast<size_t>(first + r) * p.G * 2 * N + j] = a;
+                for (int q = 0; q < kThreads / LANES; ++q) sum += from[(q ^ c) * LANES * 4];
+            } else {
+#pragma unroll
+                for (int q = 0; q < kThreads / LANES; ++q) sum += from[q * LANES * 4];
+            }
+            bc_part[static_cast<size_t>(first + r) * p.G * 2 * N + i % (2 * N)] = c ? sum : sum * kLn2;
         }
 #pragma unroll
         for (int i = 0; i < PIECES; i += 32) {
-            const int piece = i + lane, r = piece / (WCH / V), c = warp * WCH + piece % (WCH / V) * V;
-            if (piece < PIECES && r < count && c < w.count) {
-                float uu[V], dd[V], out[V], sl[V];
-                const uint4* const at = reinterpret_cast<const uint4*>(stages + r * S::kRow + c * sizeof(E));
+            const int piece = i + lane, r = piece / PER;
+            if (piece < PIECES && r < count && mine < w.count) {
+                float uu[V], vv[V], yy[V], zz[V], o1[V], o2[V], o3[V];
+                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
                 unpack(at[kU * TT * S::kRow / 16], uu, E{});
-                unpack(at[kDt * TT * S::kRow / 16], dd, E{});
+                unpack(at[kDt * TT * S::kRow / 16], vv, E{});
+                unpack(at[kDy * TT * S::kRow / 16], yy, E{});
+                if (R.gated) unpack(at[kZ * TT * S::kRow / 16], zz, E{});
                 const size_t t = first + r;
-                const int at32 = r * CH + c;
+                const int here = r * S::kPitch + mine;
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float pk = ps[at32 + k], es = xs[at32 + k];
-                    out[k] = fmaf(es, steps[at32 + k] * kLn2, skip[c + k] * pk);
-                    dskip[k] = fmaf(pk, uu[k], dskip[k]);
-                    const float ds = fmaf(es, uu[k], qs[at32 + k]);
-                    sl[k] = p.softplus ? ds * sigmoid(dd[k] + bias[c + k]) : ds;
-                    dbias[k] += sl[k];
-                }
-                store_vec<E>(du, t * p.D + c, pack(out, E{}));
-                store_vec<E>(ddt, t * p.D + c, pack(sl, E{}));
-                if (R.gated) {
-                    float zz[V];
-                    unpack(at[kDy * TT * S::kRow / 16], dd, E{});
-                    unpack(at[kZ * TT * S::kRow / 16], zz, E{});
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float s = sigmoid(zz[k]);
-                        out[k] = dd[k] * fmaf(skip[c + k], uu[k], ys[at32 + k]) * s * fmaf(zz[k], 1.f - s, 1.f);
+                for (int k = 0; k < V; k += 2) {
+                    auto two = [&](const float* from) { return *reinterpret_cast<const float2*>(from + here + k); };
+                    const float2 u = make_float2(uu[k], uu[k + 1]), dy = make_float2(yy[k], yy[k + 1]);
+                    const float2 e = two(xs);   // times log 2, as B
+                    float2 pk = dy;
+                    if (R.gated) {
+                        const float2 z = make_float2(zz[k], zz[k + 1]), f = add2(ex2_2(mul2(z, both(-kLog2e))), both(1.f));
+                        const float2 sg = make_float2(rcp_approx(f.x), rcp_approx(f.y)), gate = mul2(z, sg);
+                        pk = mul2(dy, gate);
+                        // silu'(z) = sg + z sg (1 - sg)
+                        const float2 slope = fma2(gate, fma2(sg, both(-1.f), both(1.f)), sg);
+                        const float2 v = mul2(mul2(dy, fma2(skip[k / 2], u, two(ys))), slope);
+                        o3[k] = v.x, o3[k + 1] = v.y;
                     }
-                    store_vec<E>(dz, t * p.ld_dz + c, pack(out, E{}));
+                    dskip[k / 2] = fma2(pk, u, dskip[k / 2]);
+                    const float2 v = fma2(e, two(steps), mul2(skip[k / 2], pk));
+                    o1[k] = v.x, o1[k + 1] = v.y;
+                    float2 ds = fma2(mul2(e, both(kLog2e)), u, two(ps));
+                    if (R.softplus) {
+                        const float2 f = add2(ex2_2(mul2(fma2(make_float2(vv[k], vv[k + 1]), both(kLog2e), R.bias[k / 2]), both(-1.f))), both(1.f));
+                        ds = mul2(ds, make_float2(rcp_approx(f.x), rcp_approx(f.y)));
+                    }
+                    dbias[k / 2] = add2(dbias[k / 2], ds);
+                    o2[k] = ds.x, o2[k + 1] = ds.y;
                 }
+                store_vec<E>(du, t * p.D + mine, pack(o1, E{}));
+                store_vec<E>(ddt, t * p.D + mine, pack(o2, E{}));
+                if (R.gated) store_vec<E>(dz, t * p.ld_dz + mine, pack(o3, E{}));
             }
         }
+        if (tile % kBlock == 0) flush(tile / kBlock);
     }
+    cp_async_wait<0>();
     if (w.segment == 0 && on && p.dh_in) store_states(p.dh_in + mat, N, g);
-    float* const params = p.part + (static_cast<size_t>(w.segment) * p.B + w.b) * p.D * (N + 2);
-    if (on) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) dA[k][s] = mul2(dA[k][s], both(kLn2));
-        store_states(params + static_cast<size_t>(w.first + quad) * N + n4, N, dA);
-    }
-    // a channel's sums over the rows that its lanes took
-    constexpr int PER = WCH / V;   // lanes l, l + PER, ... have the same channels
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-#pragma unroll
-        for (int o = 16; o >= PER; o >>= 1) {
-            dskip[k] += __shfl_xor_sync(0xffffffffu, dskip[k], o);
-            dbias[k] += __shfl_xor_sync(0xffffffffu, dbias[k], o);
-        }
-    }
-    if (lane < PER) {
-        const int c = warp * WCH + lane * V;
-        if (c < w.count)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                params[static_cast<size_t>(p.D) * N + w.first + c + k] = dskip[k];
-                params[static_cast<size_t>(p.D) * (N + 1) + w.first + c + k] = dbias[k];
-            }
-    }
 }
 
 // dB and dC: the partials' sums over the ranges of a group's channels; zeros past the end.
@@ -518,14 +552,14 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const __grid_constant__ Ssm
 }
 
 struct Plan {
-    int segments, seg_len, chan_tiles;
+    int segments, seg_len, chan_tiles, blocks;   // blocks: of a segment, with partial sums of their own
     long long ctas;   // of one segment
 };
 
 Plan plan_of(int B, int T, int D, int N, int G)
 {
     const int ch = kWarps * 128 / (N / 4), dg = D / G;
-    Plan plan{1, std::max(1, T), (dg + ch - 1) / ch, 0};
+    Plan plan{1, std::max(1, T), (dg + ch - 1) / ch, (std::max(1, T) + kBlock * TT - 1) / (kBlock * TT), 0};
     plan.ctas = static_cast<long long>(B) * G * plan.chan_tiles;
     const int most = std::max(1, T / (8 * TT));
     const int segments = plan.ctas >= 2 * kSms ? 1 : static_cast<int>(std::min<long long>(most, std::min<long long>(64, (2 * kSms + plan.ctas - 1) / plan.ctas)));
@@ -533,6 +567,7 @@ Plan plan_of(int B, int T, int D, int N, int G)
     const int tiles = (T + TT - 1) / TT, per = (tiles + segments - 1) / segments;
     plan.segments = (tiles + per - 1) / per;
     plan.seg_len = per * TT;
+    plan.blocks = (per + kBlock - 1) / kBlock;
     return plan;
 }
 
@@ -557,7 +592,7 @@ Regions regions_of(const Plan& plan, int B, int T, int D, int N, int G)
     r.seg_dt = take(seg * streams);
     r.check = take(static_cast<size_t>((T + TT - 1) / TT) * streams * N);
     r.bc_part = take(static_cast<size_t>(plan.chan_tiles) * B * T * G * 2 * N);
-    r.part = take(static_cast<size_t>(plan.segments) * B * D * (N + 2));
+    r.part = take(static_cast<size_t>(plan.segments) * plan.blocks * B * D * (N + 2));
     r.bytes = std::max<size_t>(256, at * 4);
     return r;
 }
@@ -578,13 +613,13 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         rc = launched();
         if (rc != SRWM_OK) return rc;
     }
-    ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(p);
+    ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(p, plan.blocks);
     rc = launched();
     if (rc != SRWM_OK) return rc;
     const long long quads = static_cast<long long>(p.B) * p.T * (2 * p.G * N / 4);
     if (quads > 0) rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, p, plan.chan_tiles);
     if (rc != SRWM_OK) return rc;
-    const long long rows = static_cast<long long>(plan.segments) * p.B;
+    const long long rows = static_cast<long long>(plan.segments) * p.B * plan.blocks;
     return sum_launch({p.part, rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}}, st);
 }
 
