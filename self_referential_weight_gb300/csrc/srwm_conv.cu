@@ -171,32 +171,6 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p)
     for (int i = 0; i < W - 1; ++i) store_vec<E>(p.state_out, states + static_cast<size_t>(i) * p.D, row[i + 1]);
 }
 
-// Four channels of a row: half a vector of the 16-bit types.
-template <typename E> struct Quad { using type = uint2; };
-template <> struct Quad<float> { using type = uint4; };
-
-template <typename E>
-__device__ __forceinline__ typename Quad<E>::type load_quad(const void* p, size_t element)
-{
-    return __ldg(reinterpret_cast<const typename Quad<E>::type*>(static_cast<const E*>(p) + element));
-}
-__device__ __forceinline__ void unpack_quad(const uint4& u, float (&f)[4], float) { unpack(u, f, 0.f); }
-template <typename E>
-__device__ __forceinline__ void unpack_quad(const uint2& u, float (&f)[4], E)
-{
-    float e[8];
-    unpack(make_uint4(u.x, u.y, 0u, 0u), e, E{});
-    f[0] = e[0], f[1] = e[1], f[2] = e[2], f[3] = e[3];
-}
-__device__ __forceinline__ uint4 pack_quad(const float (&f)[4], float) { return pack(f, 0.f); }
-template <typename E>
-__device__ __forceinline__ uint2 pack_quad(const float (&f)[4], E) { return make_uint2(pack2(f[0], f[1], E{}), pack2(f[2], f[3], E{})); }
-template <typename E>
-__device__ __forceinline__ void store_quad(void* p, size_t element, const typename Quad<E>::type& v)
-{
-    *reinterpret_cast<typename Quad<E>::type*>(static_cast<E*>(p) + element) = v;
-}
-
 // How the threads of conv_grad_kernel share the channels: groups of up to 32 vectors of four channels, a run per slot.
 struct GradPlan {
     int groups, vecs, slots, parts, runs;

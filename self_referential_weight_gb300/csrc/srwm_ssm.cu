@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
 
     const Place w = place_of<S::kCh>(p);
     const int n = valid_tokens(p.lengths, w.b, p.T);
-    const int t0 = w.segment * p.seg_len, t1 = min(p.T, t0 + p.seg_len), live = min(n, t1);
-    const int last = n > 0 ? (n - 1) / p.seg_len : 0;   // the segment at whose end the sequence ends
+    const int t0 = w.segment * w.seg_len, t1 = min(p.T, t0 + w.seg_len), live = min(n, t1);
+    const int last = n > 0 ? (n - 1) / w.seg_len : 0;   // the segment at whose end the sequence ends
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int own = warp * WCH + lane % S::kSets * kLaneCh, n8 = lane / S::kSets * 8;   // this lane's channels and states
     const bool on = own < w.count;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
     if (tiles > 0) load(0);
     cp_async_commit();
 
-    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + own) * N + n8, all = static_cast<size_t>(p.B) * p.D * N;
+    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + own) * N + n8;
     float2 A[kLaneCh][4], h[kLaneCh][4];
 #pragma unroll
     for (int c = 0; c < kLaneCh; ++c) {
@@ -168,11 +168,12 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
         griddep_wait();
         for (int j = 0; j < w.segment; ++j) {
             float sum[kLaneCh] = {};
-            if (on) load_ch(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + own, sum);
+            const size_t at = segment_at(p, w, j) + own;
+            if (on) load_ch(p.seg_dt + at, sum);
 #pragma unroll
             for (int c = 0; c < kLaneCh; ++c) {
                 float2 part[4];
-                load8(p.seg_state + j * all + mat + c * N, on, part);
+                load8(p.seg_state + (at + c) * N + n8, on, part);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) h[c][s] = fma2(ex2_2(mul2(both(sum[c]), A[c][s])), h[c][s], part[s]);
             }
@@ -304,10 +305,10 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
             for (int c = 0; c < kLaneCh; ++c) store8(p.h_out + mat + c * N, h[c]);
     } else if (on) {
 #pragma unroll
-        for (int c = 0; c < kLaneCh; ++c) store8(p.seg_state + w.segment * all + mat + c * N, h[c]);
+        for (int c = 0; c < kLaneCh; ++c) store8(p.seg_state + (segment_at(p, w, w.segment) + own + c) * N + n8, h[c]);
         if (n8 == 0)
 #pragma unroll
-            for (int c = 0; c < kLaneCh; ++c) p.seg_dt[(static_cast<size_t>(w.segment) * p.B + w.b) * p.D + w.first + own + c] = total[c];
+            for (int c = 0; c < kLaneCh; ++c) p.seg_dt[segment_at(p, w, w.segment) + own + c] = total[c];
     }
     cp_async_wait<0>();
 }
@@ -350,20 +351,11 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constan
     static_cast<E*>(p.y)[static_cast<size_t>(b) * p.D + c] = from_f<E>(o);
 }
 
-struct Plan {
-    int segments, seg_len;
-};
-
-// Segments of whole tiles, where whole sequences would leave most of the SMs idle.
-Plan plan_of(int B, int T, int D, int N, int G)
+// Seven CTAs on an SM.
+Split plan_of(int B, int T, int D, int N, int G)
 {
     const int ch = kPromptWarps * kLaneCh * 256 / N, dg = D / G;
-    const long long ctas = static_cast<long long>(B) * G * ((dg + ch - 1) / ch);
-    const int most = std::max(1, T / (4 * kWhole));
-    const int segments = ctas >= 4 * kSms ? 1 : static_cast<int>(std::min<long long>(most, std::min<long long>(64, (8 * kSms + ctas - 1) / ctas)));
-    if (segments <= 1) return {1, std::max(1, T)};
-    const int tiles = (T + kWhole - 1) / kWhole, per = (tiles + segments - 1) / segments;
-    return {(tiles + per - 1) / per, per * kWhole};
+    return split_of(B, static_cast<long long>(G) * ((dg + ch - 1) / ch), T, 7 * kSms, 0.25, kWhole, 4 * kWhole);
 }
 
 template <typename E, int N>
@@ -371,18 +363,20 @@ int forward(const SsmParams& p, cudaStream_t st)
 {
     using S = Tile<E, N>;
     const int dg = p.D / p.G;
-    const unsigned grid = static_cast<unsigned>(p.B) * p.G * ((dg + S::kCh - 1) / S::kCh);
+    const unsigned ctas = static_cast<unsigned>(p.G) * ((dg + S::kCh - 1) / S::kCh), split = ctas * (p.B - p.whole);
     if (cudaFuncSetAttribute(ssm_kernel<E, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(ssm_kernel<E, N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
         cudaGetLastError();
         return SRWM_ERR_CUDA;
     }
-    if (p.segments > 1) {
-        ssm_kernel<E, N, false><<<grid * (p.segments - 1), kPromptThreads, S::kSmem, st>>>(p);
+    if (split > 0) {
+        SsmParams q = p;
+        q.first = static_cast<int>(ctas * p.whole);
+        ssm_kernel<E, N, false><<<split * (p.segments - 1), kPromptThreads, S::kSmem, st>>>(q);
         const int rc = launched();
         if (rc != SRWM_OK) return rc;
     }
-    ssm_kernel<E, N, true><<<grid * p.segments, kPromptThreads, S::kSmem, st>>>(p);
+    ssm_kernel<E, N, true><<<ctas * p.whole + split * p.segments, kPromptThreads, S::kSmem, st>>>(p);
     return launched();
 }
 
@@ -413,16 +407,16 @@ int by_type(bool one, int dtype, const SsmParams& p, cudaStream_t st)
 
 size_t ssm_scratch(int B, int T, int D, int N, int G)
 {
-    const Plan plan = plan_of(B, T, D, N, G);
-    return plan.segments > 1 ? round256(static_cast<size_t>(plan.segments) * B * D * (N + 1) * 4) : 256;
+    const Split plan = plan_of(B, T, D, N, G);
+    return std::max<size_t>(256, round256(static_cast<size_t>(plan.segments) * (B - plan.whole) * D * (N + 1) * 4));
 }
 
 int ssm_launch(int dtype, SsmParams& p, void* workspace, cudaStream_t st)
 {
-    const Plan plan = plan_of(p.B, p.T, p.D, p.N, p.G);
-    p.segments = plan.segments, p.seg_len = plan.seg_len;
+    const Split plan = plan_of(p.B, p.T, p.D, p.N, p.G);
+    p.whole = plan.whole, p.segments = plan.segments, p.seg_len = plan.seg_len;
     p.seg_state = static_cast<float*>(workspace);
-    p.seg_dt = p.seg_state + static_cast<size_t>(plan.segments) * p.B * p.D * p.N;
+    p.seg_dt = p.seg_state + static_cast<size_t>(plan.segments) * (p.B - plan.whole) * p.D * p.N;
     return by_type(false, dtype, p, st);
 }
 

@@ -17,7 +17,7 @@ namespace ssm {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;
+constexpr int kWarps = 2;
 constexpr int kThreads = 32 * kWarps;
 
 template <int N>
@@ -82,25 +82,50 @@ __device__ __forceinline__ int valid_tokens(const int* lengths, int b, int T)
     return lengths ? min(max(__ldg(lengths + b), 0), T) : T;
 }
 
-// A CTA's place: a segment of a sequence and a range of a group's channels.
+// A CTA's place: a sequence, or a segment of one, and a range of a group's channels.
 struct Place {
-    int b, group, first, count, segment;   // channels first .. first + count - 1 of D
+    int b, group, first, count;   // channels first .. first + count - 1 of D
+    int segment, seg_len;
 };
 template <int CH>
 __device__ __forceinline__ Place place_of(const SsmParams& p)
 {
     const int dg = p.D / p.G, tiles = (dg + CH - 1) / CH;
-    unsigned i = blockIdx.x;
+    const unsigned i = blockIdx.x + p.first, range = i % (p.G * tiles), row = i / (p.G * tiles), split = row - p.whole;
     Place w;
-    const int tile = static_cast<int>(i % tiles);
-    i /= tiles;
-    w.group = static_cast<int>(i % p.G);
-    i /= p.G;
-    w.b = static_cast<int>(i % p.B);
-    w.segment = static_cast<int>(i / p.B);
+    const bool whole = row < static_cast<unsigned>(p.whole);
+    w.b = static_cast<int>(whole ? row : p.whole + split % (p.B - p.whole));
+    w.segment = static_cast<int>(whole ? 0 : split / (p.B - p.whole));
+    w.seg_len = whole ? max(p.T, 1) : p.seg_len;
+    w.group = static_cast<int>(range) / tiles;
+    const int tile = static_cast<int>(range) % tiles;
     w.first = w.group * dg + tile * CH;
     w.count = min(CH, dg - tile * CH);
     return w;
+}
+// Where segment j of the place's sequence has its channels in the segments' arrays, [segments, B - whole, D].
+__device__ __forceinline__ size_t segment_at(const SsmParams& p, const Place& w, int j)
+{
+    return (static_cast<size_t>(j) * (p.B - p.whole) + (w.b - p.whole)) * p.D + w.first;
+}
+
+// Which sequences run whole and how the others are cut, for a kernel of `ctas` CTAs a sequence of which `slots` run at once.
+// Waves of whole sequences fill the GPU; what is left over is cut into as many segments as fill it once more where it is
+// less than `share` of it: a CTA by itself takes a large part of a full wave's time, the cut some more work.
+struct Split {
+    int whole, segments, seg_len;
+};
+inline Split split_of(long long B, long long ctas, int T, int slots, double share, int unit, int least)
+{
+    const Split uncut{static_cast<int>(B), 1, T > 0 ? T : 1};
+    const long long whole = B * ctas / slots * slots / ctas, rest = (B - whole) * ctas;
+    if (rest == 0 || rest > share * slots) return uncut;
+    long long segments = slots / rest;
+    if (segments > T / least) segments = T / least;
+    if (segments > 64) segments = 64;
+    if (segments < 2) return uncut;
+    const int units = (T + unit - 1) / unit, per = static_cast<int>((units + segments - 1) / segments);
+    return {static_cast<int>(whole), (units + per - 1) / per, per * unit};
 }
 
 // Four states of each of four channels, [.., D, N] from channel c and state n on: pairs are of channels.

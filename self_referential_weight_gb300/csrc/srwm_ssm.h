@@ -15,9 +15,10 @@ struct SsmParams {
     float* h_out;                              // [B, D, N] or NULL
     long long ld_u, ld_dt, ld_z, ld_bc;
     int B, T, D, N, G, softplus;
-    // the axis in segments of seg_len tokens, and their own results (from zero) in the workspace
-    int segments, seg_len;
-    float *seg_state, *seg_dt;                 // [segments, B, D, N], [segments, B, D]
+    // the first `whole` sequences run whole; the others' axis is cut into segments of seg_len tokens, whose own results
+    // (from zero) are in the workspace.  first: of the blocks of all of these, the launch's first
+    int whole, segments, seg_len, first;
+    float *seg_state, *seg_dt;                 // [segments, B - whole, D, N], [segments, B - whole, D]
     // backward
     const void* dy;                            // [B, T, D]
     const float* dh_out;                       // [B, D, N] or NULL

@@ -40,7 +40,8 @@ struct Tile {
     static constexpr int kPitch = kCh + 4;                            // floats of a token's channels: other banks than the next's
     static constexpr int kRow = kCh * static_cast<int>(sizeof(E));
     static constexpr int kBc = N * static_cast<int>(sizeof(E));
-    static constexpr int kStage = TT * (4 * kRow + 2 * kBc);          // u | dt | z | dy | B | C as they land
+    static constexpr int kHalf = TT * (2 * kRow + kBc);               // u | dt | B as they land
+    static constexpr int kStage = 2 * kHalf;                          // .. | z | dy | C
     static constexpr int kWide = TT * kPitch * 4;                     // a token's channels in fp32
     static constexpr int kWideBc = TT * 2 * N * 4;                    // B | C in fp32
     static constexpr int kStates = TT / 2 * kThreads * 64;            // states before every other token
@@ -51,7 +52,8 @@ struct Tile {
 // What both kernels have of their place, its rows and the channels that a lane widens and stores.
 template <typename E, int N>
 struct Rows {
-    static constexpr int V = vec<E>, WCH = Lay<N>::kWarpCh, PER = WCH / V, PIECES = TT * PER;
+    static constexpr int V = vec<E>, WCH = Lay<N>::kWarpCh;
+    static constexpr int PER = WCH / 4, PIECES = TT * PER;   // four channels a lane
     Place w;
     int n, t0, t1, live, last, mine, tiles;
     const E* row[4];
@@ -59,17 +61,17 @@ struct Rows {
     const E* bc[2];
     long long ld_bc;
     bool gated, softplus;
-    float2 bias[V / 2];   // in units of log 2
+    float2 bias[2];   // in units of log 2
 
     __device__ __forceinline__ explicit Rows(const SsmParams& p) : w(place_of<Lay<N>::kCh>(p))
     {
         n = valid_tokens(p.lengths, w.b, p.T);
-        t0 = w.segment * p.seg_len;
-        t1 = min(p.T, t0 + p.seg_len);
+        t0 = w.segment * w.seg_len;
+        t1 = min(p.T, t0 + w.seg_len);
         live = min(n, t1);
-        last = n > 0 ? (n - 1) / p.seg_len : 0;
+        last = n > 0 ? (n - 1) / w.seg_len : 0;
         tiles = live > t0 ? (live - t0 + TT - 1) / TT : 0;
-        mine = (threadIdx.x >> 5) * WCH + (threadIdx.x & 31) % PER * V;
+        mine = (threadIdx.x >> 5) * WCH + (threadIdx.x & 31) % PER * 4;
         const size_t tokens = static_cast<size_t>(w.b) * p.T;
         gated = p.z != nullptr;
         softplus = p.softplus != 0;
@@ -82,9 +84,13 @@ struct Rows {
         bc[1] = static_cast<const E*>(p.Ct) + tokens * p.ld_bc + w.group * N;
         ld_bc = p.ld_bc;
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k)
+        for (int k = 0; k < 2; ++k)
             bias[k] = mine < w.count && p.dt_bias ? mul2(*reinterpret_cast<const float2*>(p.dt_bias + w.first + mine + 2 * k), both(kLog2e)) : both(0.f);
     }
+
+    // Where row kind k's tile, and B's or C's, begin within a stage.
+    static __device__ __forceinline__ constexpr int row_at(int k) { return k / 2 * Tile<E, N>::kHalf + k % 2 * TT * Tile<E, N>::kRow; }
+    static __device__ __forceinline__ constexpr int bc_at(int k) { return k * Tile<E, N>::kHalf + 2 * TT * Tile<E, N>::kRow; }
 
     // Tile `tile`'s rows to shared memory at `to`; WHOLE: all of them, else u, dt and B.  Zeros past the end and the channels.
     template <bool WHOLE>
@@ -96,12 +102,12 @@ struct Rows {
         for (int k = 0; k < (WHOLE ? 4 : 2); ++k) {
             if (k == kZ && !gated) continue;
 #pragma unroll
-            for (int i = 0; i < PIECES; i += 32) {   // a warp's own channels
-                const int piece = i + lane, r = piece / PER;
-                const bool ok = piece < PIECES && first + r < live && mine < w.count;
-                if (piece < PIECES)
-                    cp_async16(to + k * TT * S::kRow + r * S::kRow + mine * static_cast<int>(sizeof(E)),
-                               row[k] + (ok ? static_cast<long long>(first + r) * ld[k] + mine : 0), ok);
+            for (int i = 0; i < TT * WCH / V; i += 32) {   // a warp's own channels
+                const int piece = i + lane, r = piece / (WCH / V), c = (threadIdx.x >> 5) * WCH + piece % (WCH / V) * V;
+                const bool ok = piece < TT * WCH / V && first + r < live && c < w.count;
+                if (piece < TT * WCH / V)
+                    cp_async16(to + row_at(k) + r * S::kRow + c * static_cast<int>(sizeof(E)),
+                               row[k] + (ok ? static_cast<long long>(first + r) * ld[k] + c : 0), ok);
             }
         }
 #pragma unroll
@@ -109,9 +115,15 @@ struct Rows {
             for (int i = threadIdx.x; i < TT * N / V; i += kThreads) {
                 const int r = i / (N / V), c = i % (N / V) * V;
                 const bool ok = first + r < live;
-                cp_async16(to + 4 * TT * S::kRow + (k * TT + r) * S::kBc + c * static_cast<int>(sizeof(E)),
+                cp_async16(to + bc_at(k) + r * S::kBc + c * static_cast<int>(sizeof(E)),
                            bc[k] + (ok ? static_cast<long long>(first + r) * ld_bc + c : 0), ok);
             }
+    }
+
+    // Four values of row kind k, `at` the place within a row of the first kind.
+    static __device__ __forceinline__ void get(const unsigned char* at, int k, float (&f)[4])
+    {
+        unpack_quad(*reinterpret_cast<const typename Quad<E>::type*>(at + row_at(k)), f, E{});
     }
 
     // A landed tile in fp32: steps (in units of log 2) and inputs (times 1 / log 2: B has the factor), and with WHOLE p; B
@@ -125,39 +137,32 @@ struct Rows {
         for (int i = 0; i < PIECES; i += 32) {
             const int piece = i + lane, r = piece / PER;
             if (piece < PIECES) {
-                float uu[V], dd[V];
-                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
+                float uu[4], dd[4];
+                const unsigned char* const at = raw + r * S::kRow + mine * static_cast<int>(sizeof(E));
                 const int to = r * S::kPitch + mine;
-                unpack(at[kU * TT * S::kRow / 16], uu, E{});
-                unpack(at[kDt * TT * S::kRow / 16], dd, E{});
-#pragma unroll
-                for (int k = 0; k < V; k += 4) {
-                    float2 s0 = fma2(make_float2(dd[k], dd[k + 1]), both(kLog2e), bias[k / 2]);
-                    float2 s1 = fma2(make_float2(dd[k + 2], dd[k + 3]), both(kLog2e), bias[k / 2 + 1]);
-                    if (softplus) s0 = softplus2(s0), s1 = softplus2(s1);
-                    if (r >= count) s0 = s1 = both(0.f);
-                    const float2 x0 = mul2(s0, make_float2(uu[k], uu[k + 1])), x1 = mul2(s1, make_float2(uu[k + 2], uu[k + 3]));
-                    *reinterpret_cast<float4*>(steps + to + k) = make_float4(s0.x, s0.y, s1.x, s1.y);
-                    *reinterpret_cast<float4*>(xs + to + k) = make_float4(x0.x, x0.y, x1.x, x1.y);
-                }
+                get(at, kU, uu);
+                get(at, kDt, dd);
+                float2 s0 = fma2(make_float2(dd[0], dd[1]), both(kLog2e), bias[0]);
+                float2 s1 = fma2(make_float2(dd[2], dd[3]), both(kLog2e), bias[1]);
+                if (softplus) s0 = softplus2(s0), s1 = softplus2(s1);
+                if (r >= count) s0 = s1 = both(0.f);
+                const float2 x0 = mul2(s0, make_float2(uu[0], uu[1])), x1 = mul2(s1, make_float2(uu[2], uu[3]));
+                *reinterpret_cast<float4*>(steps + to) = make_float4(s0.x, s0.y, s1.x, s1.y);
+                *reinterpret_cast<float4*>(xs + to) = make_float4(x0.x, x0.y, x1.x, x1.y);
                 if constexpr (WHOLE) {   // rows past the end came as zeros
-                    unpack(at[kDy * TT * S::kRow / 16], uu, E{});
+                    get(at, kDy, uu);
+                    float2 p0 = make_float2(uu[0], uu[1]), p1 = make_float2(uu[2], uu[3]);
                     if (gated) {
-                        unpack(at[kZ * TT * S::kRow / 16], dd, E{});
-#pragma unroll
-                        for (int k = 0; k < V; k += 2) {
-                            const float2 v = mul2(silu(make_float2(dd[k], dd[k + 1])), make_float2(uu[k], uu[k + 1]));
-                            uu[k] = v.x, uu[k + 1] = v.y;
-                        }
+                        get(at, kZ, dd);
+                        p0 = mul2(silu(make_float2(dd[0], dd[1])), p0), p1 = mul2(silu(make_float2(dd[2], dd[3])), p1);
                     }
-#pragma unroll
-                    for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(ps + to + k) = make_float4(uu[k], uu[k + 1], uu[k + 2], uu[k + 3]);
+                    *reinterpret_cast<float4*>(ps + to) = make_float4(p0.x, p0.y, p1.x, p1.y);
                 }
             }
         }
         for (int i = threadIdx.x; i < (WHOLE ? 2 : 1) * TT * N / V; i += kThreads) {
             float v[V];
-            unpack(reinterpret_cast<const uint4*>(raw + 4 * TT * S::kRow)[i], v, E{});
+            unpack(reinterpret_cast<const uint4*>(raw + bc_at(i >= TT * N / V))[i % (TT * N / V)], v, E{});
             if (i < TT * N / V)
 #pragma unroll
                 for (int k = 0; k < V; ++k) v[k] *= kLn2;
@@ -246,14 +251,19 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
     }
     cp_async_wait<0>();
     if (!on) return;
-    const size_t at = (static_cast<size_t>(R.w.segment) * p.B + R.w.b) * p.D + R.w.first + quad;
+    const size_t at = segment_at(p, R.w, R.w.segment) + quad;
     store_states(p.seg_state + at * N + n4, N, h);
     store_states(p.seg_grad + at * N + n4, N, g);
     if (n4 == 0) *reinterpret_cast<float4*>(p.seg_dt + at) = make_float4(total[0].x, total[0].y, total[1].x, total[1].y);
 }
 
+// Blocks of tiles of a whole sequence, and of a segment: each has a row of the parameters' partial sums.
+struct Blocks {
+    int whole, cut;
+};
+
 template <typename E, int N>
-__global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_kernel(const __grid_constant__ SsmParams p, int blocks)
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_kernel(const __grid_constant__ SsmParams p, const Blocks count)
 {
     using S = Tile<E, N>;
     using L = Lay<N>;
@@ -282,23 +292,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
         store_vec<E>(ddt, t * p.D + c, make_uint4(0, 0, 0, 0));
         if (R.gated) store_vec<E>(dz, t * p.ld_dz + c, make_uint4(0, 0, 0, 0));
     }
-    float2 skip[V / 2];
+    float2 skip[2];
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k)
+    for (int k = 0; k < 2; ++k)
         skip[k] = mine < w.count && p.skip ? *reinterpret_cast<const float2*>(p.skip + w.first + mine + 2 * k) : both(0.f);
     const uint32_t stage0 = smem_u32(stages);
-    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + quad) * N + n4, all = static_cast<size_t>(p.B) * p.D * N;
+    const size_t mat = (static_cast<size_t>(w.b) * p.D + w.first + quad) * N + n4;
     float2 A[2][4], h[2][4], g[2][4];
     load_states(p.A + static_cast<size_t>(w.first + quad) * N + n4, N, on, A);
     load_states(p.h_in + mat, N, on && p.h_in, h);
     load_states(p.dh_out + mat, N, on && p.dh_out, g);
-    if (p.segments > 1 && w.segment <= R.last) {
+    if (w.b >= p.whole && w.segment <= R.last) {
         griddep_wait();
         auto join = [&](int j, const float* from, float2 (&v)[2][4]) {   // v = own + exp(A sum of steps) v
             float2 own[2][4], sum[2];
-            load_states(from + j * all + mat, N, on, own);
+            const size_t at = segment_at(p, w, j) + quad;
+            load_states(from + at * N + n4, N, on, own);
             sum[0] = sum[1] = both(0.f);
-            if (on) pairs(p.seg_dt + (static_cast<size_t>(j) * p.B + w.b) * p.D + w.first + quad, sum);
+            if (on) pairs(p.seg_dt + at, sum);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -311,15 +322,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
     float* const check = p.check + (static_cast<size_t>(w.b) * ((p.T + TT - 1) / TT) + R.t0 / TT) * p.D * N +
                          static_cast<size_t>(w.first + quad) * N + n4;
     const size_t check_step = static_cast<size_t>(p.D) * N;
-    if (tiles > 0) R.template load<false>(0, stage0);
-    cp_async_commit();
-    for (int tile = 0; tile < tiles; ++tile) {
-        cp_async_wait<0>();
-        __syncthreads();   // the tile has landed, and all warps are done with the one before
-        if (tile + 1 < tiles)
-            R.template load<false>(tile + 1, stage0 + ((tile + 1) & 1) * S::kStage);
+#pragma unroll
+    for (int tile = 0; tile < 3; ++tile) {   // four tiles of u, dt and B have room
+        if (tile < tiles) R.template load<false>(tile, stage0 + tile * S::kHalf);
         cp_async_commit();
-        R.template widen<false>(tile, stages + (tile & 1) * S::kStage, steps, xs, ps, Bf);
+    }
+    for (int tile = 0; tile < tiles; ++tile) {
+        cp_async_wait<2>();
+        __syncthreads();   // the tile has landed, and all warps are done with the one before
+        if (tile + 3 < tiles) R.template load<false>(tile + 3, stage0 + ((tile + 3) & 3) * S::kHalf);
+        cp_async_commit();
+        R.template widen<false>(tile, stages + (tile & 3) * S::kHalf, steps, xs, ps, Bf);
         __syncthreads();
         if (on) store_states(check + tile * check_step, N, h);
 #pragma unroll 2
@@ -336,16 +349,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
     __syncthreads();
     if (tiles > 0) R.template load<true>(tiles - 1, stage0 + ((tiles - 1) & 1) * S::kStage);
     cp_async_commit();
-    float* const params = p.part + (static_cast<size_t>(w.segment) * p.B + w.b) * blocks * p.D * (N + 2);
+    const int blocks = w.b < p.whole ? count.whole : count.cut;
+    float* const params = p.part + (w.b < p.whole ? static_cast<size_t>(w.b) * blocks : static_cast<size_t>(p.whole) * count.whole +
+                                    (static_cast<size_t>(w.segment) * (p.B - p.whole) + (w.b - p.whole)) * blocks) * p.D * (N + 2);
     const size_t param_step = static_cast<size_t>(p.D) * (N + 2);
-    float2 dA[2][4], dskip[V / 2], dbias[V / 2];
+    float2 dA[2][4], dskip[2], dbias[2];
     auto clear = [&]() {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int s = 0; s < 4; ++s) dA[k][s] = both(0.f);
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) dskip[k] = dbias[k] = both(0.f);
+        for (int k = 0; k < 2; ++k) dskip[k] = dbias[k] = both(0.f);
     };
     auto flush = [&](int block) {   // a block's sums to its row of the partials
         float* const to = params + block * param_step;
@@ -357,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
             store_states(to + static_cast<size_t>(w.first + quad) * N + n4, N, dA);
         }
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {   // lanes l, l + PER, ... have the same channels
+        for (int k = 0; k < 2; ++k) {   // lanes l, l + PER, ... have the same channels
 #pragma unroll
             for (int o = 16; o >= PER; o >>= 1) {
                 dskip[k].x += __shfl_xor_sync(0xffffffffu, dskip[k].x, o), dskip[k].y += __shfl_xor_sync(0xffffffffu, dskip[k].y, o);
@@ -373,15 +388,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
     clear();
     for (int block = blocks - 1; block >= 0 && block * kBlock >= tiles; --block) flush(block);
     float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / S::kCh) * p.B * p.T + tokens) * p.G + w.group) * 2 * N;
+    float2 start[2][4];   // the states before the tile
+    load_states(check + (tiles - 1) * check_step, N, on && tiles > 0, start);
     for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int first = R.t0 + tile * TT, count = min(TT, R.live - first);
+        const int first = R.t0 + tile * TT, rows = min(TT, R.live - first);
         const unsigned char* const raw = stages + (tile & 1) * S::kStage;
         cp_async_wait<0>();
         __syncthreads();
         if (tile > 0) R.template load<true>(tile - 1, stage0 + ((tile - 1) & 1) * S::kStage);
         cp_async_commit();
-        float2 start[2][4];
-        load_states(check + tile * check_step, N, on, start);
         R.template widen<true>(tile, raw, steps, xs, ps, Bf);
         __syncthreads();
 #pragma unroll
@@ -402,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
                 advance(a, xx, bb, start, start);
             }
         }
-#pragma unroll 1
+#pragma unroll 2
         for (int j = TT / 2 - 1; j >= 0; --j) {   // backwards, two tokens at a time
             const int r = 2 * j;
             float2 before[2][4], between[2][4], a[2][4], dd[2], xx[2], bb[4];
@@ -465,63 +480,67 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 2 : 3) ssm_grad_ker
 #pragma unroll
                 for (int s = 0; s < 4; ++s) h[k][s] = before[k][s];
         }
+        load_states(check + (tile - 1) * check_step, N, on && tile > 0, start);
         __syncthreads();
         // dB and dC of the tile: each of a token's 2 N sums runs over the CTA's channel quads
-        const float* const parts = reinterpret_cast<const float*>(smem);
-        for (int i = threadIdx.x; i < count * 2 * N; i += kThreads) {
-            const int r = i / (2 * N), c = i % (2 * N) / N, n = i % N;   // B's, then C's
-            const float* const from = parts + ((r / 2 * 4 + r % 2 * 2 + c) * kThreads + n / 4) * 4 + n % 4;
-            float sum = 0.f;
-            if (N == 16) {   // C's lanes one quad ahead: other banks
+        for (int i = threadIdx.x; i < TT * 2 * LANES; i += kThreads) {
+            const int lane4 = i % LANES, c = i / LANES % 2, r = i / (2 * LANES);   // four of B's states, then of C's
+            const float4* const from = reinterpret_cast<const float4*>(smem) + (r / 2 * 4 + r % 2 * 2 + c) * kThreads + lane4;
+            float2 lo = both(0.f), hi = both(0.f);
 #pragma unroll
-                for (int q = 0; q < kThreads / LANES; ++q) sum += from[(q ^ c) * LANES * 4];
-            } else {
-#pragma unroll
-                for (int q = 0; q < kThreads / LANES; ++q) sum += from[q * LANES * 4];
+            for (int q = 0; q < kThreads / LANES; ++q) {
+                const float4 v = from[(N == 16 ? q ^ c : q) * LANES];   // of 16 states: C's lanes one quad aside, in other banks
+                lo = add2(lo, make_float2(v.x, v.y)), hi = add2(hi, make_float2(v.z, v.w));
             }
-            bc_part[static_cast<size_t>(first + r) * p.G * 2 * N + i % (2 * N)] = c ? sum : sum * kLn2;
+            if (c == 0) lo = mul2(lo, both(kLn2)), hi = mul2(hi, both(kLn2));
+            if (r < rows)
+                *reinterpret_cast<float4*>(bc_part + static_cast<size_t>(first + r) * p.G * 2 * N + c * N + lane4 * 4) = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
 #pragma unroll
         for (int i = 0; i < PIECES; i += 32) {
             const int piece = i + lane, r = piece / PER;
-            if (piece < PIECES && r < count && mine < w.count) {
-                float uu[V], vv[V], yy[V], zz[V], o1[V], o2[V], o3[V];
-                const uint4* const at = reinterpret_cast<const uint4*>(raw + r * S::kRow + mine * sizeof(E));
-                unpack(at[kU * TT * S::kRow / 16], uu, E{});
-                unpack(at[kDt * TT * S::kRow / 16], vv, E{});
-                unpack(at[kDy * TT * S::kRow / 16], yy, E{});
-                if (R.gated) unpack(at[kZ * TT * S::kRow / 16], zz, E{});
+            if (piece < PIECES && r < rows && mine < w.count) {
+                float uu[4], vv[4], yy[4], zz[4], o1[4], o2[4], o3[4];
+                const unsigned char* const at = raw + r * S::kRow + mine * static_cast<int>(sizeof(E));
+                R.get(at, kU, uu);
+                R.get(at, kDt, vv);
+                R.get(at, kDy, yy);
+                if (R.gated) R.get(at, kZ, zz);
                 const size_t t = first + r;
                 const int here = r * S::kPitch + mine;
+                float2 step[2], e[2], qa[2], o[2];   // e: times log 2, as B
+                pairs(steps + here, step);
+                pairs(xs + here, e);
+                pairs(ps + here, qa);
+                pairs(ys + here, o);
 #pragma unroll
-                for (int k = 0; k < V; k += 2) {
-                    auto two = [&](const float* from) { return *reinterpret_cast<const float2*>(from + here + k); };
-                    const float2 u = make_float2(uu[k], uu[k + 1]), dy = make_float2(yy[k], yy[k + 1]);
-                    const float2 e = two(xs);   // times log 2, as B
+                for (int k = 0; k < 2; ++k) {
+                    const float2 u = make_float2(uu[2 * k], uu[2 * k + 1]), dy = make_float2(yy[2 * k], yy[2 * k + 1]);
                     float2 pk = dy;
                     if (R.gated) {
-                        const float2 z = make_float2(zz[k], zz[k + 1]), f = add2(ex2_2(mul2(z, both(-kLog2e))), both(1.f));
+                        const float2 z = make_float2(zz[2 * k], zz[2 * k + 1]), f = add2(ex2_2(mul2(z, both(-kLog2e))), both(1.f));
                         const float2 sg = make_float2(rcp_approx(f.x), rcp_approx(f.y)), gate = mul2(z, sg);
                         pk = mul2(dy, gate);
                         // silu'(z) = sg + z sg (1 - sg)
                         const float2 slope = fma2(gate, fma2(sg, both(-1.f), both(1.f)), sg);
-                        const float2 v = mul2(mul2(dy, fma2(skip[k / 2], u, two(ys))), slope);
-                        o3[k] = v.x, o3[k + 1] = v.y;
+                        const float2 v = mul2(mul2(dy, fma2(skip[k], u, o[k])), slope);
+                        o3[2 * k] = v.x, o3[2 * k + 1] = v.y;
                     }
-                    dskip[k / 2] = fma2(pk, u, dskip[k / 2]);
-                    const float2 v = fma2(e, two(steps), mul2(skip[k / 2], pk));
-                    o1[k] = v.x, o1[k + 1] = v.y;
-                    float2 ds = fma2(mul2(e, both(kLog2e)), u, two(ps));
-                    if (R.softplus) {
-                        const float2 f = add2(ex2_2(mul2(fma2(make_float2(vv[k], vv[k + 1]), both(kLog2e), R.bias[k / 2]), both(-1.f))), both(1.f));
+                    dskip[k] = fma2(pk, u, dskip[k]);
+                    const float2 v = fma2(e[k], step[k], mul2(skip[k], pk));
+                    o1[2 * k] = v.x, o1[2 * k + 1] = v.y;
+                    float2 ds = fma2(mul2(e[k], both(kLog2e)), u, qa[k]);
+                    if (R.softplus) {   // sigmoid(dt + dt_bias)
+                        const float2 a = fma2(make_float2(vv[2 * k], vv[2 * k + 1]), both(kLog2e), R.bias[k]);
+                        const float2 f = add2(make_float2(ex2(-a.x), ex2(-a.y)), both(1.f));
                         ds = mul2(ds, make_float2(rcp_approx(f.x), rcp_approx(f.y)));
                     }
-                    dbias[k / 2] = add2(dbias[k / 2], ds);
-                    o2[k] = ds.x, o2[k + 1] = ds.y;
+                    dbias[k] = add2(dbias[k], ds);
+                    o2[2 * k] = ds.x, o2[2 * k + 1] = ds.y;
                 }
-                store_vec<E>(du, t * p.D + mine, pack(o1, E{}));
-                store_vec<E>(ddt, t * p.D + mine, pack(o2, E{}));
-                if (R.gated) store_vec<E>(dz, t * p.ld_dz + mine, pack(o3, E{}));
+                store_quad<E>(du, t * p.D + mine, pack_quad(o1, E{}));
+                store_quad<E>(ddt, t * p.D + mine, pack_quad(o2, E{}));
+                if (R.gated) store_quad<E>(dz, t * p.ld_dz + mine, pack_quad(o3, E{}));
             }
         }
         if (tile % kBlock == 0) flush(tile / kBlock);
@@ -552,22 +571,24 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const __grid_constant__ Ssm
 }
 
 struct Plan {
-    int segments, seg_len, chan_tiles, blocks;   // blocks: of a segment, with partial sums of their own
-    long long ctas;   // of one segment
+    Split split;
+    Blocks blocks;
+    int chan_tiles;
+    long long ctas, rows;   // CTAs of a sequence (or of a segment); rows of the parameters' partial sums
 };
 
-Plan plan_of(int B, int T, int D, int N, int G)
+// Six CTAs on an SM (four in fp32, by shared memory).
+Plan plan_of(size_t e, int B, int T, int D, int N, int G)
 {
     const int ch = kWarps * 128 / (N / 4), dg = D / G;
-    Plan plan{1, std::max(1, T), (dg + ch - 1) / ch, (std::max(1, T) + kBlock * TT - 1) / (kBlock * TT), 0};
-    plan.ctas = static_cast<long long>(B) * G * plan.chan_tiles;
-    const int most = std::max(1, T / (8 * TT));
-    const int segments = plan.ctas >= 2 * kSms ? 1 : static_cast<int>(std::min<long long>(most, std::min<long long>(64, (2 * kSms + plan.ctas - 1) / plan.ctas)));
-    if (segments <= 1) return plan;
-    const int tiles = (T + TT - 1) / TT, per = (tiles + segments - 1) / segments;
-    plan.segments = (tiles + per - 1) / per;
-    plan.seg_len = per * TT;
-    plan.blocks = (per + kBlock - 1) / kBlock;
+    Plan plan{};
+    plan.chan_tiles = (dg + ch - 1) / ch;
+    plan.ctas = static_cast<long long>(G) * plan.chan_tiles;
+    plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 0.28, TT, 8 * TT);
+    auto blocks = [](int tokens) { return (std::max(1, tokens) + kBlock * TT - 1) / (kBlock * TT); };
+    plan.blocks = {blocks(T), blocks(plan.split.seg_len)};
+    plan.rows = static_cast<long long>(plan.split.whole) * plan.blocks.whole +
+                static_cast<long long>(B - plan.split.whole) * plan.split.segments * plan.blocks.cut;
     return plan;
 }
 
@@ -586,13 +607,13 @@ Regions regions_of(const Plan& plan, int B, int T, int D, int N, int G)
         return here;
     };
     Regions r{};
-    const size_t seg = plan.segments > 1 ? plan.segments : 0;
-    r.seg_state = take(seg * streams * N);
-    r.seg_grad = take(seg * streams * N);
-    r.seg_dt = take(seg * streams);
+    const size_t cut = static_cast<size_t>(plan.split.segments) * (B - plan.split.whole) * D;
+    r.seg_state = take(cut * N);
+    r.seg_grad = take(cut * N);
+    r.seg_dt = take(cut);
     r.check = take(static_cast<size_t>((T + TT - 1) / TT) * streams * N);
     r.bc_part = take(static_cast<size_t>(plan.chan_tiles) * B * T * G * 2 * N);
-    r.part = take(static_cast<size_t>(plan.segments) * plan.blocks * B * D * (N + 2));
+    r.part = take(static_cast<size_t>(plan.rows) * D * (N + 2));
     r.bytes = std::max<size_t>(256, at * 4);
     return r;
 }
@@ -606,21 +627,22 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         cudaGetLastError();
         return SRWM_ERR_CUDA;
     }
-    const unsigned grid = static_cast<unsigned>(plan.ctas * plan.segments);
+    const unsigned whole = static_cast<unsigned>(plan.ctas * p.whole), cut = static_cast<unsigned>(plan.ctas * (p.B - p.whole) * p.segments);
     int rc = SRWM_OK;
-    if (plan.segments > 1) {
-        ssm_local_kernel<E, N><<<grid, kThreads, S::kSmemLocal, st>>>(p);
+    if (cut > 0) {
+        SsmParams q = p;
+        q.first = static_cast<int>(whole);
+        ssm_local_kernel<E, N><<<cut, kThreads, S::kSmemLocal, st>>>(q);
         rc = launched();
         if (rc != SRWM_OK) return rc;
     }
-    ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(p, plan.blocks);
+    ssm_grad_kernel<E, N><<<whole + cut, kThreads, S::kSmem, st>>>(p, plan.blocks);
     rc = launched();
     if (rc != SRWM_OK) return rc;
     const long long quads = static_cast<long long>(p.B) * p.T * (2 * p.G * N / 4);
     if (quads > 0) rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, p, plan.chan_tiles);
     if (rc != SRWM_OK) return rc;
-    const long long rows = static_cast<long long>(plan.segments) * p.B * plan.blocks;
-    return sum_launch({p.part, rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}}, st);
+    return sum_launch({p.part, plan.rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}}, st);
 }
 
 template <typename E>
@@ -631,14 +653,17 @@ int by_states(const SsmParams& p, const Plan& plan, cudaStream_t st)
 
 }  // namespace
 
-size_t ssm_backward_scratch(int B, int T, int D, int N, int G) { return regions_of(plan_of(B, T, D, N, G), B, T, D, N, G).bytes; }
+size_t ssm_backward_scratch(int B, int T, int D, int N, int G)
+{
+    return std::max(regions_of(plan_of(4, B, T, D, N, G), B, T, D, N, G).bytes, regions_of(plan_of(2, B, T, D, N, G), B, T, D, N, G).bytes);
+}
 
 int ssm_backward_launch(int dtype, SsmParams& p, void* workspace, cudaStream_t st)
 {
-    const Plan plan = plan_of(p.B, p.T, p.D, p.N, p.G);
+    const Plan plan = plan_of(dtype_bytes(dtype), p.B, p.T, p.D, p.N, p.G);
     const Regions r = regions_of(plan, p.B, p.T, p.D, p.N, p.G);
     float* const base = static_cast<float*>(workspace);
-    p.segments = plan.segments, p.seg_len = plan.seg_len;
+    p.whole = plan.split.whole, p.segments = plan.split.segments, p.seg_len = plan.split.seg_len;
     p.seg_state = base + r.seg_state, p.seg_grad = base + r.seg_grad, p.seg_dt = base + r.seg_dt;
     p.check = base + r.check, p.bc_part = base + r.bc_part, p.part = base + r.part;
     if (dtype == SRWM_F32) return by_states<float>(p, plan, st);

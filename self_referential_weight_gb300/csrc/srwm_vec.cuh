@@ -63,6 +63,32 @@ __device__ __forceinline__ void store_vec(void* p, size_t element, const uint4& 
     *reinterpret_cast<uint4*>(static_cast<E*>(p) + element) = v;
 }
 
+// Four neighbouring elements: half a vector of the 16-bit types.
+template <typename E> struct Quad { using type = uint2; };
+template <> struct Quad<float> { using type = uint4; };
+
+template <typename E>
+__device__ __forceinline__ typename Quad<E>::type load_quad(const void* p, size_t element)
+{
+    return __ldg(reinterpret_cast<const typename Quad<E>::type*>(static_cast<const E*>(p) + element));
+}
+__device__ __forceinline__ void unpack_quad(const uint4& u, float (&f)[4], float) { unpack(u, f, 0.f); }
+template <typename E>
+__device__ __forceinline__ void unpack_quad(const uint2& u, float (&f)[4], E)
+{
+    float e[8];
+    unpack(make_uint4(u.x, u.y, 0u, 0u), e, E{});
+    f[0] = e[0], f[1] = e[1], f[2] = e[2], f[3] = e[3];
+}
+__device__ __forceinline__ uint4 pack_quad(const float (&f)[4], float) { return pack(f, 0.f); }
+template <typename E>
+__device__ __forceinline__ uint2 pack_quad(const float (&f)[4], E) { return make_uint2(pack2(f[0], f[1], E{}), pack2(f[2], f[3], E{})); }
+template <typename E>
+__device__ __forceinline__ void store_quad(void* p, size_t element, const typename Quad<E>::type& v)
+{
+    *reinterpret_cast<typename Quad<E>::type*>(static_cast<E*>(p) + element) = v;
+}
+
 // sigmoid(z), good to about (|z| + 3) 2^-23 of itself for z < 0, where the rounding of exp's argument grows with it,
 // and to 3 * 2^-23 above: exp underflows to 0 and overflows to infinity, whose reciprocal is 0.
 __device__ __forceinline__ float sigmoid(float z)
