@@ -6,9 +6,10 @@
 //   dw_j = sum g_t x_{t-W+1+j},   dbias = sum g_t
 // Memory bounds it: x (and dy) is to be read once and y (dx) written once.  A
 // thread takes one vector of channels over a run of tokens, with the last W - 1
-// inputs, the weights and the gradients' partial sums in registers, and several
-// tokens' loads in flight; a run begins by reading the W - 1 rows in front of it
-// again, from L2.  Inputs before the first token, and the state that goes out,
+// inputs, the weights and the gradients' partial sums in registers.  Its rows
+// come by asynchronous copies into a ring of its own in shared memory, so what is
+// in flight takes no registers and no barrier; a run begins by reading the W - 1
+// rows in front of it again, from L2.  Inputs before the first token, and the state that goes out,
 // are rows of the state: row i of it stands W - 1 - i tokens before token 0, or
 // before the sequence's end.
 #include <cuda_runtime.h>
@@ -24,11 +25,12 @@
 namespace srwm {
 namespace {
 
+constexpr int kSms = 152;
 constexpr int kThreads = 128;
-constexpr int kRun = 32;          // tokens of a thread's run
-constexpr int kAhead = 8;         // of which are loaded at once
-constexpr int kGradThreads = 256;
-constexpr int kGradParts = 608;   // partial sums of a channel's parameters: four CTAs on each SM
+constexpr int kGroup = 4;         // tokens whose copies are waited for together
+constexpr int kGroups = 4;        // groups of a thread's ring, all but one of them in flight
+constexpr int kGradGroups = 3;
+constexpr int kGradParts = 608;   // CTAs that take turns on the gradients' runs: four on each SM
 
 template <int ACT>
 __device__ __forceinline__ float conv_act(float v) { return ACT == SRWM_ACT_SILU ? v * sigmoid(v) : v; }
@@ -41,6 +43,14 @@ __device__ __forceinline__ float conv_slope(float v)
         return e * fmaf(v, 1.f - e, 1.f);
     }
     return 1.f;
+}
+
+// Tokens of a thread's run: as long as keeps the SMs full, since each begins with an empty ring and rows read again.
+int run_of(int B, int T, int vecs)
+{
+    int run = 32;
+    while (run < 256 && static_cast<long long>(B) * vecs * ((T + 2 * run - 1) / (2 * run)) >= kSms * 512) run *= 2;
+    return run;
 }
 
 __device__ __forceinline__ int valid_tokens(const int* lengths, int b, int T)
@@ -73,10 +83,21 @@ __device__ __forceinline__ void load_bias(const ConvParams& p, int c, float (&bi
     }
 }
 
+// The window moves on by one token: with several tokens unrolled these are other registers' names.
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&win)[W][V])
+{
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) win[j][k] = win[j + 1][k];
+}
+
 template <typename E, int W, int ACT>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int runs)
+__global__ void __launch_bounds__(kThreads, 5) conv_kernel(const ConvParams p, int run_len, int runs)
 {
     constexpr int V = vec<E>;
+    extern __shared__ __align__(16) uint4 ring[];   // [groups][tokens][threads]: a thread's own rows on their way
     const int nv = p.D / V;
     const long long item = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
     const int c = static_cast<int>(item % nv) * V;
@@ -85,58 +106,65 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
     if (br / runs >= p.B) return;
     const int b = static_cast<int>(br / runs);
     const int n = valid_tokens(p.lengths, b, p.T);
-    const int t0 = run * kRun, t1 = min(p.T, t0 + kRun), live = min(t1, n);
+    const int t0 = run * run_len, t1 = min(p.T, t0 + run_len), live = min(t1, n);
     const E* const x = static_cast<const E*>(p.x) + static_cast<size_t>(b) * p.T * p.ld + c;
     const size_t states = static_cast<size_t>(b) * (W - 1) * p.D + c;
     E* const y = static_cast<E*>(p.y) + static_cast<size_t>(b) * p.T * p.D + c;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const bool last = run == (n > 0 ? (n - 1) / kRun : 0);
-    int t = t0;
-    if (t0 < live || last) {
+    // row i of the state or, past it, of the tokens
+    auto row = [&](int i) {
+        return i >= W - 1 ? load_vec<E>(x, static_cast<size_t>(i - (W - 1)) * p.ld)
+               : p.state_in ? load_vec<E>(p.state_in, states + static_cast<size_t>(i) * p.D) : zero;
+    };
+    auto copy = [&](int group) {
+#pragma unroll
+        for (int a = 0; a < kGroup; ++a) {
+            const int t = t0 + group * kGroup + a;
+            if (t < live) cp_async16(smem_u32(ring + (group % kGroups * kGroup + a) * kThreads + threadIdx.x), x + static_cast<long long>(t) * p.ld, true);
+        }
+        cp_async_commit();
+    };
+    if (t0 < live) {
+#pragma unroll
+        for (int g = 0; g < kGroups - 1; ++g) copy(g);
         float w[W][V], bias[V], win[W][V];
+        uint4 raw[W - 1];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) raw[i] = row(t0 + i);
         load_weights<W, V>(p, c, w);
         load_bias<V>(p, c, bias);
-        uint4 old[W - 1];   // rows as they came: the state that goes out is not rounded again
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-            const int from = t0 - (W - 1) + i;
-            old[i] = from >= 0 ? load_vec<E>(x, static_cast<size_t>(from) * p.ld)
-                     : p.state_in ? load_vec<E>(p.state_in, states + static_cast<size_t>(t0 + i) * p.D) : zero;
-            unpack(old[i], win[i], E{});
-        }
-        while (t < live) {
-            uint4 raw[kAhead];
+        for (int i = 0; i < W - 1; ++i) unpack(raw[i], win[i], E{});
+        auto token = [&](int t, const uint4& v) {
+            unpack(v, win[W - 1], E{});
+            float out[V];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (t + a < live) raw[a] = load_vec<E>(x, static_cast<size_t>(t + a) * p.ld);
+            for (int k = 0; k < V; ++k) {
+                out[k] = bias[k];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (t + a >= live) break;
-                unpack(raw[a], win[W - 1], E{});
-                float out[V];
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float v = bias[k];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v = fmaf(w[j][k], win[j][k], v);
-                    out[k] = conv_act<ACT>(v);
-                }
-                store_vec<E>(y, static_cast<size_t>(t + a) * p.D, pack(out, E{}));
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    old[j] = j < W - 2 ? old[j + 1] : raw[a];
-#pragma unroll
-                    for (int k = 0; k < V; ++k) win[j][k] = win[j + 1][k];
-                }
+                for (int j = 0; j < W; ++j) out[k] = fmaf(w[j][k], win[j][k], out[k]);
+                out[k] = conv_act<ACT>(out[k]);
             }
-            t = min(t + kAhead, live);
-        }
-        if (last && p.state_out) {
+            store_vec<E>(y, static_cast<size_t>(t) * p.D, pack(out, E{}));
+            shift(win);
+        };
+        for (int g = 0, t = t0; t < live; ++g, t += kGroup) {
+            copy(g + kGroups - 1);
+            cp_async_wait<kGroups - 1>();
+            const uint4* const at = ring + g % kGroups * kGroup * kThreads + threadIdx.x;
+            if (t + kGroup <= live) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) store_vec<E>(p.state_out, states + static_cast<size_t>(i) * p.D, old[i]);
+                for (int a = 0; a < kGroup; ++a) token(t + a, at[a * kThreads]);
+            } else {
+#pragma unroll 1
+                for (int a = 0; t + a < live; ++a) token(t + a, at[a * kThreads]);
+            }
         }
     }
-    for (t = max(t0, live); t < t1; ++t) store_vec<E>(y, static_cast<size_t>(t) * p.D, zero);
+    for (int t = max(t0, live); t < t1; ++t) store_vec<E>(y, static_cast<size_t>(t) * p.D, zero);
+    if (p.state_out && run == (n > 0 ? (n - 1) / run_len : 0))   // the sequence ends here: its last rows, as they came
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) store_vec<E>(p.state_out, states + static_cast<size_t>(i) * p.D, row(n + i));
 }
 
 template <typename E, int W, int ACT>
@@ -173,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p)
 
 // How the threads of conv_grad_kernel share the channels: groups of up to 32 vectors of four channels, a run per slot.
 struct GradPlan {
-    int groups, vecs, slots, parts, runs;
+    int groups, vecs, slots, parts, run_len, runs;
 };
 
 GradPlan grad_plan(int B, int T, int D)
@@ -182,8 +210,9 @@ GradPlan grad_plan(int B, int T, int D)
     const int nv = D / 4;
     g.vecs = std::min(nv, 32);
     g.groups = (nv + 31) / 32;
-    g.slots = kGradThreads / g.vecs;
-    g.runs = std::max(1, (T + kRun - 1) / kRun);
+    g.slots = kThreads / g.vecs;
+    g.run_len = run_of(B, T, nv);
+    g.runs = std::max(1, (T + g.run_len - 1) / g.run_len);
     const long long items = static_cast<long long>(B) * g.runs;
     g.parts = static_cast<int>(std::max(1LL, std::min<long long>((items + g.slots - 1) / g.slots, std::max(1, kGradParts / g.groups))));
     return g;
@@ -192,11 +221,13 @@ GradPlan grad_plan(int B, int T, int D)
 // dx (and dL/dstate_in) of every token, and a CTA's part of the parameters' gradients: part [parts, D W + D].
 // At time t the inputs of rows t .. t + W - 1 (row i is token i - W + 1) get w_j g_t; row t is complete then.
 template <typename E, int W, int ACT>
-__global__ void __launch_bounds__(kGradThreads) conv_grad_kernel(const ConvParams p, const GradPlan g)
+__global__ void __launch_bounds__(kThreads, 4) conv_grad_kernel(const ConvParams p, const GradPlan g)
 {
-    constexpr int V = 4, U = 4;
+    constexpr int V = 4;
     using Q = typename Quad<E>::type;
-    __shared__ float sums[kGradThreads][V];
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    Q* const ring = reinterpret_cast<Q*>(ring_bytes) + threadIdx.x;   // [groups][tokens][x | dy][threads]: a thread's own rows
+    float (*const sums)[V] = reinterpret_cast<float (*)[V]>(ring_bytes);   // at the end, when no copy is on its way
     const int group = blockIdx.x % g.groups, part = blockIdx.x / g.groups;
     const int lane = threadIdx.x % g.vecs, slot = threadIdx.x / g.vecs;
     const int c = (group * 32 + lane) * V;
@@ -216,17 +247,34 @@ __global__ void __launch_bounds__(kGradThreads) conv_grad_kernel(const ConvParam
     for (long long item = static_cast<long long>(part) * g.slots + slot; item < items; item += static_cast<long long>(g.parts) * g.slots) {
         const int b = static_cast<int>(item / g.runs), run = static_cast<int>(item % g.runs);
         const int n = valid_tokens(p.lengths, b, p.T);
-        const int t0 = run * kRun, t1 = min(p.T, t0 + kRun);
+        const int t0 = run * g.run_len, t1 = min(p.T, t0 + g.run_len);
         const E* const x = static_cast<const E*>(p.x) + static_cast<size_t>(b) * p.T * p.ld + c;
         const E* const dy = static_cast<const E*>(p.dy) + static_cast<size_t>(b) * p.T * p.D + c;
         E* const dx = static_cast<E*>(p.dx) + static_cast<size_t>(b) * p.T * p.ld_grad + c;
         const size_t states = static_cast<size_t>(b) * (W - 1) * p.D + c;
-        float win[W][V], acc[W][V];   // inputs of rows t .. t + W - 1; their gradients so far
+        const float none[V] = {};
+        int t = t0;
+        if (t0 < n || run == 0) {
+            const int inner = min(t1, n), reach = min(t1 + W - 1, n);   // own tokens, and those that reach back to them
+            auto copy = [&](int group) {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
+                for (int a = 0; a < kGroup; ++a) {
+                    const int i = t0 + group * kGroup + a;
+                    if (i < reach) {
+                        Q* const to = ring + (group % kGradGroups * kGroup + a) * 2 * kThreads;
+                        cp_async_own<sizeof(Q)>(smem_u32(to), x + static_cast<long long>(i) * p.ld);
+                        cp_async_own<sizeof(Q)>(smem_u32(to + kThreads), dy + static_cast<long long>(i) * p.D);
+                    }
+                }
+                cp_async_commit();
+            };
 #pragma unroll
-            for (int k = 0; k < V; ++k) win[i][k] = acc[i][k] = 0.f;
-        if (t0 < n)
+            for (int q = 0; q < kGradGroups - 1; ++q) copy(q);
+            float win[W][V], acc[W][V];   // inputs of rows t .. t + W - 1; their gradients so far
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) win[i][k] = acc[i][k] = 0.f;
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
                 const int from = t0 - (W - 1) + i;
@@ -235,63 +283,69 @@ __global__ void __launch_bounds__(kGradThreads) conv_grad_kernel(const ConvParam
                 else if (p.state_in)
                     unpack_quad(load_quad<E>(p.state_in, states + static_cast<size_t>(t0 + i) * p.D), win[i], E{});
             }
-        const int end = t1 + W - 1;
-        for (int t = t0; t < end; t += U) {
-            Q rx[U], rd[U];
+            // the gradient of a valid token's sum reaches its inputs and, for the run's own tokens, the parameters
+            auto token = [&](const Q& rx, const Q& rd, bool mine) {
+                float d[V];
+                unpack_quad(rx, win[W - 1], E{});
+                unpack_quad(rd, d, E{});
 #pragma unroll
-            for (int a = 0; a < U; ++a)
-                if (t + a < end && t + a < n) {
-                    rx[a] = load_quad<E>(x, static_cast<size_t>(t + a) * p.ld);
-                    rd[a] = load_quad<E>(dy, static_cast<size_t>(t + a) * p.D);
-                }
+                for (int k = 0; k < V; ++k) {
+                    float v = bias[k];
 #pragma unroll
-            for (int a = 0; a < U; ++a) {
-                const int now = t + a;
-                if (now >= end) break;
-                if (now < n) {
-                    float d[V];
-                    unpack_quad(rx[a], win[W - 1], E{});
-                    unpack_quad(rd[a], d, E{});
-                    const bool mine = now < t1;
+                    for (int j = 0; j < W; ++j) v = fmaf(w[j][k], win[j][k], v);
+                    const float gr = d[k] * conv_slope<ACT>(v);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        float v = bias[k];
+                    for (int j = 0; j < W; ++j) acc[j][k] = j < W - 1 ? fmaf(w[j][k], gr, acc[j][k]) : w[j][k] * gr;
+                    if (mine) {
+                        db[k] += gr;
 #pragma unroll
-                        for (int j = 0; j < W; ++j) v = fmaf(w[j][k], win[j][k], v);
-                        const float gr = d[k] * conv_slope<ACT>(v);
-#pragma unroll
-                        for (int j = 0; j < W; ++j) acc[j][k] = fmaf(w[j][k], gr, acc[j][k]);
-                        if (mine) {
-                            db[k] += gr;
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][k] = fmaf(gr, win[j][k], dw[j][k]);
-                        }
+                        for (int j = 0; j < W; ++j) dw[j][k] = fmaf(gr, win[j][k], dw[j][k]);
                     }
                 }
-                const int token = now - (W - 1);
-                if (now >= n && token < n && p.dstate) {   // row `now` is row now - n of the state that went out
+            };
+            // row `now` is complete: a token's dx, or a row of the state that came in
+            auto emit = [&](int now) {
+                const int at = now - (W - 1);
+                if (at >= t0)
+                    store_quad<E>(dx, static_cast<size_t>(at) * p.ld_grad, pack_quad(acc[0], E{}));
+                else if (at < 0 && p.state_out)
+                    store_quad<E>(p.state_out, states + static_cast<size_t>(now) * p.D, pack_quad(acc[0], E{}));
+                shift(acc);
+                shift(win);
+            };
+            for (int q = 0; t < reach; ++q, t += kGroup) {
+                copy(q + kGradGroups - 1);
+                cp_async_wait<kGradGroups - 1>();
+                const Q* const at = ring + q % kGradGroups * kGroup * 2 * kThreads;
+                if (t + kGroup <= inner) {
+#pragma unroll
+                    for (int a = 0; a < kGroup; ++a) {
+                        token(at[a * 2 * kThreads], at[(a * 2 + 1) * kThreads], true);
+                        emit(t + a);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int a = 0; a < kGroup && t + a < reach; ++a) {
+                        token(at[a * 2 * kThreads], at[(a * 2 + 1) * kThreads], t + a < t1);
+                        emit(t + a);
+                    }
+                }
+            }
+            // the rows behind the sequence's end belong to the state that went out
+            for (t = reach; t < inner + W - 1; ++t) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[W - 1][k] = 0.f;
+                if (p.dstate) {
                     float d[V];
-                    unpack_quad(load_quad<E>(p.dstate, states + static_cast<size_t>(now - n) * p.D), d, E{});
+                    unpack_quad(load_quad<E>(p.dstate, states + static_cast<size_t>(t - n) * p.D), d, E{});
 #pragma unroll
                     for (int k = 0; k < V; ++k) acc[0][k] += d[k];
                 }
-                if (token >= t0) {
-                    if (token >= n)
-#pragma unroll
-                        for (int k = 0; k < V; ++k) acc[0][k] = 0.f;
-                    store_quad<E>(dx, static_cast<size_t>(token) * p.ld_grad, pack_quad(acc[0], E{}));
-                } else if (token < 0 && run == 0 && p.state_out) {
-                    store_quad<E>(p.state_out, states + static_cast<size_t>(now) * p.D, pack_quad(acc[0], E{}));
-                }
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        acc[j][k] = j < W - 1 ? acc[j + 1][k] : 0.f;
-                        if (j < W - 1) win[j][k] = win[j + 1][k];
-                    }
+                emit(t);
             }
+            t = inner;   // dx is written up to here
         }
+        for (t = max(t, t0); t < t1; ++t) store_quad<E>(dx, static_cast<size_t>(t) * p.ld_grad, pack_quad(none, E{}));
     }
     griddep_launch();
     if (!p.part) return;
@@ -302,7 +356,7 @@ __global__ void __launch_bounds__(kGradThreads) conv_grad_kernel(const ConvParam
 #pragma unroll
         for (int k = 0; k < V; ++k) sums[threadIdx.x][k] = j < W ? dw[j < W ? j : 0][k] : db[k];
         __syncthreads();
-        for (int i = threadIdx.x; i < g.vecs * V; i += kGradThreads) {
+        for (int i = threadIdx.x; i < g.vecs * V; i += kThreads) {
             const int at = group * 32 * V + i;
             if (at >= p.D) continue;
             float a = 0.f;
@@ -315,9 +369,10 @@ __global__ void __launch_bounds__(kGradThreads) conv_grad_kernel(const ConvParam
 template <typename E, int W, int ACT>
 int forward(const ConvParams& p, cudaStream_t st)
 {
-    const int runs = std::max(1, (p.T + kRun - 1) / kRun);
+    const int run = run_of(p.B, p.T, p.D / vec<E>), runs = std::max(1, (p.T + run - 1) / run);
     const long long items = static_cast<long long>(p.D / vec<E>) * runs * p.B;
-    conv_kernel<E, W, ACT><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(p, runs);
+    constexpr int smem = kGroups * kGroup * kThreads * 16;
+    conv_kernel<E, W, ACT><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, smem, st>>>(p, run, runs);
     return launched();
 }
 
@@ -336,7 +391,8 @@ int backward(const ConvParams& p0, cudaStream_t st)
     const GradPlan g = grad_plan(p.B, p.T, p.D);
     const bool params = p.dweight || p.dbias;
     if (!params) p.part = nullptr;
-    conv_grad_kernel<E, W, ACT><<<static_cast<unsigned>(g.groups) * g.parts, kGradThreads, 0, st>>>(p, g);
+    constexpr int smem = kGradGroups * kGroup * 2 * kThreads * static_cast<int>(sizeof(typename Quad<E>::type));
+    conv_grad_kernel<E, W, ACT><<<static_cast<unsigned>(g.groups) * g.parts, kThreads, smem, st>>>(p, g);
     const int rc = launched();
     if (rc != SRWM_OK || !params) return rc;
     return sum_launch({p.part, g.parts, {p.dweight, p.dbias, nullptr}, {static_cast<long long>(p.D) * W, p.D, 0}}, st);
