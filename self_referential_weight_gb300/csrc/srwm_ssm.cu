@@ -313,42 +313,61 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
     cp_async_wait<0>();
 }
 
-// One token: a thread holds four states of one channel, so its N / 4 lanes sum y.
-template <typename E, int N>
+// Four neighbouring values of B or C.
+template <typename E>
+__device__ __forceinline__ void quad_at(const void* p, size_t element, float (&f)[4])
+{
+    unpack_quad(load_quad<E>(p, element), f, E{});
+}
+
+// One token: a thread holds four states of one channel for ROWS sequences, all of whose loads are on their way at once; the
+// channel's N / 4 lanes sum y.
+template <typename E, int N, int ROWS>
 __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constant__ SsmParams p)
 {
     constexpr int LANES = N / 4;
+    const int items = p.D * LANES, sets = (p.B + ROWS - 1) / ROWS;
     const long long item = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    const int c = static_cast<int>(item / LANES % p.D), n4 = static_cast<int>(item % LANES) * 4;
-    const long long row = item / LANES / p.D;
-    const bool on = row < p.B;
-    const long long b = on ? row : 0;
+    const int at = static_cast<int>(item % items), c = at / LANES, n4 = at % LANES * 4;
+    const long long set = item / items;
+    if (__all_sync(0xffffffffu, set >= sets)) return;
     const int group = c / (p.D / p.G);
-    const size_t mat = (static_cast<size_t>(b) * p.D + c) * N + n4;
-    const float4 h = *reinterpret_cast<const float4*>(p.h_in + mat);
     const float4 A = __ldg(reinterpret_cast<const float4*>(p.A + static_cast<size_t>(c) * N + n4));
-    const E* const Bt = static_cast<const E*>(p.Bt) + b * p.ld_bc + group * N + n4;
-    const E* const Ct = static_cast<const E*>(p.Ct) + b * p.ld_bc + group * N + n4;
-    const float u = to_f(static_cast<const E*>(p.u)[b * p.ld_u + c]);
-    const float v = fmaf(to_f(static_cast<const E*>(p.dt)[b * p.ld_dt + c]), kLog2e, p.dt_bias ? __ldg(p.dt_bias + c) * kLog2e : 0.f);
-    const float d = p.softplus ? softplus2(both(v)).x : v, x = d * kLn2 * u;
-    float4 g;
-    g.x = fmaf(ex2(d * A.x), h.x, x * to_f(Bt[0]));
-    g.y = fmaf(ex2(d * A.y), h.y, x * to_f(Bt[1]));
-    g.z = fmaf(ex2(d * A.z), h.z, x * to_f(Bt[2]));
-    g.w = fmaf(ex2(d * A.w), h.w, x * to_f(Bt[3]));
-    float o = fmaf(to_f(Ct[0]), g.x, to_f(Ct[1]) * g.y) + fmaf(to_f(Ct[2]), g.z, to_f(Ct[3]) * g.w);
+    float4 h[ROWS];
+    float B[ROWS][4], C[ROWS][4], u[ROWS], v[ROWS], z[ROWS];
+    bool on[ROWS];
 #pragma unroll
-    for (int k = LANES / 2; k > 0; k >>= 1) o += __shfl_xor_sync(0xffffffffu, o, k);
-    if (!on) return;
-    *reinterpret_cast<float4*>(p.h_out + mat) = g;
-    if (n4 != 0) return;
-    if (p.skip) o = fmaf(__ldg(p.skip + c), u, o);
-    if (p.z) {
-        const float z = to_f(static_cast<const E*>(p.z)[b * p.ld_z + c]);
-        o *= z * sigmoid(z);
+    for (int i = 0; i < ROWS; ++i) {
+        const long long row = set + static_cast<long long>(i) * sets, b = row < p.B ? row : 0;
+        on[i] = set < sets && row < p.B;
+        h[i] = *reinterpret_cast<const float4*>(p.h_in + (static_cast<size_t>(b) * p.D + c) * N + n4);
+        quad_at<E>(p.Bt, static_cast<size_t>(b) * p.ld_bc + group * N + n4, B[i]);
+        quad_at<E>(p.Ct, static_cast<size_t>(b) * p.ld_bc + group * N + n4, C[i]);
+        u[i] = to_f(static_cast<const E*>(p.u)[b * p.ld_u + c]);
+        v[i] = to_f(static_cast<const E*>(p.dt)[b * p.ld_dt + c]);
+        z[i] = p.z ? to_f(static_cast<const E*>(p.z)[b * p.ld_z + c]) : 0.f;
     }
-    static_cast<E*>(p.y)[static_cast<size_t>(b) * p.D + c] = from_f<E>(o);
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + c) * kLog2e : 0.f, skip = p.skip ? __ldg(p.skip + c) : 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const float a = fmaf(v[i], kLog2e, bias);
+        const float d = p.softplus ? softplus2(both(a)).x : a, x = d * kLn2 * u[i];
+        float4 g;
+        g.x = fmaf(ex2(d * A.x), h[i].x, x * B[i][0]);
+        g.y = fmaf(ex2(d * A.y), h[i].y, x * B[i][1]);
+        g.z = fmaf(ex2(d * A.z), h[i].z, x * B[i][2]);
+        g.w = fmaf(ex2(d * A.w), h[i].w, x * B[i][3]);
+        float o = fmaf(C[i][0], g.x, C[i][1] * g.y) + fmaf(C[i][2], g.z, C[i][3] * g.w);
+#pragma unroll
+        for (int k = LANES / 2; k > 0; k >>= 1) o += __shfl_xor_sync(0xffffffffu, o, k);
+        if (!on[i]) continue;
+        const size_t b = static_cast<size_t>(set + static_cast<long long>(i) * sets);
+        *reinterpret_cast<float4*>(p.h_out + (b * p.D + c) * N + n4) = g;
+        if (n4 != 0) continue;
+        o = fmaf(skip, u[i], o);
+        if (p.z) o *= z[i] * sigmoid(z[i]);
+        static_cast<E*>(p.y)[b * p.D + c] = from_f<E>(o);
+    }
 }
 
 // Seven CTAs on an SM.
@@ -380,12 +399,19 @@ int forward(const SsmParams& p, cudaStream_t st)
     return launched();
 }
 
+template <typename E, int N, int ROWS>
+int step_rows(const SsmParams& p, cudaStream_t st)
+{
+    const long long items = static_cast<long long>((p.B + ROWS - 1) / ROWS) * p.D * (N / 4);
+    ssm_step_kernel<E, N, ROWS><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
+    return launched();
+}
+
+// Several sequences a thread once the SMs are full of threads all the same.
 template <typename E, int N>
 int step(const SsmParams& p, cudaStream_t st)
 {
-    const long long items = static_cast<long long>(p.B) * p.D * (N / 4);
-    ssm_step_kernel<E, N><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
-    return launched();
+    return static_cast<long long>(p.B) * p.D * (N / 4) >= 4LL * kSms * 1024 ? step_rows<E, N, 4>(p, st) : step_rows<E, N, 1>(p, st);
 }
 
 template <typename E>
