@@ -313,60 +313,71 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
     cp_async_wait<0>();
 }
 
-// Four neighbouring values of B or C.
-template <typename E>
-__device__ __forceinline__ void quad_at(const void* p, size_t element, float (&f)[4])
-{
-    unpack_quad(load_quad<E>(p, element), f, E{});
-}
-
-// One token: a thread holds four states of one channel for ROWS sequences, all of whose loads are on their way at once; the
-// channel's N / 4 lanes sum y.
+// One token: a lane holds four states of each of four channels (as srwm_ssm.cuh) for ROWS sequences, all of whose loads are
+// on their way at once.  Each lane forms one channel's step and input, which the others get by shuffles.
 template <typename E, int N, int ROWS>
 __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constant__ SsmParams p)
 {
     constexpr int LANES = N / 4;
-    const int items = p.D * LANES, sets = (p.B + ROWS - 1) / ROWS;
+    const int items = p.D / 4 * LANES, sets = (p.B + ROWS - 1) / ROWS;
     const long long item = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    const int at = static_cast<int>(item % items), c = at / LANES, n4 = at % LANES * 4;
     const long long set = item / items;
     if (__all_sync(0xffffffffu, set >= sets)) return;
-    const int group = c / (p.D / p.G);
-    const float4 A = __ldg(reinterpret_cast<const float4*>(p.A + static_cast<size_t>(c) * N + n4));
-    float4 h[ROWS];
-    float B[ROWS][4], C[ROWS][4], u[ROWS], v[ROWS], z[ROWS];
+    const int at = static_cast<int>(item % items), quad = at / LANES * 4, n4 = at % LANES * 4, own = quad + quad_channel<LANES>();
+    const int group = quad / (p.D / p.G);
+    const bool live = set < sets;
+    const size_t first = live ? set : 0;
+    const E* const u0 = static_cast<const E*>(p.u) + first * p.ld_u + own;
+    const E* const d0 = static_cast<const E*>(p.dt) + first * p.ld_dt + own;
+    const E* const z0 = static_cast<const E*>(p.z) + (p.z ? first * p.ld_z + own : 0);
+    const size_t bc = first * p.ld_bc + group * N + n4, mat = (first * p.D + quad) * N + n4;
+    float2 A[2][4], h[ROWS][2][4];
+    typename Quad<E>::type B[ROWS], C[ROWS];
+    float u[ROWS], v[ROWS], z[ROWS];
     bool on[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const long long row = set + static_cast<long long>(i) * sets, b = row < p.B ? row : 0;
-        on[i] = set < sets && row < p.B;
-        h[i] = *reinterpret_cast<const float4*>(p.h_in + (static_cast<size_t>(b) * p.D + c) * N + n4);
-        quad_at<E>(p.Bt, static_cast<size_t>(b) * p.ld_bc + group * N + n4, B[i]);
-        quad_at<E>(p.Ct, static_cast<size_t>(b) * p.ld_bc + group * N + n4, C[i]);
-        u[i] = to_f(static_cast<const E*>(p.u)[b * p.ld_u + c]);
-        v[i] = to_f(static_cast<const E*>(p.dt)[b * p.ld_dt + c]);
-        z[i] = p.z ? to_f(static_cast<const E*>(p.z)[b * p.ld_z + c]) : 0.f;
+        on[i] = live && set + i * sets < p.B;
+        const size_t skip = on[i] ? static_cast<size_t>(i) * sets : 0;   // sequences between this and the thread's first
+        load_states(p.h_in + mat + skip * p.D * N, N, true, h[i]);
+        B[i] = load_quad<E>(p.Bt, bc + skip * p.ld_bc);
+        C[i] = load_quad<E>(p.Ct, bc + skip * p.ld_bc);
+        u[i] = to_f(u0[skip * p.ld_u]);
+        v[i] = to_f(d0[skip * p.ld_dt]);
+        z[i] = p.z ? to_f(z0[skip * p.ld_z]) : 0.f;
     }
-    const float bias = p.dt_bias ? __ldg(p.dt_bias + c) * kLog2e : 0.f, skip = p.skip ? __ldg(p.skip + c) : 0.f;
+    load_states(p.A + static_cast<size_t>(quad) * N + n4, N, true, A);
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + own) * kLog2e : 0.f, skip = p.skip ? __ldg(p.skip + own) : 0.f;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const float a = fmaf(v[i], kLog2e, bias);
         const float d = p.softplus ? softplus2(both(a)).x : a, x = d * kLn2 * u[i];
-        float4 g;
-        g.x = fmaf(ex2(d * A.x), h[i].x, x * B[i][0]);
-        g.y = fmaf(ex2(d * A.y), h[i].y, x * B[i][1]);
-        g.z = fmaf(ex2(d * A.z), h[i].z, x * B[i][2]);
-        g.w = fmaf(ex2(d * A.w), h[i].w, x * B[i][3]);
-        float o = fmaf(C[i][0], g.x, C[i][1] * g.y) + fmaf(C[i][2], g.z, C[i][3] * g.w);
+        float dk[4], xk[4], bk[4], ck[4];
 #pragma unroll
-        for (int k = LANES / 2; k > 0; k >>= 1) o += __shfl_xor_sync(0xffffffffu, o, k);
+        for (int k = 0; k < 4; ++k) {
+            dk[k] = __shfl_sync(0xffffffffu, d, k * (LANES / 4), LANES);
+            xk[k] = __shfl_sync(0xffffffffu, x, k * (LANES / 4), LANES);
+        }
+        unpack_quad(B[i], bk, E{});
+        unpack_quad(C[i], ck, E{});
+        float2 o[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 dd = make_float2(dk[2 * k], dk[2 * k + 1]), xx = make_float2(xk[2 * k], xk[2 * k + 1]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                h[i][k][s] = fma2(ex2_2(mul2(dd, A[k][s])), h[i][k][s], mul2(xx, both(bk[s])));
+                o[k] = s ? fma2(both(ck[s]), h[i][k][s], o[k]) : mul2(both(ck[s]), h[i][k][s]);
+            }
+        }
+        float y = quad_sum<LANES>(o[0].x, o[0].y, o[1].x, o[1].y);
         if (!on[i]) continue;
-        const size_t b = static_cast<size_t>(set + static_cast<long long>(i) * sets);
-        *reinterpret_cast<float4*>(p.h_out + (b * p.D + c) * N + n4) = g;
-        if (n4 != 0) continue;
-        o = fmaf(skip, u[i], o);
-        if (p.z) o *= z[i] * sigmoid(z[i]);
-        static_cast<E*>(p.y)[b * p.D + c] = from_f<E>(o);
+        const size_t b = first + static_cast<size_t>(i) * sets;
+        store_states(p.h_out + mat + static_cast<size_t>(i) * sets * p.D * N, N, h[i]);
+        if (!quad_leader<LANES>()) continue;
+        y = fmaf(skip, u[i], y);
+        if (p.z) y *= z[i] * sigmoid(z[i]);
+        static_cast<E*>(p.y)[b * p.D + own] = from_f<E>(y);
     }
 }
 
@@ -402,16 +413,16 @@ int forward(const SsmParams& p, cudaStream_t st)
 template <typename E, int N, int ROWS>
 int step_rows(const SsmParams& p, cudaStream_t st)
 {
-    const long long items = static_cast<long long>((p.B + ROWS - 1) / ROWS) * p.D * (N / 4);
+    const long long items = static_cast<long long>((p.B + ROWS - 1) / ROWS) * (p.D / 4) * (N / 4);
     ssm_step_kernel<E, N, ROWS><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
     return launched();
 }
 
-// Several sequences a thread once the SMs are full of threads all the same.
+// Two sequences a thread once the SMs are full of threads all the same.
 template <typename E, int N>
 int step(const SsmParams& p, cudaStream_t st)
 {
-    return static_cast<long long>(p.B) * p.D * (N / 4) >= 4LL * kSms * 1024 ? step_rows<E, N, 4>(p, st) : step_rows<E, N, 1>(p, st);
+    return static_cast<long long>(p.B) * p.D * (N / 16) >= 2LL * kSms * 1024 ? step_rows<E, N, 2>(p, st) : step_rows<E, N, 1>(p, st);
 }
 
 template <typename E>

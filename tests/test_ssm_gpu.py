@@ -175,7 +175,7 @@ def test_strong_decays_keep_their_gradients():
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("N", [16, 32, 64])
-@pytest.mark.parametrize("B,D,G", [(1, 8, 1), (3, 40, 1), (70, 264, 3)])
+@pytest.mark.parametrize("B,D,G", [(1, 8, 1), (3, 40, 1), (70, 264, 3), (301, 1032, 3)])
 def test_step(B, D, G, N, dtype):
     for packed in (False, True):
         a, _, _ = make(B + N, B, 1, D, N, G, dtype, packed=packed)
