@@ -26,13 +26,6 @@ constexpr int kSms = 152;
 constexpr int kMostThreads = 512;
 constexpr float kE4m3Max = 448.f;
 
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // The larger value, or NaN where one is (fmaxf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -81,8 +74,10 @@ __device__ __forceinline__ void gamma_of(const RmsParams& p, int c, float (&g)[8
     for (int k = 0; k < 4; ++k) g[k] = a[k], g[k + 4] = b[k];
 }
 
+enum Out { kSame, kE4m3Rows, kE4m3Blocks };   // a scale for a row, or for 128 channels
+
 // warps: of a row; with one, a CTA's warps take a row each.
-template <typename E, int K, bool E4M3>
+template <typename E, int K, int OUT>
 __global__ void __launch_bounds__(kMostThreads) rms_kernel(const RmsParams p, int warps)
 {
     constexpr int V = vec<E>;
@@ -133,18 +128,17 @@ __global__ void __launch_bounds__(kMostThreads) rms_kernel(const RmsParams p, in
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 h[k][i] = h[k][i] * rstd * g[i];
-                if (E4M3) top = max_nan(top, fabsf(h[k][i]));
+                if (OUT == kE4m3Rows) top = max_nan(top, fabsf(h[k][i]));
             }
-            if (!E4M3) store_vec<E>(p.y, base + v * V, pack(h[k], E{}));
+            if (OUT == kSame) store_vec<E>(p.y, base + v * V, pack(h[k], E{}));
         }
     }
-    if constexpr (E4M3) {
-        const bool whole = p.block == p.C;
-        if (whole) top = row_join<true>(top, warps, s);
+    if constexpr (OUT != kSame) {
+        if (OUT == kE4m3Rows) top = row_join<true>(top, warps, s);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int v = at + k * tpr;
-            if (!whole) {   // 128 channels: as many neighbouring lanes as they have vectors
+            if constexpr (OUT == kE4m3Blocks) {   // 128 channels: as many neighbouring lanes as they have vectors
                 top = 0.f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) top = max_nan(top, fabsf(h[k][i]));
@@ -153,14 +147,18 @@ __global__ void __launch_bounds__(kMostThreads) rms_kernel(const RmsParams p, in
             }
             if (v >= nv) continue;
             // a block next to zero is lifted first: 448 / top has to stay finite
-            const float lift = top < 0x1p-100f ? 0x1p64f : 1.f;
-            const float inv = top == 0.f ? 0.f : kE4m3Max / (top * lift);
+            float inv = 1.f / top * kE4m3Max;
+            if (top < 0x1p-100f) {
+                inv = top == 0.f ? 0.f : kE4m3Max / (top * 0x1p64f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[k][i] *= 0x1p64f;
+            }
             uint32_t q[V / 4];
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
                 float f[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = h[k][i + j] * lift * inv;
+                for (int j = 0; j < 4; ++j) f[j] = h[k][i + j] * inv;
                 q[i / 4] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
             }
             unsigned char* const to = static_cast<unsigned char*>(p.y) + base + v * V;
@@ -168,8 +166,8 @@ __global__ void __launch_bounds__(kMostThreads) rms_kernel(const RmsParams p, in
                 *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
             else
                 *reinterpret_cast<uint32_t*>(to) = q[0];
-            if (whole ? v == 0 : v % (128 / V) == 0)
-                p.scale[row * (p.C / p.block) + (whole ? 0 : v / (128 / V))] = top / kE4m3Max;
+            if (OUT == kE4m3Rows ? v == 0 : v % (128 / V) == 0)
+                p.scale[OUT == kE4m3Rows ? row : row * (p.C / 128) + v / (128 / V)] = top / kE4m3Max;
         }
     }
 }
@@ -179,6 +177,7 @@ template <typename E, int K>
 __global__ void __launch_bounds__(kMostThreads) rms_grad_kernel(const RmsParams p, int warps, int parts)
 {
     constexpr int V = vec<E>;
+    constexpr bool AHEAD = K < 4;     // the next row's loads are on their way while one is worked on: where registers hold both
     extern __shared__ float sums[];   // [rows of the CTA, C] where a warp takes a row
     __shared__ float s[kMostThreads / 32];
     const int tpr = warps * 32, rows = warps == 1 ? blockDim.x / 32 : 1;
@@ -189,19 +188,31 @@ __global__ void __launch_bounds__(kMostThreads) rms_grad_kernel(const RmsParams 
 #pragma unroll
         for (int i = 0; i < V; ++i) dg[k][i] = 0.f;
     const float inv = 1.f / p.C;
-    for (long long row = static_cast<long long>(blockIdx.x) * rows + mine; row < p.N; row += static_cast<long long>(parts) * rows) {
+    struct Row {
+        uint4 h[K], d[K], t[K];
+        float rstd;
+    };
+    auto load = [&](long long row, Row& r) {
         const size_t base = static_cast<size_t>(row) * p.C;
-        uint4 rh[K], rd[K], rt[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int v = at + k * tpr;
             if (v < nv) {
-                rh[k] = load_vec<E>(p.x, base + v * V);
-                rd[k] = load_vec<E>(p.dy, base + v * V);
-                if (p.dtotal) rt[k] = load_vec<E>(p.dtotal, base + v * V);
+                r.h[k] = load_vec<E>(p.x, base + v * V);
+                r.d[k] = load_vec<E>(p.dy, base + v * V);
+                if (p.dtotal) r.t[k] = load_vec<E>(p.dtotal, base + v * V);
             }
         }
-        const float rstd = __ldg(p.rstd + row);
+        r.rstd = __ldg(p.rstd + row);
+    };
+    const long long step = static_cast<long long>(parts) * rows;
+    long long row = static_cast<long long>(blockIdx.x) * rows + mine;
+    Row now, next;
+    if (AHEAD && row < p.N) load(row, now);
+    for (; row < p.N; row += step) {
+        if (!AHEAD) load(row, now);
+        if (AHEAD && row + step < p.N) load(row + step, next);
+        const size_t base = static_cast<size_t>(row) * p.C;
         float xh[K][V], d[K][V], dot = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -209,11 +220,11 @@ __global__ void __launch_bounds__(kMostThreads) rms_grad_kernel(const RmsParams 
             if (v < nv) {
                 float g[V];
                 gamma_of(p, v * V, g);
-                unpack(rh[k], xh[k], E{});
-                unpack(rd[k], d[k], E{});
+                unpack(now.h[k], xh[k], E{});
+                unpack(now.d[k], d[k], E{});
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    xh[k][i] *= rstd;
+                    xh[k][i] *= now.rstd;
                     dg[k][i] = fmaf(d[k][i], xh[k][i], dg[k][i]);
                     d[k][i] *= g[i];
                     dot = fmaf(d[k][i], xh[k][i], dot);
@@ -227,15 +238,16 @@ __global__ void __launch_bounds__(kMostThreads) rms_grad_kernel(const RmsParams 
             if (v < nv) {
                 float out[V];
                 if (p.dtotal)
-                    unpack(rt[k], out, E{});
+                    unpack(now.t[k], out, E{});
                 else
 #pragma unroll
                     for (int i = 0; i < V; ++i) out[i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) out[i] = fmaf(rstd, d[k][i] - xh[k][i] * m, out[i]);
+                for (int i = 0; i < V; ++i) out[i] = fmaf(now.rstd, fmaf(-xh[k][i], m, d[k][i]), out[i]);
                 store_vec<E>(p.dx, base + v * V, pack(out, E{}));
             }
         }
+        if (AHEAD) now = next;
     }
     griddep_launch();
     if (!p.part) return;
@@ -274,9 +286,21 @@ RowPlan row_plan(size_t e, long long N, int C)
     return r;
 }
 
+// The gradients' rows take up to two vectors a thread where they fit (their partial sums stay in registers), and as many
+// CTAs as run at once.
+RowPlan grad_plan(size_t e, long long N, int C)
+{
+    const int nv = C / static_cast<int>(16 / e);
+    RowPlan r{};
+    r.vectors = nv <= 32 ? 1 : nv <= 2 * kMostThreads ? 2 : 4;
+    r.warps = ((nv + r.vectors - 1) / r.vectors + 31) / 32;
+    r.rows = r.warps == 1 ? 4 : 1;
+    return r;
+}
+
 int grad_parts(const RowPlan& r, long long N)
 {
-    const long long most = kSms * std::max(1, 32 / (r.warps * r.rows));   // CTAs that share the SMs
+    const long long most = kSms * std::max(1, 16 / (r.warps * r.rows));   // CTAs that share the SMs
     return static_cast<int>(std::max(1LL, std::min<long long>((N + r.rows - 1) / r.rows, most)));
 }
 
@@ -285,10 +309,12 @@ int forward(const RmsParams& p, const RowPlan& r, int out, cudaStream_t st)
 {
     const unsigned grid = static_cast<unsigned>((p.N + r.rows - 1) / r.rows);
     const int threads = 32 * r.warps * r.rows;
-    if (out)
-        rms_kernel<E, K, true><<<grid, threads, 0, st>>>(p, r.warps);
+    if (!out)
+        rms_kernel<E, K, kSame><<<grid, threads, 0, st>>>(p, r.warps);
+    else if (p.block == 128 && p.C != 128)
+        rms_kernel<E, K, kE4m3Blocks><<<grid, threads, 0, st>>>(p, r.warps);
     else
-        rms_kernel<E, K, false><<<grid, threads, 0, st>>>(p, r.warps);
+        rms_kernel<E, K, kE4m3Rows><<<grid, threads, 0, st>>>(p, r.warps);
     return launched();
 }
 
@@ -315,15 +341,17 @@ int by_vectors(const RmsParams& p, int out, cudaStream_t st)
 template <typename E>
 int grad_by_vectors(const RmsParams& p, cudaStream_t st)
 {
-    const RowPlan r = row_plan(sizeof(E), p.N, p.C);
-    return r.vectors == 1 ? backward<E, 1>(p, r, st) : r.vectors == 2 ? backward<E, 2>(p, r, st) : backward<E, 4>(p, r, st);
+    const RowPlan r = grad_plan(sizeof(E), p.N, p.C);
+    if constexpr (sizeof(E) == 4)
+        if (r.vectors == 4) return backward<E, 4>(p, r, st);   // more than 4096 channels
+    return r.vectors == 1 ? backward<E, 1>(p, r, st) : backward<E, 2>(p, r, st);
 }
 
 }  // namespace
 
 size_t rmsnorm_backward_scratch(long long N, int C)
 {
-    const int parts = std::max(grad_parts(row_plan(4, N, C), N), grad_parts(row_plan(2, N, C), N));
+    const int parts = std::max(grad_parts(grad_plan(4, N, C), N), grad_parts(grad_plan(2, N, C), N));
     return round256(static_cast<size_t>(parts) * C * 4);
 }
 
