@@ -46,10 +46,10 @@ __device__ __forceinline__ float conv_slope(float v)
 }
 
 // Tokens of a thread's run: as long as keeps the SMs full, since each begins with an empty ring and rows read again.
-int run_of(int B, int T, int vecs)
+int run_of(int B, int T, int vecs, int most, int threads)
 {
     int run = 32;
-    while (run < 256 && static_cast<long long>(B) * vecs * ((T + 2 * run - 1) / (2 * run)) >= kSms * 512) run *= 2;
+    while (run < most && static_cast<long long>(B) * vecs * ((T + 2 * run - 1) / (2 * run)) >= kSms * threads) run *= 2;
     return run;
 }
 
@@ -94,7 +94,7 @@ __device__ __forceinline__ void shift(float (&win)[W][V])
 }
 
 template <typename E, int W, int ACT>
-__global__ void __launch_bounds__(kThreads, 5) conv_kernel(const ConvParams p, int run_len, int runs)
+__global__ void __launch_bounds__(kThreads, 4) conv_kernel(const ConvParams p, int run_len, int runs)
 {
     constexpr int V = vec<E>;
     extern __shared__ __align__(16) uint4 ring[];   // [groups][tokens][threads]: a thread's own rows on their way
@@ -211,7 +211,7 @@ GradPlan grad_plan(int B, int T, int D)
     g.vecs = std::min(nv, 32);
     g.groups = (nv + 31) / 32;
     g.slots = kThreads / g.vecs;
-    g.run_len = run_of(B, T, nv);
+    g.run_len = run_of(B, T, nv, 256, 512);
     g.runs = std::max(1, (T + g.run_len - 1) / g.run_len);
     const long long items = static_cast<long long>(B) * g.runs;
     g.parts = static_cast<int>(std::max(1LL, std::min<long long>((items + g.slots - 1) / g.slots, std::max(1, kGradParts / g.groups))));
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_grad_kernel(const ConvParams
 template <typename E, int W, int ACT>
 int forward(const ConvParams& p, cudaStream_t st)
 {
-    const int run = run_of(p.B, p.T, p.D / vec<E>), runs = std::max(1, (p.T + run - 1) / run);
+    const int run = run_of(p.B, p.T, p.D / vec<E>, 256, 1024), runs = std::max(1, (p.T + run - 1) / run);
     const long long items = static_cast<long long>(p.D / vec<E>) * runs * p.B;
     constexpr int smem = kGroups * kGroup * kThreads * 16;
     conv_kernel<E, W, ACT><<<static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, smem, st>>>(p, run, runs);
