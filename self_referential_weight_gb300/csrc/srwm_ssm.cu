@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
                 float2 sum;
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    h[c][s] = fma2(ex2_2(mul2(d, A[c][s])), h[c][s], mul2(x, now.b[s]));
+                    h[c][s] = fma2(decay2(d, A[c][s]), h[c][s], mul2(x, now.b[s]));
                     if (OUT) sum = s ? fma2(now.c[s], h[c][s], sum) : mul2(now.c[s], h[c][s]);
                 }
                 if (OUT) o[c] = sum.x + sum.y;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constan
             const float2 dd = make_float2(dk[2 * k], dk[2 * k + 1]), xx = make_float2(xk[2 * k], xk[2 * k + 1]);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                h[i][k][s] = fma2(ex2_2(mul2(dd, A[k][s])), h[i][k][s], mul2(xx, both(bk[s])));
+                h[i][k][s] = fma2(decay2(dd, A[k][s]), h[i][k][s], mul2(xx, both(bk[s])));
                 o[k] = s ? fma2(both(ck[s]), h[i][k][s], o[k]) : mul2(both(ck[s]), h[i][k][s]);
             }
         }

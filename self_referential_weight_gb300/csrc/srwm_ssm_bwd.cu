@@ -189,7 +189,7 @@ __device__ __forceinline__ void decays(const float2 (&dd)[2], const float2 (&A)[
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) a[k][s] = ex2_2(mul2(dd[k], A[k][s]));
+        for (int s = 0; s < 4; ++s) a[k][s] = decay2(dd[k], A[k][s]);
 }
 __device__ __forceinline__ void advance(const float2 (&a)[2][4], const float2 (&xx)[2], const float2 (&bb)[4], const float2 (&from)[2][4], float2 (&h)[2][4])
 {
@@ -315,7 +315,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
 #pragma unroll
                 for (int s = 0; s < 4; ++s) v[k][s] = fma2(ex2_2(mul2(sum[k], A[k][s])), v[k][s], own[k][s]);
         };
+#pragma unroll 2
         for (int j = 0; j < w.segment; ++j) join(j, p.seg_state, h);
+#pragma unroll 2
         for (int j = R.last; j > w.segment; --j) join(j, p.seg_grad, g);
     }
     // forwards: the states at every tile's start, and at the end
