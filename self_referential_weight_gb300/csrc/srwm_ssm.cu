@@ -381,11 +381,13 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constan
     }
 }
 
-// Seven CTAs on an SM.
+// Eight CTAs on an SM, of which segments fill half (2 x 8192 x 1024 channels fp32: 148 us with 19 segments, 152 with 27, 154
+// with 37: each starts from those before it).  Cut against whole: 8 x 1024 x 1024 channels bf16 (128 CTAs) 88 and 124 us, 14
+// sequences (224) 144 and 130.
 Split plan_of(int B, int T, int D, int N, int G)
 {
     const int ch = kPromptWarps * kLaneCh * 256 / N, dg = D / G;
-    return split_of(B, static_cast<long long>(G) * ((dg + ch - 1) / ch), T, 7 * kSms, 0.25, kWhole, 4 * kWhole);
+    return split_of(B, static_cast<long long>(G) * ((dg + ch - 1) / ch), T, 8 * kSms, 4 * kSms, 0.14, kWhole, 4 * kWhole);
 }
 
 template <typename E, int N>

@@ -115,17 +115,17 @@ __device__ __forceinline__ size_t segment_at(const SsmParams& p, const Place& w,
 }
 
 // Which sequences run whole and how the others are cut, for a kernel of `ctas` CTAs a sequence of which `slots` run at once.
-// Waves of whole sequences fill the GPU; what is left over is cut into as many segments as fill it once more where it is
-// less than `share` of it: a CTA by itself takes a large part of a full wave's time, the cut some more work.
+// Waves of whole sequences fill the GPU; what is left over is cut into segments, up to `fill` CTAs of them, where it is less
+// than `share` of a wave: a CTA by itself takes a large part of a full wave's time, the cut some more work.
 struct Split {
     int whole, segments, seg_len;
 };
-inline Split split_of(long long B, long long ctas, int T, int slots, double share, int unit, int least)
+inline Split split_of(long long B, long long ctas, int T, int slots, int fill, double share, int unit, int least)
 {
     const Split uncut{static_cast<int>(B), 1, T > 0 ? T : 1};
     const long long whole = B * ctas / slots * slots / ctas, rest = (B - whole) * ctas;
     if (rest == 0 || rest > share * slots) return uncut;
-    long long segments = slots / rest;
+    long long segments = fill / rest;
     if (segments > T / least) segments = T / least;
     if (segments > 64) segments = 64;
     if (segments < 2) return uncut;

@@ -476,7 +476,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
                 decays(d1, A, a1);
                 back(r + 1, a1, d1, x1, b1, between, h, 1);
             }
-            back(r, a, dd, xx, bb, before, between, 0);
+            {   // the first token's operands once more: registers for them all along cost more (64 x 1024 x 1024 channels bf16: 2 to 5 %)
+                float2 d0[2], x0[2], b0[4];
+                pairs(steps + r * S::kPitch + quad, d0);
+                pairs(xs + r * S::kPitch + quad, x0);
+                spread(Bf + r * N + n4, b0);
+                back(r, a, d0, x0, b0, before, between, 0);
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -579,14 +585,15 @@ struct Plan {
     long long ctas, rows;   // CTAs of a sequence (or of a segment); rows of the parameters' partial sums
 };
 
-// Six CTAs on an SM (four in fp32, by shared memory).
+// Six CTAs on an SM (four in fp32, by shared memory).  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
+// CTAs) 232 and 592 us, 14 372 and 608, 20 707 and 812; what is left over of 64 (112 CTAs) 1218 and 1560.
 Plan plan_of(size_t e, int B, int T, int D, int N, int G)
 {
     const int ch = kWarps * 128 / (N / 4), dg = D / G;
     Plan plan{};
     plan.chan_tiles = (dg + ch - 1) / ch;
     plan.ctas = static_cast<long long>(G) * plan.chan_tiles;
-    plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 0.28, TT, 8 * TT);
+    plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 6 * kSms, 0.5, TT, 8 * TT);
     auto blocks = [](int tokens) { return (std::max(1, tokens) + kBlock * TT - 1) / (kBlock * TT); };
     plan.blocks = {blocks(T), blocks(plan.split.seg_len)};
     plan.rows = static_cast<long long>(plan.split.whole) * plan.blocks.whole +
