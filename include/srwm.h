@@ -628,7 +628,8 @@ int srwm_ssm_step(const void* u, long long ld_u, const void* dt, long long ld_dt
  *   dh_init    [B, D, N] fp32, written; or NULL
  *   workspace  device scratch of srwm_ssm_backward_workspace_bytes(...) bytes:
  *              mostly the states of every eighth token, N / 2 bytes for each
- *              token and channel
+ *              token and channel of as many sequences as fill the GPU (or as
+ *              2 GB hold, where that is more): the others follow in their place
  * Rows at and past a sequence's length get zeros.  All sums run in fp32 in an
  * order that depends on the sizes alone.
  */

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
         for (int j = R.last; j > w.segment; --j) join(j, p.seg_grad, g);
     }
     // forwards: the states at every tile's start, and at the end
-    float* const check = p.check + (static_cast<size_t>(w.b) * ((p.T + TT - 1) / TT) + R.t0 / TT) * p.D * N +
+    float* const check = p.check + (static_cast<size_t>(w.b - p.base) * ((p.T + TT - 1) / TT) + R.t0 / TT) * p.D * N +
                          static_cast<size_t>(w.first + quad) * N + n4;
     const size_t check_step = static_cast<size_t>(p.D) * N;
 #pragma unroll
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
     };
     clear();
     for (int block = blocks - 1; block >= 0 && block * kBlock >= tiles; --block) flush(block);
-    float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / S::kCh) * p.B * p.T + tokens) * p.G + w.group) * 2 * N;
+    float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / S::kCh) * p.span + (w.b - p.base)) * p.T * p.G + w.group) * 2 * N;
     float2 start[2][4];   // the states before the tile
     load_states(check + (tiles - 1) * check_step, N, on && tiles > 0, start);
     for (int tile = tiles - 1; tile >= 0; --tile) {
@@ -563,10 +563,10 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const __grid_constant__ Ssm
 {
     griddep_wait();
     const int width = 2 * p.G * p.N;
-    const long long rows = static_cast<long long>(p.B) * p.T, i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long rows = static_cast<long long>(p.span) * p.T, i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long token = i / (width / 4);
     if (token >= rows) return;
-    const int j = static_cast<int>(i % (width / 4)) * 4, b = static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
+    const int j = static_cast<int>(i % (width / 4)) * 4, b = p.base + static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
     const int group = j / (2 * p.N), k = j % (2 * p.N);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < valid_tokens(p.lengths, b, p.T))
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const __grid_constant__ Ssm
             const float4 v = *reinterpret_cast<const float4*>(p.bc_part + (static_cast<size_t>(c) * rows + token) * width + j);
             a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
         }
-    E* const to = static_cast<E*>(k < p.N ? p.dB : p.dC) + token * p.ld_dbc + group * p.N + k % p.N;
+    E* const to = static_cast<E*>(k < p.N ? p.dB : p.dC) + (static_cast<long long>(b) * p.T + t) * p.ld_dbc + group * p.N + k % p.N;
     to[0] = from_f<E>(a.x), to[1] = from_f<E>(a.y), to[2] = from_f<E>(a.z), to[3] = from_f<E>(a.w);
 }
 
@@ -582,8 +582,11 @@ struct Plan {
     Split split;
     Blocks blocks;
     int chan_tiles;
+    int slice;              // whole sequences of one launch: the workspace holds the states and partials of these alone
     long long ctas, rows;   // CTAs of a sequence (or of a segment); rows of the parameters' partial sums
 };
+
+constexpr double kSliceBytes = 2e9;   // of the workspace, or one wave's need where that is more
 
 // Six CTAs on an SM (four in fp32, by shared memory).  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
 // CTAs) 232 and 592 us, 14 372 and 608, 20 707 and 812; what is left over of 64 (112 CTAs) 1218 and 1560.
@@ -596,6 +599,9 @@ Plan plan_of(size_t e, int B, int T, int D, int N, int G)
     plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 6 * kSms, 0.5, TT, 8 * TT);
     auto blocks = [](int tokens) { return (std::max(1, tokens) + kBlock * TT - 1) / (kBlock * TT); };
     plan.blocks = {blocks(T), blocks(plan.split.seg_len)};
+    const double each = static_cast<double>(T) * (static_cast<double>(D) * N * 4 / TT + plan.chan_tiles * 8.0 * G * N);
+    const long long wave = (6LL * kSms + plan.ctas - 1) / plan.ctas, room = each > 0 ? static_cast<long long>(kSliceBytes / each) : B;
+    plan.slice = static_cast<int>(std::min<long long>(B, std::max(wave, room / wave * wave)));
     plan.rows = static_cast<long long>(plan.split.whole) * plan.blocks.whole +
                 static_cast<long long>(B - plan.split.whole) * plan.split.segments * plan.blocks.cut;
     return plan;
@@ -608,7 +614,6 @@ struct Regions {
 
 Regions regions_of(const Plan& plan, int B, int T, int D, int N, int G)
 {
-    const size_t streams = static_cast<size_t>(B) * D;
     size_t at = 0;
     auto take = [&](size_t floats) {
         const size_t here = at;
@@ -620,8 +625,9 @@ Regions regions_of(const Plan& plan, int B, int T, int D, int N, int G)
     r.seg_state = take(cut * N);
     r.seg_grad = take(cut * N);
     r.seg_dt = take(cut);
-    r.check = take(static_cast<size_t>((T + TT - 1) / TT) * streams * N);
-    r.bc_part = take(static_cast<size_t>(plan.chan_tiles) * B * T * G * 2 * N);
+    const size_t held = std::max(plan.slice, B - plan.split.whole);   // sequences
+    r.check = take(static_cast<size_t>((T + TT - 1) / TT) * held * D * N);
+    r.bc_part = take(static_cast<size_t>(plan.chan_tiles) * held * T * G * 2 * N);
     r.part = take(static_cast<size_t>(plan.rows) * D * (N + 2));
     r.bytes = std::max<size_t>(256, at * 4);
     return r;
@@ -643,13 +649,22 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         q.first = static_cast<int>(whole);
         ssm_local_kernel<E, N><<<cut, kThreads, S::kSmemLocal, st>>>(q);
         rc = launched();
-        if (rc != SRWM_OK) return rc;
     }
-    ssm_grad_kernel<E, N><<<whole + cut, kThreads, S::kSmem, st>>>(p, plan.blocks);
-    rc = launched();
-    if (rc != SRWM_OK) return rc;
-    const long long quads = static_cast<long long>(p.B) * p.T * (2 * p.G * N / 4);
-    if (quads > 0) rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, p, plan.chan_tiles);
+    // one launch where the workspace holds all sequences; else a slice of whole ones at a time, and those that are cut
+    const bool at_once = plan.slice >= p.B;
+    for (int base = 0; base < p.B && rc == SRWM_OK;) {
+        SsmParams q = p;
+        const bool last = base >= p.whole;
+        q.base = base, q.span = at_once ? p.B : last ? p.B - p.whole : std::min(plan.slice, p.whole - base);
+        q.first = static_cast<int>(plan.ctas * base);
+        const unsigned grid = at_once ? whole + cut : last ? cut : static_cast<unsigned>(plan.ctas * q.span);
+        ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(q, plan.blocks);
+        rc = launched();
+        const long long quads = static_cast<long long>(q.span) * p.T * (2 * p.G * N / 4);
+        if (quads > 0 && rc == SRWM_OK)
+            rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, q, plan.chan_tiles);
+        base += q.span;
+    }
     if (rc != SRWM_OK) return rc;
     return sum_launch({p.part, plan.rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}}, st);
 }

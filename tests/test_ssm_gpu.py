@@ -325,6 +325,35 @@ def test_many_streams():
             near(x[pick], ref[name], err[name], "d" + name)
 
 
+def test_gradients_in_slices():
+    """More sequences than the workspace holds states for, the last two of them cut: single sequences against the oracle,
+    and the parameters' gradients against those of the two halves (a slice left out would miss a third)."""
+    B, T, D, N = 66, 300, 2048, 64
+    a, dy, dh = make(8, B, T, D, N, 1, BF16)
+    lengths = (torch.arange(B, device=DEV, dtype=torch.int32) * 37) % (T + 1)
+    lengths[[0, 33, 65]] = torch.tensor([300, 41, 299], device=DEV, dtype=torch.int32)
+    assert binding.srwm_ssm_backward_workspace_bytes(B, T, D, N, 1) < 0.8 * B * T * D * N
+
+    def run(part):
+        one = {k: v[part].contiguous() if k in ("u", "dt", "Bt", "Ct", "z", "h_init") else v for k, v in a.items()}
+        rest = {k: v for k, v in one.items() if k not in ("u", "dt", "A", "Bt", "Ct")}
+        return binding.srwm_ssm_backward(one["u"], one["dt"], one["A"], one["Bt"], one["Ct"], dy[part].contiguous(), **rest,
+                                         lengths=lengths[part].contiguous(), dh_final=dh[part].contiguous())
+
+    got, first, second = run(slice(0, B)), run(slice(0, 33)), run(slice(33, B))
+    pick = torch.tensor([0, 33, 65], device=DEV)
+    sub = {k: v[pick] if k in ("u", "dt", "Bt", "Ct", "z", "h_init") else v for k, v in a.items()}
+    ref = oracle.grads(dy[pick], sub, True, lengths[pick], dh[pick])
+    _, _, err = oracle.errors(dy[pick], sub, True, lengths[pick], dh[pick])
+    for name, x, p, q in zip(oracle.NAMES, got, first, second):
+        if name in ("A", "skip", "dt_bias"):
+            assert float((x - p - q).norm()) <= 1e-4 * float(x.norm()), name
+        else:
+            near(x[pick], ref[name], err[name], "d" + name, joins=64)
+            part = torch.cat([p, q])
+            assert float((x.float() - part.float()).norm()) <= 2.0 ** -8 * float(part.float().norm()), name
+
+
 def test_binding_refuses():
     a, dy, _ = make(1, 2, 5, 24, 16, 1, F32)
     call = lambda **kw: binding.srwm_ssm_forward(**{**a, **kw})  # noqa: E731
