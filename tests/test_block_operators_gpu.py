@@ -113,3 +113,96 @@ def test_gradients_through_the_block():
     assert set(got) == set(ref)
     for name in ref:
         close(got[name], ref[name], name)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured into a graph: no operator needs one outside it."""
+    code = """
+import torch
+from self_referential_weight_gb300 import binding as b
+torch.manual_seed(0)
+n = lambda *s: torch.randn(*s, device="cuda")
+x, w, wb, gamma = n(2, 300, 64), n(64, 4), n(64), n(64)
+A, B, C, dtb, z = -torch.exp(n(64, 16)), n(2, 300, 1, 16), n(2, 300, 1, 16), n(64) - 2, n(2, 300, 64)
+def run():
+    y, _, t, r = b.srwm_rmsnorm_forward(x.view(-1, 64), gamma, residual=z.view(-1, 64))
+    y8, s, _, _ = b.srwm_rmsnorm_forward(x.view(-1, 64), gamma, out="e4m3")
+    u, cs = b.srwm_conv_forward(y.view(2, 300, 64), w, wb)
+    o, h = b.srwm_ssm_forward(u, x, A, B, C, z=z, dt_bias=dtb)
+    g = b.srwm_ssm_backward(u, x, A, B, C, o, z=z, dt_bias=dtb)
+    d = b.srwm_conv_backward(y.view(2, 300, 64), w, wb, g[0])
+    e = b.srwm_rmsnorm_backward(t, gamma, r, d[0].view(-1, 64))
+    ut, _ = b.srwm_conv_step(x[:, 0], w, wb, cs)
+    ot, ht = b.srwm_ssm_step(ut, x[:, 0], A, B[:, 0], C[:, 0], h, z_t=z[:, 0], dt_bias=dtb)
+    return [v for v in (y, y8.view(torch.uint8), s, u, cs, o, h, *g, *d, *e, ut, ot, ht) if v is not None]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, run()))
+"""
+    import pathlib
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], cwd=pathlib.Path(__file__).parent.parent, capture_output=True, text=True,
+                       timeout=200)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs that are replayed one after the other may hold the same workspace; what they leave in it does not matter."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    sets = []
+    for T in (40, 700):
+        a = [n(2, T, 64), n(2, T, 64), -torch.exp(n(64, 16)), n(2, T, 1, 16), n(2, T, 1, 16)]
+        sets.append((a, n(2, T, 64), binding.srwm_ssm_forward(*a), binding.srwm_ssm_backward(*a, a[0])))
+    need = max(max(binding.srwm_ssm_backward_workspace_bytes(2, T, 64, 16, 1), binding.srwm_ssm_workspace_bytes(2, T, 64, 16, 1)) for T in (40, 700))
+    ws = torch.full((need,), 255, device=DEV, dtype=torch.uint8)      # NaN where it is read before it is written
+    graphs, outs = [], []
+    for a, _, _, _ in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append((*binding.srwm_ssm_forward(*a, workspace=ws), *binding.srwm_ssm_backward(*a, a[0], workspace=ws)))
+    for i in (0, 1, 0, 1, 1, 0):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for x, r in zip(outs[i], (*sets[i][2], *sets[i][3])):
+            assert (x is None) == (r is None) and (x is None or torch.equal(x, r))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in a tensor: the last sequence (or rows) against calls of their own."""
+    B, T, width = 300, 1000, 7200
+    assert B * T * width > 1 << 31
+    x = torch.randn(B, T, width, device=DEV, dtype=torch.bfloat16)
+    one = x[-1:].contiguous()
+    w, b, A = torch.randn(width, 4, device=DEV), torch.randn(width, device=DEV), -torch.exp(torch.randn(width, 16, device=DEV))
+    y, s = binding.srwm_conv_forward(x, w, b)
+    y1, s1 = binding.srwm_conv_forward(one, w, b)
+    assert torch.equal(y[-1:], y1) and torch.equal(s[-1:], s1)
+    d, d1 = binding.srwm_conv_backward(x, w, b, y)[0], binding.srwm_conv_backward(one, w, b, y1)[0]
+    assert torch.equal(d[-1:], d1)
+    del y, d
+    rows = x.view(B * T, width)
+    y, _, t, r = binding.srwm_rmsnorm_forward(rows, b, residual=rows)
+    y1, _, t1, r1 = binding.srwm_rmsnorm_forward(rows[-700:].contiguous(), b, residual=rows[-700:].contiguous())
+    assert torch.equal(y[-700:], y1) and torch.equal(t[-700:], t1) and torch.equal(r[-700:], r1)
+    e = binding.srwm_rmsnorm_backward(t, b, r, rows)[0]
+    assert torch.equal(e[-700:], binding.srwm_rmsnorm_backward(t1, b, r1, rows[-700:].contiguous())[0])
+    del y, t, e
+    bc = torch.randn(B, T, 2, 16, device=DEV, dtype=torch.bfloat16).unsqueeze(3).unbind(2)
+    ones = [v[-1:] for v in bc]
+    y, h = binding.srwm_ssm_forward(x, x, A, *bc)
+    y1, h1 = binding.srwm_ssm_forward(one, one, A, *ones)
+
+    def close(p, q):          # one sequence alone is cut along its axis: other roundings, then bf16's
+        assert float((p.double() - q.double()).norm()) <= 2.0 ** -8 * float(q.double().norm())
+
+    close(y[-1:], y1)
+    close(h[-1:], h1)
+    got, want = binding.srwm_ssm_backward(x, x, A, *bc, y), binding.srwm_ssm_backward(one, one, A, *ones, y1)
+    for i in (0, 1, 3, 4):
+        close(got[i][-1:], want[i])
