@@ -48,7 +48,7 @@ __device__ __forceinline__ float conv_slope(float v)
 // Tokens of a thread's run: as long as keeps the SMs full, since each begins with an empty ring and rows read again.
 int run_of(int B, int T, int vecs, int most, int threads)
 {
-    int run = 32;
+    int run = 8;
     while (run < most && static_cast<long long>(B) * vecs * ((T + 2 * run - 1) / (2 * run)) >= kSms * threads) run *= 2;
     return run;
 }

@@ -103,13 +103,19 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int own = warp * WCH + lane % S::kSets * kLaneCh, n8 = lane / S::kSets * 8;   // this lane's channels and states
     const bool on = own < w.count;
-    if (!OUT && w.segment >= last) return;   // nothing comes after it
+    if (!OUT) {
+        griddep_launch();   // the second kernel's CTAs find their places beside this one's
+        if (w.segment >= last) return;   // nothing comes after it
+    }
 
     E* const y = static_cast<E*>(p.y) + static_cast<size_t>(w.b) * p.T * p.D + w.first;
     if constexpr (OUT)   // rows past the end
         for (int i = threadIdx.x; i < (t1 - max(t0, live)) * (w.count / V); i += kPromptThreads)
             store_vec<E>(y, static_cast<size_t>(max(t0, live) + i / (w.count / V)) * p.D + i % (w.count / V) * V, make_uint4(0, 0, 0, 0));
-    if (w.segment > last) return;
+    if (w.segment > last) {
+        griddep_wait();
+        return;
+    }
 
     // the channels that this lane widens and stores, in every tile
     const int mine = warp * WCH + lane % (WCH / V) * V;
@@ -311,6 +317,7 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
             for (int c = 0; c < kLaneCh; ++c) p.seg_dt[segment_at(p, w, w.segment) + own + c] = total[c];
     }
     cp_async_wait<0>();
+    if (OUT) griddep_wait();   // no CTA of the second kernel ends before the first kernel has
 }
 
 // One token: a lane holds four states of each of four channels (as srwm_ssm.cuh) for ROWS sequences, all of whose loads are
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const __grid_constan
 Split plan_of(int B, int T, int D, int N, int G)
 {
     const int ch = kPromptWarps * kLaneCh * 256 / N, dg = D / G;
-    return split_of(B, static_cast<long long>(G) * ((dg + ch - 1) / ch), T, 8 * kSms, 4 * kSms, 0.14, kWhole, 4 * kWhole);
+    return split_of(B, static_cast<long long>(G) * ((dg + ch - 1) / ch), T, 8 * kSms, 4 * kSms, 0.14, kWhole, 2 * kWhole);
 }
 
 template <typename E, int N>
@@ -408,7 +415,9 @@ int forward(const SsmParams& p, cudaStream_t st)
         const int rc = launched();
         if (rc != SRWM_OK) return rc;
     }
-    ssm_kernel<E, N, true><<<ctas * p.whole + split * p.segments, kPromptThreads, S::kSmem, st>>>(p);
+    const unsigned grid = ctas * p.whole + split * p.segments;
+    if (split > 0) return launch_behind(ssm_kernel<E, N, true>, dim3(grid), kPromptThreads, S::kSmem, st, p);
+    ssm_kernel<E, N, true><<<grid, kPromptThreads, S::kSmem, st>>>(p);
     return launched();
 }
 

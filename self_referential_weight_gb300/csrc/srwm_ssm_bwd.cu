@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
     float* const steps = reinterpret_cast<float*>(smem + 2 * S::kStage);
     float *const xs = steps + S::kWide / 4, *const ps = xs + S::kWide / 4, *const Bf = ps + S::kWide / 4, *const Cf = Bf + TT * N;
     const Rows<E, N> R(p);
+    griddep_launch();   // the second kernel's CTAs find their places beside this one's
     if (R.w.segment > R.last) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp * L::kWarpCh + lane / L::kLanes * 4, n4 = lane % L::kLanes * 4;
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
     }
     cp_async_wait<0>();
     if (w.segment == 0 && on && p.dh_in) store_states(p.dh_in + mat, N, g);
+    griddep_wait();   // no CTA of this kernel ends before the one in front of it has
 }
 
 // dB and dC: the partials' sums over the ranges of a group's channels; zeros past the end.
@@ -596,7 +598,7 @@ Plan plan_of(size_t e, int B, int T, int D, int N, int G)
     Plan plan{};
     plan.chan_tiles = (dg + ch - 1) / ch;
     plan.ctas = static_cast<long long>(G) * plan.chan_tiles;
-    plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 6 * kSms, 0.5, TT, 8 * TT);
+    plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 6 * kSms, 0.5, TT, 4 * TT);
     auto blocks = [](int tokens) { return (std::max(1, tokens) + kBlock * TT - 1) / (kBlock * TT); };
     plan.blocks = {blocks(T), blocks(plan.split.seg_len)};
     const double each = static_cast<double>(T) * (static_cast<double>(D) * N * 4 / TT + plan.chan_tiles * 8.0 * G * N);
@@ -658,8 +660,12 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         q.base = base, q.span = at_once ? p.B : last ? p.B - p.whole : std::min(plan.slice, p.whole - base);
         q.first = static_cast<int>(plan.ctas * base);
         const unsigned grid = at_once ? whole + cut : last ? cut : static_cast<unsigned>(plan.ctas * q.span);
-        ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(q, plan.blocks);
-        rc = launched();
+        if (cut > 0 && base == 0)
+            rc = launch_behind(ssm_grad_kernel<E, N>, dim3(grid), kThreads, S::kSmem, st, q, plan.blocks);
+        else {
+            ssm_grad_kernel<E, N><<<grid, kThreads, S::kSmem, st>>>(q, plan.blocks);
+            rc = launched();
+        }
         const long long quads = static_cast<long long>(q.span) * p.T * (2 * p.G * N / 4);
         if (quads > 0 && rc == SRWM_OK)
             rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, q, plan.chan_tiles);
