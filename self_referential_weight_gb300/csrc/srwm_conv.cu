@@ -211,7 +211,7 @@ GradPlan grad_plan(int B, int T, int D)
     g.vecs = std::min(nv, 32);
     g.groups = (nv + 31) / 32;
     g.slots = kThreads / g.vecs;
-    g.run_len = run_of(B, T, nv, 256, 512);
+    g.run_len = run_of(B, T, nv, 256, 2048);
     g.runs = std::max(1, (T + g.run_len - 1) / g.run_len);
     const long long items = static_cast<long long>(B) * g.runs;
     g.parts = static_cast<int>(std::max(1LL, std::min<long long>((items + g.slots - 1) / g.slots, std::max(1, kGradParts / g.groups))));
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_grad_kernel(const ConvParams
         load_bias<V>(p, c, bias);
     }
     for (long long item = static_cast<long long>(part) * g.slots + slot; item < items; item += static_cast<long long>(g.parts) * g.slots) {
-        const int b = static_cast<int>(item / g.runs), run = static_cast<int>(item % g.runs);
+        const int b = static_cast<int>(item % p.B), run = static_cast<int>(item / p.B);   // a thread's runs begin at different tokens: of uneven sequences the later ones are short
         const int n = valid_tokens(p.lengths, b, p.T);
         const int t0 = run * g.run_len, t1 = min(p.T, t0 + g.run_len);
         const E* const x = static_cast<const E*>(p.x) + static_cast<size_t>(b) * p.T * p.ld + c;
