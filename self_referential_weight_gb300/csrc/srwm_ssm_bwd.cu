@@ -591,7 +591,7 @@ struct Plan {
 constexpr double kSliceBytes = 2e9;   // of the workspace, or one wave's need where that is more
 
 // Six CTAs on an SM (four in fp32, by shared memory).  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
-// CTAs) 232 and 592 us, 14 372 and 608, 20 707 and 812; what is left over of 64 (112 CTAs) 1218 and 1560.
+// CTAs) 229 and 599 us, 14 372 and 608, 20 714 and 816, 64 (of whose 1024 CTAs 112 are left over) 1222 and 1586.
 Plan plan_of(size_t e, int B, int T, int D, int N, int G)
 {
     const int ch = kWarps * 128 / (N / 4), dg = D / G;
