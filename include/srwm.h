@@ -506,7 +506,7 @@ int srwm_groupnorm_backward(const void* x, const float* gamma, const float* beta
  *   state_final [B, W-1, D] of `dtype`, contiguous, written: the last W - 1 of
  *              the state's rows and the valid tokens, copied; or NULL
  *
- * Supported: W in {2, 3, 4}, D a multiple of 8; T = 0 is valid (x and y may be
+ * Supported: W in {2, 3, 4}, D a multiple of 8 up to 2^24; T = 0 is valid (x and y may be
  * NULL then).  Sums are fp32 and rounded once.  An infinity or NaN reaches the
  * W outputs that see it.
  */
@@ -583,9 +583,9 @@ int srwm_conv_backward(const void* x, long long ld, const float* weight, const f
  *              aligned, contents irrelevant on entry, untouched by others
  *              until the work on `stream` ends
  *
- * Supported: N in {16, 32, 64}, G divides D, D / G a multiple of 8; T = 0 is
- * valid (u, dt, Bt, Ct and y may be NULL then).  States, steps and sums are
- * fp32; y is rounded once.  An infinity or NaN in a valid token stays within
+ * Supported: N in {16, 32, 64}, G divides D, D / G a multiple of 8, D at most
+ * 2^24; A finite; T = 0 is valid (u, dt, Bt, Ct and y may be NULL then).
+ * States, steps and sums are fp32; y is rounded once.  An infinity or NaN in a valid token stays within
  * its sequence, and within its channel where it stands in u, dt or z.
  */
 size_t srwm_ssm_workspace_bytes(int B, int T, int D, int N, int G);
@@ -666,7 +666,8 @@ int srwm_ssm_backward(const void* u, long long ld_u, const void* dt, long long l
  *   rstd      [N] fp32, written (srwm_rmsnorm_backward reads it); or NULL
  *
  * Supported: C a multiple of 8 and at most 8192, N >= 0 below 2^31 (N = 0 does
- * nothing; x, y and scale may be NULL then).
+ * nothing; x, y and scale may be NULL then).  mean(h^2) must stay within fp32's
+ * range: a row whose squares overflow gets zeros, as rstd is 0 then.
  */
 int srwm_rmsnorm_forward(const void* x, const void* residual, const float* gamma, int dtype, long long N, int C, float eps,
                          int out, int block, void* y, float* scale, void* total, float* rstd, void* stream);

@@ -14,7 +14,7 @@ using srwm::Region;
 bool sizes_ok(long long B, long long T, long long D)
 {
     if (B <= 0 || T < 0 || D <= 0) return false;
-    return B <= 0x3fffffffLL && T <= 0x3fffffffLL && D <= 0x3fffffffLL && B <= (1LL << 38) / D && (T == 0 || B * D <= (1LL << 42) / T);
+    return B <= 0x3fffffffLL && T <= 0x3fffffffLL && D <= (1LL << 24) && B <= (1LL << 38) / D && (T == 0 || B * D <= (1LL << 42) / T);
 }
 
 bool supported(int D, int W, int activation)

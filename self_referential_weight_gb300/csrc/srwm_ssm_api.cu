@@ -14,7 +14,7 @@ using srwm::Region;
 bool sizes_ok(long long B, long long T, long long D, long long N, long long G)
 {
     if (B <= 0 || T < 0 || D <= 0 || N <= 0 || G <= 0 || D % G != 0) return false;
-    if (B > (1LL << 30) / D || T > 0x3fffffffLL || G * N > (1LL << 30)) return false;
+    if (D > (1LL << 24) || B > (1LL << 30) / D || T > 0x3fffffffLL || G * N > (1LL << 30)) return false;
     return T == 0 || B * (D + 2 * G * N) <= (1LL << 40) / T;
 }
 

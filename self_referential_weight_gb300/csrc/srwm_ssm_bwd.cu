@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
     for (int block = blocks - 1; block >= 0 && block * kBlock >= tiles; --block) flush(block);
     float* const bc_part = p.bc_part + ((static_cast<size_t>((w.first - w.group * (p.D / p.G)) / S::kCh) * p.span + (w.b - p.base)) * p.T * p.G + w.group) * 2 * N;
     float2 start[2][4];   // the states before the tile
-    load_states(check + (tiles - 1) * check_step, N, on && tiles > 0, start);
+    load_states(check + max(tiles - 1, 0) * check_step, N, on && tiles > 0, start);
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int first = R.t0 + tile * TT, rows = min(TT, R.live - first);
         const unsigned char* const raw = stages + (tile & 1) * S::kStage;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
 #pragma unroll
                 for (int s = 0; s < 4; ++s) h[k][s] = before[k][s];
         }
-        load_states(check + (tile - 1) * check_step, N, on && tile > 0, start);
+        load_states(check + max(tile - 1, 0) * check_step, N, on && tile > 0, start);
         __syncthreads();
         // dB and dC of the tile: each of a token's 2 N sums runs over the CTA's channel quads
         for (int i = threadIdx.x; i < TT * 2 * LANES; i += kThreads) {
