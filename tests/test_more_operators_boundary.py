@@ -57,7 +57,7 @@ def test_conv_refuses(lib):
         assert call(B=0) == 2 and call(D=0) == 2 and call(B=1 << 29, D=1 << 20) == 2
         assert call(D=12) == 3 and call(W=1) == 3 and call(W=5) == 3 and call(act=2) == 3 and call(dt=3) == 3
         assert call(ld=8) == 2 and call(ld=18) == 2 and call(x=A + 4) == 4 and call(w=A + M + 8) == 4
-    assert f(T=-1) == 2 and f(n=A + 5 * M + 2) == 4 and f(B=1 << 10, T=1 << 29, D=1 << 10, ld=1 << 10) == 2
+    assert f(D=1 << 25, ld=1 << 25) == 2 and f(T=-1) == 2 and f(n=A + 5 * M + 2) == 4 and f(B=1 << 10, T=1 << 29, D=1 << 10, ld=1 << 10) == 2
     assert f(y=A) == 5 and f(so=A + 3 * M + 64) == 5 and f(y=A + 16, ld=64) == 5 and f(s=A + 4 * M) == 5
     assert s(so=A + 5 * M + 16) == 5 and s(y=A) == 5 and s(so=A + 5 * M) not in ARGUMENTS   # exactly in place
     assert g(ldg=8) == 2 and g(wb=16) == 2 and g(dx=A) == 5 and g(db=A + 5 * M) == 5 and g(ws=A + 4 * M) == 5
