@@ -294,7 +294,7 @@ RowPlan grad_plan(size_t e, long long N, int C)
     RowPlan r{};
     r.vectors = nv <= 32 ? 1 : nv <= 2 * kMostThreads ? 2 : 4;
     r.warps = ((nv + r.vectors - 1) / r.vectors + 31) / 32;
-    r.rows = r.warps == 1 ? 4 : 1;
+    r.rows = r.warps == 1 ? 8 : 1;
     return r;
 }
 

@@ -1,7 +1,7 @@
 // srwm_sum.cu -- sums of partial results over their index, in a fixed order: the
 // last step of parameter gradients, whose partials come from a few hundred CTAs.
 // One CTA takes 32 columns with 32 rows in flight, so a row's reads are whole
-// 128-byte lines; the 32 sums of a column are joined in order.
+// 128-byte lines; a column's 32 sums are joined by a warp, always in the same way.
 #include <cuda_runtime.h>
 
 #include "srwm.h"
@@ -25,10 +25,11 @@ __global__ void __launch_bounds__(1024) sum_kernel(const SumJob job)
     }
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
-    if (threadIdx.y != 0 || c >= width) return;
+    a = s[threadIdx.x][threadIdx.y];   // a warp joins one column
 #pragma unroll
-    for (int k = 1; k < 32; ++k) a += s[k][threadIdx.x];
-    long long at = c;
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    long long at = static_cast<long long>(blockIdx.x) * 32 + threadIdx.y;
+    if (threadIdx.x != 0 || at >= width) return;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         if (at < job.n[k]) {
