@@ -73,7 +73,7 @@ def _link_module(obj: str, torch_dir: str):
     lib = os.path.join(torch_dir, "lib")
     tmp = MODULE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", PKG, "-l:libsrwm.so", "-L", lib, "-ltorch_python",
-           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"linking _srwm_torch.so failed:\n{res.stdout}\n{res.stderr}")

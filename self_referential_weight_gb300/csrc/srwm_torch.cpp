@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/DimVector.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -60,10 +60,16 @@ void* optional(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarT
     return o == Py_None ? nullptr : address(o, name, shape, type);
 }
 
+// A new tensor beside `like`, straight from the allocator: through the dispatcher it takes as long as a launch.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like)
+{
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
 // The caller's output tensor, checked, or a new one.
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like)
 {
-    if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+    if (o == Py_None) return fresh(shape, type, like);
     const at::Tensor& t = tensor(o, name);
     address(t, name, shape, type);
     return t;
@@ -75,7 +81,7 @@ float* floats(const at::Tensor& t) { return static_cast<float*>(data(t)); }
 at::Tensor scratch(PyObject* o, size_t need, const at::Tensor& like)
 {
     if (o == Py_None)
-        return at::empty({static_cast<int64_t>(need > 16 ? need : 16)}, like.options().dtype(at::kByte));
+        return fresh({static_cast<int64_t>(need > 16 ? need : 16)}, at::kByte, like);
     const at::Tensor& t = tensor(o, "workspace");
     TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
     return t;
@@ -125,7 +131,7 @@ int64_t row_distance(const at::Tensor& t, const char* name, at::IntArrayRef shap
 // The caller's output, whose rows may lie apart, or a new one.
 at::Tensor row_output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like)
 {
-    return o == Py_None ? at::empty(shape, like.options().dtype(type)) : tensor(o, name);
+    return o == Py_None ? fresh(shape, type, like) : tensor(o, name);
 }
 
 // The operator's own output where it is wanted, or an undefined tensor (None).
@@ -256,7 +262,7 @@ PyObject* linattn_backward(PyObject*, PyObject* const* a, Py_ssize_t na)
     const int given = (a[9] != Py_None) + (a[10] != Py_None) + (a[11] != Py_None);
     TORCH_CHECK_VALUE(given == 0 || given == 3, "dq, dk and dv: give all three or none");
     auto grad = [&](PyObject* o, const char* name) {
-        return given ? tensor(o, name) : at::empty(q.sizes(), q.options());
+        return given ? tensor(o, name) : fresh(q.sizes(), q.scalar_type(), q);
     };
     const at::Tensor dq = grad(a[9], "dq"), dk = grad(a[10], "dk"), dv = grad(a[11], "dv");
     const int64_t ldg = token_distance({{&dq, "dq"}, {&dk, "dk"}, {&dv, "dv"}}, q.sizes(), q.scalar_type());
