@@ -7,8 +7,11 @@
 //   d = dy gamma,  dx = dtotal + r (d - h r mean(d h r)),  dgamma = sum dy h r
 // Memory bounds it: each row is read once and waits in registers for its sum of
 // squares.  h enters the norm before it is rounded to its type on its way out.
-// A row takes TPR threads (a warp where that is enough) with K vectors each, all
-// of whose loads are issued at once.
+// A row takes a warp where that is enough, else a CTA of up to 16, with one to four
+// vectors a thread, all of whose loads are issued at once.  65536 rows of 1024
+// channels in bf16 into 8 bits with scales of 128 channels take 73.4 us, 6.4 TB/s
+// (0.95 of the copy rate); gradients of 65536 x 512 take 46 us and 5 for dgamma's
+// partial sums.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -270,7 +273,9 @@ __global__ void __launch_bounds__(kMostThreads) rms_grad_kernel(const RmsParams 
     }
 }
 
-// Warps of a row and vectors of a thread: four vectors where there are rows enough to fill the SMs, else one or two.
+// Warps of a row and vectors of a thread: four vectors, or one (where 512 threads hold a row) while there are too few of them
+// to fill the SMs.  One against four, 4096 channels in fp16: 96 rows 2.7 and 3.2 us, 300 3.2 and 3.6, 600 4.5 and 4.0; 1024
+// channels in bf16: 600 rows 2.6 and 3.1, 2400 3.8 and 3.8.
 struct RowPlan {
     int warps, vectors, rows;   // rows: of a CTA
 };
@@ -280,7 +285,7 @@ RowPlan row_plan(size_t e, long long N, int C)
     const int nv = C / static_cast<int>(16 / e);
     RowPlan r{};
     r.vectors = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
-    while (r.vectors > 1 && N < 4 * kSms && (nv + r.vectors / 2 - 1) / (r.vectors / 2) <= kMostThreads) r.vectors /= 2;
+    while (r.vectors > 1 && N * nv < (1 << 18) && (nv + r.vectors / 2 - 1) / (r.vectors / 2) <= kMostThreads) r.vectors /= 2;
     r.warps = ((nv + r.vectors - 1) / r.vectors + 31) / 32;
     r.rows = r.warps == 1 ? 4 : 1;
     return r;

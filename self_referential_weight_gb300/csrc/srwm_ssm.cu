@@ -8,9 +8,18 @@
 // inputs in fp32, runs its states (in registers throughout) over the tile, and
 // gates and stores the outputs.  Past a sequence's end a token's step is 0, which
 // leaves the state as it is.
-// Few streams: the axis is cut into segments.  A first kernel runs every segment
-// but the last from a zero state; the second starts each from the states before
-// it, H = exp(A sum s) H + H', and writes y.
+// Few streams, or a last wave nearly empty: the axis is cut into segments.  A first
+// kernel runs every segment but the last from a zero state; the second starts each
+// from the states before it, H = exp(A sum s) H + H', and writes y.
+//
+// What bounds it: four fp32 operations and one exponential for each token, channel
+// and state, all in registers, and issue around them.  64 x 1024 tokens of 1024
+// channels of 16 states, gated, in bf16 take 321 us: 545 MB at 1.7 TB/s, the fp32
+// pipe at 48 % and 60 % of the issue slots, where a two-wide operation holds two.
+// 2048 warps are 3.4 a scheduler, and those with four set the time.  Two warps a
+// CTA against one or four: 343, 353 and 482 us; eight states of two channels a
+// lane against four of four: 352 and 407.  A token in decoding is bound by
+// memory: 512 x 1024 channels of 64 states in bf16 take 45 us, 6.0 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -429,7 +438,8 @@ int step_rows(const SsmParams& p, cudaStream_t st)
     return launched();
 }
 
-// Two sequences a thread once the SMs are full of threads all the same.
+// Two sequences a thread once the SMs are full of threads all the same (512 x 1024 channels of 64 states: 45.3 us, by one
+// 47.2, by four 48.0).
 template <typename E, int N>
 int step(const SsmParams& p, cudaStream_t st)
 {

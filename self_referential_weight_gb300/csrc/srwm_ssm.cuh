@@ -1,12 +1,13 @@
-// srwm_ssm.cuh -- what the selective scan's kernels share: the layout of a
-// warp's states, its sums over lanes, and the step's softplus.
+// srwm_ssm.cuh -- what the selective scan's kernels share: the step's softplus
+// and the decays, a CTA's place and how the axis is cut, and the layout of the
+// gradients' and the single token's lanes.
 //
-// A lane holds four states of each of four channels.  The N / 4 lanes of a
-// channel quad follow each other, so a warp holds 128 / (N / 4) channels.  A
-// token costs it, per state, two products, two sums of products and one
-// exponential; a token's step and input come as one 16-byte load for four
-// channels, B and C for four states, and y leaves through three or more
-// shuffles for all four channels.
+// There a lane holds four states of each of four channels, and the N / 4 lanes of
+// a channel quad follow each other, so a warp holds 128 / (N / 4) channels.  A
+// token's step and input come as one 16-byte load for four channels, B and C for
+// four states, and a sum over states leaves through three or more shuffles for
+// all four channels.  (The prompt's kernel, which has one such sum and not three,
+// takes eight states of two channels: one shuffle.)
 #pragma once
 
 #include "srwm_ssm.h"
