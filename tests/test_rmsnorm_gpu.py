@@ -155,6 +155,40 @@ def test_codes_are_the_nearest():
     assert torch.equal(got[127:], torch.where(low % 2 == 0, low, low + 1))
 
 
+def nearest_code(y, scale):
+    """Codes of positive y / scale to the nearest, ties to even, in whole fp64 arithmetic: a border between two codes has at
+    most 5 significant bits and a scale 24, so their product and its comparison with y are exact."""
+    codes = oracle.e4m3_values()[:127].to(DEV)
+    borders = (codes[:-1] + codes[1:]) / 2 * scale.double()
+    low = torch.searchsorted(borders, y.double())               # borders below y
+    tie = (low < 126) & (borders[low.clamp(max=125)] == y.double())
+    return torch.where(tie & (low % 2 == 1), low + 1, low)
+
+
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("power", [0, 90, -40, -55, -70, -95, -110])
+def test_codes_are_the_nearest_at_any_scale(power, block):
+    """Results on the borders between two codes and one step of fp32 beside them, at scales that are no powers of two: with
+    rows of ones and a factor of 1 the results are gamma itself, so every code is known exactly."""
+    g = torch.Generator().manual_seed(power + 200)
+    short = [int(v) * 2 + 1 for v in torch.randint(1 << 7, 1 << 8, (12,), generator=g)]        # scales whose borders are exact
+    long = [int(v) * 2 + 1 for v in torch.randint(1 << 22, 1 << 23, (12,), generator=g)]       # and of 24 bits
+    codes = oracle.e4m3_values()[:127].to(DEV)
+    mids = (codes[:-1] + codes[1:]) / 2
+    x = torch.ones(2, 384, device=DEV)
+    for m in short + long:
+        top = torch.tensor(448.0 * m / 2 ** m.bit_length() * 2.0 ** power, dtype=torch.float64).float()
+        top, scale = top.to(DEV), (top / 448).to(DEV)            # fp32's own division, on the CPU
+        at = (mids * scale.double()).float()
+        rows = torch.stack([at, torch.nextafter(at, top), torch.nextafter(at, -top)]).T.reshape(-1)     # 378 results
+        gamma = torch.cat([rows[:127], top[None], rows[127:254], top[None], rows[254:], rows[:3], top[None]])
+        y, s, _, rstd = binding.srwm_rmsnorm_forward(x, gamma, eps=2.0 ** -40, out="e4m3", block=block)
+        assert (rstd == 1).all() and (s == scale).all(), m
+        want = nearest_code(gamma, scale)
+        for row in y.view(torch.uint8).long():
+            assert torch.equal(row, want), (m, int((row != want).sum()))
+
+
 def test_residual_stream_in_place():
     x, r, g, _, _ = make(7, 300, 512, BF16)
     y, total, _ = check_forward(x, g, r)
