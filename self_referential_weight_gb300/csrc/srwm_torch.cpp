@@ -169,7 +169,8 @@ long long integer(PyObject* o)
     return v;
 }
 
-int as_int(int64_t v) { return v > 0x7fffffff ? -1 : static_cast<int>(v); }   // the library refuses what does not fit
+// The library refuses what does not fit: to either side, since what a cut leaves of a number below -2^31 can be one that it takes.
+int as_int(int64_t v) { return v < 0 || v > 0x7fffffff ? -1 : static_cast<int>(v); }
 
 void* stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 

@@ -255,3 +255,11 @@ def test_binding_refuses():
             binding.srwm_rmsnorm_forward(**{**dict(x=x, gamma=g), **bad})
     with pytest.raises(binding.SrwmError):
         binding.srwm_rmsnorm_backward(x, g, torch.ones(4, device=DEV), dy, workspace=torch.empty(16, device=DEV, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("block", [-1, -128, 128 - 2 ** 32, -2 ** 32, 2 ** 31, 2 ** 32 + 128, 2 ** 63 - 1, -2 ** 63])
+def test_binding_refuses_blocks_that_do_not_fit(block):
+    """Among them numbers whose lower 32 bits are a block that there is: for it the scales would need more room."""
+    x, _, g, _, _ = make(1, 4, 512, F32)
+    with pytest.raises(binding.SrwmError):
+        binding.srwm_rmsnorm_forward(x, g, out="e4m3", block=block)
