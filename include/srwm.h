@@ -655,9 +655,9 @@ int srwm_ssm_backward(const void* u, long long ld_u, const void* dt, long long l
  *   block     with SRWM_OUT_E4M3 the channels of one scale: 0 for a whole row,
  *             or 128 (C a multiple of it); else 0
  *   y         [N, C] of `dtype`, written; with SRWM_OUT_E4M3 [N, C] bytes of
- *             e4m3: the result (the fp32 number that `out` 0 in fp32 gives) over its
- *             block's scale, the exact quotient to the nearest (ties to even;
- *             a scale below 2^-126 counts with 24 bits here)
+ *             e4m3: the result, in fp32, over its block's scale, rounded once: to
+ *             the nearest, ties to even (a scale below 2^-126 counts with all
+ *             24 bits of the division here)
  *   scale     [N, C / block] fp32 ([N, 1] for a whole row), written with
  *             SRWM_OUT_E4M3: the block's largest magnitude over 448, so
  *             y * scale is the result; 0 for a block of zeros, NaN for one

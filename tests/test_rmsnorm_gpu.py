@@ -263,3 +263,20 @@ def test_binding_refuses_blocks_that_do_not_fit(block):
     x, _, g, _, _ = make(1, 4, 512, F32)
     with pytest.raises(binding.SrwmError):
         binding.srwm_rmsnorm_forward(x, g, out="e4m3", block=block)
+
+
+def test_8_bits_of_infinite_results():
+    """A result past fp32's largest number: its block's scale is infinite, its own code NaN, the block's others 0."""
+    x = torch.ones(3, 256, device=DEV)
+    x[1] = -1
+    gamma = torch.ones(256, device=DEV)
+    gamma[200] = float("inf")
+    for block, at in ((128, slice(128, 256)), (0, slice(0, 256))):
+        y, scale, _, _ = binding.srwm_rmsnorm_forward(x, gamma, out="e4m3", block=block)
+        want = torch.zeros(256, device=DEV)
+        want[200] = float("nan")
+        assert torch.isinf(scale[:, -1]).all()
+        assert torch.equal(torch.isnan(y.float())[:, at], torch.isnan(want).expand(3, 256)[:, at])
+        assert (torch.nan_to_num(y.float())[:, at] == 0).all()
+        if block:
+            assert torch.isfinite(scale[:, 0]).all() and (y.float()[:, :128].abs() == 448).all()
