@@ -627,9 +627,12 @@ int srwm_ssm_step(const void* u, long long ld_u, const void* dt, long long ld_dt
  *   ddt_bias   [D] fp32, written; or NULL
  *   dh_init    [B, D, N] fp32, written; or NULL
  *   workspace  device scratch of srwm_ssm_backward_workspace_bytes(...) bytes:
- *              mostly the states of every eighth token, N / 2 bytes for each
- *              token and channel of as many sequences as fill the GPU (or as
- *              2 GB hold, where that is more): the others follow in their place
+ *              the states of every eighth token (N / 2 bytes for each token and
+ *              channel), the parts of dB and dC (8 N bytes a token for each
+ *              1024 / N channels of a group) and those of dA, dskip and
+ *              ddt_bias (4 N + 8 bytes a channel for each 256 tokens), of as
+ *              many sequences as fill the GPU (or as 2 GB hold, where that is
+ *              more): the others follow in their place
  * Rows at and past a sequence's length get zeros.  All sums run in fp32 in an
  * order that depends on the sizes alone.
  */

@@ -399,7 +399,7 @@ int backward(const ConvParams& p0, cudaStream_t st)
     conv_grad_kernel<E, W, ACT><<<static_cast<unsigned>(g.groups) * g.parts, kThreads, smem, st>>>(p, g);
     const int rc = launched();
     if (rc != SRWM_OK || !params) return rc;
-    return sum_launch({p.part, g.parts, {p.dweight, p.dbias, nullptr}, {static_cast<long long>(p.D) * W, p.D, 0}}, st);
+    return sum_launch({p.part, g.parts, {p.dweight, p.dbias, nullptr}, {static_cast<long long>(p.D) * W, p.D, 0}, false}, st);
 }
 
 enum Way { kForward, kStep, kBackward };

@@ -371,7 +371,7 @@ int backward(const RmsParams& p0, const RowPlan& r, cudaStream_t st)
     rms_grad_kernel<E, K><<<parts, 32 * r.warps * r.rows, smem, st>>>(p, r.warps, parts);
     const int rc = launched();
     if (rc != SRWM_OK || !p.dgamma) return rc;
-    return sum_launch({p.part, parts, {p.dgamma, nullptr, nullptr}, {p.C, 0, 0}}, st);
+    return sum_launch({p.part, parts, {p.dgamma, nullptr, nullptr}, {p.C, 0, 0}, false}, st);
 }
 
 template <typename E>

@@ -26,7 +26,8 @@ struct SsmParams {
     long long ld_dz, ld_dbc;
     float *dA, *dskip, *ddt_bias, *dh_in;      // [D, N]; [D] or NULL; [B, D, N] or NULL
     float *seg_grad, *check, *bc_part, *part;  // workspace
-    int base, span;                            // check and bc_part hold sequences base .. base + span - 1
+    int base, span;                            // check, bc_part and part hold sequences base .. base + span - 1
+    long long cut_row;                         // part's first row of the sequences that are cut
 };
 
 size_t ssm_scratch(int B, int T, int D, int N, int G);

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
     if (tiles > 0) R.template load<true>(tiles - 1, stage0 + ((tiles - 1) & 1) * S::kStage);
     cp_async_commit();
     const int blocks = w.b < p.whole ? count.whole : count.cut;
-    float* const params = p.part + (w.b < p.whole ? static_cast<size_t>(w.b) * blocks : static_cast<size_t>(p.whole) * count.whole +
+    float* const params = p.part + (w.b < p.whole ? static_cast<size_t>(w.b - p.base) * blocks : static_cast<size_t>(p.cut_row) +
                                     (static_cast<size_t>(w.segment) * (p.B - p.whole) + (w.b - p.whole)) * blocks) * p.D * (N + 2);
     const size_t param_step = static_cast<size_t>(p.D) * (N + 2);
     float2 dA[2][4], dskip[2], dbias[2];
@@ -591,10 +591,11 @@ struct Plan {
     Blocks blocks;
     int chan_tiles;
     int slice;              // whole sequences of one launch: the workspace holds the states and partials of these alone
-    long long ctas, rows;   // CTAs of a sequence (or of a segment); rows of the parameters' partial sums
+    long long ctas;         // of a sequence (or of a segment)
+    long long whole_rows, cut_rows;   // rows of the parameters' partial sums, of the whole sequences of a launch and of the others
 };
 
-constexpr double kSliceBytes = 2e9;   // of the workspace, or one wave's need where that is more
+constexpr double kSliceBytes = 2e9;   // of the workspace's arrays by sequence, or one wave's need where that is more
 
 // Six CTAs on an SM (four in fp32, by shared memory).  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
 // CTAs) 229 and 599 us, 14 372 and 608, 20 714 and 816, 64 (of whose 1024 CTAs 112 are left over) 1222 and 1586.
@@ -607,11 +608,13 @@ Plan plan_of(size_t e, int B, int T, int D, int N, int G)
     plan.split = split_of(B, plan.ctas, T, (e == 4 ? 4 : 6) * kSms, 6 * kSms, 0.5, TT, 4 * TT);
     auto blocks = [](int tokens) { return (std::max(1, tokens) + kBlock * TT - 1) / (kBlock * TT); };
     plan.blocks = {blocks(T), blocks(plan.split.seg_len)};
-    const double each = static_cast<double>(T) * (static_cast<double>(D) * N * 4 / TT + plan.chan_tiles * 8.0 * G * N);
-    const long long wave = (6LL * kSms + plan.ctas - 1) / plan.ctas, room = each > 0 ? static_cast<long long>(kSliceBytes / each) : B;
+    // of one sequence: the states of every eighth token, dB's and dC's partials, the parameters'
+    const double each = static_cast<double>((T + TT - 1) / TT) * D * N * 4 + static_cast<double>(T) * plan.chan_tiles * 8.0 * G * N +
+                        static_cast<double>(plan.blocks.whole) * D * (N + 2) * 4;
+    const long long wave = (6LL * kSms + plan.ctas - 1) / plan.ctas, room = static_cast<long long>(kSliceBytes / each);
     plan.slice = static_cast<int>(std::min<long long>(B, std::max(wave, room / wave * wave)));
-    plan.rows = static_cast<long long>(plan.split.whole) * plan.blocks.whole +
-                static_cast<long long>(B - plan.split.whole) * plan.split.segments * plan.blocks.cut;
+    plan.whole_rows = static_cast<long long>(std::min(plan.slice, plan.split.whole)) * plan.blocks.whole;
+    plan.cut_rows = static_cast<long long>(B - plan.split.whole) * plan.split.segments * plan.blocks.cut;
     return plan;
 }
 
@@ -636,7 +639,8 @@ Regions regions_of(const Plan& plan, int B, int T, int D, int N, int G)
     const size_t held = std::max(plan.slice, B - plan.split.whole);   // sequences
     r.check = take(static_cast<size_t>((T + TT - 1) / TT) * held * D * N);
     r.bc_part = take(static_cast<size_t>(plan.chan_tiles) * held * T * G * 2 * N);
-    r.part = take(static_cast<size_t>(plan.rows) * D * (N + 2));
+    const long long rows = plan.slice >= B ? plan.whole_rows + plan.cut_rows : std::max(plan.whole_rows, plan.cut_rows);
+    r.part = take(static_cast<size_t>(rows) * D * (N + 2));
     r.bytes = std::max<size_t>(256, at * 4);
     return r;
 }
@@ -658,13 +662,16 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         ssm_local_kernel<E, N><<<cut, kThreads, S::kSmemLocal, st>>>(q);
         rc = launched();
     }
-    // one launch where the workspace holds all sequences; else a slice of whole ones at a time, and those that are cut
+    // one launch where the workspace holds all sequences; else a slice of whole ones at a time, and those that are cut; each
+    // adds its parameters' sums to those before it
     const bool at_once = plan.slice >= p.B;
     for (int base = 0; base < p.B && rc == SRWM_OK;) {
         SsmParams q = p;
         const bool last = base >= p.whole;
         q.base = base, q.span = at_once ? p.B : last ? p.B - p.whole : std::min(plan.slice, p.whole - base);
         q.first = static_cast<int>(plan.ctas * base);
+        q.cut_row = at_once ? plan.whole_rows : 0;
+        const long long rows = at_once ? plan.whole_rows + plan.cut_rows : last ? plan.cut_rows : static_cast<long long>(q.span) * plan.blocks.whole;
         const unsigned grid = at_once ? whole + cut : last ? cut : static_cast<unsigned>(plan.ctas * q.span);
         if (cut > 0 && base == 0)
             rc = launch_behind(ssm_grad_kernel<E, N>, dim3(grid), kThreads, S::kSmem, st, q, plan.blocks);
@@ -675,10 +682,11 @@ int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
         const long long quads = static_cast<long long>(q.span) * p.T * (2 * p.G * N / 4);
         if (quads > 0 && rc == SRWM_OK)
             rc = launch_behind(ssm_bc_kernel<E>, dim3(static_cast<unsigned>((quads + 255) / 256)), 256, 0, st, q, plan.chan_tiles);
+        if (rc == SRWM_OK)
+            rc = sum_launch({p.part, rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}, base > 0}, st);
         base += q.span;
     }
-    if (rc != SRWM_OK) return rc;
-    return sum_launch({p.part, plan.rows, {p.dA, p.dskip, p.ddt_bias}, {static_cast<long long>(p.D) * N, p.D, p.D}}, st);
+    return rc;
 }
 
 template <typename E>

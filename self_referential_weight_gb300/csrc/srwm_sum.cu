@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(1024) sum_kernel(const SumJob job)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         if (at < job.n[k]) {
-            if (job.out[k]) job.out[k][at] = a;
+            if (job.out[k]) job.out[k][at] = job.add ? job.out[k][at] + a : a;
             return;
         }
         at -= job.n[k];

@@ -117,6 +117,20 @@ def test_rmsnorm_refuses(lib):
     assert lib.srwm_rmsnorm_backward_workspace_bytes(4, 256) > 0 and lib.srwm_rmsnorm_backward_workspace_bytes(4, 20) == 0
 
 
+@pytest.mark.parametrize("B,T,D,N,G", [
+    (65536, 26, 256, 16, 1), (1 << 20, 8, 1024, 16, 1), (65536, 16, 1024, 64, 1), (4096, 26, 1024, 64, 1), (512, 8192, 2048, 64, 1),
+    (1 << 20, 0, 1024, 16, 1), (1 << 20, 1, 64, 32, 2), (70000, 257, 256, 16, 4), (64, 1024, 1024, 16, 1), (3, 100000, 512, 32, 1)])
+def test_ssm_gradients_workspace_is_bounded(lib, B, T, D, N, G):
+    """What the header says each sequence takes, for as many as fill the GPU (912 ranges of 1024 / N channels) or as 2 GB
+    hold; and what the segments of at most one such wave take beside it."""
+    ranges = G * -(-(D // G) // (1024 // N))
+    each = -(-T // 8) * D * N * 4 + T * ranges * 8 * N + max(1, -(-T // 256)) * D * (N + 2) * 4
+    wave = min(B, -(-912 // ranges))
+    segments = 912 * (1024 // N) * 4 * ((2 * N + 1) + (N + 2) * (T // 512 + 2))
+    need = lib.srwm_ssm_backward_workspace_bytes(B, T, D, N, G)
+    assert 0 < need <= max(2e9, wave * each) + segments + 4096
+
+
 def test_binding_refuses_what_is_not_on_a_gpu():
     x = torch.zeros(2, 3, 16)
     with pytest.raises(ValueError, match="CUDA"):

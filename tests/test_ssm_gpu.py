@@ -354,6 +354,34 @@ def test_gradients_in_slices():
             assert float((x.float() - part.float()).norm()) <= 2.0 ** -8 * float(part.float().norm()), name
 
 
+def param_grads(a, dy, lengths, **kw):
+    rest = {k: v for k, v in a.items() if k not in ("u", "dt", "A", "Bt", "Ct")}
+    return dict(zip(oracle.NAMES, binding.srwm_ssm_backward(a["u"], a["dt"], a["A"], a["Bt"], a["Ct"], dy, **rest, lengths=lengths, **kw)))
+
+
+@pytest.mark.parametrize("D,N,T,copies", [(1024, 16, 8, 640), (512, 64, 26, 100)])
+def test_parameter_gradients_of_large_batches(D, N, T, copies):
+    """Copies of 64 sequences, more than the workspace holds: the parameters' gradients are as many times the 64 sequences',
+    and each copy's own gradients are theirs.  What adding up the copies costs beside the 64 sequences' own bound: partial
+    sums in chains of at most a 32nd of the sequences, 5 joins and a few slices, each addition rounding by 2^-24 of the sum of
+    magnitudes, which that bound holds 64 T times."""
+    B = 64 * copies
+    a, dy, _ = make(T, 64, T, D, N, 1, BF16, state=False)
+    lengths = torch.arange(64, device=DEV, dtype=torch.int32) * 5 % (T + 1)
+    many = {k: v.repeat(copies, *[1] * (v.dim() - 1)) if k in ("u", "dt", "Bt", "Ct", "z") else v for k, v in a.items()}
+    each = T / 8 * D * N * 4 + T * -(-D // (1024 // N)) * 8 * N + D * (N + 2) * 4
+    assert B * each > 2.2e9 and binding.srwm_ssm_backward_workspace_bytes(B, T, D, N, 1) < 2.1e9
+    got = param_grads(many, dy.repeat(copies, 1, 1), lengths.repeat(copies))
+    ref = oracle.grads(dy, a, True, lengths)
+    _, _, err = oracle.errors(dy, a, True, lengths)
+    for name, x in got.items():
+        if name in ("A", "skip", "dt_bias"):
+            near(x, copies * ref[name], copies * err[name] * (1 + (B / 32 + 64) / (64 * T)), "d" + name)
+        elif x is not None:
+            assert torch.equal(x, x[:64].repeat(copies, *[1] * (x.dim() - 1))), "d" + name
+            near(x[:64], ref[name], err[name], "d" + name)
+
+
 def test_binding_refuses():
     a, dy, _ = make(1, 2, 5, 24, 16, 1, F32)
     call = lambda **kw: binding.srwm_ssm_forward(**{**a, **kw})  # noqa: E731
