@@ -359,6 +359,33 @@ def param_grads(a, dy, lengths, **kw):
     return dict(zip(oracle.NAMES, binding.srwm_ssm_backward(a["u"], a["dt"], a["A"], a["Bt"], a["Ct"], dy, **rest, lengths=lengths, **kw)))
 
 
+@pytest.mark.parametrize("T", [255, 256, 257, 600])
+def test_parameter_gradients_of_whole_sequences(T):
+    """Blocks of 256 tokens have partial sums of their own: inside, at and behind a block's end, and ragged lengths that leave
+    the last ones empty.  The 640 CTAs of 40 sequences are more than half of a wave of 912: nothing is cut."""
+    B, D, N = 40, 1024, 16
+    a, dy, dh = make(T, B, T, D, N, 1, BF16)
+    lengths = torch.tensor([T, 1, 0, 256, 255, 257, T - 1, 300], device=DEV, dtype=torch.int32).repeat(5)
+    for n in (None, lengths):
+        check_backward(a, dy, n, dh)
+
+
+def test_parameter_gradients_of_segments_of_several_blocks():
+    """448 CTAs of 7 sequences: two segments of 312 tokens each, with two blocks of partial sums; ragged ends in either."""
+    a, dy, dh = make(3, 7, 620, 4096, 16, 1, BF16)
+    lengths = torch.tensor([620, 600, 312, 313, 200, 0, 570], device=DEV, dtype=torch.int32)
+    for n in (None, lengths):
+        check_backward(a, dy, n, dh, joins=64)
+
+
+def test_parameter_gradients_of_whole_and_cut_sequences():
+    """fp32: 38 of 40 sequences fill a wave of 608 CTAs, the other two are cut; partial sums of both kinds beside each other."""
+    a, dy, dh = make(4, 40, 300, 1024, 16, 1, F32)
+    lengths = torch.arange(40, device=DEV, dtype=torch.int32) * 7 + 27
+    for n in (None, lengths):
+        check_backward(a, dy, n, dh, joins=64)
+
+
 @pytest.mark.parametrize("D,N,T,copies", [(1024, 16, 8, 640), (512, 64, 26, 100)])
 def test_parameter_gradients_of_large_batches(D, N, T, copies):
     """Copies of 64 sequences, more than the workspace holds: the parameters' gradients are as many times the 64 sequences',
