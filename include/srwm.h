@@ -584,7 +584,8 @@ int srwm_conv_backward(const void* x, long long ld, const float* weight, const f
  *              until the work on `stream` ends
  *
  * Supported: N in {16, 32, 64}, G divides D, D / G a multiple of 8, D at most
- * 2^24; A finite; T = 0 is valid (u, dt, Bt, Ct and y may be NULL then).
+ * 2^24; A finite, and a token's exp(s A), where it grows, within fp32's range;
+ * T = 0 is valid (u, dt, Bt, Ct and y may be NULL then).
  * States, steps and sums are fp32; y is rounded once.  An infinity or NaN in a valid token stays within
  * its sequence, and within its channel where it stands in u, dt or z.
  */

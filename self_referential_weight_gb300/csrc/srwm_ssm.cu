@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
                 float2 part[4];
                 load8(p.seg_state + (at + c) * N + n8, on, part);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) h[c][s] = fma2(ex2_2(mul2(both(sum[c]), A[c][s])), h[c][s], part[s]);
+                for (int s = 0; s < 4; ++s) h[c][s] = past_segment(both(sum[c]), A[c][s], h[c][s], part[s]);
             }
         }
     }

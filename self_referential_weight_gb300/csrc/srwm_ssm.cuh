@@ -42,6 +42,23 @@ __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x),
 // larger by 2e-8 centres them (64 x 1024 tokens, dL/dA: 1.8e-6 -> 0.8e-6 of itself off).  A step of 0 still gives exactly 1.
 __device__ __forceinline__ float2 decay2(float2 d, float2 A) { return ex2_2(fma2(d, A, both(2.0e-8f))); }
 
+// The smaller value, or NaN where one is.
+__device__ __forceinline__ float2 min2(float2 v, float most)
+{
+    float2 r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(v.x), "f"(most));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(v.y), "f"(most));
+    return r;
+}
+
+// What a segment leaves of the state (or gradient) v that comes to it, and its own: 2^(A sum) v + own.  In two halves, each
+// finite: growth past fp32's range keeps a state of 0 at 0, as it does token by token.
+__device__ __forceinline__ float2 past_segment(float2 sum, float2 A, float2 v, float2 own)
+{
+    const float2 half = ex2_2(min2(mul2(mul2(sum, both(0.5f)), A), 126.f));
+    return fma2(half, mul2(half, v), own);
+}
+
 // A step in units of log 2, log2(1 + 2^v) of its argument in these units: max(v, 0) + log2(1 + e), e = 2^-|v| in (0, 1].
 // log(1 + e) = 2 artanh(e / (2 + e)), and artanh(s) / s is a polynomial in s^2 <= 1/9 (minimax over that range by Remez'
 // exchange: within 4e-9 of itself), here in w = (2 s)^2 and times log2 e.  Far negative arguments keep the relative

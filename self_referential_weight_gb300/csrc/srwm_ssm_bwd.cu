@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "srwm.h"
 #include "srwm_check.h"
@@ -228,13 +229,15 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int s = 0; s < 4; ++s) h[k][s] = g[k][s] = both(0.f), far[k][s] = both(1.f);
-    for (int tile = 0; tile < R.tiles; ++tile) {
-        cp_async_wait<0>();
-        __syncthreads();   // the tile has landed, and all warps are done with the one before
-        if (tile + 1 < R.tiles) R.template load<true>(tile + 1, smem_u32(smem) + ((tile + 1) & 1) * S::kStage);
-        cp_async_commit();
-        R.template widen<true>(tile, smem + (tile & 1) * S::kStage, steps, xs, ps, Bf);
-        __syncthreads();
+    // where a decay can be above 1, far can be infinite, and a token without a gradient is to add nothing all the same
+    // (14 x 1024 x 1024 channels bf16: 367 us either way, 375 with the question asked of every warp)
+    bool grows = !R.softplus;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) grows |= A[k][s].x > 0.f || A[k][s].y > 0.f;
+    grows = __any_sync(0xffffffffu, grows);
+    auto run = [&](auto careful) {   // a tile's tokens
 #pragma unroll 2
         for (int r = 0; r < TT; ++r) {
             float2 dd[2], xx[2], pp[2], bb[4], cc[4], a[2][4];
@@ -251,10 +254,28 @@ __global__ void __launch_bounds__(kThreads) ssm_local_kernel(const __grid_consta
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     far[k][s] = mul2(far[k][s], a[k][s]);
-                    g[k][s] = fma2(far[k][s], mul2(cc[s], pp[k]), g[k][s]);
+                    const float2 c = mul2(cc[s], pp[k]);
+                    if constexpr (decltype(careful)::value) {
+                        if (c.x != 0.f) g[k][s].x = fmaf(far[k][s].x, c.x, g[k][s].x);
+                        if (c.y != 0.f) g[k][s].y = fmaf(far[k][s].y, c.y, g[k][s].y);
+                    } else {
+                        g[k][s] = fma2(far[k][s], c, g[k][s]);
+                    }
                 }
             }
         }
+    };
+    for (int tile = 0; tile < R.tiles; ++tile) {
+        cp_async_wait<0>();
+        __syncthreads();   // the tile has landed, and all warps are done with the one before
+        if (tile + 1 < R.tiles) R.template load<true>(tile + 1, smem_u32(smem) + ((tile + 1) & 1) * S::kStage);
+        cp_async_commit();
+        R.template widen<true>(tile, smem + (tile & 1) * S::kStage, steps, xs, ps, Bf);
+        __syncthreads();
+        if (grows)
+            run(std::true_type{});
+        else
+            run(std::false_type{});
     }
     cp_async_wait<0>();
     if (!on) return;
@@ -320,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 4 ? 4 : 6) ssm_grad_ker
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) v[k][s] = fma2(ex2_2(mul2(sum[k], A[k][s])), v[k][s], own[k][s]);
+                for (int s = 0; s < 4; ++s) v[k][s] = past_segment(sum[k], A[k][s], v[k][s], own[k][s]);
         };
 #pragma unroll 2
         for (int j = 0; j < w.segment; ++j) join(j, p.seg_state, h);

@@ -386,6 +386,22 @@ def test_parameter_gradients_of_whole_and_cut_sequences():
         check_backward(a, dy, n, dh, joins=64)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D,N", [(1, 1500, 64, 16), (2, 1031, 24, 32), (1, 700, 72, 64)])
+def test_growth_past_fp32_leaves_zeros(B, T, D, N, dtype):
+    """A cut axis, and half of the channels growing by e^100 and more over a segment: states that are 0 until the last token
+    and gradients that are 0 from the second token on stay so, as token by token."""
+    a, dy, _ = make(T + 1, B, T, D, N, 1, dtype, state=False, top=3.5)
+    assert binding.srwm_ssm_workspace_bytes(B, T, D, N, 1) > 256
+    a["A"][::2] = 3 + torch.rand(D // 2, N, device=DEV)
+    a["dt"] = a["dt"].clamp(-1, 1)
+    a["dt_bias"] = a["dt_bias"].clamp(0, 3)       # steps of 0.3 to 4: a decay of e^16 at most
+    a["u"][:, :-1, ::2] = 0
+    dy[:, 1:, ::2] = 0
+    check_forward(a, joins=64)
+    check_backward(a, dy, joins=64)
+
+
 @pytest.mark.parametrize("D,N,T,copies", [(1024, 16, 8, 640), (512, 64, 26, 100)])
 def test_parameter_gradients_of_large_batches(D, N, T, copies):
     """Copies of 64 sequences, more than the workspace holds: the parameters' gradients are as many times the 64 sequences',
