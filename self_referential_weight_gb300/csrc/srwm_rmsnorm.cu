@@ -331,7 +331,7 @@ RowPlan row_plan(size_t e, long long N, int C)
 
 // The gradients' rows take up to two vectors a thread where they fit (their partial sums stay in registers), and as many
 // CTAs as run at once.
-RowPlan grad_plan(size_t e, long long N, int C)
+RowPlan grad_plan(size_t e, int C)
 {
     const int nv = C / static_cast<int>(16 / e);
     RowPlan r{};
@@ -367,7 +367,7 @@ int backward(const RmsParams& p0, const RowPlan& r, cudaStream_t st)
     RmsParams p = p0;
     if (!p.dgamma) p.part = nullptr;
     const int parts = grad_parts(r, p.N);
-    const size_t smem = r.rows > 1 && p.part ? static_cast<size_t>(r.rows) * p.C * 4 : 0;   // a warp's row: at most 16 KB for four
+    const size_t smem = r.rows > 1 && p.part ? static_cast<size_t>(r.rows) * p.C * 4 : 0;   // a warp's row: at most 16 KB for eight
     rms_grad_kernel<E, K><<<parts, 32 * r.warps * r.rows, smem, st>>>(p, r.warps, parts);
     const int rc = launched();
     if (rc != SRWM_OK || !p.dgamma) return rc;
@@ -384,7 +384,7 @@ int by_vectors(const RmsParams& p, int out, cudaStream_t st)
 template <typename E>
 int grad_by_vectors(const RmsParams& p, cudaStream_t st)
 {
-    const RowPlan r = grad_plan(sizeof(E), p.N, p.C);
+    const RowPlan r = grad_plan(sizeof(E), p.C);
     if constexpr (sizeof(E) == 4)
         if (r.vectors == 4) return backward<E, 4>(p, r, st);   // more than 4096 channels
     return r.vectors == 1 ? backward<E, 1>(p, r, st) : backward<E, 2>(p, r, st);
@@ -394,7 +394,7 @@ int grad_by_vectors(const RmsParams& p, cudaStream_t st)
 
 size_t rmsnorm_backward_scratch(long long N, int C)
 {
-    const int parts = std::max(grad_parts(grad_plan(4, N, C), N), grad_parts(grad_plan(2, N, C), N));
+    const int parts = std::max(grad_parts(grad_plan(4, C), N), grad_parts(grad_plan(2, C), N));
     return round256(static_cast<size_t>(parts) * C * 4);
 }
 

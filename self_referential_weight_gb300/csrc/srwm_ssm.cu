@@ -35,7 +35,7 @@ using namespace ssm;
 
 constexpr int kSms = 152;
 constexpr int kWhole = 16;   // segments are multiples of this many tokens, whole tiles of either size
-constexpr int kLaneCh = 2;
+constexpr int kLaneCh = 2;   // as one float2 of their floats, and one shuffle between the two halves of a warp
 constexpr int kPromptWarps = 2;
 constexpr int kPromptThreads = 32 * kPromptWarps;
 
@@ -67,16 +67,11 @@ __device__ __forceinline__ void store8(float* to, const float2 (&h)[4])
     *reinterpret_cast<float4*>(to + 4) = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
 }
 
-// kLaneCh neighbouring floats.
+// A lane's neighbouring channels.
 __device__ __forceinline__ void load_ch(const float* from, float (&v)[kLaneCh])
 {
-    if constexpr (kLaneCh == 4) {
-        const float4 q = *reinterpret_cast<const float4*>(from);
-        v[0] = q.x, v[1] = q.y, v[kLaneCh - 2] = q.z, v[kLaneCh - 1] = q.w;
-    } else {
-        const float2 q = *reinterpret_cast<const float2*>(from);
-        v[0] = q.x, v[1] = q.y;
-    }
+    const float2 q = *reinterpret_cast<const float2*>(from);
+    v[0] = q.x, v[1] = q.y;
 }
 
 // What one token takes from shared memory.
@@ -257,23 +252,13 @@ __global__ void __launch_bounds__(kPromptThreads, 7) ssm_kernel(const __grid_con
                 if (OUT) o[c] = sum.x + sum.y;
                 if (!OUT) total[c] += now.d[c];
             }
-            if constexpr (OUT) {   // the channels' sums over their lanes: each half of these takes half of the channels
+            if constexpr (OUT) {   // the channels' sums over their lanes: each half of these takes one of the two
                 const bool up = lane & 16;
-                float v[kLaneCh / 2];
+                float v = (up ? o[1] : o[0]) + __shfl_xor_sync(0xffffffffu, up ? o[0] : o[1], 16);
 #pragma unroll
-                for (int c = 0; c < kLaneCh / 2; ++c) {
-                    v[c] = (up ? o[kLaneCh / 2 + c] : o[c]) + __shfl_xor_sync(0xffffffffu, up ? o[c] : o[kLaneCh / 2 + c], 16);
-#pragma unroll
-                    for (int k = 8; k >= S::kSets; k >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], k);
-                }
+                for (int k = 8; k >= S::kSets; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
                 // in their inputs' place, which all lanes have read
-                if (S::kSets == 16 || (lane & 15) < S::kSets) {
-                    float* const to = xs + r * S::kPitch + own + (up ? kLaneCh / 2 : 0);
-                    if constexpr (kLaneCh == 4)
-                        *reinterpret_cast<float2*>(to) = make_float2(v[0], v[kLaneCh / 2 - 1]);
-                    else
-                        *to = v[0];
-                }
+                if (S::kSets == 16 || (lane & 15) < S::kSets) xs[r * S::kPitch + own + up] = v;
             }
             now = next;
         };
@@ -412,11 +397,7 @@ int forward(const SsmParams& p, cudaStream_t st)
     using S = Tile<E, N>;
     const int dg = p.D / p.G;
     const unsigned ctas = static_cast<unsigned>(p.G) * ((dg + S::kCh - 1) / S::kCh), split = ctas * (p.B - p.whole);
-    if (cudaFuncSetAttribute(ssm_kernel<E, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(ssm_kernel<E, N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return SRWM_ERR_CUDA;
-    }
+    static_assert(S::kSmem <= 48 * 1024, "more needs the kernels' attribute");
     if (split > 0) {
         SsmParams q = p;
         q.first = static_cast<int>(ctas * p.whole);

@@ -670,11 +670,7 @@ template <typename E, int N>
 int backward(const SsmParams& p, const Plan& plan, cudaStream_t st)
 {
     using S = Tile<E, N>;
-    if (cudaFuncSetAttribute(ssm_grad_kernel<E, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(ssm_local_kernel<E, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemLocal) != cudaSuccess) {
-        cudaGetLastError();
-        return SRWM_ERR_CUDA;
-    }
+    static_assert(S::kSmem <= 48 * 1024 && S::kSmemLocal <= 48 * 1024, "more needs the kernels' attribute");
     const unsigned whole = static_cast<unsigned>(plan.ctas * p.whole), cut = static_cast<unsigned>(plan.ctas * (p.B - p.whole) * p.segments);
     int rc = SRWM_OK;
     if (cut > 0) {
