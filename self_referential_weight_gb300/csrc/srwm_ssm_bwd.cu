@@ -16,8 +16,9 @@
 //
 // What bounds it: 17 fp32 operations and three exponentials for each token, channel and state (three forwards, two and a
 // quarter forwards once more, the rest backwards), with issue around them and shared memory's rate near.  64 x 1024 tokens
-// of 1024 channels of 16 states, gated, in bf16 take 1.22 ms: 948 MB, the fp32 pipe at 48 %, shared memory at 64 %, 53 %
-// of the issue slots, where a two-wide operation holds two.  States of every other token in shared memory, and 168
+// of 1024 channels of 16 states, gated, in bf16 take 1.22 ms: 948 MB of inputs and gradients and 0.7 GB of states and
+// partial sums, written and read, the fp32 pipe at 48 %, shared memory at 64 %, 53 % of the issue slots, where a two-wide
+// operation holds two.  States of every other token in shared memory, and 168
 // registers, leave room for six CTAs of two warps on an SM (57 sequences: 1167 us; four with 250 registers: 1372).
 #include <cuda_runtime.h>
 
@@ -618,7 +619,9 @@ struct Plan {
 
 constexpr double kSliceBytes = 2e9;   // of the workspace's arrays by sequence, or one wave's need where that is more
 
-// Six CTAs on an SM (four in fp32, by shared memory).  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
+// Six CTAs on an SM, in fp32 four: with 255 registers no more fit, and with fewer (five, spilling none) 64 x 1024 x 1024
+// channels take 1506 us instead of 1626, but 38 sequences, which fill a wave of four, 847 instead of 835 and 128 x 26 x 256
+// 35.4 instead of 34.9.  Cut against whole, N x 1024 x 1024 channels bf16: 8 sequences (128
 // CTAs) 229 and 599 us, 14 372 and 608, 20 714 and 816, 64 (of whose 1024 CTAs 112 are left over) 1222 and 1586.
 Plan plan_of(size_t e, int B, int T, int D, int N, int G)
 {
